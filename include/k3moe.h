@@ -320,6 +320,90 @@ int k3moe_layer(k3moe_shape s, const float *logits, const uint16_t *x, const k3m
 int k3moe_combine_residual(k3moe_shape s, const float *Y, const float *w, const int32_t *inv, const uint16_t *residual,
                            uint16_t *out, float *out_f32, k3moe_stream_t stream);
 
+/* ---- The operators around the MoE path in a decoder layer ------------------
+ * RMS norm with the residual's addition (before the attention, and before the
+ * router and the experts), the paged key-value cache and attention of one new
+ * token over it.  No counterpart API on the pages (they name the attention and a
+ * cache of 96 heads, not an interface).
+ *
+ * 8-bit data: E4M3 codes (OCP 8-bit floating point, "FP8": largest value 448, 0x7F /
+ * 0xFF NaN) and one E8M0 byte per group (value 2^(byte-127), 255 NaN).  The scale is the
+ * smallest power of two X with max|v| <= 448 X, its exponent clamped to -127 ..
+ * 127 (an all-zero group: byte 0); a code is v / X rounded to nearest, ties to even.  A
+ * group holding a NaN or an infinity has byte 255 and codes 0x7F. */
+
+/* RMS norm of T rows of H values (H a multiple of 32 in [32, 16384]):
+ *   a = x + residual  (fp32; a = x when residual is NULL)
+ *   y = a * rsqrt(mean(a^2) + eps) * weight  (fp32)
+ * and any of
+ *   residual_out : uint16 [T][H], bf16_rne(a), or NULL
+ *   y            : uint16 [T][H], bf16_rne(y), or NULL
+ *   codes        : uint8  [T][H] E4M3 codes of y (from the fp32 values) with
+ *   scales       : uint8  [T][H/32] their E8M0 scales, one per 32 values; both or neither
+ * x, residual : uint16 [T][H] bf16;  weight : uint16 [H] bf16;  eps finite, >= 0.
+ * residual_out and y may each be the same buffer as x or residual (not both the same
+ * one).  All arrays but scales 16-byte aligned (K3MOE_ERR_ALIGN).  No output
+ * at all, or one of codes / scales alone -> K3MOE_ERR_ARG. */
+int k3moe_rmsnorm(int32_t T, int32_t H, const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps,
+                  uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales, k3moe_stream_t stream);
+
+/* A paged key-value cache of one layer, in the caller's device memory:
+ *   k, v : [pages][heads][page_size][dim], bf16 values or E4M3 codes (16-byte aligned)
+ *   k_scales, v_scales : uint8 [pages][heads][page_size] E8M0, one per (token, head)
+ *                        vector (K3MOE_KV_E4M3; NULL for K3MOE_KV_BF16)
+ * pages >= 1, page_size a power of two in [16, 1024], heads in [1, 1024], dim 64, 128 or
+ * 256, pages * page_size < 2^31 (else K3MOE_ERR_SHAPE).  A slot, page * page_size +
+ * place, names one token's position. */
+#define K3MOE_KV_BF16 0
+#define K3MOE_KV_E4M3 1
+typedef struct {
+  int32_t pages, page_size, heads, dim, format;
+  void *k, *v;
+  uint8_t *k_scales, *v_scales;
+} k3moe_kv_cache;
+
+/* Write n tokens' keys and values into their slots, quantised for K3MOE_KV_E4M3.
+ *   k, v  : bf16; token t's vectors are [heads][dim] starting k_stride (v_stride) * t
+ *           values in (strides >= heads * dim, multiples of 8; slices of a fused
+ *           projection need no copy); 16-byte aligned
+ *   slots : int32 [n], distinct where not negative (two tokens on one slot: one of them
+ *           remains); negative = padding, not written; past the end: not written and
+ *           K3MOE_DEV_BOUNDS */
+int k3moe_kv_write(const k3moe_kv_cache *cache, int32_t n, const uint16_t *k, const uint16_t *v, int64_t k_stride,
+                   int64_t v_stride, const int32_t *slots, int32_t *dev_status, k3moe_stream_t stream);
+
+/* Read n slots back as bf16 (code * scale, rounded once):
+ *   k, v : uint16 [n][heads][dim], 16-byte aligned; zeros for a negative slot, and for one
+ *          past the end (K3MOE_DEV_BOUNDS) */
+int k3moe_kv_read(const k3moe_kv_cache *cache, int32_t n, const int32_t *slots, uint16_t *k, uint16_t *v,
+                  int32_t *dev_status, k3moe_stream_t stream);
+
+/* Attention of one new token of each of B sequences over the cache: query head h
+ * reads key-value head h / (Hq / heads).  With n = seq_lens[b] (the new token's own key
+ * and value included, if it is to see itself: write them first), the places seen are
+ * max(0, n - window) .. n - 1 (window 0: all), place i lying in page
+ * block_table[b][i / page_size]:
+ *   s_i = scale * q . K_i ;  out = sum softmax(s)_i V_i ;  lse = log sum exp(s_i)
+ * A row that sees nothing gives out = 0, lse = -inf.  What lies in places not seen is
+ * not used, whatever it holds.
+ *   q           : bf16; sequence b's [Hq][dim] starts q_stride * b values in (q_stride >=
+ *                 Hq * dim, a multiple of 8), 16-byte aligned
+ *   block_table : int32 [B][max_pages]; entries past a sequence's length are not read
+ *   seq_lens    : int32 [B]; negative counts as 0 and more than max_pages * page_size as
+ *                 that, both with K3MOE_DEV_BOUNDS
+ *   scale       : finite (commonly dim^-1/2)
+ *   out         : uint16 [B][Hq][dim] bf16, 16-byte aligned
+ *   lse         : float [B][Hq] or NULL
+ *   ws          : k3moe_attn_decode_workspace_bytes(cache, B, Hq) bytes, 256-byte aligned
+ * A page number outside the cache sets K3MOE_DEV_BOUNDS; its places count as not seen.
+ * Accumulation: exact products summed in fp32, softmax in fp32; before the product with V
+ * the weights are rounded (bf16 cache: to bf16; E4M3 cache: to f16, together with the
+ * scale of V).  Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, max_pages >= 1. */
+size_t k3moe_attn_decode_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t Hq);
+int k3moe_attn_decode(const k3moe_kv_cache *cache, int32_t B, int32_t Hq, const uint16_t *q, int64_t q_stride,
+                      const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, float scale,
+                      uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, k3moe_stream_t stream);
+
 /* Self-test of the bounded waits (a test hook, not part of the path): one
  * thread waits, with the iteration bound every mbarrier wait in the tensor-core
  * kernels uses, on a phase that nothing completes, so the wait runs out: the

@@ -26,6 +26,7 @@ K3MOE_NOALLOC_SCRATCH_BYTES = 8 << 20
 K3MOE_DEV_NONFINITE, K3MOE_DEV_BOUNDS, K3MOE_DEV_TIMEOUT = 1, 2, 4
 K3MOE_FFN_AUTO, K3MOE_FFN_GEMV, K3MOE_FFN_STREAM, K3MOE_FFN_GEMM, K3MOE_FFN_W4A4 = 0, 1, 2, 3, 4
 K3MOE_OP_BUCKET, K3MOE_OP_EXPERT_FFN, K3MOE_OP_LAYER = 1, 2, 3
+K3MOE_KV_BF16, K3MOE_KV_E4M3 = 0, 1
 
 
 class K3moeError(RuntimeError):
@@ -49,6 +50,12 @@ class Shape(ctypes.Structure):
 class _WeightsC(ctypes.Structure):
     _fields_ = [("w13_codes", ctypes.c_void_p), ("w13_scales", ctypes.c_void_p),
                 ("w2_codes", ctypes.c_void_p), ("w2_scales", ctypes.c_void_p)]
+
+
+class _KVCacheC(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("format", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -99,6 +106,17 @@ def lib():
             L.k3moe_layer.restype = i32
             L.k3moe_layer.argtypes = [Shape, vp, vp, ctypes.POINTER(_WeightsC), vp, vp, vp, vp, vp, vp, vp, vp, vp, i32,
                                       vp, sz, vp, vp]
+            i64, f32, kvc = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(_KVCacheC)
+            L.k3moe_rmsnorm.restype = i32
+            L.k3moe_rmsnorm.argtypes = [i32, i32, vp, vp, vp, f32, vp, vp, vp, vp, vp]
+            L.k3moe_kv_write.restype = i32
+            L.k3moe_kv_write.argtypes = [kvc, i32, vp, vp, i64, i64, vp, vp, vp]
+            L.k3moe_kv_read.restype = i32
+            L.k3moe_kv_read.argtypes = [kvc, i32, vp, vp, vp, vp, vp]
+            L.k3moe_attn_decode_workspace_bytes.restype = sz
+            L.k3moe_attn_decode_workspace_bytes.argtypes = [kvc, i32, i32]
+            L.k3moe_attn_decode.restype = i32
+            L.k3moe_attn_decode.argtypes = [kvc, i32, i32, vp, i64, vp, i32, vp, i32, f32, vp, vp, vp, sz, vp, vp]
             L.k3moe_selftest_bounded_wait.restype = i32
             L.k3moe_selftest_bounded_wait.argtypes = [vp, vp, vp]
             L.k3moe_status_string.restype = ctypes.c_char_p
@@ -316,3 +334,137 @@ def k3moe_layer(shape, logits, x, weights: Weights, idx, w, counts, offsets, per
                            _ptr(ws, None, "ws"), ws_bytes, _ptr(dev_status, torch.int32, "dev_status"),
                            _stream(stream))
     _check("k3moe_layer", rc)
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)   # E4M3 codes, or their bytes
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)  # E8M0 scales, or their bytes
+
+
+def _want(t, shape, name):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def k3moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, stream=None):
+    """RMS norm of the rows of x [T, H] (bf16), a = x + residual first: any of
+    residual_out = bf16(a), y = bf16(norm * weight), and codes [T, H] (E4M3) with
+    scales [T, H/32] (E8M0) of the norm times weight."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x: expected a tensor [T, H]")
+    T, H = x.shape
+    if weight is not None:
+        _want(weight, (H,), "weight")
+    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (y, "y"), (codes, "codes")):
+        if t is not None:
+            _want(t, (T, H), name)
+    if scales is not None:
+        _want(scales, (T, H // 32), "scales")
+    rc = lib().k3moe_rmsnorm(T, H, _ptr(x, _BF16, "x"), _ptr(residual, _BF16, "residual"),
+                             _ptr(weight, _BF16, "weight"), float(eps), _ptr(residual_out, _BF16, "residual_out"),
+                             _ptr(y, _BF16, "y"), _ptr(codes, _CODES, "codes"), _ptr(scales, _SCALES, "scales"),
+                             _stream(stream))
+    _check("k3moe_rmsnorm", rc)
+
+
+class KVCache:
+    """A paged key-value cache over the caller's CUDA tensors: k, v [pages, heads,
+    page_size, dim] in bf16, or E4M3 codes (float8_e4m3fn or uint8) with E8M0 scales
+    [pages, heads, page_size] (float8_e8m0fnu or uint8)."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k: expected a tensor [pages, heads, page_size, dim]")
+        quantised = k.dtype in _CODES
+        pages, heads, page_size, dim = k.shape
+        _want(v, tuple(k.shape), "v")
+        if quantised != (k_scales is not None) or quantised != (v_scales is not None):
+            raise ValueError("k_scales and v_scales belong to an 8-bit cache, and only to one")
+        if quantised:
+            _want(k_scales, (pages, heads, page_size), "k_scales")
+            _want(v_scales, (pages, heads, page_size), "v_scales")
+        kind = _CODES if quantised else _BF16
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
+        self.format = K3MOE_KV_E4M3 if quantised else K3MOE_KV_BF16
+        self._c = _KVCacheC(pages, page_size, heads, dim, self.format, _ptr(k, kind, "k"), _ptr(v, kind, "v"),
+                            _ptr(k_scales, _SCALES, "k_scales"), _ptr(v_scales, _SCALES, "v_scales"))
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, dim: int, fmt: int = K3MOE_KV_E4M3, device="cuda"):
+        """A cache in new memory (its contents are undefined until they are written)."""
+        def new(shape, dtype):
+            return torch.empty(shape, dtype=dtype, device=device)
+        shape = (pages, heads, page_size, dim)
+        if fmt == K3MOE_KV_E4M3:
+            return cls(new(shape, torch.uint8), new(shape, torch.uint8), new(shape[:3], torch.uint8),
+                       new(shape[:3], torch.uint8))
+        return cls(new(shape, torch.bfloat16), new(shape, torch.bfloat16))
+
+
+def _rows(t, shape, name):
+    """Pointer and stride (values) of tokens' vectors [n, heads, dim]: packed but for the first axis."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
+    _want(t, shape, name)
+    n, heads, dim = shape
+    if n == 0:
+        return None, heads * dim
+    _, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
+        raise ValueError(f"{name}: heads and dim must be packed (only the first axis may have a stride)")
+    return t.data_ptr(), t.stride(0) if n > 1 else heads * dim
+
+
+def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
+    """Keys and values k, v [n, heads, dim] (bf16; the first axis may be strided) into
+    the cache's slots [n] (int32, page * page_size + place; negative = padding)."""
+    shape = (slots.numel(), cache.heads, cache.dim)
+    kp, ks = _rows(k, shape, "k")
+    vp, vs = _rows(v, shape, "v")
+    rc = lib().k3moe_kv_write(cache._ref, shape[0], kp, vp, ks, vs, _ptr(slots, torch.int32, "slots"),
+                              _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check("k3moe_kv_write", rc)
+
+
+def k3moe_kv_read(cache: KVCache, slots, k, v, dev_status=None, stream=None):
+    """The cache's slots [n] (int32) as bf16 keys and values k, v [n, heads, dim] (zeros
+    for a negative slot)."""
+    shape = (slots.numel(), cache.heads, cache.dim)
+    _want(k, shape, "k")
+    _want(v, shape, "v")
+    rc = lib().k3moe_kv_read(cache._ref, shape[0], _ptr(slots, torch.int32, "slots"), _ptr(k, _BF16, "k"),
+                             _ptr(v, _BF16, "v"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check("k3moe_kv_read", rc)
+
+
+def k3moe_attn_decode_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> int:
+    return int(lib().k3moe_attn_decode_workspace_bytes(cache._ref, batch, q_heads))
+
+
+def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, scale=None, window: int = 0, ws=None,
+                      dev_status=None, stream=None):
+    """Attention of one new token per sequence: q [B, Hq, dim] (bf16; the first axis
+    may be strided), block_table [B, max_pages] and seq_lens [B] (int32) -> out
+    [B, Hq, dim] (bf16), lse [B, Hq] (fp32).  scale defaults to dim^-1/2; window > 0
+    sees only the last that many tokens; ws: k3moe_attn_decode_workspace_bytes."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or block_table.dim() != 2:
+        raise ValueError("q: expected a tensor [B, Hq, dim], block_table: [B, max_pages]")
+    B, Hq, _ = q.shape
+    shape = (B, Hq, cache.dim)
+    qp, qs = _rows(q, shape, "q")
+    _want(out, shape, "out")
+    _want(seq_lens, (B,), "seq_lens")
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table: expected {B} rows, got {block_table.shape[0]}")
+    if lse is not None:
+        _want(lse, (B, Hq), "lse")
+    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    rc = lib().k3moe_attn_decode(cache._ref, B, Hq, qp, qs, _ptr(block_table, torch.int32, "block_table"),
+                                 block_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens"), int(window),
+                                 cache.dim ** -0.5 if scale is None else float(scale), _ptr(out, _BF16, "out"),
+                                 _ptr(lse, torch.float32, "lse"), _ptr(ws, None, "ws"), ws_bytes,
+                                 _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    _check("k3moe_attn_decode", rc)

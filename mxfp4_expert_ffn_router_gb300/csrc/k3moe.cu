@@ -3,6 +3,7 @@
 // otherwise enqueues its kernels on the caller's stream without synchronising.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "../../include/k3moe.h"
@@ -292,6 +293,94 @@ int k3moe_combine_residual(k3moe_shape s, const float *Y, const float *w, const 
   if ((rc = abi_check_arch())) return rc;
   return abi_launched(
       k3moe::launch_combine(s, Y, w, inv, residual, out, out_f32, reinterpret_cast<k3moe_stream>(stream)));
+}
+
+int k3moe_rmsnorm(int32_t T, int32_t H, const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps,
+                  uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales, k3moe_stream_t stream) {
+  if (T < 0 || H < 32 || H > 16384 || H % 32) return K3MOE_ERR_SHAPE;
+  if (!(eps >= 0.f) || std::isinf(eps)) return K3MOE_ERR_ARG;
+  if (T == 0) return K3MOE_OK;
+  if (!x || !weight || (!residual_out && !y && !codes) || !codes != !scales) return K3MOE_ERR_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) || !aligned16(y) ||
+      !aligned16(codes))
+    return K3MOE_ERR_ALIGN;
+  int rc;
+  if ((rc = abi_check_arch())) return rc;
+  return abi_launched(k3moe::launch_rmsnorm(T, H, x, residual, weight, eps, residual_out, y, codes, scales,
+                                            reinterpret_cast<k3moe_stream>(stream)));
+}
+
+// The cache's shape, then its pointers.
+static int kv_check(const k3moe_kv_cache *c) {
+  if (!c) return K3MOE_ERR_ARG;
+  if (c->format != K3MOE_KV_BF16 && c->format != K3MOE_KV_E4M3) return K3MOE_ERR_ARG;
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256) return K3MOE_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return K3MOE_ERR_SHAPE;
+  if (c->heads < 1 || c->heads > 1024 || c->pages < 1) return K3MOE_ERR_SHAPE;
+  if (static_cast<long long>(c->pages) * c->page_size >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+  if (!c->k || !c->v) return K3MOE_ERR_ARG;
+  if (c->format == K3MOE_KV_E4M3 && (!c->k_scales || !c->v_scales)) return K3MOE_ERR_ARG;
+  if (!aligned16(c->k) || !aligned16(c->v)) return K3MOE_ERR_ALIGN;
+  return K3MOE_OK;
+}
+
+int k3moe_kv_write(const k3moe_kv_cache *cache, int32_t n, const uint16_t *k, const uint16_t *v, int64_t k_stride,
+                   int64_t v_stride, const int32_t *slots, int32_t *dev_status, k3moe_stream_t stream) {
+  int rc = kv_check(cache);
+  if (rc) return rc;
+  if (n < 0) return K3MOE_ERR_SHAPE;
+  if (n == 0) return K3MOE_OK;
+  if (!k || !v || !slots) return K3MOE_ERR_ARG;
+  const int64_t row = static_cast<int64_t>(cache->heads) * cache->dim;
+  if (k_stride < row || v_stride < row) return K3MOE_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || k_stride % 8 || v_stride % 8) return K3MOE_ERR_ALIGN;
+  if ((rc = abi_check_arch())) return rc;
+  return abi_launched(k3moe::launch_kv_write(*cache, n, k, v, k_stride, v_stride, slots, dev_status,
+                                             reinterpret_cast<k3moe_stream>(stream)));
+}
+
+int k3moe_kv_read(const k3moe_kv_cache *cache, int32_t n, const int32_t *slots, uint16_t *k, uint16_t *v,
+                  int32_t *dev_status, k3moe_stream_t stream) {
+  int rc = kv_check(cache);
+  if (rc) return rc;
+  if (n < 0) return K3MOE_ERR_SHAPE;
+  if (n == 0) return K3MOE_OK;
+  if (!k || !v || !slots) return K3MOE_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v)) return K3MOE_ERR_ALIGN;
+  if ((rc = abi_check_arch())) return rc;
+  return abi_launched(
+      k3moe::launch_kv_read(*cache, n, slots, k, v, dev_status, reinterpret_cast<k3moe_stream>(stream)));
+}
+
+static int attn_check(const k3moe_kv_cache *c, int32_t B, int32_t Hq) {
+  const int rc = kv_check(c);
+  if (rc) return rc;
+  if (B < 0 || B > 65535 || Hq < 1 || Hq > 16384 || Hq % c->heads) return K3MOE_ERR_SHAPE;
+  return K3MOE_OK;
+}
+
+size_t k3moe_attn_decode_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t Hq) {
+  return attn_check(cache, B, Hq) ? 0 : k3moe::attn_decode_workspace(*cache, B, Hq);
+}
+
+int k3moe_attn_decode(const k3moe_kv_cache *cache, int32_t B, int32_t Hq, const uint16_t *q, int64_t q_stride,
+                      const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, float scale,
+                      uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, k3moe_stream_t stream) {
+  int rc = attn_check(cache, B, Hq);
+  if (rc) return rc;
+  if (max_pages < 1 || window < 0) return K3MOE_ERR_SHAPE;
+  if (static_cast<long long>(max_pages) * cache->page_size >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+  if (!std::isfinite(scale)) return K3MOE_ERR_ARG;
+  if (B == 0) return K3MOE_OK;
+  if (!q || !block_table || !seq_lens || !out) return K3MOE_ERR_ARG;
+  if (q_stride < static_cast<int64_t>(Hq) * cache->dim) return K3MOE_ERR_SHAPE;
+  if (!aligned16(q) || q_stride % 8 || !aligned16(out)) return K3MOE_ERR_ALIGN;
+  const size_t need = k3moe::attn_decode_workspace(*cache, B, Hq);
+  if (need && (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))) return K3MOE_ERR_WORKSPACE;
+  if ((rc = abi_check_arch())) return rc;
+  return abi_launched(k3moe::launch_attn_decode(*cache, B, Hq, q, q_stride, block_table, max_pages, seq_lens, window,
+                                                scale, out, lse, ws, dev_status,
+                                                reinterpret_cast<k3moe_stream>(stream)));
 }
 
 const char *k3moe_last_cuda_error(void) { return t_last_cuda_error; }

@@ -1,0 +1,114 @@
+// rmsnorm.cu -- root-mean-square norm of rows, with the residual's addition before
+// it and an 8-bit output beside or instead of the bf16 one.
+//
+//   a[t] = x[t] + residual[t]                          (fp32, exact sum rounded once)
+//   y[t] = a[t] * rsqrt(mean(a[t]^2) + eps) * weight   (fp32)
+//   residual_out = bf16(a),  y = bf16(y),  codes / scales = y per 32 values (mx8_quant.cuh)
+//
+// The norm is of the fp32 sum, not of the bf16 value that residual_out keeps: the sum is
+// in registers anyway, and rounding it first would only lose bits.  The mean is a fixed
+// tree: a thread's values in order, a butterfly over the warp, the warps in order.
+#include "k3moe_dev.cuh"
+#include "k3moe_launch.h"
+#include "mx8_quant.cuh"
+
+namespace k3moe {
+
+namespace {
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    v[2 * m] = __uint_as_float(w[m] << 16);
+    v[2 * m + 1] = __uint_as_float(w[m] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 f32x8_to_bf16(const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+    w[m] = f32_to_bf16_rne(v[2 * m]) | (static_cast<uint32_t>(f32_to_bf16_rne(v[2 * m + 1])) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace
+
+// One block per row; a thread holds CH chunks of 8 values (chunk = tid + i * blockDim).
+template <int CH>
+__global__ void __launch_bounds__(512)
+    rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, float eps, int H,
+                   uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
+  __shared__ float part[16];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, nth = blockDim.x, nch = H / 8;
+  const size_t row = static_cast<size_t>(blockIdx.x) * H;
+  float a[CH][8];
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * nth;
+    if (c < nch) {
+      bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(x + row) + c), a[i]);
+      if (residual) {
+        float r[8];
+        bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(residual + row) + c), r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) a[i][q] += r[q];
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sum = fmaf(a[i][q], a[i][q], sum);
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+  if ((tid & 31) == 0) part[tid >> 5] = sum;
+  __syncthreads();
+  float total = 0.f;
+  for (int w = 0; w < nth / 32; ++w) total += part[w];
+  const float inv = rsqrtf(total / static_cast<float>(H) + eps);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * nth;
+    // the four lanes of a 32-value group are in or out together (H % 32 == 0)
+    const unsigned in = __ballot_sync(0xFFFFFFFFu, c < nch);
+    if (c < nch) {
+      if (residual_out) *(reinterpret_cast<uint4 *>(residual_out + row) + c) = f32x8_to_bf16(a[i]);
+      float w[8];
+      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(weight) + c), w);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) a[i][q] = a[i][q] * inv * w[q];
+      if (y) *(reinterpret_cast<uint4 *>(y + row) + c) = f32x8_to_bf16(a[i]);
+      if (codes) {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(a[i][q]) & 0x7FFFFFFFu);
+        m = max(m, __shfl_xor_sync(in, m, 1));
+        m = max(m, __shfl_xor_sync(in, m, 2));
+        const uint32_t byte = mx8_scale_byte(m);
+        *(reinterpret_cast<uint2 *>(codes + row) + c) = mx8_codes(a[i], byte);
+        if ((c & 3) == 0) scales[(row >> 5) + (c >> 2)] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+int launch_rmsnorm(int T, int H, const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps,
+                   uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales, cudaStream_t st) {
+  const int nch = H / 8;
+  const int ch = nch <= 512 ? 1 : nch <= 1024 ? 2 : 4;  // H <= 16384: 2048 chunks
+  const int nth = ((nch + ch - 1) / ch + 31) / 32 * 32;
+  const dim3 grid(T), block(nth);
+  cudaError_t err;
+  if (ch == 1)
+    err = launch_pdl(rmsnorm_kernel<1>, grid, block, 0, st, x, residual, weight, eps, H, residual_out, y, codes, scales);
+  else if (ch == 2)
+    err = launch_pdl(rmsnorm_kernel<2>, grid, block, 0, st, x, residual, weight, eps, H, residual_out, y, codes, scales);
+  else
+    err = launch_pdl(rmsnorm_kernel<4>, grid, block, 0, st, x, residual, weight, eps, H, residual_out, y, codes, scales);
+  return err == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace k3moe
