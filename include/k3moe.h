@@ -350,7 +350,7 @@ int k3moe_rmsnorm(int32_t T, int32_t H, const uint16_t *x, const uint16_t *resid
 /* A paged key-value cache of one layer, in the caller's device memory:
  *   k, v : [pages][heads][page_size][dim], bf16 values or E4M3 codes (16-byte aligned)
  *   k_scales, v_scales : uint8 [pages][heads][page_size] E8M0, one per (token, head)
- *                        vector (K3MOE_KV_E4M3; NULL for K3MOE_KV_BF16)
+ *                        vector, 16-byte aligned (K3MOE_KV_E4M3; unused for K3MOE_KV_BF16)
  * pages >= 1, page_size a power of two in [16, 1024], heads in [1, 1024], dim 64, 128 or
  * 256, pages * page_size < 2^31 (else K3MOE_ERR_SHAPE).  A slot, page * page_size +
  * place, names one token's position. */

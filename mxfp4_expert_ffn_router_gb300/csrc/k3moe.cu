@@ -321,6 +321,7 @@ static int kv_check(const k3moe_kv_cache *c) {
   if (!c->k || !c->v) return K3MOE_ERR_ARG;
   if (c->format == K3MOE_KV_E4M3 && (!c->k_scales || !c->v_scales)) return K3MOE_ERR_ARG;
   if (!aligned16(c->k) || !aligned16(c->v)) return K3MOE_ERR_ALIGN;
+  if (c->format == K3MOE_KV_E4M3 && (!aligned16(c->k_scales) || !aligned16(c->v_scales))) return K3MOE_ERR_ALIGN;
   return K3MOE_OK;
 }
 

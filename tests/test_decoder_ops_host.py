@@ -31,7 +31,9 @@ BAD_ARGS = [dict(fmt=2), dict(fmt=-1), dict(k=0), dict(v=0), dict(ks=0), dict(vs
 
 @pytest.mark.parametrize("bad,want", [(b, k3.K3MOE_ERR_SHAPE) for b in BAD_SHAPES] +
                          [(b, k3.K3MOE_ERR_ARG) for b in BAD_ARGS] + [(dict(k=P + 8), k3.K3MOE_ERR_ALIGN),
-                                                                      (dict(v=P + 4), k3.K3MOE_ERR_ALIGN)])
+                                                                      (dict(v=P + 4), k3.K3MOE_ERR_ALIGN),
+                                                                      (dict(ks=P + 8), k3.K3MOE_ERR_ALIGN),
+                                                                      (dict(vs=P + 1), k3.K3MOE_ERR_ALIGN)])
 def test_cache_refused_by_every_call(L, bad, want):
     c = _cache(**bad)
     assert L.k3moe_kv_write(c, 1, P, P, 1 << 20, 1 << 20, P, None, None) == want
