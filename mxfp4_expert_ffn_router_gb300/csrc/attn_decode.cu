@@ -12,18 +12,18 @@
 // HBM rate.  All the rest serves to keep those loads in flight.
 //
 //  * Work.  An item is (sequence, key-value head, up to 8 NT of the query heads that
-//    share it); a unit is 64 of its tokens.  All items' units form one line, cut into
+//    share it); a unit is 64 or 128 of its tokens.  All items' units form one line, cut into
 //    equal pieces, one per block: blocks end together however uneven the lengths are,
 //    and one long sequence fills the GPU.  Lengths are read on the device, so a captured
 //    graph follows them.  A piece covers the end of one item, some whole items and the
 //    start of another; only the cut ones leave partial sums in the workspace, at
 //    most two a block, which attn_join_kernel adds in order.  When every item
-//    is short (kDirectUnits), a block takes one item and nothing is cut or joined.
-//  * Loads.  Each of the four warps streams every fourth run of 16 tokens through a ring
+//    is short (kDirectTokens), a block takes one item and nothing is cut or joined.
+//  * Loads.  Each of the four warps streams every fourth run of 16 or 32 tokens through a ring
 //    of its own in shared memory with 16-byte cp.async (stages - 1 runs ahead, across items),
-//    so no warp waits for another except where an item ends.  Runs never straddle a page
-//    (pages hold a multiple of 16 places); the next run's page number is loaded a step
-//    ahead.  Places not seen are filled with zeros by the copy, so that nothing they hold
+//    so no warp waits for another except where an item ends.  16 tokens from a multiple of
+//    16 on never straddle a page (pages hold a multiple of 16 places); the next run's page
+//    numbers are loaded a step ahead.  Places not seen are filled with zeros by the copy, so that nothing they hold
 //    (NaN, infinities) reaches a product.
 //  * Products.  mma.sync m16n8k16 (f16 or bf16, fp32 sums): with at most 16 query heads
 //    sharing a key the products are a small part of the time even at this instruction's
@@ -32,9 +32,12 @@
 //    and 8 query heads as columns, so that S's registers are P^T's.  The order of
 //    dimensions and tokens inside a product is free as long as both operands agree, and
 //    is chosen so that a lane's share of K and V is whole 16-byte words.
-//  * E4M3 (f16 products).  Codes are exact in f16; a query row is scaled by a power of two
-//    to a maximum in [2^14, 2^15), exact but for values below 2^-28 of it.  K's scale
-//    multiplies the score.  V's scale 2^e joins the weight: w_i = exp2(s_i + e_i - m')
+//  * E4M3.  K's codes enter their products as they are (m16n8k32): a query row is scaled by a
+//    power of two to a maximum in [128, 256) and split as q = hi + lo / 16 into two E4M3
+//    values of 4 bits each, which is exact (bf16 has 8) but for values below 2^-13 of the row's
+//    maximum, and off by at most 2^-22 of that for them; hi and lo are two rows of the product, so that
+//    8 query heads fill its 16.  K's scale multiplies the score.  V's codes are converted to
+//    f16 (exact); V's scale 2^e joins the weight: w_i = exp2(s_i + e_i - m')
 //    with its own running maximum m' of s_i + e_i, times 2^14, rounded to f16 (11 bits
 //    down to 2^-28 of the largest, so that a token with a large score and a tiny value
 //    costs the others nothing), while l sums exp2(s_i - m) in fp32 with m = max s_i.
@@ -50,13 +53,33 @@ namespace k3moe {
 
 namespace {
 
+#ifndef KRR
+#define KRR (ROWB <= 128 && NT == 1 ? 2 : ROWB <= 64 ? 2 : 1)
+#endif
+#ifndef KST
+#define KST (ROWB <= 64 ? 4 : RR == 2 ? 2 : 3)
+#endif
+#ifndef KQS
+#define KQS 32
+#endif
+#ifndef KF
+#define KF 4
+#endif
+#ifndef KBL
+#define KBL (ROWB <= 128 ? 3 : ROWB <= 256 ? 2 : 1)
+#endif
 constexpr int kAdWarps = 4;
 constexpr int kAdThreads = kAdWarps * 32;
-constexpr int kRun = 16;                 // tokens of a warp's step
-constexpr int kUnit = kRun * kAdWarps;   // tokens of a block's step
-constexpr int kDirectUnits = 8;          // items of at most this many units are never cut
-constexpr int kMinUnits = 4;             // smallest piece of a block, in units
-constexpr int kAdMostBlocks = 152 * 4;   // pieces (bounds the workspace and the join)
+constexpr int kRun = 16;                 // tokens of a product
+constexpr int kDirectTokens = 512;       // items of at most this many tokens are never cut
+constexpr int kMinTokens = 256;          // smallest piece of a block
+#ifndef KWU
+#define KWU 4
+#define KWI 3
+#endif
+constexpr int kUnitLen = KWU, kItemLen = KWI;  // length on the line of a unit, and of an item beside its units
+constexpr int kJoinParts = 8;            // parts of an item that one warp joins
+constexpr int kAdMostBlocks = 152 * 12;  // pieces (bounds the workspace)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -66,7 +89,10 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool on) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_or_zeros(uint32_t dst, const void *src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -105,6 +131,14 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d += a b, m16n8k32, E4M3 operands.
+__device__ __forceinline__ void mma32_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                           uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 template <bool H>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   uint32_t r;
@@ -115,9 +149,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// Scale byte -> exponent as a float (NaN for 255).
-__device__ __forceinline__ float e8m0_exp(uint32_t b) {
-  return b == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(0x4B000000u | b) - 8388735.0f;
+// Not 0 where a byte of w is 255.
+__device__ __forceinline__ uint32_t byte_255(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
 }
 
 struct AdParams {
@@ -133,15 +167,22 @@ struct AdParams {
   float scale;
   uint16_t *out;
   float *lse;
-  int4 *meta;    // [blocks]: {parts, first slot, item's first query head, sequence} of a cut item that starts here
+  int4 *meta;    // [2 blocks]: {first slot, parts, item, sequence} of the cut items of a piece: one that began
+                 // before it, one that begins in it and goes on (parts 0: none)
   float4 *stat;  // [2 blocks][8 NT]: {m', m, l, -}
   float4 *part;  // [2 blocks][accumulator quads][32 lanes]
   int32_t *status;
 };
 
-// The tokens of one sequence that are seen, and the place its units count from.
+// a / b for a, b >= 0: mostly both fit 32 bits, where a division costs a fifth.
+__device__ __forceinline__ long long div_small(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// The tokens of one sequence that are seen, lo .. n - 1, and the place its units count from.
 struct Seen {
-  int n, lo, t0, units;
+  int n, lo, t0;
 };
 __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   Seen s;
@@ -154,26 +195,55 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   }
   s.lo = P.window > 0 && s.n > P.window ? s.n - P.window : 0;
   s.t0 = s.lo & ~(kRun - 1);
-  s.units = static_cast<int>((static_cast<unsigned>(s.n - s.t0) + (kUnit - 1)) / kUnit);
   return s;
 }
+template <int UNIT>
+__device__ __forceinline__ int units_of(const Seen &s) {
+  return static_cast<int>((static_cast<unsigned>(s.n - s.t0) + (UNIT - 1)) / UNIT);
+}
 
-// Walks a block's piece of the line of units.
-struct Cursor {
-  int b, it, u;  // sequence, item of it, unit of that
-  Seen s;
-  __device__ __forceinline__ void next(const AdParams &P, int items) {
-    if (++u < s.units) return;
-    u = 0;
-    if (++it < items) return;
-    it = 0;
-    do {
-      if (++b >= P.B) {  // past the last unit of all
-        s.units = 0;
-        return;
+// A block's piece [from, to) of the line, and where one warp is in it.  An item that begins at
+// `begin` lies on the line as kItemLen, then kUnitLen for each of its units; a unit belongs
+// to the piece in which it begins.
+template <int UNIT>
+struct Walk {
+  int b, head, group;    // sequence, key-value head, which of its items
+  int n, lo, t0;
+  unsigned tok, stop;    // the warp's next run begins at tok; the piece holds the item's runs below stop
+  long long begin;       // of the item
+  bool more;             // whether a run is left
+  __device__ __forceinline__ int units() const { return units_of<UNIT>({n, lo, t0}); }
+  // The item's first unit at or past place x of the line.
+  __device__ __forceinline__ int unit_at(long long x) const {
+    const long long u = (x - begin - kItemLen + kUnitLen - 1) / kUnitLen;
+    return u < 0 ? 0 : u > units() ? units() : static_cast<int>(u);
+  }
+  // Begins the item at `begin`, from its first unit in [from, to) on; first: the warp's place in a unit.
+  __device__ __forceinline__ void enter(long long from, long long to, int first) {
+    tok = static_cast<unsigned>(t0) + static_cast<unsigned>(unit_at(from)) * UNIT + first;
+    stop = static_cast<unsigned>(t0) + static_cast<unsigned>(unit_at(to)) * UNIT + first;
+  }
+  __device__ __forceinline__ void set(const Seen &s) { n = s.n, lo = s.lo, t0 = s.t0; }
+  __device__ __forceinline__ void next_item(const AdParams &P, long long from, long long to, int first) {
+    begin += static_cast<long long>(units()) * kUnitLen + kItemLen;
+    more = begin + kItemLen < to;
+    if (!more) return;
+    if (++group == P.groups) {
+      group = 0;
+      if (++head == P.heads) {
+        head = 0;
+        Seen s;
+        do {
+          if (++b >= P.B) {  // past the last unit of all
+            more = false;
+            return;
+          }
+          s = seen_of(P, b, false);
+        } while (s.n <= s.t0);
+        set(s);
       }
-      s = seen_of(P, b, false);
-    } while (s.units == 0);
+    }
+    enter(from, to, first);
   }
 };
 
@@ -182,16 +252,38 @@ struct AdShape {
   static constexpr int ESZ = E4M3 ? 1 : 2;
   static constexpr int ROWB = D * ESZ;            // bytes of a cached vector
   static constexpr int C = ROWB / 16;             // 16-byte words of it
-  static constexpr int KB = kRun * ROWB;          // bytes of a run's keys
-  static constexpr int STAGE = 2 * KB + (E4M3 ? 32 : 0);
-  static constexpr int MM = D / 16;               // products (16 dimensions each) of a run and 8 query heads
+  static constexpr int KB = kRun * ROWB;          // bytes of 16 tokens' keys
+  static constexpr int MM = D / 16;               // products (16 dimensions each) of 16 tokens and 8 query heads
   static constexpr int QUADS = MM * NT;           // accumulator quads per lane
+  // A warp's step is RR times 16 tokens: 4 to 16 KB, so that what a step costs besides its bytes counts little
+  static constexpr int RR = KRR;
+  static constexpr int RUN = RR * kRun;
+  static constexpr int UNIT = RUN * kAdWarps;     // tokens of a block's step
+  static constexpr int SUB = 2 * KB;              // keys and values of 16 tokens; a multiple of 128: words swizzle by xor
+  static constexpr int SCALES = E4M3 ? 32 : 0;    // scale bytes of 16 tokens, after all stages
   // stages and blocks per SM: about 100 KB of loads in flight per SM
-  static constexpr int STAGES = ROWB <= 64 ? 4 : 3;
-  static constexpr int BLOCKS = ROWB <= 128 ? 3 : ROWB <= 256 ? 2 : 1;
-  static constexpr int MERGE = kAdWarps * 4 * 32 * 16;  // four quads of each warp
-  static constexpr int SMEM = kAdWarps * STAGES * STAGE + MERGE;
+  static constexpr int STAGES = KST;
+  static constexpr int BLOCKS = KBL;
+  // quads that the warps exchange at once where an item ends, each in the stage it has just used
+  static constexpr int QR = RR * SUB / 512 < QUADS ? RR * SUB / 512 : QUADS;
+  // query fragments: in registers, or from 32 of them on in shared memory (the same for all warps)
+  static constexpr int QREGS = E4M3 ? D / 32 * 4 * NT : D / 16 * 2 * NT;
+  static constexpr int QSMEM = QREGS >= KQS ? QREGS * 32 * 4 : 0;
+  static constexpr int SMEM = kAdWarps * STAGES * RR * (SUB + SCALES) + QSMEM + 128;
 };
+
+// First of the two neighbouring dimensions that a lane of group g holds of product m.
+template <int D, bool E4M3, int NT>
+__device__ __forceinline__ int quad_dim(int m, int g) {
+  constexpr int PER = 16 / AdShape<D, E4M3, NT>::ESZ;  // dimensions of a 16-byte word
+  const int dl = 2 * m;                                // of the lane's dimensions
+  return AdShape<D, E4M3, NT>::C >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
+}
+
+// Two neighbouring dimensions of a row, times f (0: a row without weight, whatever the sums are).
+__device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float b, bool on) {
+  if (on) *reinterpret_cast<uint32_t *>(p) = f == 0.f ? 0u : pack2<false>(a * f, b * f);
+}
 
 }  // namespace
 
@@ -199,33 +291,36 @@ template <int D, bool E4M3, int NT, bool DIRECT>
 __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     attn_decode_kernel(const AdParams P) {
   using S = AdShape<D, E4M3, NT>;
-  constexpr int C = S::C, MM = S::MM, ST = S::STAGES, NQ = 8 * NT;
+  constexpr int C = S::C, MM = S::MM, ST = S::STAGES, RR = S::RR, UNIT = S::UNIT, NQ = 8 * NT;
   constexpr int KL = C / 4;             // words of a key a lane reads
   constexpr int SP = E4M3 ? 4 : 2;      // products of 16 dimensions per such word
   constexpr int VL = C >= 8 ? C / 8 : 1;  // words of a value a lane reads
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_fac[kAdWarps][NQ], s_m[kAdWarps][NQ], s_l[kAdWarps][NQ];
-  __shared__ float s_fin[NQ];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((128u - (su32(smem_raw) & 127u)) & 127u);
+  __shared__ __align__(16) float s_mp[NQ][kAdWarps], s_m[NQ][kAdWarps], s_l[NQ][kAdWarps];
   __shared__ long long s_scan[kAdWarps];
-  __shared__ int s_start[4];
+  __shared__ long long s_begin;
+  __shared__ int s_start[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int items = P.heads * P.groups;
+  const int items = P.heads * P.groups, first = warp * S::RUN;
   pdl_wait();
   pdl_trigger();
 
   // ---- this block's piece
-  Cursor cur;
-  int steps;
-  long long f0 = 0, share = 0;
+  Walk<UNIT> cur;
+  long long from = 0, to = 1LL << 62, share = 0;
   if constexpr (DIRECT) {
     cur.b = blockIdx.x / items;
-    cur.it = blockIdx.x - cur.b * items;
-    cur.u = 0;
-    cur.s = seen_of(P, cur.b, tid == 0);
-    steps = cur.s.units;
-    if (steps == 0) {  // sees nothing
-      const int h0 = (cur.it / P.groups) * P.G + (cur.it % P.groups) * NQ;
-      const int rows = min(NQ, P.G - (cur.it % P.groups) * NQ);
+    const int item = blockIdx.x - cur.b * items;
+    cur.head = item / P.groups;
+    cur.group = item - cur.head * P.groups;
+    cur.set(seen_of(P, cur.b, tid == 0));
+    cur.begin = 0;
+    cur.more = true;
+    cur.enter(from, to, first);
+    if (cur.n <= cur.t0) {  // sees nothing
+      const int h0 = cur.head * P.G + cur.group * NQ;
+      const int rows = min(NQ, P.G - cur.group * NQ);
       const size_t row = static_cast<size_t>(cur.b) * P.Hq + h0;
       for (int i = tid; i < rows * D / 8; i += kAdThreads)
         reinterpret_cast<uint4 *>(P.out + row * D)[i] = make_uint4(0, 0, 0, 0);
@@ -233,11 +328,15 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
       return;
     }
   } else {
-    // thread t counts the units of sequences [t per, t per + per); a scan finds the piece
+    // thread t measures sequences [t per, t per + per); a scan finds the piece
     const int per = (P.B + kAdThreads - 1) / kAdThreads;
     const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
+    auto length = [&](int b, bool report) {  // of an item of sequence b on the line
+      const int u = units_of<UNIT>(seen_of(P, b, report));
+      return u ? static_cast<long long>(u) * kUnitLen + kItemLen : 0LL;
+    };
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seen_of(P, b, blockIdx.x == 0).units;
+    for (int b = b0; b < b1; ++b) mine += length(b, blockIdx.x == 0);
     mine *= items;
     long long incl = mine;
 #pragma unroll
@@ -253,128 +352,189 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
       if (w < warp) before += s_scan[w];
       total += s_scan[w];
     }
-    share = max(static_cast<long long>(kMinUnits), (total + gridDim.x - 1) / gridDim.x);
-    f0 = static_cast<long long>(blockIdx.x) * share;
-    const long long first = before + incl - mine;  // of this thread's sequences
-    steps = static_cast<int>(max(0LL, min(share, total - f0)));
-    if (steps > 0 && f0 >= first && f0 < first + mine) {
-      long long at = first;
+    share = max(static_cast<long long>(kMinTokens / UNIT * kUnitLen), div_small(total + gridDim.x - 1, gridDim.x));
+    from = static_cast<long long>(blockIdx.x) * share;
+    to = min(total, from + share);
+    const long long ahead = before + incl - mine;  // of this thread's sequences
+    if (from < to && from >= ahead && from < ahead + mine) {
+      long long at = ahead, len;
       int b = b0;
-      Seen s;
       for (;; ++b) {
-        s = seen_of(P, b, false);
-        const long long here = static_cast<long long>(s.units) * items;
-        if (f0 < at + here) break;
-        at += here;
+        len = length(b, false);
+        if (from < at + len * items) break;
+        at += len * items;
       }
-      const long long r = f0 - at;
+      const int item = static_cast<int>(div_small(from - at, len));
+      s_begin = at + item * len;
       s_start[0] = b;
-      s_start[1] = static_cast<int>(r / s.units);
-      s_start[2] = static_cast<int>(r % s.units);
+      s_start[1] = item;
     }
-    if (tid == 0) P.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (tid < 2) P.meta[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
     // rows that see nothing
-    for (int b = blockIdx.x; b < P.B; b += gridDim.x)
-      if (seen_of(P, b, false).units == 0) {
-        for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += kAdThreads)
-          reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
-        if (P.lse)
-          for (int i = tid; i < P.Hq; i += kAdThreads) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
-      }
+    for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
+      const Seen s = seen_of(P, b, false);
+      if (s.n > s.t0) continue;
+      for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += kAdThreads)
+        reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+      if (P.lse)
+        for (int i = tid; i < P.Hq; i += kAdThreads) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
+    }
     __syncthreads();
-    if (steps == 0) return;
+    if (from >= to) return;
     cur.b = s_start[0];
-    cur.it = s_start[1];
-    cur.u = s_start[2];
-    cur.s = seen_of(P, cur.b, false);
+    cur.head = s_start[1] / P.groups;
+    cur.group = s_start[1] - cur.head * P.groups;
+    cur.set(seen_of(P, cur.b, false));
+    cur.begin = s_begin;
+    cur.more = true;
+    cur.enter(from, to, first);
+    if (cur.tok >= cur.stop) cur.next_item(P, from, to, first);  // the piece begins behind the item's last unit
+    if (!cur.more || cur.tok >= cur.stop) return;                // or ends before its first
   }
 
-  // ---- loads: run `warp` of the unit at `pre` into stage st
-  const uint32_t ring = su32(smem) + warp * (ST * S::STAGE);
-  Cursor pre = cur;
-  uint32_t bad = 0;  // stages whose page number lies outside the cache
-  int page = -1;
-  auto next_page = [&]() {
-    const int tok = pre.s.t0 + pre.u * kUnit + warp * kRun;
-    page = -1;
-    if (pre.s.units && tok < pre.s.n) page = __ldg(P.table + static_cast<size_t>(pre.b) * P.max_pages + (tok >> P.page_shift));
+  // ---- loads: the run at `pre` into stage st.  Lane l copies words l, l + 32, .. of 16 tokens' keys
+  // and values: row lr + i RI, word lx.  Word w of key row r lies at w ^ 4 (r & 1), of value row r at
+  // w ^ 2 (r / 4): the reads of fragments below then meet all banks evenly.
+  constexpr int RI = C >= 32 ? 1 : 32 / C;  // rows between a lane's words
+  const uint32_t ring = su32(smem) + warp * (ST * RR * S::SUB);
+  const uint32_t sring = su32(smem) + kAdWarps * ST * RR * S::SUB + warp * (ST * RR * S::SCALES);
+  const int lr = lane / C, lx = lane % C;
+  const uint32_t kdst = lr * S::ROWB + ((C == 8 || C == 16 ? lx ^ (4 * (lr & 1)) : lx) << 4);
+  const uint32_t vdst = S::KB + lr * S::ROWB + (lx << 4);
+  const uint8_t *const klane = P.k + lane * 16, *const vlane = P.v + lane * 16;
+  const unsigned place = (1u << P.page_shift) - 1u, page_vecs = static_cast<unsigned>(P.heads) << P.page_shift;
+  Walk<UNIT> pre = cur;
+  uint32_t bad = 0;    // bit st RR + r: a page number outside the cache
+  int page[RR];
+  auto pages = [&]() {  // of the run at `pre`
+    const int32_t *row = P.table + static_cast<size_t>(pre.b) * P.max_pages;
+#pragma unroll
+    for (int r = 0; r < RR; ++r) {
+      const unsigned tok = pre.tok + r * kRun;
+      page[r] = tok < static_cast<unsigned>(pre.n) ? __ldg(row + (tok >> P.page_shift)) : -1;
+    }
   };
   auto issue = [&](int st) {
-    const int tok = pre.s.t0 + pre.u * kUnit + warp * kRun;
-    bad &= ~(1u << st);
-    if (tok < pre.s.n) {
-      if (page < 0 || page >= P.pages) {
-        bad |= 1u << st;
-        if (lane == 0) set_status(P.status, K3MOE_DEV_BOUNDS);
-      } else {
-        const size_t vec = ((static_cast<size_t>(page) * P.heads + pre.it / P.groups) << P.page_shift) +
-                           (tok & ((1 << P.page_shift) - 1));
-        const uint8_t *kp = P.k + vec * S::ROWB, *vp = P.v + vec * S::ROWB;
-        const uint32_t dst = ring + st * S::STAGE;
+    if (pre.more) {
 #pragma unroll
-        for (int i = 0; i < C / 2; ++i) {
-          const int w = lane + 32 * i, r = w / C, x = w % C;
-          const bool on = tok + r >= pre.s.lo && tok + r < pre.s.n;
-          cp16(dst + r * S::ROWB + ((C >= 8 ? x ^ (4 * (r & 1)) : x) << 4), kp + w * 16, on);
-          cp16(dst + S::KB + r * S::ROWB + ((C >= 8 ? x ^ (2 * ((r >> 2) & 3)) : x) << 4), vp + w * 16, on);
+      for (int r = 0; r < RR; ++r) {
+        const unsigned tok = pre.tok + r * kRun;
+        const int tile = st * RR + r;
+        if (tok < static_cast<unsigned>(pre.n)) {
+          if (static_cast<unsigned>(page[r]) >= static_cast<unsigned>(P.pages)) {
+            bad |= 1u << tile;
+            if (lane == 0) set_status(P.status, K3MOE_DEV_BOUNDS);
+          } else {
+            if (bad) bad &= ~(1u << tile);
+            const size_t vec = static_cast<size_t>(static_cast<unsigned>(page[r])) * page_vecs +
+                               ((static_cast<unsigned>(pre.head) << P.page_shift) + (tok & place));
+            const uint8_t *kp = klane + vec * S::ROWB, *vp = vlane + vec * S::ROWB;
+            const uint32_t kd = ring + tile * S::SUB + kdst, vd = ring + tile * S::SUB + vdst;
+            const bool whole = tok >= static_cast<unsigned>(pre.lo) && tok + kRun <= static_cast<unsigned>(pre.n);
+#pragma unroll
+            for (int i = 0; i < C / 2; ++i) {
+              // the part of the swizzles that varies with i
+              const uint32_t ki = C == 32 ? (i & 1) << 6 : 0, vi = C >= 8 ? ((i * RI) >> 2) << 5 : 0;
+              if (whole) {
+                cp16(((kd ^ ki) + i * RI * S::ROWB), kp + i * 512);
+                cp16(((vd ^ vi) + i * RI * S::ROWB), vp + i * 512);
+              } else {
+                const unsigned at = tok + lr + i * RI;
+                const bool on = at >= static_cast<unsigned>(pre.lo) && at < static_cast<unsigned>(pre.n);
+                cp16_or_zeros((kd ^ ki) + i * RI * S::ROWB, kp + i * 512, on);
+                cp16_or_zeros((vd ^ vi) + i * RI * S::ROWB, vp + i * 512, on);
+              }
+            }
+            if (E4M3 && lane < 2) cp16(sring + tile * S::SCALES + 16 * lane, (lane ? P.vs : P.ks) + vec);
+          }
         }
-        if (E4M3 && lane < 2) cp16(dst + 2 * S::KB + 16 * lane, (lane ? P.vs : P.ks) + vec, true);
       }
+      pre.tok += UNIT;
+      if (pre.tok >= pre.stop) {
+        if (DIRECT)
+          pre.more = false;
+        else
+          pre.next_item(P, from, to, first);
+      }
+      if (pre.more) pages();
     }
     cp_commit();
-    pre.next(P, items);
-    next_page();
   };
-  next_page();
-  int ahead = 0;
-  for (; ahead < ST - 1; ++ahead) {
-    if (ahead < steps)
-      issue(ahead);
-    else
-      cp_commit();
-  }
+  pages();
+#pragma unroll
+  for (int st = 0; st < ST - 1; ++st) issue(st);
 
-  uint32_t qf[D / 16][2 * NT];
+  constexpr int QN = E4M3 ? D / 32 : D / 16;  // products along the dimensions
+  constexpr bool QS = S::QSMEM > 0;
+  uint32_t qf[QS ? 1 : QN][E4M3 ? 4 * NT : 2 * NT];
+  uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + kAdWarps * ST * RR * (S::SUB + S::SCALES));
+  uint2 raw[D / 16][NT];
   float sq[NT];  // scale of a raw score, in powers of two
   float o[NT][MM][4], mrun[NT], m_l[NT], l[NT];
-  auto start_item = [&]() {
-    const int gi = cur.it % P.groups;
-    const int h0 = (cur.it / P.groups) * P.G + gi * NQ, rows = min(NQ, P.G - gi * NQ);
+  auto load_q = [&](const Walk<UNIT> &at) {
+    const int h0 = at.head * P.G + at.group * NQ, rows = min(NQ, P.G - at.group * NQ);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = g + 8 * t;
-      const uint16_t *qp = P.q + cur.b * P.q_stride + static_cast<size_t>(h0 + r) * D;
-      uint2 raw[D / 16];
-      uint32_t mx = 0;
+      const uint16_t *qp = P.q + at.b * P.q_stride + static_cast<size_t>(h0 + r) * D + c * (16 / S::ESZ);
 #pragma unroll
       for (int i = 0; i < KL; ++i)
 #pragma unroll
-        for (int w = 0; w < SP; ++w) {
-          const int d = (c + 4 * i) * (16 / S::ESZ) + 4 * w;
-          const uint2 u = r < rows ? __ldg(reinterpret_cast<const uint2 *>(qp + d)) : make_uint2(0, 0);
-          raw[i * SP + w] = u;
+        for (int w = 0; w < SP; ++w)
+          raw[i * SP + w][t] =
+              r < rows ? __ldg(reinterpret_cast<const uint2 *>(qp + i * (64 / S::ESZ) + 4 * w)) : make_uint2(0, 0);
+    }
+  };
+  auto start_item = [&]() {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if constexpr (E4M3) {
+        uint32_t mx = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint2 u = raw[i][t];
           mx = max(mx, max(max((u.x << 16) & 0x7FFFFFFFu, u.x & 0x7FFF0000u),
                            max((u.y << 16) & 0x7FFFFFFFu, u.y & 0x7FFF0000u)));
         }
-      float up = 1.f;
-      if constexpr (E4M3) {
         mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        // 2^(14 - floor(log2 max)), as far as fp32 has it
-        const int e = mx == 0 ? 0 : max(-126, min(127, 14 + 127 - static_cast<int>(mx >> 23)));
-        up = exp2i(e);
-        sq[t] = P.scale * kLog2e * mx_pow2(-e);
+        // 2^(7 - floor(log2 max)), as far as fp32 has it; a row that is not finite gives NaN
+        const int e = mx == 0 ? 0 : max(-126, min(127, 7 + 127 - static_cast<int>(mx >> 23)));
+        const float up = exp2i(e);
+        sq[t] = mx >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : P.scale * kLog2e * mx_pow2(-e);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint2 u = raw[i][t];
+          const float v[4] = {__uint_as_float(u.x << 16) * up, __uint_as_float(u.x & 0xFFFF0000u) * up,
+                              __uint_as_float(u.y << 16) * up, __uint_as_float(u.y & 0xFFFF0000u) * up};
+          const uint32_t h0 = e4m3x2(v[0], v[1]), h1 = e4m3x2(v[2], v[3]);
+          uint32_t fh[2];
+          e4m3x4_to_f16x2(h0 | (h1 << 16), fh[0], fh[1]);
+          const float2 d0 = __half22float2(*reinterpret_cast<const __half2 *>(&fh[0]));
+          const float2 d1 = __half22float2(*reinterpret_cast<const __half2 *>(&fh[1]));
+          // word i of the lane's: product i / 2, first or second four of its eight dimensions there
+          const uint32_t hi = h0 | (h1 << 16);
+          const uint32_t lo = e4m3x2((v[0] - d0.x) * 16.f, (v[1] - d0.y) * 16.f) |
+                              (e4m3x2((v[2] - d1.x) * 16.f, (v[3] - d1.y) * 16.f) << 16);
+          if constexpr (QS) {  // (every warp writes the same)
+            reinterpret_cast<uint2 *>(&q_sm[((i >> 1) * NT + t) * 32 + lane])[i & 1] = make_uint2(hi, lo);
+          } else {
+            qf[i >> 1][4 * t + 2 * (i & 1)] = hi;
+            qf[i >> 1][4 * t + 2 * (i & 1) + 1] = lo;
+          }
+        }
       } else {
         sq[t] = P.scale * kLog2e;
-      }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        if constexpr (E4M3) {
-          qf[i][t] = pack2<true>(__uint_as_float(raw[i].x << 16) * up, __uint_as_float(raw[i].x & 0xFFFF0000u) * up);
-          qf[i][NT + t] = pack2<true>(__uint_as_float(raw[i].y << 16) * up, __uint_as_float(raw[i].y & 0xFFFF0000u) * up);
-        } else {
-          qf[i][t] = raw[i].x;
-          qf[i][NT + t] = raw[i].y;
+        for (int i = 0; i < D / 16; ++i) {
+          if constexpr (QS) {
+            uint32_t *const to_sm = reinterpret_cast<uint32_t *>(&q_sm[(NT == 1 ? i / 2 : i) * 32 + lane]);
+            to_sm[NT == 1 ? 2 * (i & 1) : t] = raw[i][t].x;
+            to_sm[NT == 1 ? 2 * (i & 1) + 1 : NT + t] = raw[i][t].y;
+          } else {
+            qf[i][t] = raw[i][t].x;
+            qf[i][NT + t] = raw[i][t].y;
+          }
         }
       }
       mrun[t] = m_l[t] = -INFINITY;
@@ -386,83 +546,150 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     }
   };
 
-  int item_u0 = cur.u;  // first unit of the item in this piece
+  constexpr bool kEarlyQ = D / 16 * NT <= 8;  // as far as there are registers for it
   bool first_item = true;
-  int stage = 0;
+  int stage = 0, after = ST - 1;  // the stage in use, and the one that is loaded next
+  load_q(cur);
   start_item();
-  for (int step = 0; step < steps; ++step) {
+  if (QS) __syncthreads();
+  for (;;) {
     __syncwarp();  // every lane is done with the stage that is loaded next
-    if (ahead < steps)
-      issue(stage == 0 ? ST - 1 : stage - 1);
-    else
-      cp_commit();
-    ++ahead;
+    issue(after);
+    after = after + 1 == ST ? 0 : after + 1;
     cp_wait<ST - 1>();
     __syncwarp();
-    const int tok = cur.s.t0 + cur.u * kUnit + warp * kRun;
-    if (tok < cur.s.n && !((bad >> stage) & 1u)) {
-      const uint32_t kb = ring + stage * S::STAGE, vb = kb + S::KB;
-      // S: columns 2c, 2c+1 of product j are tokens 4c + 2j, 4c + 2j + 1
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-      const int kr = 4 * (g >> 1) + (g & 1);
+    if (cur.tok < static_cast<unsigned>(cur.n)) {
+      const uint32_t base0 = ring + stage * (RR * S::SUB), sbase = sring + stage * (RR * S::SCALES);
+      const bool whole = cur.tok >= static_cast<unsigned>(cur.lo) &&
+                         cur.tok + S::RUN <= static_cast<unsigned>(cur.n) && bad == 0u;
+      // S: columns 2c, 2c+1 of product j of 16 tokens are tokens 4c + 2j, 4c + 2j + 1.  CH partial
+      // sums each, so that a product does not wait for the one before it
+      constexpr int CH = !E4M3 && RR == 1 ? 2 : 1;
+      constexpr int SN = E4M3 ? NT : 1;  // products of 16 rows: 8 query heads (hi, lo), or 16
+      float s[RR][SN * CH][2][4] = {};
+      const uint32_t kofs = (4 * (g >> 1) + (g & 1)) * S::ROWB + (c << 4) + (C >= 8 ? (g & 1) << 6 : 0);
 #pragma unroll
       for (int i = 0; i < KL; ++i) {
-        const int x = c + 4 * i;
-        uint4 kw[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          kw[j] = lds128(kb + (kr + 2 * j) * S::ROWB + ((C >= 8 ? x ^ (4 * (g & 1)) : x) << 4));
+        for (int r = 0; r < RR; ++r) {
+          uint4 kw[2];
 #pragma unroll
-        for (int w = 0; w < SP; ++w) {
-          const int qi = i * SP + w;
+          for (int j = 0; j < 2; ++j)
+            kw[j] = lds128(((base0 + r * S::SUB + kofs) ^ ((i & 1) << 6)) + (i >> 1) * 128 + 2 * j * S::ROWB);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t kk[4] = {kw[j].x, kw[j].y, kw[j].z, kw[j].w};
-            uint32_t b0, b1;
-            if constexpr (E4M3)
-              e4m3x4_to_f16x2(kk[w], b0, b1);
-            else
-              b0 = kk[2 * w], b1 = kk[2 * w + 1];
-            if constexpr (NT == 1)
-              mma16<E4M3>(s[j], qf[qi][0], 0u, qf[qi][1], 0u, b0, b1);
-            else
-              mma16<E4M3>(s[j], qf[qi][0], qf[qi][1], qf[qi][2], qf[qi][3], b0, b1);
+          for (int w = 0; w < 2; ++w) {
+            const int qi = i * 2 + w;
+            uint32_t a[E4M3 ? 4 * NT : 2 * NT];
+            if constexpr (QS) {
+              if constexpr (E4M3) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                  *reinterpret_cast<uint4 *>(&a[4 * t]) = q_sm[(qi * NT + t) * 32 + lane];
+              } else if constexpr (NT == 1) {
+                *reinterpret_cast<uint2 *>(a) = reinterpret_cast<const uint2 *>(&q_sm[i * 32 + lane])[w];
+              } else {
+                *reinterpret_cast<uint4 *>(a) = q_sm[qi * 32 + lane];
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < (E4M3 ? 4 * NT : 2 * NT); ++x) a[x] = qf[qi][x];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t b0 = w ? kw[j].z : kw[j].x, b1 = w ? kw[j].w : kw[j].y;
+              if constexpr (E4M3) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                  mma32_e4m3(s[r][t][j], a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3], b0, b1);
+              } else if constexpr (NT == 1) {
+                mma16<false>(s[r][qi & (CH - 1)][j], a[0], 0u, a[1], 0u, b0, b1);
+              } else {
+                mma16<false>(s[r][qi & (CH - 1)][j], a[0], a[1], a[2], a[3], b0, b1);
+              }
+            }
           }
         }
       }
-      // weights of tokens 4c .. 4c+3, in powers of two
-      float kx[4], ve[4];
+      // weights of tokens 4c .. 4c+3 of each 16, in powers of two
+      float sc[NT][4 * RR], ve[4 * RR];
       if constexpr (E4M3) {
-        const uint32_t kw = lds32(vb + S::KB + 4 * c), vw = lds32(vb + S::KB + 16 + 4 * c);
+        float kx[4 * RR];
+        uint32_t kw[RR], vw[RR], odd = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          kx[j] = e8m0_to_f32((kw >> (8 * j)) & 255u);
-          ve[j] = e8m0_exp((vw >> (8 * j)) & 255u);
+        for (int r = 0; r < RR; ++r) {
+          kw[r] = lds32(sbase + r * S::SCALES + 4 * c);
+          vw[r] = lds32(sbase + r * S::SCALES + 16 + 4 * c);
+          odd |= byte_255(kw[r]) | byte_255(vw[r]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // byte j << 23 (0 stands for 2^-127), and byte j - 127
+            kx[4 * r + j] = fmaxf(__uint_as_float(__byte_perm(kw[r], 0u, 0x0444 | (j << 12)) >> 1),
+                                  __uint_as_float(0x00400000u));
+            ve[4 * r + j] = __uint_as_float(__byte_perm(vw[r], 0x4B000000u, 0x7440 | j)) - 8388735.0f;
+          }
         }
+        if (odd) {  // NaN
+#pragma unroll
+          for (int j = 0; j < 4 * RR; ++j) {
+            if (((kw[j >> 2] >> (8 * (j & 3))) & 255u) == 255u) kx[j] = __uint_as_float(0x7FC00000u);
+            if (((vw[j >> 2] >> (8 * (j & 3))) & 255u) == 255u) ve[j] = __uint_as_float(0x7FC00000u);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4 * RR; ++j) sc[t][j] = sq[t] * kx[j];
+      } else {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int j = 0; j < 4 * RR; ++j) sc[t][j] = sq[t];
       }
-      const bool whole = tok >= cur.s.lo && tok + kRun <= cur.s.n;
-      float sc[NT][4], top[NT];
-      bool grows = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sc[t][j] = s[j >> 1][2 * t + (j & 1)] * (E4M3 ? sq[t] * kx[j] : sq[t]);
-          if (!whole && (tok + 4 * c + j < cur.s.lo || tok + 4 * c + j >= cur.s.n)) {
-            sc[t][j] = -INFINITY;
+        for (int j = 0; j < 4 * RR; ++j) {
+          const int h = (j >> 1) & 1, x = j & 1;
+          float raw_s;
+          if constexpr (E4M3) {
+            raw_s = fmaf(s[j >> 2][t][h][2 + x], 0.0625f, s[j >> 2][t][h][x]);
+          } else {
+            raw_s = s[j >> 2][0][h][2 * t + x];
+            if constexpr (CH == 2) raw_s += s[j >> 2][CH - 1][h][2 * t + x];
+          }
+          sc[t][j] *= raw_s;
+        }
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < 4 * RR; ++j) {
+          const unsigned tok = cur.tok + (j >> 2) * kRun + 4 * c + (j & 3);
+          if (tok < static_cast<unsigned>(cur.lo) || tok >= static_cast<unsigned>(cur.n) ||
+              ((bad >> (stage * RR + (j >> 2))) & 1u)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sc[t][j] = -INFINITY;
             if (E4M3) ve[j] = 0.f;
           }
         }
+      }
+      float top[NT];
+      bool grows = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
         if constexpr (E4M3) {  // l and its maximum, of this lane's tokens alone
-          const float mn = fmaxf(m_l[t], fmaxf(fmaxf(sc[t][0], sc[t][1]), fmaxf(sc[t][2], sc[t][3])));
+          float mn = m_l[t], add = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4 * RR; ++j) mn = fmaxf(mn, sc[t][j]);
           const float base = mn == -INFINITY ? 0.f : mn;
-          l[t] = l[t] * ex2(m_l[t] - base) + ((ex2(sc[t][0] - base) + ex2(sc[t][1] - base)) +
-                                              (ex2(sc[t][2] - base) + ex2(sc[t][3] - base)));
+#pragma unroll
+          for (int j = 0; j < 4 * RR; j += 2) add += ex2(sc[t][j] - base) + ex2(sc[t][j + 1] - base);
+          l[t] = l[t] * ex2(m_l[t] - base) + add;
           m_l[t] = mn;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sc[t][j] += ve[j];
+          for (int j = 0; j < 4 * RR; ++j) sc[t][j] += ve[j];
         }
-        top[t] = fmaxf(fmaxf(sc[t][0], sc[t][1]), fmaxf(sc[t][2], sc[t][3]));
+        top[t] = sc[t][0];
+#pragma unroll
+        for (int j = 1; j < 4 * RR; ++j) top[t] = fmaxf(top[t], sc[t][j]);
         grows |= top[t] > mrun[t];
       }
       if (__any_sync(0xFFFFFFFFu, grows)) {
@@ -484,67 +711,80 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
           }
         }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[RR][NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float base = (mrun[t] == -INFINITY ? 0.f : mrun[t]) - (E4M3 ? 14.f : 0.f);
-        float p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) p[j] = ex2(sc[t][j] - base);
-        if (!E4M3) l[t] += (p[0] + p[1]) + (p[2] + p[3]);
-        pf[t][0] = pack2<E4M3>(p[0], p[1]);
-        pf[t][1] = pack2<E4M3>(p[2], p[3]);
-      }
-      // O^T: rows g and g + 8 of product m are this lane's dimensions 2m and 2m + 1
+        for (int r = 0; r < RR; ++r) {
+          float p[4];
 #pragma unroll
-      for (int i = 0; i < VL; ++i) {
-        uint32_t vw[4][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t row = vb + (4 * c + j) * S::ROWB;
-          if constexpr (C >= 8) {
-            const uint4 u = lds128(row + (((g + 8 * i) ^ (2 * c)) << 4));
-            vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = u.z, vw[j][3] = u.w;
-          } else {
-            const uint2 u = lds64(row + g * 8);
-            vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = vw[j][3] = 0u;
-          }
+          for (int j = 0; j < 4; ++j) p[j] = ex2(sc[t][4 * r + j] - base);
+          if (!E4M3) l[t] += (p[0] + p[1]) + (p[2] + p[3]);
+          pf[r][t][0] = pack2<E4M3>(p[0], p[1]);
+          pf[r][t][1] = pack2<E4M3>(p[2], p[3]);
         }
-        constexpr int W = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
+      }
+      // O^T: rows g and g + 8 of product m are this lane's dimensions 2m and 2m + 1.  16 tokens that are
+      // not seen at all (past the end, or of a bad page) were not loaded and are left out
 #pragma unroll
-        for (int w = 0; w < W; ++w) {
-          if constexpr (E4M3) {
+      for (int r = 0; r < RR; ++r) {
+        if (r > 0 && cur.tok + r * kRun >= static_cast<unsigned>(cur.n)) break;
+        if (bad && ((bad >> (stage * RR + r)) & 1u)) continue;
+        const uint32_t vb = base0 + r * S::SUB + S::KB + 4 * c * S::ROWB + (C >= 8 ? (g ^ (2 * c)) << 4 : g * 8);
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_f16x2(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), a0, a1);
-              e4m3x4_to_f16x2(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), a2, a3);
+        for (int i = 0; i < VL; ++i) {
+          uint32_t vw[4][4];
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma16<true>(o[t][(i * W + w) * 2 + hf], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (C >= 8) {
+              const uint4 u = lds128(vb + j * S::ROWB + i * 128);
+              vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = u.z, vw[j][3] = u.w;
+            } else {
+              const uint2 u = lds64(vb + j * S::ROWB);
+              vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = vw[j][3] = 0u;
             }
-          } else {
-            const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-            const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410), a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+          }
+          constexpr int W = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
 #pragma unroll
-            for (int t = 0; t < NT; ++t) mma16<false>(o[t][i * W + w], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+          for (int w = 0; w < W; ++w) {
+            if constexpr (E4M3) {
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16x2(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), a0, a1);
+                e4m3x4_to_f16x2(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                  mma16<true>(o[t][(i * W + w) * 2 + hf], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+              const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410), a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16<false>(o[t][i * W + w], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
+            }
           }
         }
       }
     }
+    const int used = stage;
     stage = stage + 1 == ST ? 0 : stage + 1;
+    cur.tok += UNIT;
+    if (cur.tok < cur.stop) continue;
 
-    const bool last = step + 1 == steps;
-    if (cur.u + 1 < cur.s.units && !last) {
-      ++cur.u;
-      continue;
-    }
     // ---- the item ends here (or is cut here): join the warps
-    const bool cut = item_u0 > 0 || cur.u + 1 < cur.s.units;
-    const int gi = cur.it % P.groups;
-    const int h0 = (cur.it / P.groups) * P.G + gi * NQ, rows = min(NQ, P.G - gi * NQ);
+    const Walk<UNIT> done = cur;
+    const bool began_before = !DIRECT && done.unit_at(from) > 0, cut = began_before || (!DIRECT && done.unit_at(to) < done.units());
+    const int h0 = done.head * P.G + done.group * NQ, rows = min(NQ, P.G - done.group * NQ);
+    if (DIRECT)
+      cur.more = false;
+    else
+      cur.next_item(P, from, to, first);
+    if (kEarlyQ && cur.more) load_q(cur);  // arrives while the warps join
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float m = E4M3 ? m_l[t] : mrun[t];
+      const float m = E4M3 ? m_l[t] : mrun[t];
       float mm = m;
       mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 1));
       mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 2));
@@ -552,169 +792,191 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
       lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 1);
       lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 2);
       if (c == 0) {
-        s_fac[warp][g + 8 * t] = mrun[t];
-        s_m[warp][g + 8 * t] = mm;
-        s_l[warp][g + 8 * t] = lt;
+        s_mp[g + 8 * t][warp] = mrun[t];
+        s_m[g + 8 * t][warp] = mm;
+        s_l[g + 8 * t][warp] = lt;
       }
     }
-    __syncthreads();
-    if (tid < NQ) {
-      float mp = -INFINITY, mt = -INFINITY, lt = 0.f;
+    // quad x of warp w: in the stage that the warp has just used, and loads again only after this
+    float4 *buf = reinterpret_cast<float4 *>(smem + used * (RR * S::SUB));
+    constexpr int WARP = ST * RR * S::SUB / 16;  // from one warp's stages to the next's
+    const int slot = 2 * blockIdx.x + (first_item ? 0 : 1);
+    float fin[2], fac[2][kAdWarps];
+    int t_of = -1;
+    __syncwarp();
 #pragma unroll
-      for (int w = 0; w < kAdWarps; ++w) {
-        mp = fmaxf(mp, s_fac[w][tid]);
-        mt = fmaxf(mt, s_m[w][tid]);
-      }
+    for (int q0 = 0; q0 < S::QUADS; q0 += S::QR) {
 #pragma unroll
-      for (int w = 0; w < kAdWarps; ++w) {
-        lt += mt == -INFINITY ? s_l[w][tid] : s_l[w][tid] * ex2(s_m[w][tid] - mt);
-        s_fac[w][tid] = mp == -INFINITY ? 1.f : ex2(s_fac[w][tid] - mp);
-      }
-      if (cut) {
-        const int slot = 2 * blockIdx.x + (first_item ? 0 : 1);
-        P.stat[static_cast<size_t>(slot) * NQ + tid] = make_float4(mp, mt, lt, 0.f);
-      } else {
-        // out = O' 2^(m' - m - 14) / l
-        const float fin = (mp == -INFINITY ? 1.f : exp2f(mp - mt - (E4M3 ? 14.f : 0.f))) / lt;
-        s_fin[tid] = lt == 0.f ? 0.f : fin;
-        if (P.lse && tid < rows)
-          P.lse[static_cast<size_t>(cur.b) * P.Hq + h0 + tid] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
-      }
-    }
-    __syncthreads();
-    float4 *buf = reinterpret_cast<float4 *>(smem + kAdWarps * ST * S::STAGE);
-#pragma unroll
-    for (int rd = 0; rd < S::QUADS / 4; ++rd) {
-      if (rd) __syncthreads();
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int t = (rd * 4 + x) / MM, m = (rd * 4 + x) % MM;
-        const float f0w = s_fac[warp][8 * t + 2 * c], f1w = s_fac[warp][8 * t + 2 * c + 1];
-        buf[(warp * 4 + x) * 32 + lane] = make_float4(o[t][m][0] * f0w, o[t][m][1] * f1w, o[t][m][2] * f0w, o[t][m][3] * f1w);
+      for (int x = 0; x < S::QR; ++x) {
+        const int t = (q0 + x) / MM, m = (q0 + x) % MM;
+        buf[warp * WARP + x * 32 + lane] = make_float4(o[t][m][0], o[t][m][1], o[t][m][2], o[t][m][3]);
       }
       __syncthreads();
-      const int quad = rd * 4 + warp, t = quad / MM, m = quad % MM;
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      // this warp's share of the quads, summed over the warps at their common maximum
 #pragma unroll
-      for (int w = 0; w < kAdWarps; ++w) {
-        const float4 u = buf[(w * 4 + warp) * 32 + lane];
-        v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      for (int x0 = 0; x0 < S::QR; x0 += kAdWarps) {
+        const int x = x0 + warp, quad = q0 + x, t = quad / MM, m = quad % MM;
+        if (S::QR % kAdWarps && x >= S::QR) continue;
+        if (t != t_of) {
+          t_of = t;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * t + 2 * c + e;
+            const float4 mp4 = *reinterpret_cast<const float4 *>(s_mp[r]), m4 = *reinterpret_cast<const float4 *>(s_m[r]),
+                         l4 = *reinterpret_cast<const float4 *>(s_l[r]);
+            const float mp = fmaxf(fmaxf(mp4.x, mp4.y), fmaxf(mp4.z, mp4.w));
+            const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+            const float mb = mt == -INFINITY ? 0.f : mt, pb = mp == -INFINITY ? 0.f : mp;
+            const float lt = (l4.x * ex2(m4.x - mb) + l4.y * ex2(m4.y - mb)) + (l4.z * ex2(m4.z - mb) + l4.w * ex2(m4.w - mb));
+            fac[e][0] = ex2(mp4.x - pb), fac[e][1] = ex2(mp4.y - pb), fac[e][2] = ex2(mp4.z - pb), fac[e][3] = ex2(mp4.w - pb);
+            // out = O' 2^(m' - m - 14) / l; a row without weight is 0
+            fin[e] = lt == 0.f ? 0.f : __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt);
+            if (m == 0 && g == 0) {
+              if (cut)
+                P.stat[static_cast<size_t>(slot) * NQ + r] = make_float4(mp, mt, lt, 0.f);
+              else if (P.lse && r < rows)
+                P.lse[static_cast<size_t>(done.b) * P.Hq + h0 + r] = lt == 0.f ? -INFINITY : (mb + log2f(lt)) * kLn2;
+            }
+          }
+        }
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kAdWarps; ++w) {
+          const float4 u = buf[w * WARP + x * 32 + lane];
+          v.x = fmaf(u.x, fac[0][w], v.x);
+          v.y = fmaf(u.y, fac[1][w], v.y);
+          v.z = fmaf(u.z, fac[0][w], v.z);
+          v.w = fmaf(u.w, fac[1][w], v.w);
+        }
+        if (cut) {
+          P.part[(static_cast<size_t>(slot) * S::QUADS + quad) * 32 + lane] = v;
+        } else {
+          const int r0 = 8 * t + 2 * c;
+          uint16_t *op = P.out + (static_cast<size_t>(done.b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3, NT>(m, g);
+          store_row2(op, fin[0], v.x, v.z, r0 < rows);
+          store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
+        }
       }
-      if (cut) {
-        const int slot = 2 * blockIdx.x + (first_item ? 0 : 1);
-        P.part[(static_cast<size_t>(slot) * S::QUADS + quad) * 32 + lane] = v;
-      } else {
-        const int r0 = 8 * t + 2 * c;
-        const float x0 = s_fin[r0], x1 = s_fin[r0 + 1];
-        constexpr int PER = 16 / S::ESZ;  // dimensions of a 16-byte word
-        const int dl = 2 * m;             // of the lane's dimensions
-        const int d = C >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
-        uint16_t *op = P.out + (static_cast<size_t>(cur.b) * P.Hq + h0 + r0) * D + d;
-        // a row without weight is 0 (its sums are 0, or its scale is)
-        if (r0 < rows) *reinterpret_cast<uint32_t *>(op) = pack2<false>(x0 == 0.f ? 0.f : v.x * x0, x0 == 0.f ? 0.f : v.z * x0);
-        if (r0 + 1 < rows)
-          *reinterpret_cast<uint32_t *>(op + D) = pack2<false>(x1 == 0.f ? 0.f : v.y * x1, x1 == 0.f ? 0.f : v.w * x1);
-      }
+      __syncthreads();
     }
     if constexpr (!DIRECT) {
-      if (tid == 0 && item_u0 == 0 && cur.u + 1 < cur.s.units) {
-        // a cut item that starts here: the blocks whose pieces it covers
-        const long long end = f0 + step + (cur.s.units - cur.u) - 1;  // its last unit on the line
-        P.meta[blockIdx.x] = make_int4(static_cast<int>(end / share) - static_cast<int>(blockIdx.x) + 1,
-                                       2 * static_cast<int>(blockIdx.x) + (first_item ? 0 : 1), cur.it, cur.b);
+      if (tid == 0 && cut) {  // the blocks whose pieces the item covers
+        const long long unit0 = done.begin + kItemLen;
+        const int b0 = static_cast<int>(div_small(unit0, share));
+        P.meta[2 * blockIdx.x + (began_before ? 0 : 1)] = make_int4(
+            // not the first item of its block if the one before has a unit there
+            2 * b0 + (done.begin - kUnitLen >= b0 * share ? 1 : 0),
+            static_cast<int>(div_small(unit0 + static_cast<long long>(done.units() - 1) * kUnitLen, share)) - b0 + 1,
+            done.head * P.groups + done.group, done.b);
       }
     }
+    if (!cur.more) break;
     first_item = false;
-    if (last) break;
-    cur.next(P, items);
-    item_u0 = 0;
-    __syncthreads();
+    if (!kEarlyQ) load_q(cur);
     start_item();
+    if (QS) __syncthreads();
   }
   cp_wait<0>();
 }
 
-// Adds the partial sums of the items that were cut, in the order of their pieces: block
-// i joins the item that starts in block i's piece and goes on, if there is one.
+// Adds the partial sums of the items that were cut, in the order of their pieces.  The
+// blocks are those of the kernel before; each takes its share of the accumulator quads
+// of the (at most two) cut items that it holds a piece of, so that an item of many pieces
+// is joined by many blocks.  A warp adds up to kJoinParts parts of a quad, their
+// statistics and sums loaded together; where there are more, warps share a quad.
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(512) attn_join_kernel(const AdParams P) {
+__global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
   using S = AdShape<D, E4M3, NT>;
-  constexpr int NQ = 8 * NT, QUADS = S::QUADS, MM = S::MM, C = S::C;
-  constexpr int SPLIT = QUADS >= 16 ? 1 : 16 / QUADS;  // warps that share a quad's parts
-  extern __shared__ float fac[];                       // [parts][NQ]
-  __shared__ float s_fin[NQ];
-  __shared__ float4 s_sum[16][32];
+  constexpr int NQ = 8 * NT, QUADS = S::QUADS, MM = S::MM;
+  __shared__ float4 s_sum[8][32], s_stat[8][2][4];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_trigger();
-  const int4 me = P.meta[blockIdx.x];
-  const int parts = me.x;
-  if (parts < 2) return;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int gi = me.z % P.groups, h0 = (me.z / P.groups) * P.G + gi * NQ, rows = min(NQ, P.G - gi * NQ);
-  // part i is the first slot of block blockIdx.x + i, except part 0
-  auto slot = [&](int i) { return i == 0 ? me.y : 2 * (static_cast<int>(blockIdx.x) + i); };
-  if (warp < NQ) {
-    for (int r = warp; r < NQ; r += 16) {
-      float mp = -INFINITY, mt = -INFINITY;
-      for (int i = lane; i < parts; i += 32) {
-        const float4 s = P.stat[static_cast<size_t>(slot(i)) * NQ + r];
-        mp = fmaxf(mp, s.x);
-        mt = fmaxf(mt, s.y);
-      }
+  const int4 both[2] = {P.meta[2 * blockIdx.x], P.meta[2 * blockIdx.x + 1]};
+  // quads of each item that are this block's: mine, mine + parts, ..; warps that share one
+  int count[2], split[2];
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        mp = fmaxf(mp, __shfl_xor_sync(0xFFFFFFFFu, mp, off));
-        mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, off));
-      }
-      float lt = 0.f;
-      for (int i = lane; i < parts; i += 32) {
-        const float4 s = P.stat[static_cast<size_t>(slot(i)) * NQ + r];
-        lt += mt == -INFINITY ? s.z : s.z * ex2(s.y - mt);
-        fac[i * NQ + r] = mp == -INFINITY ? 1.f : ex2(s.x - mp);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, off);
-      if (lane == 0) {
-        const float fin = (mp == -INFINITY ? 1.f : exp2f(mp - mt - (E4M3 ? 14.f : 0.f))) / lt;
-        s_fin[r] = lt == 0.f ? 0.f : fin;
-        if (P.lse && r < rows)
-          P.lse[static_cast<size_t>(me.w) * P.Hq + h0 + r] = lt == 0.f ? -INFINITY : (mt + log2f(lt)) * kLn2;
-      }
-    }
+  for (int e = 0; e < 2; ++e) {
+    const int parts = both[e].y, mine = static_cast<int>(blockIdx.x) - (both[e].x >> 1);
+    count[e] = parts > 1 && mine < QUADS ? (QUADS - 1 - mine) / parts + 1 : 0;
+    split[e] = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
   }
-  __syncthreads();
-  for (int q0 = 0; q0 < QUADS; q0 += 16 / SPLIT) {
-    const int quad = q0 + warp / SPLIT, sub = warp % SPLIT, t = quad / MM, m = quad % MM;
+  // a quad's warps lie in one round of eight: splits are powers of two, and the second item's
+  // tasks start at a multiple of its split
+  const int tasks0 = count[0] * split[0], from1 = (tasks0 + split[1] - 1) / split[1] * split[1];
+  const int tasks = count[1] ? from1 + count[1] * split[1] : tasks0;
+  for (int base = 0; base < tasks; base += 8) {
+    int task = base + warp;
+    const int e = task < tasks0 ? 0 : 1;
+    if (e) task -= from1;
+    const int sp = split[e], sub = task & (sp - 1), q = task / sp;
+    const bool in = task >= 0 && q < count[e];
+    const int4 me = both[e];
+    const int parts = me.y, b0 = me.x >> 1, quad = static_cast<int>(blockIdx.x) - b0 + q * parts;
+    const int t = quad / MM, m = quad - t * MM, r0 = 8 * t + 2 * c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = sub; i < parts; i += SPLIT) {
-      const float4 u = P.part[(static_cast<size_t>(slot(i)) * QUADS + quad) * 32 + lane];
-      const float a0 = fac[i * NQ + 8 * t + 2 * c], a1 = fac[i * NQ + 8 * t + 2 * c + 1];
-      v.x = fmaf(u.x, a0, v.x);
-      v.y = fmaf(u.y, a1, v.y);
-      v.z = fmaf(u.z, a0, v.z);
-      v.w = fmaf(u.w, a1, v.w);
-    }
-    if constexpr (SPLIT > 1) {
-      s_sum[warp][lane] = v;
-      __syncthreads();
-      if (sub == 0) {
+    float mp[2] = {-INFINITY, -INFINITY}, mt[2] = {-INFINITY, -INFINITY}, lt[2] = {0.f, 0.f};
+    auto add = [&](const float4 &s0, const float4 &s1, const float4 &u) {
+      float f[2], h[2];
 #pragma unroll
-        for (int x = 1; x < SPLIT; ++x) {
-          const float4 u = s_sum[warp + x][lane];
-          v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+      for (int x = 0; x < 2; ++x) {
+        const float4 &s = x ? s1 : s0;
+        const float np = fmaxf(mp[x], s.x), nt = fmaxf(mt[x], s.y);
+        const float pb = np == -INFINITY ? 0.f : np, mb = nt == -INFINITY ? 0.f : nt;
+        f[x] = ex2(mp[x] - pb);
+        h[x] = ex2(s.x - pb);
+        lt[x] = lt[x] * ex2(mt[x] - mb) + s.z * ex2(s.y - mb);
+        mp[x] = np;
+        mt[x] = nt;
+      }
+      v.x = v.x * f[0] + u.x * h[0];
+      v.y = v.y * f[1] + u.y * h[1];
+      v.z = v.z * f[0] + u.z * h[0];
+      v.w = v.w * f[1] + u.w * h[1];
+    };
+    if (in) {
+      // part i lies in the first slot of block b0 + i, part 0 in me.x; this warp adds a run of them
+      const int i0 = parts * sub / sp, i1 = parts * (sub + 1) / sp;
+      for (int i = i0; i < i1; i += kJoinParts) {
+        float4 s[kJoinParts][2], u[kJoinParts];
+#pragma unroll
+        for (int x = 0; x < kJoinParts; ++x) {
+          const int at = min(i + x, i1 - 1);
+          const size_t slot = static_cast<size_t>(at == 0 ? me.x : 2 * (b0 + at));
+          s[x][0] = P.stat[slot * NQ + r0];
+          s[x][1] = P.stat[slot * NQ + r0 + 1];
+          u[x] = P.part[(slot * QUADS + quad) * 32 + lane];
         }
+#pragma unroll
+        for (int x = 0; x < kJoinParts; ++x)
+          if (i + x < i1) add(s[x][0], s[x][1], u[x]);
       }
     }
-    if (sub == 0) {
-      const int r0 = 8 * t + 2 * c;
-      const float x0 = s_fin[r0], x1 = s_fin[r0 + 1];
-      constexpr int PER = 16 / S::ESZ;
-      const int dl = 2 * m, d = C >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
-      uint16_t *op = P.out + (static_cast<size_t>(me.w) * P.Hq + h0 + r0) * D + d;
-      if (r0 < rows) *reinterpret_cast<uint32_t *>(op) = pack2<false>(x0 == 0.f ? 0.f : v.x * x0, x0 == 0.f ? 0.f : v.z * x0);
-      if (r0 + 1 < rows)
-        *reinterpret_cast<uint32_t *>(op + D) = pack2<false>(x1 == 0.f ? 0.f : v.y * x1, x1 == 0.f ? 0.f : v.w * x1);
+    if (max(split[0], split[1]) > 1) {  // (uniform: the block's)
+      s_sum[warp][lane] = v;
+      if (g == 0) {
+        s_stat[warp][0][c] = make_float4(mp[0], mt[0], lt[0], 0.f);
+        s_stat[warp][1][c] = make_float4(mp[1], mt[1], lt[1], 0.f);
+      }
+      __syncthreads();
+      if (in && sub == 0)
+        for (int x = 1; x < sp; ++x) add(s_stat[warp + x][0][c], s_stat[warp + x][1][c], s_sum[warp + x][lane]);
+      __syncthreads();
+    }
+    if (in && sub == 0) {
+      const int head = me.z / P.groups, group = me.z - head * P.groups;
+      const int h0 = head * P.G + group * NQ, rows = min(NQ, P.G - group * NQ);
+      float fin[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float mb = mt[x] == -INFINITY ? 0.f : mt[x], pb = mp[x] == -INFINITY ? 0.f : mp[x];
+        fin[x] = lt[x] == 0.f ? 0.f : exp2f(pb - mb - (E4M3 ? 14.f : 0.f)) / lt[x];
+        if (P.lse && m == 0 && g == 0 && r0 + x < rows)
+          P.lse[static_cast<size_t>(me.w) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
+      }
+      uint16_t *op = P.out + (static_cast<size_t>(me.w) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3, NT>(m, g);
+      store_row2(op, fin[0], v.x, v.z, r0 < rows);
+      store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
     }
   }
 }
@@ -734,7 +996,7 @@ AdPlan plan_of(const k3moe_kv_cache &c, int Hq) {
   p.quads = c.dim / 16 * p.NT;
   const size_t slots = 2 * static_cast<size_t>(kAdMostBlocks);
   p.meta = 0;
-  p.stat = (kAdMostBlocks * sizeof(int4) + 255) / 256 * 256;
+  p.stat = slots * sizeof(int4);
   p.part = p.stat + slots * 8 * p.NT * sizeof(float4);
   p.bytes = p.part + slots * p.quads * 32 * sizeof(float4);
   return p;
@@ -746,7 +1008,6 @@ int launch_attn(AdParams &P, cudaStream_t st) {
   const long long items = static_cast<long long>(P.B) * P.heads * P.groups;
   const int visible = P.max_pages << P.page_shift;  // most tokens an item can have
   const int tokens = P.window > 0 && P.window < visible ? P.window + kRun - 1 : visible;
-  const int units = (tokens + kUnit - 1) / kUnit;
   static bool attr = false;
   if (!attr) {
     if (cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -756,18 +1017,18 @@ int launch_attn(AdParams &P, cudaStream_t st) {
       return -1;
     attr = true;
   }
-  if (units <= kDirectUnits && items < (1LL << 31))
+  if (tokens <= kDirectTokens && items < (1LL << 31))
     return launch_pdl(attn_decode_kernel<D, E4M3, NT, true>, dim3(static_cast<unsigned>(items)), dim3(kAdThreads), S::SMEM,
                       st, P) == cudaSuccess
                ? 0
                : -1;
-  long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;
+  long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS * KF / 4;
   if (blocks > kAdMostBlocks) blocks = kAdMostBlocks;
-  const long long most = (items * units + kMinUnits - 1) / kMinUnits;
+  const long long most = (items * ((tokens + S::UNIT - 1) / S::UNIT * S::UNIT) + kMinTokens - 1) / kMinTokens;
   if (blocks > most) blocks = most;
   const dim3 grid(static_cast<unsigned>(blocks));
   if (launch_pdl(attn_decode_kernel<D, E4M3, NT, false>, grid, dim3(kAdThreads), S::SMEM, st, P) != cudaSuccess) return -1;
-  return launch_pdl(attn_join_kernel<D, E4M3, NT>, grid, dim3(512), blocks * 8 * NT * sizeof(float), st, P) == cudaSuccess
+  return launch_pdl(attn_join_kernel<D, E4M3, NT>, grid, dim3(256), 0, st, P) == cudaSuccess
              ? 0
              : -1;
 }
