@@ -32,17 +32,17 @@
 //    and 8 query heads as columns, so that S's registers are P^T's.  The order of
 //    dimensions and tokens inside a product is free as long as both operands agree, and
 //    is chosen so that a lane's share of K and V is whole 16-byte words.
-//  * E4M3.  K's codes enter their products as they are (m16n8k32): a query row is scaled by a
-//    power of two to a maximum in [128, 256) and split as q = hi + lo / 16 into two E4M3
-//    values of 4 bits each, which is exact (bf16 has 8) but for values below 2^-13 of the row's
-//    maximum, and off by at most 2^-22 of that for them; hi and lo are two rows of the product, so that
-//    8 query heads fill its 16.  K's scale multiplies the score.  V's codes are converted to
-//    f16 (exact); V's scale 2^e joins the weight: w_i = exp2(s_i + e_i - m')
+//  * E4M3.  Codes are converted to f16 (exact; the E4M3 form of this instruction does the
+//    same within, on both operands and for every product: measured slower).  A query row is
+//    scaled by a power of two to a maximum in [2^14, 2^15), exact but for values below 2^-28
+//    of it.  K's scale multiplies the score.  V's scale 2^e joins the weight: w_i = exp2(s_i + e_i - m')
 //    with its own running maximum m' of s_i + e_i, times 2^14, rounded to f16 (11 bits
 //    down to 2^-28 of the largest, so that a token with a large score and a tiny value
 //    costs the others nothing), while l sums exp2(s_i - m) in fp32 with m = max s_i.
 //  * bf16.  Q, K and V enter as they are; the weights are rounded to bf16, as V is.
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "k3moe_dev.cuh"
 #include "k3moe_launch.h"
@@ -54,10 +54,10 @@ namespace k3moe {
 namespace {
 
 #ifndef KRR
-#define KRR (ROWB <= 128 && NT == 1 ? 2 : ROWB <= 64 ? 2 : 1)
+#define KRR (ROWB <= 64 ? 4 : ROWB <= 128 ? 2 : 1)
 #endif
 #ifndef KST
-#define KST (ROWB <= 64 ? 4 : RR == 2 ? 2 : 3)
+#define KST 3
 #endif
 #ifndef KQS
 #define KQS 32
@@ -66,7 +66,7 @@ namespace {
 #define KF 4
 #endif
 #ifndef KBL
-#define KBL (ROWB <= 128 ? 3 : ROWB <= 256 ? 2 : 1)
+#define KBL (ROWB <= 256 ? 2 : 1)
 #endif
 constexpr int kAdWarps = 4;
 constexpr int kAdThreads = kAdWarps * 32;
@@ -75,7 +75,7 @@ constexpr int kDirectTokens = 512;       // items of at most this many tokens ar
 constexpr int kMinTokens = 256;          // smallest piece of a block
 #ifndef KWU
 #define KWU 4
-#define KWI 3
+#define KWI 6
 #endif
 constexpr int kUnitLen = KWU, kItemLen = KWI;  // length on the line of a unit, and of an item beside its units
 constexpr int kJoinParts = 8;            // parts of an item that one warp joins
@@ -131,12 +131,18 @@ __device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, u
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// d += a b, m16n8k32, E4M3 operands.
-__device__ __forceinline__ void mma32_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                           uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// The same from zero: d = a b.
+template <bool H>
+__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                            uint32_t b1) {
+  if constexpr (H)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 template <bool H>
@@ -267,7 +273,7 @@ struct AdShape {
   // quads that the warps exchange at once where an item ends, each in the stage it has just used
   static constexpr int QR = RR * SUB / 512 < QUADS ? RR * SUB / 512 : QUADS;
   // query fragments: in registers, or from 32 of them on in shared memory (the same for all warps)
-  static constexpr int QREGS = E4M3 ? D / 32 * 4 * NT : D / 16 * 2 * NT;
+  static constexpr int QREGS = D / 16 * 2 * NT;
   static constexpr int QSMEM = QREGS >= KQS ? QREGS * 32 * 4 : 0;
   static constexpr int SMEM = kAdWarps * STAGES * RR * (SUB + SCALES) + QSMEM + 128;
 };
@@ -305,6 +311,17 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
   const int items = P.heads * P.groups, first = warp * S::RUN;
   pdl_wait();
   pdl_trigger();
+
+  auto zero_rows = [&]() {  // of the sequences that see nothing; every block takes its share
+    for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
+      const Seen s = seen_of(P, b, false);
+      if (s.n > s.t0) continue;
+      for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += kAdThreads)
+        reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+      if (P.lse)
+        for (int i = tid; i < P.Hq; i += kAdThreads) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
+    }
+  };
 
   // ---- this block's piece
   Walk<UNIT> cur;
@@ -370,17 +387,11 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
       s_start[1] = item;
     }
     if (tid < 2) P.meta[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
-    // rows that see nothing
-    for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-      const Seen s = seen_of(P, b, false);
-      if (s.n > s.t0) continue;
-      for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += kAdThreads)
-        reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
-      if (P.lse)
-        for (int i = tid; i < P.Hq; i += kAdThreads) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
-    }
     __syncthreads();
-    if (from >= to) return;
+    if (from >= to) {
+      zero_rows();
+      return;
+    }
     cur.b = s_start[0];
     cur.head = s_start[1] / P.groups;
     cur.group = s_start[1] - cur.head * P.groups;
@@ -389,7 +400,10 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     cur.more = true;
     cur.enter(from, to, first);
     if (cur.tok >= cur.stop) cur.next_item(P, from, to, first);  // the piece begins behind the item's last unit
-    if (!cur.more || cur.tok >= cur.stop) return;                // or ends before its first
+    if (!cur.more || cur.tok >= cur.stop) {                      // or ends before its first
+      zero_rows();
+      return;
+    }
   }
 
   // ---- loads: the run at `pre` into stage st.  Lane l copies words l, l + 32, .. of 16 tokens' keys
@@ -464,9 +478,9 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
 #pragma unroll
   for (int st = 0; st < ST - 1; ++st) issue(st);
 
-  constexpr int QN = E4M3 ? D / 32 : D / 16;  // products along the dimensions
+  constexpr int QN = D / 16, QW = 2 * NT;  // products along the dimensions, registers of the query rows in each
   constexpr bool QS = S::QSMEM > 0;
-  uint32_t qf[QS ? 1 : QN][E4M3 ? 4 * NT : 2 * NT];
+  uint32_t qf[QS ? 1 : QN][QW];
   uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + kAdWarps * ST * RR * (S::SUB + S::SCALES));
   uint2 raw[D / 16][NT];
   float sq[NT];  // scale of a raw score, in powers of two
@@ -488,53 +502,36 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
   auto start_item = [&]() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      float up = 1.f;
+      sq[t] = P.scale * kLog2e;
       if constexpr (E4M3) {
         uint32_t mx = 0;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
+        for (int i = 0; i < QN; ++i) {
           const uint2 u = raw[i][t];
           mx = max(mx, max(max((u.x << 16) & 0x7FFFFFFFu, u.x & 0x7FFF0000u),
                            max((u.y << 16) & 0x7FFFFFFFu, u.y & 0x7FFF0000u)));
         }
         mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-        // 2^(7 - floor(log2 max)), as far as fp32 has it; a row that is not finite gives NaN
-        const int e = mx == 0 ? 0 : max(-126, min(127, 7 + 127 - static_cast<int>(mx >> 23)));
-        const float up = exp2i(e);
-        sq[t] = mx >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : P.scale * kLog2e * mx_pow2(-e);
+        // 2^(14 - floor(log2 max)), as far as fp32 has it
+        const int e = mx == 0 ? 0 : max(-126, min(127, 14 + 127 - static_cast<int>(mx >> 23)));
+        up = exp2i(e);
+        sq[t] *= mx_pow2(-e);
+      }
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint2 u = raw[i][t];
-          const float v[4] = {__uint_as_float(u.x << 16) * up, __uint_as_float(u.x & 0xFFFF0000u) * up,
-                              __uint_as_float(u.y << 16) * up, __uint_as_float(u.y & 0xFFFF0000u) * up};
-          const uint32_t h0 = e4m3x2(v[0], v[1]), h1 = e4m3x2(v[2], v[3]);
-          uint32_t fh[2];
-          e4m3x4_to_f16x2(h0 | (h1 << 16), fh[0], fh[1]);
-          const float2 d0 = __half22float2(*reinterpret_cast<const __half2 *>(&fh[0]));
-          const float2 d1 = __half22float2(*reinterpret_cast<const __half2 *>(&fh[1]));
-          // word i of the lane's: product i / 2, first or second four of its eight dimensions there
-          const uint32_t hi = h0 | (h1 << 16);
-          const uint32_t lo = e4m3x2((v[0] - d0.x) * 16.f, (v[1] - d0.y) * 16.f) |
-                              (e4m3x2((v[2] - d1.x) * 16.f, (v[3] - d1.y) * 16.f) << 16);
-          if constexpr (QS) {  // (every warp writes the same)
-            reinterpret_cast<uint2 *>(&q_sm[((i >> 1) * NT + t) * 32 + lane])[i & 1] = make_uint2(hi, lo);
-          } else {
-            qf[i >> 1][4 * t + 2 * (i & 1)] = hi;
-            qf[i >> 1][4 * t + 2 * (i & 1) + 1] = lo;
-          }
-        }
-      } else {
-        sq[t] = P.scale * kLog2e;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          if constexpr (QS) {
-            uint32_t *const to_sm = reinterpret_cast<uint32_t *>(&q_sm[(NT == 1 ? i / 2 : i) * 32 + lane]);
-            to_sm[NT == 1 ? 2 * (i & 1) : t] = raw[i][t].x;
-            to_sm[NT == 1 ? 2 * (i & 1) + 1 : NT + t] = raw[i][t].y;
-          } else {
-            qf[i][t] = raw[i][t].x;
-            qf[i][NT + t] = raw[i][t].y;
-          }
+      for (int i = 0; i < QN; ++i) {
+        uint2 u = raw[i][t];
+        if constexpr (E4M3)
+          u = make_uint2(pack2<true>(__uint_as_float(u.x << 16) * up, __uint_as_float(u.x & 0xFFFF0000u) * up),
+                         pack2<true>(__uint_as_float(u.y << 16) * up, __uint_as_float(u.y & 0xFFFF0000u) * up));
+        if constexpr (QS) {  // (every warp writes the same)
+          uint32_t *const to_sm = reinterpret_cast<uint32_t *>(&q_sm[(NT == 1 ? i / 2 : i) * 32 + lane]);
+          to_sm[NT == 1 ? 2 * (i & 1) : t] = u.x;
+          to_sm[NT == 1 ? 2 * (i & 1) + 1 : NT + t] = u.y;
+        } else {
+          qf[i][t] = u.x;
+          qf[i][NT + t] = u.y;
         }
       }
       mrun[t] = m_l[t] = -INFINITY;
@@ -562,11 +559,10 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
       const uint32_t base0 = ring + stage * (RR * S::SUB), sbase = sring + stage * (RR * S::SCALES);
       const bool whole = cur.tok >= static_cast<unsigned>(cur.lo) &&
                          cur.tok + S::RUN <= static_cast<unsigned>(cur.n) && bad == 0u;
-      // S: columns 2c, 2c+1 of product j of 16 tokens are tokens 4c + 2j, 4c + 2j + 1.  CH partial
-      // sums each, so that a product does not wait for the one before it
-      constexpr int CH = !E4M3 && RR == 1 ? 2 : 1;
-      constexpr int SN = E4M3 ? NT : 1;  // products of 16 rows: 8 query heads (hi, lo), or 16
-      float s[RR][SN * CH][2][4] = {};
+      // S: columns 2c, 2c+1 of product j of 16 tokens are tokens 4c + 2j, 4c + 2j + 1.  Where a step
+      // has 16 tokens there are two partial sums each, so that a product does not wait for the one before it
+      constexpr int CH = RR == 1 ? 2 : 1;
+      float s[RR][CH][2][4];
       const uint32_t kofs = (4 * (g >> 1) + (g & 1)) * S::ROWB + (c << 4) + (C >= 8 ? (g & 1) << 6 : 0);
 #pragma unroll
       for (int i = 0; i < KL; ++i) {
@@ -577,35 +573,32 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
           for (int j = 0; j < 2; ++j)
             kw[j] = lds128(((base0 + r * S::SUB + kofs) ^ ((i & 1) << 6)) + (i >> 1) * 128 + 2 * j * S::ROWB);
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const int qi = i * 2 + w;
-            uint32_t a[E4M3 ? 4 * NT : 2 * NT];
+          for (int w = 0; w < SP; ++w) {
+            const int qi = i * SP + w;
+            uint32_t a[QW];
             if constexpr (QS) {
-              if constexpr (E4M3) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                  *reinterpret_cast<uint4 *>(&a[4 * t]) = q_sm[(qi * NT + t) * 32 + lane];
-              } else if constexpr (NT == 1) {
-                *reinterpret_cast<uint2 *>(a) = reinterpret_cast<const uint2 *>(&q_sm[i * 32 + lane])[w];
-              } else {
+              if constexpr (NT == 1)
+                *reinterpret_cast<uint2 *>(a) = reinterpret_cast<const uint2 *>(&q_sm[(qi / 2) * 32 + lane])[qi & 1];
+              else
                 *reinterpret_cast<uint4 *>(a) = q_sm[qi * 32 + lane];
-              }
             } else {
 #pragma unroll
-              for (int x = 0; x < (E4M3 ? 4 * NT : 2 * NT); ++x) a[x] = qf[qi][x];
+              for (int x = 0; x < QW; ++x) a[x] = qf[qi][x];
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t b0 = w ? kw[j].z : kw[j].x, b1 = w ? kw[j].w : kw[j].y;
-              if constexpr (E4M3) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                  mma32_e4m3(s[r][t][j], a[4 * t], a[4 * t + 1], a[4 * t + 2], a[4 * t + 3], b0, b1);
-              } else if constexpr (NT == 1) {
-                mma16<false>(s[r][qi & (CH - 1)][j], a[0], 0u, a[1], 0u, b0, b1);
-              } else {
-                mma16<false>(s[r][qi & (CH - 1)][j], a[0], a[1], a[2], a[3], b0, b1);
-              }
+              const uint32_t kk[4] = {kw[j].x, kw[j].y, kw[j].z, kw[j].w};
+              uint32_t b0, b1;
+              if constexpr (E4M3)
+                e4m3x4_to_f16x2(kk[w], b0, b1);
+              else
+                b0 = kk[2 * w], b1 = kk[2 * w + 1];
+              float(&d)[4] = s[r][qi & (CH - 1)][j];
+              const uint32_t a1 = NT == 1 ? 0u : a[1], a2 = NT == 1 ? a[1] : a[QW - 2], a3 = NT == 1 ? 0u : a[QW - 1];
+              if (qi < CH)
+                mma16_first<E4M3>(d, a[0], a1, a2, a3, b0, b1);
+              else
+                mma16<E4M3>(d, a[0], a1, a2, a3, b0, b1);
             }
           }
         }
@@ -650,13 +643,8 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
 #pragma unroll
         for (int j = 0; j < 4 * RR; ++j) {
           const int h = (j >> 1) & 1, x = j & 1;
-          float raw_s;
-          if constexpr (E4M3) {
-            raw_s = fmaf(s[j >> 2][t][h][2 + x], 0.0625f, s[j >> 2][t][h][x]);
-          } else {
-            raw_s = s[j >> 2][0][h][2 * t + x];
-            if constexpr (CH == 2) raw_s += s[j >> 2][CH - 1][h][2 * t + x];
-          }
+          float raw_s = s[j >> 2][0][h][2 * t + x];
+          if constexpr (CH == 2) raw_s += s[j >> 2][CH - 1][h][2 * t + x];
           sc[t][j] *= raw_s;
         }
       if (!whole) {
@@ -877,6 +865,7 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     if (QS) __syncthreads();
   }
   cp_wait<0>();
+  if constexpr (!DIRECT) zero_rows();
 }
 
 // Adds the partial sums of the items that were cut, in the order of their pieces.  The
@@ -915,41 +904,48 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
     const int parts = me.y, b0 = me.x >> 1, quad = static_cast<int>(blockIdx.x) - b0 + q * parts;
     const int t = quad / MM, m = quad - t * MM, r0 = 8 * t + 2 * c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    float mp[2] = {-INFINITY, -INFINITY}, mt[2] = {-INFINITY, -INFINITY}, lt[2] = {0.f, 0.f};
-    auto add = [&](const float4 &s0, const float4 &s1, const float4 &u) {
-      float f[2], h[2];
+    float mp[2], mt[2], lt[2];
+    // the sum of N parts (statistics s of this lane's two rows, sums u), all at once
+    auto add = [&](const auto &s, const auto &u, auto N) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float4 &s = x ? s1 : s0;
-        const float np = fmaxf(mp[x], s.x), nt = fmaxf(mt[x], s.y);
+        float np = -INFINITY, nt = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N.value; ++i) np = fmaxf(np, s[i][x].x), nt = fmaxf(nt, s[i][x].y);
         const float pb = np == -INFINITY ? 0.f : np, mb = nt == -INFINITY ? 0.f : nt;
-        f[x] = ex2(mp[x] - pb);
-        h[x] = ex2(s.x - pb);
-        lt[x] = lt[x] * ex2(mt[x] - mb) + s.z * ex2(s.y - mb);
-        mp[x] = np;
-        mt[x] = nt;
+        float a = 0.f, b = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < N.value; ++i) {
+          const float f = ex2(s[i][x].x - pb);
+          a = fmaf(x ? u[i].y : u[i].x, f, a);
+          b = fmaf(x ? u[i].w : u[i].z, f, b);
+          sum = fmaf(s[i][x].z, ex2(s[i][x].y - mb), sum);
+        }
+        (x ? v.y : v.x) = a;
+        (x ? v.w : v.z) = b;
+        mp[x] = np, mt[x] = nt, lt[x] = sum;
       }
-      v.x = v.x * f[0] + u.x * h[0];
-      v.y = v.y * f[1] + u.y * h[1];
-      v.z = v.z * f[0] + u.z * h[0];
-      v.w = v.w * f[1] + u.w * h[1];
     };
+    const float4 none = make_float4(-INFINITY, -INFINITY, 0.f, 0.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    mp[0] = mp[1] = mt[0] = mt[1] = -INFINITY;
+    lt[0] = lt[1] = 0.f;
     if (in) {
       // part i lies in the first slot of block b0 + i, part 0 in me.x; this warp adds a run of them
       const int i0 = parts * sub / sp, i1 = parts * (sub + 1) / sp;
       for (int i = i0; i < i1; i += kJoinParts) {
-        float4 s[kJoinParts][2], u[kJoinParts];
+        float4 s[kJoinParts + 1][2], u[kJoinParts + 1];
 #pragma unroll
         for (int x = 0; x < kJoinParts; ++x) {
-          const int at = min(i + x, i1 - 1);
-          const size_t slot = static_cast<size_t>(at == 0 ? me.x : 2 * (b0 + at));
-          s[x][0] = P.stat[slot * NQ + r0];
-          s[x][1] = P.stat[slot * NQ + r0 + 1];
-          u[x] = P.part[(slot * QUADS + quad) * 32 + lane];
+          const bool on = i + x < i1;
+          const size_t slot = static_cast<size_t>(i + x == 0 ? me.x : 2 * (b0 + i + x));
+          s[x][0] = on ? P.stat[slot * NQ + r0] : none;
+          s[x][1] = on ? P.stat[slot * NQ + r0 + 1] : none;
+          u[x] = on ? P.part[(slot * QUADS + quad) * 32 + lane] : zero;
         }
-#pragma unroll
-        for (int x = 0; x < kJoinParts; ++x)
-          if (i + x < i1) add(s[x][0], s[x][1], u[x]);
+        s[kJoinParts][0] = make_float4(mp[0], mt[0], lt[0], 0.f);
+        s[kJoinParts][1] = make_float4(mp[1], mt[1], lt[1], 0.f);
+        u[kJoinParts] = v;
+        add(s, u, std::integral_constant<int, kJoinParts + 1>());
       }
     }
     if (max(split[0], split[1]) > 1) {  // (uniform: the block's)
@@ -959,8 +955,17 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
         s_stat[warp][1][c] = make_float4(mp[1], mt[1], lt[1], 0.f);
       }
       __syncthreads();
-      if (in && sub == 0)
-        for (int x = 1; x < sp; ++x) add(s_stat[warp + x][0][c], s_stat[warp + x][1][c], s_sum[warp + x][lane]);
+      if (in && sub == 0 && sp > 1) {
+        float4 s[8][2], u[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int w = min(warp + x, 7);
+          s[x][0] = x < sp ? s_stat[w][0][c] : none;
+          s[x][1] = x < sp ? s_stat[w][1][c] : none;
+          u[x] = x < sp ? s_sum[w][lane] : zero;
+        }
+        add(s, u, std::integral_constant<int, 8>());
+      }
       __syncthreads();
     }
     if (in && sub == 0) {
