@@ -65,6 +65,8 @@ def library_path() -> str:
 def lib():
     """Load libk3moe.so (built by ``build.build()``); raise if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_SO):
@@ -149,9 +151,16 @@ def _ptr(t, dtype=None, name="tensor"):
     return t.data_ptr() if t.numel() else None
 
 
+# the current stream's handle without a torch.cuda.Stream object around it (0.4 against 2.9 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(fn, rc):
@@ -338,11 +347,40 @@ def k3moe_layer(shape, logits, x, weights: Weights, idx, w, counts, offsets, per
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)   # E4M3 codes, or their bytes
 _SCALES = (torch.uint8, torch.float8_e8m0fnu)  # E8M0 scales, or their bytes
+_I32, _F32 = (torch.int32,), (torch.float32,)
 
 
 def _want(t, shape, name):
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _in(t, kinds, shape, name):
+    """Pointer of a packed CUDA tensor of one of the dtypes `kinds` and of shape `shape`
+    (None for None and for an empty tensor)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype in kinds and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr() or None
+    _ptr(t, kinds, name)  # says what is wrong, or
+    _want(t, shape, name)
+
+
+def _rows(t, shape, name):
+    """Pointer and stride (values) of tokens' vectors [n, heads, dim]: packed but for the first axis."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype not in _BF16:
+        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
+    if t.shape != shape:
+        _want(t, shape, name)
+    n, heads, dim = shape
+    if n == 0:
+        return None, heads * dim
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
+        raise ValueError(f"{name}: heads and dim must be packed (only the first axis may have a stride)")
+    return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
 def k3moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, codes=None, scales=None, stream=None):
@@ -351,19 +389,15 @@ def k3moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, code
     scales [T, H/32] (E8M0) of the norm times weight."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a tensor [T, H]")
-    T, H = x.shape
-    if weight is not None:
-        _want(weight, (H,), "weight")
-    for t, name in ((residual, "residual"), (residual_out, "residual_out"), (y, "y"), (codes, "codes")):
-        if t is not None:
-            _want(t, (T, H), name)
-    if scales is not None:
-        _want(scales, (T, H // 32), "scales")
-    rc = lib().k3moe_rmsnorm(T, H, _ptr(x, _BF16, "x"), _ptr(residual, _BF16, "residual"),
-                             _ptr(weight, _BF16, "weight"), float(eps), _ptr(residual_out, _BF16, "residual_out"),
-                             _ptr(y, _BF16, "y"), _ptr(codes, _CODES, "codes"), _ptr(scales, _SCALES, "scales"),
+    shape = x.shape
+    T, H = shape
+    rc = lib().k3moe_rmsnorm(T, H, _in(x, _BF16, shape, "x"), _in(residual, _BF16, shape, "residual"),
+                             _in(weight, _BF16, (H,), "weight"), eps,
+                             _in(residual_out, _BF16, shape, "residual_out"), _in(y, _BF16, shape, "y"),
+                             _in(codes, _CODES, shape, "codes"), _in(scales, _SCALES, (T, H // 32), "scales"),
                              _stream(stream))
-    _check("k3moe_rmsnorm", rc)
+    if rc:
+        _check("k3moe_rmsnorm", rc)
 
 
 class KVCache:
@@ -375,19 +409,17 @@ class KVCache:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k: expected a tensor [pages, heads, page_size, dim]")
         quantised = k.dtype in _CODES
-        pages, heads, page_size, dim = k.shape
-        _want(v, tuple(k.shape), "v")
+        shape = tuple(k.shape)
+        _want(v, shape, "v")
         if quantised != (k_scales is not None) or quantised != (v_scales is not None):
             raise ValueError("k_scales and v_scales belong to an 8-bit cache, and only to one")
-        if quantised:
-            _want(k_scales, (pages, heads, page_size), "k_scales")
-            _want(v_scales, (pages, heads, page_size), "v_scales")
         kind = _CODES if quantised else _BF16
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.pages, self.heads, self.page_size, self.dim = pages, heads, page_size, dim
+        self.pages, self.heads, self.page_size, self.dim = shape
         self.format = K3MOE_KV_E4M3 if quantised else K3MOE_KV_BF16
-        self._c = _KVCacheC(pages, page_size, heads, dim, self.format, _ptr(k, kind, "k"), _ptr(v, kind, "v"),
-                            _ptr(k_scales, _SCALES, "k_scales"), _ptr(v_scales, _SCALES, "v_scales"))
+        self._c = _KVCacheC(self.pages, self.page_size, self.heads, self.dim, self.format, _in(k, kind, shape, "k"),
+                            _in(v, kind, shape, "v"), _in(k_scales, _SCALES, shape[:3], "k_scales"),
+                            _in(v_scales, _SCALES, shape[:3], "v_scales"))
         self._ref = ctypes.byref(self._c)
 
     @classmethod
@@ -399,23 +431,9 @@ class KVCache:
         if fmt == K3MOE_KV_E4M3:
             return cls(new(shape, torch.uint8), new(shape, torch.uint8), new(shape[:3], torch.uint8),
                        new(shape[:3], torch.uint8))
+        if fmt != K3MOE_KV_BF16:
+            raise ValueError(f"fmt: expected K3MOE_KV_BF16 or K3MOE_KV_E4M3, got {fmt}")
         return cls(new(shape, torch.bfloat16), new(shape, torch.bfloat16))
-
-
-def _rows(t, shape, name):
-    """Pointer and stride (values) of tokens' vectors [n, heads, dim]: packed but for the first axis."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype not in _BF16:
-        raise TypeError(f"{name}: expected {_BF16}, got {t.dtype}")
-    _want(t, shape, name)
-    n, heads, dim = shape
-    if n == 0:
-        return None, heads * dim
-    _, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != dim):
-        raise ValueError(f"{name}: heads and dim must be packed (only the first axis may have a stride)")
-    return t.data_ptr(), t.stride(0) if n > 1 else heads * dim
 
 
 def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
@@ -424,20 +442,20 @@ def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
     shape = (slots.numel(), cache.heads, cache.dim)
     kp, ks = _rows(k, shape, "k")
     vp, vs = _rows(v, shape, "v")
-    rc = lib().k3moe_kv_write(cache._ref, shape[0], kp, vp, ks, vs, _ptr(slots, torch.int32, "slots"),
+    rc = lib().k3moe_kv_write(cache._ref, shape[0], kp, vp, ks, vs, _in(slots, _I32, shape[:1], "slots"),
                               _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
-    _check("k3moe_kv_write", rc)
+    if rc:
+        _check("k3moe_kv_write", rc)
 
 
 def k3moe_kv_read(cache: KVCache, slots, k, v, dev_status=None, stream=None):
     """The cache's slots [n] (int32) as bf16 keys and values k, v [n, heads, dim] (zeros
     for a negative slot)."""
     shape = (slots.numel(), cache.heads, cache.dim)
-    _want(k, shape, "k")
-    _want(v, shape, "v")
-    rc = lib().k3moe_kv_read(cache._ref, shape[0], _ptr(slots, torch.int32, "slots"), _ptr(k, _BF16, "k"),
-                             _ptr(v, _BF16, "v"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
-    _check("k3moe_kv_read", rc)
+    rc = lib().k3moe_kv_read(cache._ref, shape[0], _in(slots, _I32, shape[:1], "slots"), _in(k, _BF16, shape, "k"),
+                             _in(v, _BF16, shape, "v"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    if rc:
+        _check("k3moe_kv_read", rc)
 
 
 def k3moe_attn_decode_workspace_bytes(cache: KVCache, batch: int, q_heads: int) -> int:
@@ -450,21 +468,19 @@ def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, s
     may be strided), block_table [B, max_pages] and seq_lens [B] (int32) -> out
     [B, Hq, dim] (bf16), lse [B, Hq] (fp32).  scale defaults to dim^-1/2; window > 0
     sees only the last that many tokens; ws: k3moe_attn_decode_workspace_bytes."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or block_table.dim() != 2:
-        raise ValueError("q: expected a tensor [B, Hq, dim], block_table: [B, max_pages]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected a tensor [B, Hq, dim]")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table: expected a tensor [B, max_pages]")
     B, Hq, _ = q.shape
     shape = (B, Hq, cache.dim)
     qp, qs = _rows(q, shape, "q")
-    _want(out, shape, "out")
-    _want(seq_lens, (B,), "seq_lens")
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected {B} rows, got {block_table.shape[0]}")
-    if lse is not None:
-        _want(lse, (B, Hq), "lse")
-    ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    rc = lib().k3moe_attn_decode(cache._ref, B, Hq, qp, qs, _ptr(block_table, torch.int32, "block_table"),
-                                 block_table.shape[1], _ptr(seq_lens, torch.int32, "seq_lens"), int(window),
-                                 cache.dim ** -0.5 if scale is None else float(scale), _ptr(out, _BF16, "out"),
-                                 _ptr(lse, torch.float32, "lse"), _ptr(ws, None, "ws"), ws_bytes,
-                                 _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
-    _check("k3moe_attn_decode", rc)
+    pages = block_table.shape[1]
+    rc = lib().k3moe_attn_decode(cache._ref, B, Hq, qp, qs, _in(block_table, _I32, (B, pages), "block_table"), pages,
+                                 _in(seq_lens, _I32, (B,), "seq_lens"), window,
+                                 cache.dim ** -0.5 if scale is None else scale, _in(out, _BF16, shape, "out"),
+                                 _in(lse, _F32, (B, Hq), "lse"), _ptr(ws, None, "ws"),
+                                 ws.nbytes if ws is not None else 0, _ptr(dev_status, torch.int32, "dev_status"),
+                                 _stream(stream))
+    if rc:
+        _check("k3moe_attn_decode", rc)

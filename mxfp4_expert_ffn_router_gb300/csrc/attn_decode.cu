@@ -44,8 +44,8 @@
 
 #include <type_traits>
 
+#include "decoder_ops.h"
 #include "k3moe_dev.cuh"
-#include "k3moe_launch.h"
 #include "mx8_quant.cuh"
 #include "tc_sm103.cuh"
 
@@ -62,16 +62,17 @@ namespace {
 #ifndef KQS
 #define KQS 32
 #endif
-#ifndef KF
-#define KF 4
-#endif
 #ifndef KBL
-#define KBL (ROWB <= 256 ? 2 : 1)
+#define KBL (ROWB <= 256 && W == 4 ? 2 : 1)
 #endif
-constexpr int kAdWarps = 4;
-constexpr int kAdThreads = kAdWarps * 32;
 constexpr int kRun = 16;                 // tokens of a product
-constexpr int kDirectTokens = 512;       // items of at most this many tokens are never cut
+#ifndef KDT
+#define KDT 1024
+#endif
+#ifndef KDW
+#define KDW 2048
+#endif
+constexpr int kDirectTokens = KDT, kWideTokens = KDW;       // items of at most this many tokens are never cut
 constexpr int kMinTokens = 256;          // smallest piece of a block
 #ifndef KWU
 #define KWU 4
@@ -99,6 +100,10 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -253,7 +258,7 @@ struct Walk {
   }
 };
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, int W>
 struct AdShape {
   static constexpr int ESZ = E4M3 ? 1 : 2;
   static constexpr int ROWB = D * ESZ;            // bytes of a cached vector
@@ -264,7 +269,7 @@ struct AdShape {
   // A warp's step is RR times 16 tokens: 4 to 16 KB, so that what a step costs besides its bytes counts little
   static constexpr int RR = KRR;
   static constexpr int RUN = RR * kRun;
-  static constexpr int UNIT = RUN * kAdWarps;     // tokens of a block's step
+  static constexpr int UNIT = RUN * W;            // tokens of a block's step
   static constexpr int SUB = 2 * KB;              // keys and values of 16 tokens; a multiple of 128: words swizzle by xor
   static constexpr int SCALES = E4M3 ? 32 : 0;    // scale bytes of 16 tokens, after all stages
   // stages and blocks per SM: about 100 KB of loads in flight per SM
@@ -275,15 +280,15 @@ struct AdShape {
   // query fragments: in registers, or from 32 of them on in shared memory (the same for all warps)
   static constexpr int QREGS = D / 16 * 2 * NT;
   static constexpr int QSMEM = QREGS >= KQS ? QREGS * 32 * 4 : 0;
-  static constexpr int SMEM = kAdWarps * STAGES * RR * (SUB + SCALES) + QSMEM + 128;
+  static constexpr int SMEM = W * STAGES * RR * (SUB + SCALES) + QSMEM + 128;
 };
 
 // First of the two neighbouring dimensions that a lane of group g holds of product m.
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3>
 __device__ __forceinline__ int quad_dim(int m, int g) {
-  constexpr int PER = 16 / AdShape<D, E4M3, NT>::ESZ;  // dimensions of a 16-byte word
-  const int dl = 2 * m;                                // of the lane's dimensions
-  return AdShape<D, E4M3, NT>::C >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
+  constexpr int PER = E4M3 ? 16 : 8;  // dimensions of a 16-byte word
+  const int dl = 2 * m;               // of the lane's dimensions
+  return D / PER >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
 }
 
 // Two neighbouring dimensions of a row, times f (0: a row without weight, whatever the sums are).
@@ -293,22 +298,25 @@ __device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float 
 
 }  // namespace
 
-template <int D, bool E4M3, int NT, bool DIRECT>
-__global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
+template <int D, bool E4M3, int NT, int W, bool DIRECT>
+__global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
     attn_decode_kernel(const AdParams P) {
-  using S = AdShape<D, E4M3, NT>;
+  using S = AdShape<D, E4M3, NT, W>;
+  constexpr int THREADS = W * 32;
   constexpr int C = S::C, MM = S::MM, ST = S::STAGES, RR = S::RR, UNIT = S::UNIT, NQ = 8 * NT;
   constexpr int KL = C / 4;             // words of a key a lane reads
   constexpr int SP = E4M3 ? 4 : 2;      // products of 16 dimensions per such word
   constexpr int VL = C >= 8 ? C / 8 : 1;  // words of a value a lane reads
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((128u - (su32(smem_raw) & 127u)) & 127u);
-  __shared__ __align__(16) float s_mp[NQ][kAdWarps], s_m[NQ][kAdWarps], s_l[NQ][kAdWarps];
-  __shared__ long long s_scan[kAdWarps];
+  __shared__ __align__(16) float s_mp[NQ][W], s_m[NQ][W], s_l[NQ][W];
+  __shared__ long long s_scan[W];
   __shared__ long long s_begin;
   __shared__ int s_start[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int items = P.heads * P.groups, first = warp * S::RUN;
+  // hints only: nothing of these is read before the wait
+  if (tid < (P.B + 31) / 32) prefetch_l2(P.lens + 32 * tid);
   pdl_wait();
   pdl_trigger();
 
@@ -316,10 +324,10 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
       const Seen s = seen_of(P, b, false);
       if (s.n > s.t0) continue;
-      for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += kAdThreads)
+      for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += THREADS)
         reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
       if (P.lse)
-        for (int i = tid; i < P.Hq; i += kAdThreads) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
+        for (int i = tid; i < P.Hq; i += THREADS) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
     }
   };
 
@@ -339,14 +347,14 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
       const int h0 = cur.head * P.G + cur.group * NQ;
       const int rows = min(NQ, P.G - cur.group * NQ);
       const size_t row = static_cast<size_t>(cur.b) * P.Hq + h0;
-      for (int i = tid; i < rows * D / 8; i += kAdThreads)
+      for (int i = tid; i < rows * D / 8; i += THREADS)
         reinterpret_cast<uint4 *>(P.out + row * D)[i] = make_uint4(0, 0, 0, 0);
       if (P.lse && tid < rows) P.lse[row + tid] = -INFINITY;
       return;
     }
   } else {
     // thread t measures sequences [t per, t per + per); a scan finds the piece
-    const int per = (P.B + kAdThreads - 1) / kAdThreads;
+    const int per = (P.B + THREADS - 1) / THREADS;
     const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
     auto length = [&](int b, bool report) {  // of an item of sequence b on the line
       const int u = units_of<UNIT>(seen_of(P, b, report));
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     __syncthreads();
     long long total = 0, before = 0;
 #pragma unroll
-    for (int w = 0; w < kAdWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       if (w < warp) before += s_scan[w];
       total += s_scan[w];
     }
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
   // w ^ 2 (r / 4): the reads of fragments below then meet all banks evenly.
   constexpr int RI = C >= 32 ? 1 : 32 / C;  // rows between a lane's words
   const uint32_t ring = su32(smem) + warp * (ST * RR * S::SUB);
-  const uint32_t sring = su32(smem) + kAdWarps * ST * RR * S::SUB + warp * (ST * RR * S::SCALES);
+  const uint32_t sring = su32(smem) + W * ST * RR * S::SUB + warp * (ST * RR * S::SCALES);
   const int lr = lane / C, lx = lane % C;
   const uint32_t kdst = lr * S::ROWB + ((C == 8 || C == 16 ? lx ^ (4 * (lr & 1)) : lx) << 4);
   const uint32_t vdst = S::KB + lr * S::ROWB + (lx << 4);
@@ -481,7 +489,7 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
   constexpr int QN = D / 16, QW = 2 * NT;  // products along the dimensions, registers of the query rows in each
   constexpr bool QS = S::QSMEM > 0;
   uint32_t qf[QS ? 1 : QN][QW];
-  uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + kAdWarps * ST * RR * (S::SUB + S::SCALES));
+  uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + W * ST * RR * (S::SUB + S::SCALES));
   uint2 raw[D / 16][NT];
   float sq[NT];  // scale of a raw score, in powers of two
   float o[NT][MM][4], mrun[NT], m_l[NT], l[NT];
@@ -733,9 +741,9 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
               vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = vw[j][3] = 0u;
             }
           }
-          constexpr int W = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
+            constexpr int VW = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
+          for (int w = 0; w < VW; ++w) {
             if constexpr (E4M3) {
 #pragma unroll
               for (int hf = 0; hf < 2; ++hf) {
@@ -744,13 +752,13 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
                 e4m3x4_to_f16x2(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                  mma16<true>(o[t][(i * W + w) * 2 + hf], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
+                  mma16<true>(o[t][(i * VW + w) * 2 + hf], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
               }
             } else {
               const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
               const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410), a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma16<false>(o[t][i * W + w], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
+              for (int t = 0; t < NT; ++t) mma16<false>(o[t][i * VW + w], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
             }
           }
         }
@@ -787,9 +795,9 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
     }
     // quad x of warp w: in the stage that the warp has just used, and loads again only after this
     float4 *buf = reinterpret_cast<float4 *>(smem + used * (RR * S::SUB));
-    constexpr int WARP = ST * RR * S::SUB / 16;  // from one warp's stages to the next's
+    constexpr int NEXT = ST * RR * S::SUB / 16;  // from one warp's stages to the next's
     const int slot = 2 * blockIdx.x + (first_item ? 0 : 1);
-    float fin[2], fac[2][kAdWarps];
+    float fin[2], fac[2][W];
     int t_of = -1;
     __syncwarp();
 #pragma unroll
@@ -797,26 +805,28 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
 #pragma unroll
       for (int x = 0; x < S::QR; ++x) {
         const int t = (q0 + x) / MM, m = (q0 + x) % MM;
-        buf[warp * WARP + x * 32 + lane] = make_float4(o[t][m][0], o[t][m][1], o[t][m][2], o[t][m][3]);
+        buf[warp * NEXT + x * 32 + lane] = make_float4(o[t][m][0], o[t][m][1], o[t][m][2], o[t][m][3]);
       }
       __syncthreads();
       // this warp's share of the quads, summed over the warps at their common maximum
 #pragma unroll
-      for (int x0 = 0; x0 < S::QR; x0 += kAdWarps) {
+      for (int x0 = 0; x0 < S::QR; x0 += W) {
         const int x = x0 + warp, quad = q0 + x, t = quad / MM, m = quad % MM;
-        if (S::QR % kAdWarps && x >= S::QR) continue;
+        if (S::QR % W && x >= S::QR) continue;
         if (t != t_of) {
           t_of = t;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 8 * t + 2 * c + e;
-            const float4 mp4 = *reinterpret_cast<const float4 *>(s_mp[r]), m4 = *reinterpret_cast<const float4 *>(s_m[r]),
-                         l4 = *reinterpret_cast<const float4 *>(s_l[r]);
-            const float mp = fmaxf(fmaxf(mp4.x, mp4.y), fmaxf(mp4.z, mp4.w));
-            const float mt = fmaxf(fmaxf(m4.x, m4.y), fmaxf(m4.z, m4.w));
+            float mp = -INFINITY, mt = -INFINITY, lt = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) mp = fmaxf(mp, s_mp[r][w]), mt = fmaxf(mt, s_m[r][w]);
             const float mb = mt == -INFINITY ? 0.f : mt, pb = mp == -INFINITY ? 0.f : mp;
-            const float lt = (l4.x * ex2(m4.x - mb) + l4.y * ex2(m4.y - mb)) + (l4.z * ex2(m4.z - mb) + l4.w * ex2(m4.w - mb));
-            fac[e][0] = ex2(mp4.x - pb), fac[e][1] = ex2(mp4.y - pb), fac[e][2] = ex2(mp4.z - pb), fac[e][3] = ex2(mp4.w - pb);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+              lt = fmaf(s_l[r][w], ex2(s_m[r][w] - mb), lt);
+              fac[e][w] = ex2(s_mp[r][w] - pb);
+            }
             // out = O' 2^(m' - m - 14) / l; a row without weight is 0
             fin[e] = lt == 0.f ? 0.f : __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt);
             if (m == 0 && g == 0) {
@@ -829,8 +839,8 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
         }
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kAdWarps; ++w) {
-          const float4 u = buf[w * WARP + x * 32 + lane];
+        for (int w = 0; w < W; ++w) {
+          const float4 u = buf[w * NEXT + x * 32 + lane];
           v.x = fmaf(u.x, fac[0][w], v.x);
           v.y = fmaf(u.y, fac[1][w], v.y);
           v.z = fmaf(u.z, fac[0][w], v.z);
@@ -840,7 +850,7 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
           P.part[(static_cast<size_t>(slot) * S::QUADS + quad) * 32 + lane] = v;
         } else {
           const int r0 = 8 * t + 2 * c;
-          uint16_t *op = P.out + (static_cast<size_t>(done.b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3, NT>(m, g);
+          uint16_t *op = P.out + (static_cast<size_t>(done.b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
           store_row2(op, fin[0], v.x, v.z, r0 < rows);
           store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
         }
@@ -875,7 +885,7 @@ __global__ void __launch_bounds__(kAdThreads, (AdShape<D, E4M3, NT>::BLOCKS))
 // statistics and sums loaded together; where there are more, warps share a quad.
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
-  using S = AdShape<D, E4M3, NT>;
+  using S = AdShape<D, E4M3, NT, 4>;
   constexpr int NQ = 8 * NT, QUADS = S::QUADS, MM = S::MM;
   __shared__ float4 s_sum[8][32], s_stat[8][2][4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -979,7 +989,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
         if (P.lse && m == 0 && g == 0 && r0 + x < rows)
           P.lse[static_cast<size_t>(me.w) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
       }
-      uint16_t *op = P.out + (static_cast<size_t>(me.w) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3, NT>(m, g);
+      uint16_t *op = P.out + (static_cast<size_t>(me.w) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
       store_row2(op, fin[0], v.x, v.z, r0 < rows);
       store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
     }
@@ -1007,33 +1017,37 @@ AdPlan plan_of(const k3moe_kv_cache &c, int Hq) {
   return p;
 }
 
+template <int D, bool E4M3, int NT, int W, bool DIRECT>
+cudaError_t start(const AdParams &P, long long blocks, cudaStream_t st) {
+  using S = AdShape<D, E4M3, NT, W>;
+  static bool attr = false;
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, W, DIRECT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
+  return launch_pdl(attn_decode_kernel<D, E4M3, NT, W, DIRECT>, dim3(static_cast<unsigned>(blocks)), dim3(W * 32), S::SMEM,
+                    st, P);
+}
+
 template <int D, bool E4M3, int NT>
-int launch_attn(AdParams &P, cudaStream_t st) {
-  using S = AdShape<D, E4M3, NT>;
+int launch_attn(const AdParams &P, cudaStream_t st) {
+  using S = AdShape<D, E4M3, NT, 4>;
   const long long items = static_cast<long long>(P.B) * P.heads * P.groups;
   const int visible = P.max_pages << P.page_shift;  // most tokens an item can have
   const int tokens = P.window > 0 && P.window < visible ? P.window + kRun - 1 : visible;
-  static bool attr = false;
-  if (!attr) {
-    if (cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::SMEM) != cudaSuccess ||
-        cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             S::SMEM) != cudaSuccess)
-      return -1;
-    attr = true;
+  if constexpr (S::ROWB <= 256) {  // (beyond, the stages of eight warps do not fit)
+    if (items <= sm_count() && tokens <= kWideTokens)
+      return start<D, E4M3, NT, 8, true>(P, items, st) == cudaSuccess ? 0 : -1;
   }
-  if (tokens <= kDirectTokens && items < (1LL << 31))
-    return launch_pdl(attn_decode_kernel<D, E4M3, NT, true>, dim3(static_cast<unsigned>(items)), dim3(kAdThreads), S::SMEM,
-                      st, P) == cudaSuccess
-               ? 0
-               : -1;
-  long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS * KF / 4;
+  if (tokens <= kDirectTokens && items < (1LL << 31)) return start<D, E4M3, NT, 4, true>(P, items, st) == cudaSuccess ? 0 : -1;
+  long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;
   if (blocks > kAdMostBlocks) blocks = kAdMostBlocks;
   const long long most = (items * ((tokens + S::UNIT - 1) / S::UNIT * S::UNIT) + kMinTokens - 1) / kMinTokens;
   if (blocks > most) blocks = most;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  if (launch_pdl(attn_decode_kernel<D, E4M3, NT, false>, grid, dim3(kAdThreads), S::SMEM, st, P) != cudaSuccess) return -1;
-  return launch_pdl(attn_join_kernel<D, E4M3, NT>, grid, dim3(256), 0, st, P) == cudaSuccess
+  if (start<D, E4M3, NT, 4, false>(P, blocks, st) != cudaSuccess) return -1;
+  return launch_pdl(attn_join_kernel<D, E4M3, NT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, P) == cudaSuccess
              ? 0
              : -1;
 }

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/k3moe.h"
+#include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "k3moe_launch.h"
 #include "tc_sm103.cuh"

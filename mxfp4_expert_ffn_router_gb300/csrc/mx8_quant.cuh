@@ -31,6 +31,13 @@ __device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t amax_bits) {
 // 1 / X for a scale byte below 255.
 __device__ __forceinline__ float mx8_inv_scale(uint32_t byte) { return mx_pow2(127 - static_cast<int>(byte)); }
 
+// Two values rounded to bf16 (to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Two values (already divided by X) -> two codes, `lo` in the low byte.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;

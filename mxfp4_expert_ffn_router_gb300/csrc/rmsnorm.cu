@@ -8,8 +8,8 @@
 // The norm is of the fp32 sum, not of the bf16 value that residual_out keeps: the sum is
 // in registers anyway, and rounding it first would only lose bits.  The mean is a fixed
 // tree: a thread's values in order, a butterfly over the warp, the warps in order.
+#include "decoder_ops.h"
 #include "k3moe_dev.cuh"
-#include "k3moe_launch.h"
 #include "mx8_quant.cuh"
 
 namespace k3moe {
@@ -26,18 +26,14 @@ __device__ __forceinline__ void bf16x8_to_f32(const uint4 u, float (&v)[8]) {
 }
 
 __device__ __forceinline__ uint4 f32x8_to_bf16(const float (&v)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int m = 0; m < 4; ++m)
-    w[m] = f32_to_bf16_rne(v[2 * m]) | (static_cast<uint32_t>(f32_to_bf16_rne(v[2 * m + 1])) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
 }
 
 }  // namespace
 
 // One block per row; a thread holds CH chunks of 8 values (chunk = tid + i * blockDim).
 template <int CH>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
     rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, float eps, int H,
                    uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
   __shared__ float part[16];
