@@ -18,6 +18,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _SO = os.path.join(_HERE, "libk3moe.so")
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the C++ way into the calls that a decode step makes back to back
 
 K3MOE_OK, K3MOE_ERR_ARG, K3MOE_ERR_SHAPE, K3MOE_ERR_ALIGN = 0, -1, -2, -3
 K3MOE_ERR_WORKSPACE, K3MOE_ERR_ARCH, K3MOE_ERR_LAUNCH, K3MOE_ERR_UNSUPPORTED = -4, -5, -6, -7
@@ -64,7 +65,7 @@ def library_path() -> str:
 
 def lib():
     """Load libk3moe.so (built by ``build.build()``); raise if it is missing."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     with _lock:
@@ -125,8 +126,17 @@ def lib():
             L.k3moe_status_string.argtypes = [i32]
             L.k3moe_last_cuda_error.restype = ctypes.c_char_p
             L.k3moe_last_cuda_error.argtypes = []
+            _fast = _load_fast(L)
             _lib = L
     return _lib
+
+
+def _load_fast(L):
+    """The binding's C++ part (csrc/torch_fast.cpp) over the loaded library."""
+    from . import _k3torch
+    _k3torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                    for f in (L.k3moe_rmsnorm, L.k3moe_kv_write, L.k3moe_kv_read, L.k3moe_attn_decode)))
+    return _k3torch
 
 
 def status_string(code: int) -> str:
@@ -387,6 +397,11 @@ def k3moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, code
     """RMS norm of the rows of x [T, H] (bf16), a = x + residual first: any of
     residual_out = bf16(a), y = bf16(norm * weight), and codes [T, H] (E4M3) with
     scales [T, H/32] (E8M0) of the norm times weight."""
+    if _fast is not None:
+        rc = _fast.rmsnorm(x, weight, eps, residual, residual_out, y, codes, scales,
+                           None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a tensor [T, H]")
     shape = x.shape
@@ -420,7 +435,7 @@ class KVCache:
         self._c = _KVCacheC(self.pages, self.page_size, self.heads, self.dim, self.format, _in(k, kind, shape, "k"),
                             _in(v, kind, shape, "v"), _in(k_scales, _SCALES, shape[:3], "k_scales"),
                             _in(v_scales, _SCALES, shape[:3], "v_scales"))
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._addr = ctypes.byref(self._c), ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, pages: int, heads: int, page_size: int, dim: int, fmt: int = K3MOE_KV_E4M3, device="cuda"):
@@ -439,6 +454,10 @@ class KVCache:
 def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
     """Keys and values k, v [n, heads, dim] (bf16; the first axis may be strided) into
     the cache's slots [n] (int32, page * page_size + place; negative = padding)."""
+    if _fast is not None:
+        rc = _fast.kv_write(cache._addr, k, v, slots, dev_status, None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return
     shape = (slots.numel(), cache.heads, cache.dim)
     kp, ks = _rows(k, shape, "k")
     vp, vs = _rows(v, shape, "v")
@@ -451,6 +470,10 @@ def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
 def k3moe_kv_read(cache: KVCache, slots, k, v, dev_status=None, stream=None):
     """The cache's slots [n] (int32) as bf16 keys and values k, v [n, heads, dim] (zeros
     for a negative slot)."""
+    if _fast is not None:
+        rc = _fast.kv_read(cache._addr, slots, k, v, dev_status, None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return
     shape = (slots.numel(), cache.heads, cache.dim)
     rc = lib().k3moe_kv_read(cache._ref, shape[0], _in(slots, _I32, shape[:1], "slots"), _in(k, _BF16, shape, "k"),
                              _in(v, _BF16, shape, "v"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
@@ -468,6 +491,12 @@ def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, s
     may be strided), block_table [B, max_pages] and seq_lens [B] (int32) -> out
     [B, Hq, dim] (bf16), lse [B, Hq] (fp32).  scale defaults to dim^-1/2; window > 0
     sees only the last that many tokens; ws: k3moe_attn_decode_workspace_bytes."""
+    if _fast is not None:
+        rc = _fast.attn_decode(cache._addr, q, block_table, seq_lens, out, lse,
+                               cache.dim ** -0.5 if scale is None else scale, window, ws, dev_status,
+                               None if stream is None else stream.cuda_stream)
+        if rc == 0:
+            return
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q: expected a tensor [B, Hq, dim]")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:

@@ -1,4 +1,5 @@
-"""Build libk3moe.so in-tree: every CUDA source compiled for sm_103a with nvcc.
+"""Build libk3moe.so in-tree: every CUDA source compiled for sm_103a with nvcc; and
+the binding's C++ part, _k3torch.so (csrc/torch_fast.cpp), against the installed torch.
 
 Usage: ``python -m mxfp4_expert_ffn_router_gb300.build [--force]``.  Sources are
 compiled in parallel into ``_build/`` and linked next to this file."""
@@ -13,6 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT = os.path.join(HERE, "libk3moe.so")
+FAST = os.path.join(HERE, "_k3torch.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["k3moe.cu", "route.cu", "bucket.cu", "ffn_gemv.cu", "ffn_gemm.cu", "combine.cu",
            "quant.cu", "k3moe_noalloc.cu", "router.cu", "expert_cache.cu", "rmsnorm.cu", "kv_cache.cu",
@@ -30,10 +32,21 @@ def _deps():
     return files
 
 
+def _fast_command(out: str) -> list:
+    import sysconfig
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-I", inc, "-I", sysconfig.get_paths()["include"],
+            "-I", cuda, os.path.join(CSRC, "torch_fast.cpp"), "-o", out, "-L", lib, "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda"]
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(OUT):
+    if not os.path.exists(OUT) or not os.path.exists(FAST):
         return False
-    t = os.path.getmtime(OUT)
+    t = min(os.path.getmtime(OUT), os.path.getmtime(FAST))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -54,7 +67,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
+    def compile_fast():
+        tmp = FAST + f".tmp{os.getpid()}"
+        r = subprocess.run(_fast_command(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for torch_fast.cpp:\n{r.stdout}\n{r.stderr}")
+        return tmp
+
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
+        fast = ex.submit(compile_fast)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = OUT + f".tmp{os.getpid()}"
     r = subprocess.run([NVCC] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"],
@@ -62,6 +83,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
+    os.replace(fast.result(), FAST)
     return OUT
 
 
