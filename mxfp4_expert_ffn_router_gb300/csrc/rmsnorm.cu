@@ -7,7 +7,7 @@
 //
 // The norm is of the fp32 sum, not of the bf16 value that residual_out keeps: the sum is
 // in registers anyway, and rounding it first would only lose bits.  The mean is a fixed
-// tree: a thread's values in order, a butterfly over the warp, the warps in order.
+// tree: a thread's values in order, a butterfly over the warp, a tree over the warps.
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
@@ -36,7 +36,7 @@ template <int CH>
 __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
     rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, float eps, int H,
                    uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
-  __shared__ float part[16];
+  __shared__ __align__(16) float part[16];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, nth = blockDim.x, nch = H / 8;
@@ -60,11 +60,21 @@ __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+  if (tid < 16 && tid >= nth / 32) part[tid] = 0.f;
   if ((tid & 31) == 0) part[tid >> 5] = sum;
   __syncthreads();
-  float total = 0.f;
-  for (int w = 0; w < nth / 32; ++w) total += part[w];
-  const float inv = rsqrtf(total / static_cast<float>(H) + eps);
+  float4 s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s[i] = reinterpret_cast<const float4 *>(part)[i];
+  const float total = (((s[0].x + s[0].y) + (s[0].z + s[0].w)) + ((s[1].x + s[1].y) + (s[1].z + s[1].w))) +
+                      (((s[2].x + s[2].y) + (s[2].z + s[2].w)) + ((s[3].x + s[3].y) + (s[3].z + s[3].w)));
+  // m^-1/2 with one Newton step on rsqrtf, 1 - m inv^2 taken from exact products
+  const float m = total / static_cast<float>(H) + eps;
+  float inv = rsqrtf(m);
+  if (m > 0.f && m < INFINITY) {
+    const float p = m * inv, r = fmaf(-p, inv, 1.f) - fmaf(m, inv, -p) * inv;
+    inv = fmaf(0.5f * inv, r, inv);
+  }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nth;
