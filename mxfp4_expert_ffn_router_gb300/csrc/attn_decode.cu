@@ -28,8 +28,9 @@
 //  * Products.  mma.sync m16n8k16 (f16 or bf16, fp32 sums): with at most 16 query heads
 //    sharing a key the products are a small part of the time even at this instruction's
 //    rate, and its operands come straight from registers, where E4M3 codes are converted.
-//    S = Q K^T has the query heads as rows; O^T = V^T P^T has dimensions as rows
-//    and 8 query heads as columns, so that S's registers are P^T's.  The order of
+//    S^T = K Q^T has 16 tokens as rows and 8 query heads as columns, O^T = V^T P^T 16
+//    dimensions and the same columns, so that a lane scales the sums of the heads whose maxima it
+//    holds; movmatrix turns S^T's registers into P^T's.  The order of
 //    dimensions and tokens inside a product is free as long as both operands agree, and
 //    is chosen so that a lane's share of K and V is whole 16-byte words.
 //  * E4M3.  Codes are converted to f16 (exact; the E4M3 form of this instruction does the
@@ -53,34 +54,12 @@ namespace k3moe {
 
 namespace {
 
-#ifndef KRR
-#define KRR (ROWB <= 64 ? 4 : ROWB <= 128 ? 2 : 1)
-#endif
-#ifndef KST
-#define KST 3
-#endif
-#ifndef KQS
-#define KQS 32
-#endif
-#ifndef KBL
-#define KBL (ROWB <= 256 && W == 4 ? 2 : 1)
-#endif
 constexpr int kRun = 16;                 // tokens of a product
-#ifndef KDT
-#define KDT 1024
-#endif
-#ifndef KDW
-#define KDW 2048
-#endif
-constexpr int kDirectTokens = KDT, kWideTokens = KDW;       // items of at most this many tokens are never cut
+constexpr int kDirectTokens = 1024;      // items that see at most this many are never cut
 constexpr int kMinTokens = 256;          // smallest piece of a block
-#ifndef KWU
-#define KWU 4
-#define KWI 6
-#endif
-constexpr int kUnitLen = KWU, kItemLen = KWI;  // length on the line of a unit, and of an item beside its units
-constexpr int kJoinParts = 8;            // parts of an item that one warp joins
-constexpr int kAdMostBlocks = 152 * 12;  // pieces (bounds the workspace)
+constexpr int kUnitLen = 4, kItemLen = 6;  // length on the line of a unit, and of an item beside its units
+constexpr int kJoinWarps = 8, kJoinParts = 4;  // warps of a joining block, parts that one adds at once
+constexpr int kAdMostBlocks = 152 * 2;   // pieces (bounds the workspace)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -160,6 +139,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// An 8 x 8 matrix of 16-bit values, row g in lanes 4g .. 4g + 3 (two values each), transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // Not 0 where a byte of w is 255.
 __device__ __forceinline__ uint32_t byte_255(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & w & 0x80808080u;
@@ -195,6 +181,7 @@ __device__ __forceinline__ long long div_small(long long a, long long b) {
 struct Seen {
   int n, lo, t0;
 };
+template <int RUN>
 __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   Seen s;
   const long long most = static_cast<long long>(P.max_pages) << P.page_shift;
@@ -205,7 +192,7 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
     s.n = len < 0 ? 0 : static_cast<int>(most);
   }
   s.lo = P.window > 0 && s.n > P.window ? s.n - P.window : 0;
-  s.t0 = s.lo & ~(kRun - 1);
+  s.t0 = s.lo & ~(RUN - 1);
   return s;
 }
 template <int UNIT>
@@ -216,7 +203,7 @@ __device__ __forceinline__ int units_of(const Seen &s) {
 // A block's piece [from, to) of the line, and where one warp is in it.  An item that begins at
 // `begin` lies on the line as kItemLen, then kUnitLen for each of its units; a unit belongs
 // to the piece in which it begins.
-template <int UNIT>
+template <int RUN, int UNIT>
 struct Walk {
   int b, head, group;    // sequence, key-value head, which of its items
   int n, lo, t0;
@@ -249,7 +236,7 @@ struct Walk {
             more = false;
             return;
           }
-          s = seen_of(P, b, false);
+          s = seen_of<RUN>(P, b, false);
         } while (s.n <= s.t0);
         set(s);
       }
@@ -258,7 +245,7 @@ struct Walk {
   }
 };
 
-template <int D, bool E4M3, int NT, int W>
+template <int D, bool E4M3, int NT, int W, bool DIRECT>
 struct AdShape {
   static constexpr int ESZ = E4M3 ? 1 : 2;
   static constexpr int ROWB = D * ESZ;            // bytes of a cached vector
@@ -267,19 +254,21 @@ struct AdShape {
   static constexpr int MM = D / 16;               // products (16 dimensions each) of 16 tokens and 8 query heads
   static constexpr int QUADS = MM * NT;           // accumulator quads per lane
   // A warp's step is RR times 16 tokens: 4 to 16 KB, so that what a step costs besides its bytes counts little
-  static constexpr int RR = KRR;
+  static constexpr int RR = ROWB <= 64 ? 4 : ROWB <= 128 ? 2 : 1;
   static constexpr int RUN = RR * kRun;
   static constexpr int UNIT = RUN * W;            // tokens of a block's step
   static constexpr int SUB = 2 * KB;              // keys and values of 16 tokens; a multiple of 128: words swizzle by xor
   static constexpr int SCALES = E4M3 ? 32 : 0;    // scale bytes of 16 tokens, after all stages
-  // stages and blocks per SM: about 100 KB of loads in flight per SM
-  static constexpr int STAGES = KST;
-  static constexpr int BLOCKS = KBL;
+  // Stages and blocks per SM: 16 (or 12) warps' loads of 100 to 200 KB in flight per SM.  Blocks of one item
+  // each spend more of their time starting and ending, which a third block covers
+  static constexpr bool THREE = DIRECT && W == 4 && ROWB <= 256 && NT == 1;
+  static constexpr int STAGES = THREE ? 2 : 3;
+  static constexpr int BLOCKS = THREE ? 3 : ROWB <= 256 && W == 4 ? 2 : 1;
   // quads that the warps exchange at once where an item ends, each in the stage it has just used
   static constexpr int QR = RR * SUB / 512 < QUADS ? RR * SUB / 512 : QUADS;
   // query fragments: in registers, or from 32 of them on in shared memory (the same for all warps)
   static constexpr int QREGS = D / 16 * 2 * NT;
-  static constexpr int QSMEM = QREGS >= KQS ? QREGS * 32 * 4 : 0;
+  static constexpr int QSMEM = QREGS >= 32 ? QREGS * 32 * 4 : 0;
   static constexpr int SMEM = W * STAGES * RR * (SUB + SCALES) + QSMEM + 128;
 };
 
@@ -299,22 +288,19 @@ __device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float 
 }  // namespace
 
 template <int D, bool E4M3, int NT, int W, bool DIRECT>
-__global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
+__global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOCKS))
     attn_decode_kernel(const AdParams P) {
-  using S = AdShape<D, E4M3, NT, W>;
+  using S = AdShape<D, E4M3, NT, W, DIRECT>;
   constexpr int THREADS = W * 32;
-  constexpr int C = S::C, MM = S::MM, ST = S::STAGES, RR = S::RR, UNIT = S::UNIT, NQ = 8 * NT;
+  constexpr int C = S::C, MM = S::MM, ST = S::STAGES, RR = S::RR, RUN = S::RUN, UNIT = S::UNIT, NQ = 8 * NT;
   constexpr int KL = C / 4;             // words of a key a lane reads
   constexpr int SP = E4M3 ? 4 : 2;      // products of 16 dimensions per such word
   constexpr int VL = C >= 8 ? C / 8 : 1;  // words of a value a lane reads
   extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((128u - (su32(smem_raw) & 127u)) & 127u);
   __shared__ __align__(16) float s_mp[NQ][W], s_m[NQ][W], s_l[NQ][W];
-  __shared__ long long s_scan[W];
-  __shared__ long long s_begin;
-  __shared__ int s_start[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int items = P.heads * P.groups, first = warp * S::RUN;
+  const int items = P.heads * P.groups, first = warp * RUN;
   // hints only: nothing of these is read before the wait
   if (tid < (P.B + 31) / 32) prefetch_l2(P.lens + 32 * tid);
   pdl_wait();
@@ -322,7 +308,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
 
   auto zero_rows = [&]() {  // of the sequences that see nothing; every block takes its share
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
-      const Seen s = seen_of(P, b, false);
+      const Seen s = seen_of<RUN>(P, b, false);
       if (s.n > s.t0) continue;
       for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += THREADS)
         reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
@@ -332,14 +318,14 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
   };
 
   // ---- this block's piece
-  Walk<UNIT> cur;
+  Walk<RUN, UNIT> cur;
   long long from = 0, to = 1LL << 62, share = 0;
   if constexpr (DIRECT) {
     cur.b = blockIdx.x / items;
     const int item = blockIdx.x - cur.b * items;
     cur.head = item / P.groups;
     cur.group = item - cur.head * P.groups;
-    cur.set(seen_of(P, cur.b, tid == 0));
+    cur.set(seen_of<RUN>(P, cur.b, tid == 0));
     cur.begin = 0;
     cur.more = true;
     cur.enter(from, to, first);
@@ -353,15 +339,15 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
       return;
     }
   } else {
-    // thread t measures sequences [t per, t per + per); a scan finds the piece
-    const int per = (P.B + THREADS - 1) / THREADS;
-    const int b0 = min(P.B, tid * per), b1 = min(P.B, b0 + per);
+    // every warp for itself: lane l measures sequences [l per, l per + per); a scan finds the piece
+    const int per = (P.B + 31) / 32;
+    const int b0 = min(P.B, lane * per), b1 = min(P.B, b0 + per);
     auto length = [&](int b, bool report) {  // of an item of sequence b on the line
-      const int u = units_of<UNIT>(seen_of(P, b, report));
+      const int u = units_of<UNIT>(seen_of<RUN>(P, b, report));
       return u ? static_cast<long long>(u) * kUnitLen + kItemLen : 0LL;
     };
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += length(b, blockIdx.x == 0);
+    for (int b = b0; b < b1; ++b) mine += length(b, blockIdx.x == 0 && warp == 0);
     mine *= items;
     long long incl = mine;
 #pragma unroll
@@ -369,42 +355,35 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
       const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
       if (lane >= off) incl += o;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    long long total = 0, before = 0;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
-    }
+    const long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
     share = max(static_cast<long long>(kMinTokens / UNIT * kUnitLen), div_small(total + gridDim.x - 1, gridDim.x));
     from = static_cast<long long>(blockIdx.x) * share;
     to = min(total, from + share);
-    const long long ahead = before + incl - mine;  // of this thread's sequences
-    if (from < to && from >= ahead && from < ahead + mine) {
-      long long at = ahead, len;
-      int b = b0;
-      for (;; ++b) {
-        len = length(b, false);
+    const bool here = from < to && from >= incl - mine && from < incl;  // in this lane's sequences
+    int at_b = b0, at_item = 0;
+    long long at = incl - mine;
+    if (here) {
+      long long len;
+      for (;; ++at_b) {
+        len = length(at_b, false);
         if (from < at + len * items) break;
         at += len * items;
       }
-      const int item = static_cast<int>(div_small(from - at, len));
-      s_begin = at + item * len;
-      s_start[0] = b;
-      s_start[1] = item;
+      at_item = static_cast<int>(div_small(from - at, len));
+      at += at_item * len;
     }
     if (tid < 2) P.meta[2 * blockIdx.x + tid] = make_int4(0, 0, 0, 0);
-    __syncthreads();
     if (from >= to) {
       zero_rows();
       return;
     }
-    cur.b = s_start[0];
-    cur.head = s_start[1] / P.groups;
-    cur.group = s_start[1] - cur.head * P.groups;
-    cur.set(seen_of(P, cur.b, false));
-    cur.begin = s_begin;
+    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+    cur.b = __shfl_sync(0xFFFFFFFFu, at_b, src);
+    at_item = __shfl_sync(0xFFFFFFFFu, at_item, src);
+    cur.head = at_item / P.groups;
+    cur.group = at_item - cur.head * P.groups;
+    cur.set(seen_of<RUN>(P, cur.b, false));
+    cur.begin = __shfl_sync(0xFFFFFFFFu, at, src);
     cur.more = true;
     cur.enter(from, to, first);
     if (cur.tok >= cur.stop) cur.next_item(P, from, to, first);  // the piece begins behind the item's last unit
@@ -425,63 +404,83 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
   const uint32_t vdst = S::KB + lr * S::ROWB + (lx << 4);
   const uint8_t *const klane = P.k + lane * 16, *const vlane = P.v + lane * 16;
   const unsigned place = (1u << P.page_shift) - 1u, page_vecs = static_cast<unsigned>(P.heads) << P.page_shift;
-  Walk<UNIT> pre = cur;
+  Walk<RUN, UNIT> pre = cur;
   uint32_t bad = 0;    // bit st RR + r: a page number outside the cache
+  // a run starts at a multiple of RUN and lies in one page if pages are no smaller
+  const bool one_page = (RUN - 1u) <= place;
   int page[RR];
+  const int32_t *row;  // of the table
+  auto new_item = [&]() { row = P.table + static_cast<size_t>(pre.b) * P.max_pages; };
   auto pages = [&]() {  // of the run at `pre`
-    const int32_t *row = P.table + static_cast<size_t>(pre.b) * P.max_pages;
 #pragma unroll
     for (int r = 0; r < RR; ++r) {
       const unsigned tok = pre.tok + r * kRun;
-      page[r] = tok < static_cast<unsigned>(pre.n) ? __ldg(row + (tok >> P.page_shift)) : -1;
+      if (r == 0 || !one_page) page[r] = tok < static_cast<unsigned>(pre.n) ? __ldg(row + (tok >> P.page_shift)) : -1;
     }
   };
   auto issue = [&](int st) {
     if (pre.more) {
+      const uint32_t kd = ring + st * RR * S::SUB + kdst, vd = ring + st * RR * S::SUB + vdst;
+      const uint32_t sd = sring + st * RR * S::SCALES;
+      auto vec_of = [&](int page, unsigned tok) {
+        return static_cast<size_t>(static_cast<unsigned>(page)) * page_vecs +
+               ((static_cast<unsigned>(pre.head) << P.page_shift) + (tok & place));
+      };
+      if (one_page && pre.tok >= static_cast<unsigned>(pre.lo) && pre.tok + RUN <= static_cast<unsigned>(pre.n) &&
+          static_cast<unsigned>(page[0]) < static_cast<unsigned>(P.pages)) {  // all of it is seen
+        if (bad) bad &= ~(((1u << RR) - 1u) << (st * RR));
+        const size_t vec = vec_of(page[0], pre.tok);
+        const uint8_t *kp = klane + vec * S::ROWB, *vp = vlane + vec * S::ROWB;
 #pragma unroll
-      for (int r = 0; r < RR; ++r) {
-        const unsigned tok = pre.tok + r * kRun;
-        const int tile = st * RR + r;
-        if (tok < static_cast<unsigned>(pre.n)) {
-          if (static_cast<unsigned>(page[r]) >= static_cast<unsigned>(P.pages)) {
+        for (int r = 0; r < RR; ++r)
+#pragma unroll
+          for (int i = 0; i < C / 2; ++i) {
+            // the part of the swizzles that varies with i
+            const uint32_t ki = C == 32 ? (i & 1) << 6 : 0, vi = C >= 8 ? ((i * RI) >> 2) << 5 : 0;
+            cp16((kd ^ ki) + r * S::SUB + i * RI * S::ROWB, kp + r * S::KB + i * 512);
+            cp16((vd ^ vi) + r * S::SUB + i * RI * S::ROWB, vp + r * S::KB + i * 512);
+          }
+        if (E4M3 && lane < 2 * RR)
+          cp16(sd + (lane >> 1) * S::SCALES + 16 * (lane & 1), (lane & 1 ? P.vs : P.ks) + vec + 16 * (lane >> 1));
+      } else {
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+          const unsigned tok = pre.tok + r * kRun;
+          const int tile = st * RR + r, pg = one_page ? page[0] : page[r];
+          if (tok >= static_cast<unsigned>(pre.n)) break;
+          if (static_cast<unsigned>(pg) >= static_cast<unsigned>(P.pages)) {
             bad |= 1u << tile;
             if (lane == 0) set_status(P.status, K3MOE_DEV_BOUNDS);
-          } else {
-            if (bad) bad &= ~(1u << tile);
-            const size_t vec = static_cast<size_t>(static_cast<unsigned>(page[r])) * page_vecs +
-                               ((static_cast<unsigned>(pre.head) << P.page_shift) + (tok & place));
-            const uint8_t *kp = klane + vec * S::ROWB, *vp = vlane + vec * S::ROWB;
-            const uint32_t kd = ring + tile * S::SUB + kdst, vd = ring + tile * S::SUB + vdst;
-            const bool whole = tok >= static_cast<unsigned>(pre.lo) && tok + kRun <= static_cast<unsigned>(pre.n);
-#pragma unroll
-            for (int i = 0; i < C / 2; ++i) {
-              // the part of the swizzles that varies with i
-              const uint32_t ki = C == 32 ? (i & 1) << 6 : 0, vi = C >= 8 ? ((i * RI) >> 2) << 5 : 0;
-              if (whole) {
-                cp16(((kd ^ ki) + i * RI * S::ROWB), kp + i * 512);
-                cp16(((vd ^ vi) + i * RI * S::ROWB), vp + i * 512);
-              } else {
-                const unsigned at = tok + lr + i * RI;
-                const bool on = at >= static_cast<unsigned>(pre.lo) && at < static_cast<unsigned>(pre.n);
-                cp16_or_zeros((kd ^ ki) + i * RI * S::ROWB, kp + i * 512, on);
-                cp16_or_zeros((vd ^ vi) + i * RI * S::ROWB, vp + i * 512, on);
-              }
-            }
-            if (E4M3 && lane < 2) cp16(sring + tile * S::SCALES + 16 * lane, (lane ? P.vs : P.ks) + vec);
+            continue;
           }
+          bad &= ~(1u << tile);
+          const size_t vec = vec_of(pg, tok);
+          const uint8_t *kp = klane + vec * S::ROWB, *vp = vlane + vec * S::ROWB;
+#pragma unroll
+          for (int i = 0; i < C / 2; ++i) {
+            const uint32_t ki = C == 32 ? (i & 1) << 6 : 0, vi = C >= 8 ? ((i * RI) >> 2) << 5 : 0;
+            const unsigned at = tok + lr + i * RI;
+            const bool on = at >= static_cast<unsigned>(pre.lo) && at < static_cast<unsigned>(pre.n);
+            cp16_or_zeros((kd ^ ki) + r * S::SUB + i * RI * S::ROWB, kp + i * 512, on);
+            cp16_or_zeros((vd ^ vi) + r * S::SUB + i * RI * S::ROWB, vp + i * 512, on);
+          }
+          if (E4M3 && lane < 2) cp16(sd + r * S::SCALES + 16 * lane, (lane ? P.vs : P.ks) + vec);
         }
       }
       pre.tok += UNIT;
       if (pre.tok >= pre.stop) {
-        if (DIRECT)
+        if (DIRECT) {
           pre.more = false;
-        else
+        } else {
           pre.next_item(P, from, to, first);
+          new_item();
+        }
       }
       if (pre.more) pages();
     }
     cp_commit();
   };
+  new_item();
   pages();
 #pragma unroll
   for (int st = 0; st < ST - 1; ++st) issue(st);
@@ -491,9 +490,9 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
   uint32_t qf[QS ? 1 : QN][QW];
   uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + W * ST * RR * (S::SUB + S::SCALES));
   uint2 raw[D / 16][NT];
-  float sq[NT];  // scale of a raw score, in powers of two
-  float o[NT][MM][4], mrun[NT], m_l[NT], l[NT];
-  auto load_q = [&](const Walk<UNIT> &at) {
+  // of query heads 8 t + 2c + x: the scale of a raw score (in powers of two), the running maxima and l
+  float sq[NT][2], o[NT][MM][4], mrun[NT][2], m_l[NT][2], l[NT][2];
+  auto load_q = [&](const Walk<RUN, UNIT> &at) {
     const int h0 = at.head * P.G + at.group * NQ, rows = min(NQ, P.G - at.group * NQ);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -510,8 +509,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
   auto start_item = [&]() {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float up = 1.f;
-      sq[t] = P.scale * kLog2e;
+      float up = 1.f, mine = P.scale * kLog2e;  // of row 8 t + g
       if constexpr (E4M3) {
         uint32_t mx = 0;
 #pragma unroll
@@ -525,7 +523,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
         // 2^(14 - floor(log2 max)), as far as fp32 has it
         const int e = mx == 0 ? 0 : max(-126, min(127, 14 + 127 - static_cast<int>(mx >> 23)));
         up = exp2i(e);
-        sq[t] *= mx_pow2(-e);
+        mine *= mx_pow2(-e);
       }
 #pragma unroll
       for (int i = 0; i < QN; ++i) {
@@ -542,8 +540,12 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
           qf[i][NT + t] = u.y;
         }
       }
-      mrun[t] = m_l[t] = -INFINITY;
-      l[t] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        sq[t][x] = E4M3 ? __shfl_sync(0xFFFFFFFFu, mine, 8 * c + 4 * x) : mine;
+        mrun[t][x] = m_l[t][x] = -INFINITY;
+        l[t][x] = 0.f;
+      }
 #pragma unroll
       for (int m = 0; m < MM; ++m)
 #pragma unroll
@@ -567,11 +569,12 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
       const uint32_t base0 = ring + stage * (RR * S::SUB), sbase = sring + stage * (RR * S::SCALES);
       const bool whole = cur.tok >= static_cast<unsigned>(cur.lo) &&
                          cur.tok + S::RUN <= static_cast<unsigned>(cur.n) && bad == 0u;
-      // S: columns 2c, 2c+1 of product j of 16 tokens are tokens 4c + 2j, 4c + 2j + 1.  Where a step
-      // has 16 tokens there are two partial sums each, so that a product does not wait for the one before it
-      constexpr int CH = RR == 1 ? 2 : 1;
-      float s[RR][CH][2][4];
-      const uint32_t kofs = (4 * (g >> 1) + (g & 1)) * S::ROWB + (c << 4) + (C >= 8 ? (g & 1) << 6 : 0);
+      // S^T: rows g and g + 8 are tokens tg and tg + 2 of the 16, tg = 4 (g / 2) + g % 2, columns 2c and
+      // 2c + 1 query heads.  CH partial sums, so that a product does not wait for the one before it
+      constexpr int CH = RR * NT >= 4 ? 1 : 2, T2 = 2 * RR;
+      float s[RR][NT][CH][4];
+      const int tg = 4 * (g >> 1) + (g & 1);
+      const uint32_t kofs = tg * S::ROWB + (c << 4) + (C >= 8 ? (g & 1) << 6 : 0);
 #pragma unroll
       for (int i = 0; i < KL; ++i) {
 #pragma unroll
@@ -580,145 +583,142 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
 #pragma unroll
           for (int j = 0; j < 2; ++j)
             kw[j] = lds128(((base0 + r * S::SUB + kofs) ^ ((i & 1) << 6)) + (i >> 1) * 128 + 2 * j * S::ROWB);
+          const uint32_t k0[4] = {kw[0].x, kw[0].y, kw[0].z, kw[0].w}, k1[4] = {kw[1].x, kw[1].y, kw[1].z, kw[1].w};
 #pragma unroll
           for (int w = 0; w < SP; ++w) {
             const int qi = i * SP + w;
-            uint32_t a[QW];
+            uint32_t b[QW], a0, a1, a2, a3;
             if constexpr (QS) {
               if constexpr (NT == 1)
-                *reinterpret_cast<uint2 *>(a) = reinterpret_cast<const uint2 *>(&q_sm[(qi / 2) * 32 + lane])[qi & 1];
+                *reinterpret_cast<uint2 *>(b) = reinterpret_cast<const uint2 *>(&q_sm[(qi / 2) * 32 + lane])[qi & 1];
               else
-                *reinterpret_cast<uint4 *>(a) = q_sm[qi * 32 + lane];
+                *reinterpret_cast<uint4 *>(b) = q_sm[qi * 32 + lane];
             } else {
 #pragma unroll
-              for (int x = 0; x < QW; ++x) a[x] = qf[qi][x];
+              for (int x = 0; x < QW; ++x) b[x] = qf[qi][x];
+            }
+            if constexpr (E4M3) {
+              e4m3x4_to_f16x2(k0[w], a0, a2);
+              e4m3x4_to_f16x2(k1[w], a1, a3);
+            } else {
+              a0 = k0[2 * w], a1 = k1[2 * w], a2 = k0[2 * w + 1], a3 = k1[2 * w + 1];
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t kk[4] = {kw[j].x, kw[j].y, kw[j].z, kw[j].w};
-              uint32_t b0, b1;
-              if constexpr (E4M3)
-                e4m3x4_to_f16x2(kk[w], b0, b1);
-              else
-                b0 = kk[2 * w], b1 = kk[2 * w + 1];
-              float(&d)[4] = s[r][qi & (CH - 1)][j];
-              const uint32_t a1 = NT == 1 ? 0u : a[1], a2 = NT == 1 ? a[1] : a[QW - 2], a3 = NT == 1 ? 0u : a[QW - 1];
+            for (int t = 0; t < NT; ++t) {
               if (qi < CH)
-                mma16_first<E4M3>(d, a[0], a1, a2, a3, b0, b1);
+                mma16_first<E4M3>(s[r][t][qi], a0, a1, a2, a3, b[t], b[NT + t]);
               else
-                mma16<E4M3>(d, a[0], a1, a2, a3, b0, b1);
+                mma16<E4M3>(s[r][t][qi & (CH - 1)], a0, a1, a2, a3, b[t], b[NT + t]);
             }
           }
         }
       }
-      // weights of tokens 4c .. 4c+3 of each 16, in powers of two
-      float sc[NT][4 * RR], ve[4 * RR];
+      // weights of tokens tg and tg + 2 of each 16, in powers of two
+      float kx[T2], ve[T2];
       if constexpr (E4M3) {
-        float kx[4 * RR];
         uint32_t kw[RR], vw[RR], odd = 0;
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
-          kw[r] = lds32(sbase + r * S::SCALES + 4 * c);
-          vw[r] = lds32(sbase + r * S::SCALES + 16 + 4 * c);
+          kw[r] = lds32(sbase + r * S::SCALES + 4 * (g >> 1)) >> (8 * (g & 1));
+          vw[r] = lds32(sbase + r * S::SCALES + 16 + 4 * (g >> 1)) >> (8 * (g & 1));
           odd |= byte_255(kw[r]) | byte_255(vw[r]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // byte j << 23 (0 stands for 2^-127), and byte j - 127
-            kx[4 * r + j] = fmaxf(__uint_as_float(__byte_perm(kw[r], 0u, 0x0444 | (j << 12)) >> 1),
+          for (int h = 0; h < 2; ++h) {
+            // byte 2h << 23 (0 stands for 2^-127), and byte 2h - 127
+            kx[2 * r + h] = fmaxf(__uint_as_float(__byte_perm(kw[r], 0u, 0x0444 | ((2 * h) << 12)) >> 1),
                                   __uint_as_float(0x00400000u));
-            ve[4 * r + j] = __uint_as_float(__byte_perm(vw[r], 0x4B000000u, 0x7440 | j)) - 8388735.0f;
+            ve[2 * r + h] = __uint_as_float(__byte_perm(vw[r], 0x4B000000u, 0x7440 | (2 * h))) - 8388735.0f;
           }
         }
         if (odd) {  // NaN
 #pragma unroll
-          for (int j = 0; j < 4 * RR; ++j) {
-            if (((kw[j >> 2] >> (8 * (j & 3))) & 255u) == 255u) kx[j] = __uint_as_float(0x7FC00000u);
-            if (((vw[j >> 2] >> (8 * (j & 3))) & 255u) == 255u) ve[j] = __uint_as_float(0x7FC00000u);
+          for (int j = 0; j < T2; ++j) {
+            if (((kw[j >> 1] >> (16 * (j & 1))) & 255u) == 255u) kx[j] = __uint_as_float(0x7FC00000u);
+            if (((vw[j >> 1] >> (16 * (j & 1))) & 255u) == 255u) ve[j] = __uint_as_float(0x7FC00000u);
           }
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < 4 * RR; ++j) sc[t][j] = sq[t] * kx[j];
-      } else {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int j = 0; j < 4 * RR; ++j) sc[t][j] = sq[t];
       }
+      float sc[NT][2][T2];
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < 4 * RR; ++j) {
-          const int h = (j >> 1) & 1, x = j & 1;
-          float raw_s = s[j >> 2][0][h][2 * t + x];
-          if constexpr (CH == 2) raw_s += s[j >> 2][CH - 1][h][2 * t + x];
-          sc[t][j] *= raw_s;
-        }
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int j = 0; j < T2; ++j) {
+            const int at = 2 * (j & 1) + x;
+            float raw_s = s[j >> 1][t][0][at];
+            if constexpr (CH == 2) raw_s += s[j >> 1][t][CH - 1][at];
+            sc[t][x][j] = raw_s * (E4M3 ? sq[t][x] * kx[j] : sq[t][x]);
+          }
       if (!whole) {
 #pragma unroll
-        for (int j = 0; j < 4 * RR; ++j) {
-          const unsigned tok = cur.tok + (j >> 2) * kRun + 4 * c + (j & 3);
+        for (int j = 0; j < T2; ++j) {
+          const unsigned tok = cur.tok + (j >> 1) * kRun + tg + 2 * (j & 1);
           if (tok < static_cast<unsigned>(cur.lo) || tok >= static_cast<unsigned>(cur.n) ||
-              ((bad >> (stage * RR + (j >> 2))) & 1u)) {
+              ((bad >> (stage * RR + (j >> 1))) & 1u)) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t][j] = -INFINITY;
+            for (int t = 0; t < NT; ++t) sc[t][0][j] = sc[t][1][j] = -INFINITY;
             if (E4M3) ve[j] = 0.f;
           }
         }
       }
-      float top[NT];
+      float top[NT][2];
       bool grows = false;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if constexpr (E4M3) {  // l and its maximum, of this lane's tokens alone
-          float mn = m_l[t], add = 0.f;
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int j = 0; j < 4 * RR; ++j) mn = fmaxf(mn, sc[t][j]);
-          const float base = mn == -INFINITY ? 0.f : mn;
+        for (int x = 0; x < 2; ++x) {
+          if constexpr (E4M3) {  // l and its maximum, of this lane's tokens alone
+            float mn = m_l[t][x], add = 0.f;
 #pragma unroll
-          for (int j = 0; j < 4 * RR; j += 2) add += ex2(sc[t][j] - base) + ex2(sc[t][j + 1] - base);
-          l[t] = l[t] * ex2(m_l[t] - base) + add;
-          m_l[t] = mn;
+            for (int j = 0; j < T2; ++j) mn = fmaxf(mn, sc[t][x][j]);
+            const float base = mn == -INFINITY ? 0.f : mn;
 #pragma unroll
-          for (int j = 0; j < 4 * RR; ++j) sc[t][j] += ve[j];
+            for (int j = 0; j < T2; j += 2) add += ex2(sc[t][x][j] - base) + ex2(sc[t][x][j + 1] - base);
+            l[t][x] = l[t][x] * ex2(m_l[t][x] - base) + add;
+            m_l[t][x] = mn;
+#pragma unroll
+            for (int j = 0; j < T2; ++j) sc[t][x][j] += ve[j];
+          }
+          top[t][x] = sc[t][x][0];
+#pragma unroll
+          for (int j = 1; j < T2; ++j) top[t][x] = fmaxf(top[t][x], sc[t][x][j]);
+          grows |= top[t][x] > mrun[t][x];
         }
-        top[t] = sc[t][0];
-#pragma unroll
-        for (int j = 1; j < 4 * RR; ++j) top[t] = fmaxf(top[t], sc[t][j]);
-        grows |= top[t] > mrun[t];
-      }
       if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          top[t] = fmaxf(top[t], __shfl_xor_sync(0xFFFFFFFFu, top[t], 1));
-          top[t] = fmaxf(top[t], __shfl_xor_sync(0xFFFFFFFFu, top[t], 2));
-          const float mn = fmaxf(mrun[t], top[t]);
-          const float al = mn > mrun[t] ? ex2(mrun[t] - mn) : 1.f;
-          mrun[t] = mn;
-          if (!E4M3) l[t] *= al;
-          const float a0 = __shfl_sync(0xFFFFFFFFu, al, 8 * c), a1 = __shfl_sync(0xFFFFFFFFu, al, 8 * c + 4);
+          float al[2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              top[t][x] = fmaxf(top[t][x], __shfl_xor_sync(0xFFFFFFFFu, top[t][x], off));
+            const float mn = fmaxf(mrun[t][x], top[t][x]);
+            al[x] = mn > mrun[t][x] ? ex2(mrun[t][x] - mn) : 1.f;
+            mrun[t][x] = mn;
+            if (!E4M3) l[t][x] *= al[x];
+          }
 #pragma unroll
           for (int m = 0; m < MM; ++m) {
-            o[t][m][0] *= a0;
-            o[t][m][1] *= a1;
-            o[t][m][2] *= a0;
-            o[t][m][3] *= a1;
+            o[t][m][0] *= al[0];
+            o[t][m][1] *= al[1];
+            o[t][m][2] *= al[0];
+            o[t][m][3] *= al[1];
           }
         }
       }
+      // P^T: eight tokens by eight query heads, turned so that a lane has two tokens of one head
       uint32_t pf[RR][NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        const float base = (mrun[t] == -INFINITY ? 0.f : mrun[t]) - (E4M3 ? 14.f : 0.f);
+        const float base[2] = {(mrun[t][0] == -INFINITY ? 0.f : mrun[t][0]) - (E4M3 ? 14.f : 0.f),
+                               (mrun[t][1] == -INFINITY ? 0.f : mrun[t][1]) - (E4M3 ? 14.f : 0.f)};
 #pragma unroll
-        for (int r = 0; r < RR; ++r) {
-          float p[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = ex2(sc[t][4 * r + j] - base);
-          if (!E4M3) l[t] += (p[0] + p[1]) + (p[2] + p[3]);
-          pf[r][t][0] = pack2<E4M3>(p[0], p[1]);
-          pf[r][t][1] = pack2<E4M3>(p[2], p[3]);
+        for (int j = 0; j < T2; ++j) {
+          const float p0 = ex2(sc[t][0][j] - base[0]), p1 = ex2(sc[t][1][j] - base[1]);
+          if (!E4M3) l[t][0] += p0, l[t][1] += p1;
+          pf[j >> 1][t][j & 1] = transpose8x8(pack2<E4M3>(p0, p1));
         }
       }
       // O^T: rows g and g + 8 of product m are this lane's dimensions 2m and 2m + 1.  16 tokens that are
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
     if (cur.tok < cur.stop) continue;
 
     // ---- the item ends here (or is cut here): join the warps
-    const Walk<UNIT> done = cur;
+    const Walk<RUN, UNIT> done = cur;
     const bool began_before = !DIRECT && done.unit_at(from) > 0, cut = began_before || (!DIRECT && done.unit_at(to) < done.units());
     const int h0 = done.head * P.G + done.group * NQ, rows = min(NQ, P.G - done.group * NQ);
     if (DIRECT)
@@ -780,17 +780,20 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
     if (kEarlyQ && cur.more) load_q(cur);  // arrives while the warps join
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const float m = E4M3 ? m_l[t] : mrun[t];
-      float mm = m;
-      mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 1));
-      mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, 2));
-      float lt = mm == -INFINITY ? l[t] : l[t] * ex2(m - mm);
-      lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 1);
-      lt += __shfl_xor_sync(0xFFFFFFFFu, lt, 2);
-      if (c == 0) {
-        s_mp[g + 8 * t][warp] = mrun[t];
-        s_m[g + 8 * t][warp] = mm;
-        s_l[g + 8 * t][warp] = lt;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float m = E4M3 ? m_l[t][x] : mrun[t][x];
+        float mm = m;
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, off));
+        float lt = mm == -INFINITY ? l[t][x] : l[t][x] * ex2(m - mm);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) lt += __shfl_xor_sync(0xFFFFFFFFu, lt, off);
+        if (g == 0) {
+          s_mp[8 * t + 2 * c + x][warp] = mrun[t][x];
+          s_m[8 * t + 2 * c + x][warp] = mm;
+          s_l[8 * t + 2 * c + x][warp] = lt;
+        }
       }
     }
     // quad x of warp w: in the stage that the warp has just used, and loads again only after this
@@ -884,33 +887,36 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W>::BLOCKS))
 // is joined by many blocks.  A warp adds up to kJoinParts parts of a quad, their
 // statistics and sums loaded together; where there are more, warps share a quad.
 template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
-  using S = AdShape<D, E4M3, NT, 4>;
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AdParams P) {
+  using S = AdShape<D, E4M3, NT, 4, false>;
   constexpr int NQ = 8 * NT, QUADS = S::QUADS, MM = S::MM;
-  __shared__ float4 s_sum[8][32], s_stat[8][2][4];
+  __shared__ float4 s_sum[kJoinWarps][32], s_stat[kJoinWarps][2][4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   pdl_wait();
   pdl_trigger();
-  const int4 both[2] = {P.meta[2 * blockIdx.x], P.meta[2 * blockIdx.x + 1]};
-  // quads of each item that are this block's: mine, mine + parts, ..; warps that share one
-  int count[2], split[2];
+  const int4 m0 = P.meta[2 * blockIdx.x], m1 = P.meta[2 * blockIdx.x + 1];
+  // quads of an item that are this block's: mine, mine + parts, ..; warps that share one
+  auto count_of = [&](const int4 &m) {
+    const int parts = m.y, mine = static_cast<int>(blockIdx.x) - (m.x >> 1);
+    return parts > 1 && mine < QUADS ? (QUADS - 1 - mine) / parts + 1 : 0;
+  };
+  auto split_of = [&](const int4 &m) {
+    int s = 1;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int parts = both[e].y, mine = static_cast<int>(blockIdx.x) - (both[e].x >> 1);
-    count[e] = parts > 1 && mine < QUADS ? (QUADS - 1 - mine) / parts + 1 : 0;
-    split[e] = parts <= 4 ? 1 : parts <= 8 ? 2 : parts <= 16 ? 4 : 8;
-  }
-  // a quad's warps lie in one round of eight: splits are powers of two, and the second item's
+    for (int w = 1; w < kJoinWarps; w *= 2) s = m.y > w * kJoinParts ? 2 * w : s;
+    return s;
+  };
+  const int n0 = count_of(m0), n1 = count_of(m1), sp0 = split_of(m0), sp1 = split_of(m1);
+  // a quad's warps lie in one round of all warps: splits are powers of two, and the second item's
   // tasks start at a multiple of its split
-  const int tasks0 = count[0] * split[0], from1 = (tasks0 + split[1] - 1) / split[1] * split[1];
-  const int tasks = count[1] ? from1 + count[1] * split[1] : tasks0;
-  for (int base = 0; base < tasks; base += 8) {
-    int task = base + warp;
-    const int e = task < tasks0 ? 0 : 1;
-    if (e) task -= from1;
-    const int sp = split[e], sub = task & (sp - 1), q = task / sp;
-    const bool in = task >= 0 && q < count[e];
-    const int4 me = both[e];
+  const int tasks0 = n0 * sp0, from1 = (tasks0 + sp1 - 1) / sp1 * sp1;
+  const int tasks = n1 ? from1 + n1 * sp1 : tasks0;
+  for (int base = 0; base < tasks; base += kJoinWarps) {
+    const bool e = base + warp >= tasks0;
+    const int task = base + warp - (e ? from1 : 0);
+    const int sp = e ? sp1 : sp0, sub = task & (sp - 1), q = task / sp;
+    const bool in = task >= 0 && q < (e ? n1 : n0);
+    const int4 me = make_int4(e ? m1.x : m0.x, e ? m1.y : m0.y, e ? m1.z : m0.z, e ? m1.w : m0.w);
     const int parts = me.y, b0 = me.x >> 1, quad = static_cast<int>(blockIdx.x) - b0 + q * parts;
     const int t = quad / MM, m = quad - t * MM, r0 = 8 * t + 2 * c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -958,7 +964,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
         add(s, u, std::integral_constant<int, kJoinParts + 1>());
       }
     }
-    if (max(split[0], split[1]) > 1) {  // (uniform: the block's)
+    if (max(sp0, sp1) > 1) {  // (uniform: the block's)
       s_sum[warp][lane] = v;
       if (g == 0) {
         s_stat[warp][0][c] = make_float4(mp[0], mt[0], lt[0], 0.f);
@@ -966,15 +972,21 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const AdParams P) {
       }
       __syncthreads();
       if (in && sub == 0 && sp > 1) {
-        float4 s[8][2], u[8];
+        for (int i = 1; i < sp; i += kJoinParts) {
+          float4 s[kJoinParts + 1][2], u[kJoinParts + 1];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int w = min(warp + x, 7);
-          s[x][0] = x < sp ? s_stat[w][0][c] : none;
-          s[x][1] = x < sp ? s_stat[w][1][c] : none;
-          u[x] = x < sp ? s_sum[w][lane] : zero;
+          for (int x = 0; x < kJoinParts; ++x) {
+            const bool on = i + x < sp;
+            const int w = on ? warp + i + x : warp;
+            s[x][0] = on ? s_stat[w][0][c] : none;
+            s[x][1] = on ? s_stat[w][1][c] : none;
+            u[x] = on ? s_sum[w][lane] : zero;
+          }
+          s[kJoinParts][0] = make_float4(mp[0], mt[0], lt[0], 0.f);
+          s[kJoinParts][1] = make_float4(mp[1], mt[1], lt[1], 0.f);
+          u[kJoinParts] = v;
+          add(s, u, std::integral_constant<int, kJoinParts + 1>());
         }
-        add(s, u, std::integral_constant<int, 8>());
       }
       __syncthreads();
     }
@@ -1019,7 +1031,7 @@ AdPlan plan_of(const k3moe_kv_cache &c, int Hq) {
 
 template <int D, bool E4M3, int NT, int W, bool DIRECT>
 cudaError_t start(const AdParams &P, long long blocks, cudaStream_t st) {
-  using S = AdShape<D, E4M3, NT, W>;
+  using S = AdShape<D, E4M3, NT, W, DIRECT>;
   static bool attr = false;
   if (!attr) {
     const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, W, DIRECT>,
@@ -1033,21 +1045,21 @@ cudaError_t start(const AdParams &P, long long blocks, cudaStream_t st) {
 
 template <int D, bool E4M3, int NT>
 int launch_attn(const AdParams &P, cudaStream_t st) {
-  using S = AdShape<D, E4M3, NT, 4>;
+  using S = AdShape<D, E4M3, NT, 4, false>;
   const long long items = static_cast<long long>(P.B) * P.heads * P.groups;
   const int visible = P.max_pages << P.page_shift;  // most tokens an item can have
-  const int tokens = P.window > 0 && P.window < visible ? P.window + kRun - 1 : visible;
+  const int tokens = P.window > 0 && P.window < visible ? P.window : visible;
   if constexpr (S::ROWB <= 256) {  // (beyond, the stages of eight warps do not fit)
-    if (items <= sm_count() && tokens <= kWideTokens)
+    if (items <= sm_count() && tokens > S::UNIT && tokens <= kDirectTokens)
       return start<D, E4M3, NT, 8, true>(P, items, st) == cudaSuccess ? 0 : -1;
   }
   if (tokens <= kDirectTokens && items < (1LL << 31)) return start<D, E4M3, NT, 4, true>(P, items, st) == cudaSuccess ? 0 : -1;
   long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;
   if (blocks > kAdMostBlocks) blocks = kAdMostBlocks;
-  const long long most = (items * ((tokens + S::UNIT - 1) / S::UNIT * S::UNIT) + kMinTokens - 1) / kMinTokens;
+  const long long most = (items * ((tokens + S::RUN + S::UNIT - 2) / S::UNIT * S::UNIT) + kMinTokens - 1) / kMinTokens;
   if (blocks > most) blocks = most;
   if (start<D, E4M3, NT, 4, false>(P, blocks, st) != cudaSuccess) return -1;
-  return launch_pdl(attn_join_kernel<D, E4M3, NT>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, P) == cudaSuccess
+  return launch_pdl(attn_join_kernel<D, E4M3, NT>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinWarps * 32), 0, st, P) == cudaSuccess
              ? 0
              : -1;
 }
