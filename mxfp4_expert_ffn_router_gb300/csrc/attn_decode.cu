@@ -12,35 +12,46 @@
 // HBM rate.  All the rest serves to keep those loads in flight.
 //
 //  * Work.  An item is (sequence, key-value head, up to 8 NT of the query heads that
-//    share it); a unit is 64 or 128 of its tokens.  All items' units form one line, cut into
+//    share it); a unit is 64 to 256 of its tokens (8 warps: twice that).  All items' units form one line, cut into
 //    equal pieces, one per block: blocks end together however uneven the lengths are,
-//    and one long sequence fills the GPU.  Lengths are read on the device, so a captured
-//    graph follows them.  A piece covers the end of one item, some whole items and the
-//    start of another; only the cut ones leave partial sums in the workspace, at
-//    most two a block, which attn_join_kernel adds in order.  When every item
-//    is short (kDirectTokens), a block takes one item and nothing is cut or joined.
-//  * Loads.  Each of the four warps streams every fourth run of 16 or 32 tokens through a ring
+//    and one long sequence fills the GPU.  An item's end costs a block about as much as 1.5 units
+//    (fitted to the blocks' end times), so it takes that much of the line: 64 sequences of 256 to 16384
+//    tokens took 124.6 us with a weight of 0.25 and 110.9 us with 1.5.  Lengths are read on the
+//    device, so a captured graph follows them.  A piece covers the end of one item, some
+//    whole items and the start of another; only the cut ones leave partial sums in the
+//    workspace, at most two a block, which attn_join_kernel adds in order.  Items of at
+//    most kDirectTokens keep one block each and are neither cut nor joined (1000 tokens of 47 rows:
+//    9.3 us against 11.5 with cutting; 2000 tokens of 8 rows: 14.7 against 11.0), of eight warps where
+//    there are no more items than SMs (7.4 against 9.3 us; beyond one run for each of four warps: 3.8
+//    against 3.5 us at 37 tokens).
+//  * Loads.  Each warp streams every fourth (eighth) run of 16 RR tokens through a ring
 //    of its own in shared memory with 16-byte cp.async (stages - 1 runs ahead, across items),
 //    so no warp waits for another except where an item ends.  16 tokens from a multiple of
 //    16 on never straddle a page (pages hold a multiple of 16 places); the next run's page
-//    numbers are loaded a step ahead.  Places not seen are filled with zeros by the copy, so that nothing they hold
-//    (NaN, infinities) reaches a product.
+//    numbers are loaded a step ahead.  Places not seen are filled with zeros by the copy, so
+//    that nothing they hold (NaN, infinities) reaches a product.  Where an item ends the
+//    warps exchange their sums through the stages they have just used.
 //  * Products.  mma.sync m16n8k16 (f16 or bf16, fp32 sums): with at most 16 query heads
 //    sharing a key the products are a small part of the time even at this instruction's
-//    rate, and its operands come straight from registers, where E4M3 codes are converted.
-//    S^T = K Q^T has 16 tokens as rows and 8 query heads as columns, O^T = V^T P^T 16
-//    dimensions and the same columns, so that a lane scales the sums of the heads whose maxima it
-//    holds; movmatrix turns S^T's registers into P^T's.  The order of
-//    dimensions and tokens inside a product is free as long as both operands agree, and
-//    is chosen so that a lane's share of K and V is whole 16-byte words.
-//  * E4M3.  Codes are converted to f16 (exact; the E4M3 form of this instruction does the
-//    same within, on both operands and for every product: measured slower).  A query row is
-//    scaled by a power of two to a maximum in [2^14, 2^15), exact but for values below 2^-28
-//    of it.  K's scale multiplies the score.  V's scale 2^e joins the weight: w_i = exp2(s_i + e_i - m')
-//    with its own running maximum m' of s_i + e_i, times 2^14, rounded to f16 (11 bits
-//    down to 2^-28 of the largest, so that a token with a large score and a tiny value
-//    costs the others nothing), while l sums exp2(s_i - m) in fp32 with m = max s_i.
+//    rate (1024 multiply-adds a clock and SM, measured), and its operands come straight
+//    from registers, where E4M3 codes are converted.  S^T = K Q^T has 16 tokens as rows and
+//    8 query heads as columns, O^T = V^T P^T 16 dimensions and the same columns, so that a
+//    lane scales the sums of the heads whose maxima it holds; movmatrix turns S^T's registers
+//    into P^T's.  The order of dimensions and tokens inside a product is free as long as both
+//    operands agree, and is chosen so that a lane's share of K and V is whole 16-byte words.
+//  * E4M3.  Codes are converted to f16 (exact; the E4M3 form of mma.sync does the same within,
+//    for both operands of every product: 100 instructions for 16 tokens' scores).  A query
+//    row is scaled by a power of two to a maximum in [2^14, 2^15), exact but for values below
+//    2^-28 of it.  K's scale multiplies the score.  V's scale 2^e joins the weight: w_i =
+//    exp2(s_i + e_i - m') with its own running maximum m' of s_i + e_i, times 2^14, rounded to
+//    f16 (11 bits down to 2^-28 of the largest, so that a token with a large score and a tiny
+//    value costs the others nothing), while l sums exp2(s_i - m) in fp32 with m = max s_i.
 //  * bf16.  Q, K and V enter as they are; the weights are rounded to bf16, as V is.
+//
+// Measured (GB300, of 6787 GB/s copy): 32 sequences of 63 to 4001 tokens, 96 heads of 128, bf16 (1.51 GB):
+// 225 to 229 us, 6.6 TB/s; 64 sequences of 256 to 16384 tokens, 64 query and 8 key-value heads, E4M3
+// (668 MB): 110 us, 6.1 TB/s; one of 131072 tokens (271 MB): 50 us, of which 8 are the start, the
+// last blocks and the join; 37 tokens of 96 heads: 3.2 us.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -1047,8 +1058,8 @@ template <int D, bool E4M3, int NT>
 int launch_attn(const AdParams &P, cudaStream_t st) {
   using S = AdShape<D, E4M3, NT, 4, false>;
   const long long items = static_cast<long long>(P.B) * P.heads * P.groups;
-  const int visible = P.max_pages << P.page_shift;  // most tokens an item can have
-  const int tokens = P.window > 0 && P.window < visible ? P.window : visible;
+  const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;  // most tokens an item can have
+  const long long tokens = P.window > 0 && P.window < visible ? P.window : visible;
   if constexpr (S::ROWB <= 256) {  // (beyond, the stages of eight warps do not fit)
     if (items <= sm_count() && tokens > S::UNIT && tokens <= kDirectTokens)
       return start<D, E4M3, NT, 8, true>(P, items, st) == cudaSuccess ? 0 : -1;

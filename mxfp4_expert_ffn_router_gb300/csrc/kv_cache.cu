@@ -8,6 +8,11 @@
 //
 // dim / 8 neighbouring lanes hold one vector (a token's key or value of one head), 16
 // bytes of bf16 each; its scale needs one maximum over those lanes.
+//
+// Bound: the bytes, once in and once out.  Four tokens in flight a thread where there are enough
+// of them: reading 16384 tokens of 8 heads of 128 (101 MB) 17.4 us, 5.8 TB/s (one in flight 22.2 us,
+// eight 19.8); writing 4096 tokens (25 MB) 5.5 us, of which about 2 are the launch (6.2 with one);
+// 13 tokens of 96 heads 1.9 us with one in flight, 2.1 with four.
 #include <cuda_fp16.h>
 
 #include <type_traits>

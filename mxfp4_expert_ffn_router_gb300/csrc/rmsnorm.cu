@@ -8,6 +8,12 @@
 // The norm is of the fp32 sum, not of the bf16 value that residual_out keeps: the sum is
 // in registers anyway, and rounding it first would only lose bits.  The mean is a fixed
 // tree: a thread's values in order, a butterfly over the warp, a tree over the warps.
+//
+// Bound: the rows' bytes, 9 of them a value with every output.  A block has one row in registers,
+// read once; four blocks an SM (32 registers a thread) overlap one row's reduction with the others'
+// loads: 4096 rows of 7168 with both outputs (265 MB) 42.5 us, 6.2 TB/s of 6.8 measured for a copy,
+// against 46.2 us at 38 registers (three blocks) and 48 us for a persistent block that loads its next
+// row early.  One row: 2.5 us, the launch and two trips to memory.
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
