@@ -19,11 +19,14 @@
 //    tokens took 124.6 us with a weight of 0.25 and 110.9 us with 1.5.  Lengths are read on the
 //    device, so a captured graph follows them.  A piece covers the end of one item, some
 //    whole items and the start of another; only the cut ones leave partial sums in the
-//    workspace, at most two a block, which attn_join_kernel adds in order.  Items of at
-//    most kDirectTokens keep one block each and are neither cut nor joined (1000 tokens of 47 rows:
-//    9.3 us against 11.5 with cutting; 2000 tokens of 8 rows: 14.7 against 11.0), of eight warps where
-//    there are no more items than SMs (7.4 against 9.3 us; beyond one run for each of four warps: 3.8
-//    against 3.5 us at 37 tokens).
+//    workspace, at most two a block, which attn_join_kernel adds in order.
+//  * Short ones.  The line costs about 10 us whatever the work.  Where no item sees more than
+//    kDirectTokens, a block takes one item and nothing is cut or joined (256 sequences of 900 tokens:
+//    80.9 us against 95.5).  Where there are no more items than SMs, blocks of eight warps take an item
+//    each, or a cluster of 2, 4 or 8 of them shares it evenly and joins its sums through
+//    distributed shared memory, up to kPartBytes of keys a block (E4M3, 8 heads: 4000 tokens of one
+//    sequence 7.4 us against 11.0 on the line, 16000 14.9 against 15.2, 40000 27.9 against 23.3; 8
+//    sequences of 3000 14.4 against 18.1).
 //  * Loads.  Each warp streams every fourth (eighth) run of 16 RR tokens through a ring
 //    of its own in shared memory with 16-byte cp.async (stages - 1 runs ahead, across items),
 //    so no warp waits for another except where an item ends.  16 tokens from a multiple of
@@ -54,8 +57,6 @@
 // last blocks and the join; 37 tokens of 96 heads: 3.2 us.
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
@@ -67,6 +68,7 @@ namespace {
 
 constexpr int kRun = 16;                 // tokens of a product
 constexpr int kDirectTokens = 1024;      // items that see at most this many are never cut
+constexpr long long kPartBytes = 256 << 10;  // most bytes of keys that one of eight-warp blocks takes
 constexpr int kMinTokens = 256;          // smallest piece of a block
 constexpr int kUnitLen = 4, kItemLen = 6;  // length on the line of a unit, and of an item beside its units
 constexpr int kJoinWarps = 8, kJoinParts = 4;  // warps of a joining block, parts that one adds at once
@@ -280,7 +282,9 @@ struct AdShape {
   // query fragments: in registers, or from 32 of them on in shared memory (the same for all warps)
   static constexpr int QREGS = D / 16 * 2 * NT;
   static constexpr int QSMEM = QREGS >= 32 ? QREGS * 32 * 4 : 0;
-  static constexpr int SMEM = W * STAGES * RR * (SUB + SCALES) + QSMEM + 128;
+  // what a cluster's blocks show one another: their sums and statistics
+  static constexpr int SHOWN = W == 8 ? QUADS * 512 + 8 * NT * 16 : 0;
+  static constexpr int SMEM = W * STAGES * RR * (SUB + SCALES) + QSMEM + SHOWN + 128;
 };
 
 // First of the two neighbouring dimensions that a lane of group g holds of product m.
@@ -294,6 +298,74 @@ __device__ __forceinline__ int quad_dim(int m, int g) {
 // Two neighbouring dimensions of a row, times f (0: a row without weight, whatever the sums are).
 __device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float b, bool on) {
   if (on) *reinterpret_cast<uint32_t *>(p) = f == 0.f ? 0u : pack2<false>(a * f, b * f);
+}
+
+// Adds N parts of a quad: statistics s (m', m, l) of this lane's two rows, sums u at m'.
+template <int N>
+__device__ __forceinline__ void add_parts(const float4 (&s)[N][2], const float4 (&u)[N], float4 &v, float (&mp)[2],
+                                          float (&mt)[2], float (&lt)[2]) {
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    float np = -INFINITY, nt = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) np = fmaxf(np, s[i][x].x), nt = fmaxf(nt, s[i][x].y);
+    const float pb = np == -INFINITY ? 0.f : np, mb = nt == -INFINITY ? 0.f : nt;
+    float a = 0.f, b = 0.f, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float f = ex2(s[i][x].x - pb);
+      a = fmaf(x ? u[i].y : u[i].x, f, a);
+      b = fmaf(x ? u[i].w : u[i].z, f, b);
+      sum = fmaf(s[i][x].z, ex2(s[i][x].y - mb), sum);
+    }
+    (x ? v.y : v.x) = a;
+    (x ? v.w : v.z) = b;
+    mp[x] = np, mt[x] = nt, lt[x] = sum;
+  }
+}
+
+// Writes a quad of rows that are complete: out = O' 2^(m' - m - 14) / l, and with the first quad lse.
+template <int D, bool E4M3>
+__device__ __forceinline__ void store_quad(const AdParams &P, int b, int h0, int rows, int t, int m, const float4 &v,
+                                           const float (&mp)[2], const float (&mt)[2], const float (&lt)[2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, r0 = 8 * t + 2 * (lane & 3);
+  float fin[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const float mb = mt[x] == -INFINITY ? 0.f : mt[x], pb = mp[x] == -INFINITY ? 0.f : mp[x];
+    fin[x] = lt[x] == 0.f ? 0.f : __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt[x]);
+    if (P.lse && m == 0 && g == 0 && r0 + x < rows)
+      P.lse[static_cast<size_t>(b) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
+  }
+  uint16_t *op = P.out + (static_cast<size_t>(b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
+  store_row2(op, fin[0], v.x, v.z, r0 < rows);
+  store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
+}
+
+// ---- thread-block clusters
+__device__ __forceinline__ int cluster_size() {
+  int n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ int cluster_rank() {
+  int r;
+  asm("mov.u32 %0, %%cluster_ctaid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Sixteen bytes at shared address a of the cluster's block `rank`.
+__device__ __forceinline__ float4 lds_of(uint32_t a, int rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(a), "r"(rank)
+      : "memory");
+  return v;
 }
 
 }  // namespace
@@ -330,17 +402,20 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 
   // ---- this block's piece
   Walk<RUN, UNIT> cur;
+  int part = 0, parts = 1;  // of an item that a cluster's blocks share
   long long from = 0, to = 1LL << 62, share = 0;
   if constexpr (DIRECT) {
-    cur.b = blockIdx.x / items;
-    const int item = blockIdx.x - cur.b * items;
+    if constexpr (W == 8) parts = cluster_size(), part = cluster_rank();
+    const int block = blockIdx.x / parts;
+    cur.b = block / items;
+    const int item = block - cur.b * items;
     cur.head = item / P.groups;
     cur.group = item - cur.head * P.groups;
     cur.set(seen_of<RUN>(P, cur.b, tid == 0));
     cur.begin = 0;
     cur.more = true;
-    cur.enter(from, to, first);
     if (cur.n <= cur.t0) {  // sees nothing
+      if (part) return;
       const int h0 = cur.head * P.G + cur.group * NQ;
       const int rows = min(NQ, P.G - cur.group * NQ);
       const size_t row = static_cast<size_t>(cur.b) * P.Hq + h0;
@@ -349,6 +424,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
       if (P.lse && tid < rows) P.lse[row + tid] = -INFINITY;
       return;
     }
+    const unsigned units = cur.units(), base = static_cast<unsigned>(cur.t0) + first;
+    cur.tok = base + units * part / parts * UNIT;
+    cur.stop = base + units * (part + 1) / parts * UNIT;
+    cur.more = cur.tok < cur.stop;  // (a part may be left without a unit)
   } else {
     // every warp for itself: lane l measures sequences [l per, l per + per); a scan finds the piece
     const int per = (P.B + 31) / 32;
@@ -492,7 +571,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     cp_commit();
   };
   new_item();
-  pages();
+  if (pre.more) pages();
 #pragma unroll
   for (int st = 0; st < ST - 1; ++st) issue(st);
 
@@ -500,6 +579,8 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   constexpr bool QS = S::QSMEM > 0;
   uint32_t qf[QS ? 1 : QN][QW];
   uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + W * ST * RR * (S::SUB + S::SCALES));
+  float4 *const shown = reinterpret_cast<float4 *>(smem + W * ST * RR * (S::SUB + S::SCALES) + S::QSMEM);
+  float4 *const shown_stat = shown + S::QUADS * 32;  // (W == 8)
   uint2 raw[D / 16][NT];
   // of query heads 8 t + 2c + x: the scale of a raw score (in powers of two), the running maxima and l
   float sq[NT][2], o[NT][MM][4], mrun[NT][2], m_l[NT][2], l[NT][2];
@@ -570,7 +651,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   load_q(cur);
   start_item();
   if (QS) __syncthreads();
-  for (;;) {
+  while (cur.more) {
     __syncwarp();  // every lane is done with the stage that is loaded next
     issue(after);
     after = after + 1 == ST ? 0 : after + 1;
@@ -811,7 +892,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     float4 *buf = reinterpret_cast<float4 *>(smem + used * (RR * S::SUB));
     constexpr int NEXT = ST * RR * S::SUB / 16;  // from one warp's stages to the next's
     const int slot = 2 * blockIdx.x + (first_item ? 0 : 1);
-    float fin[2], fac[2][W];
+    float fac[2][W], mp[2], mt[2], lt[2];
     int t_of = -1;
     __syncwarp();
 #pragma unroll
@@ -832,22 +913,19 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int r = 8 * t + 2 * c + e;
-            float mp = -INFINITY, mt = -INFINITY, lt = 0.f;
+            mp[e] = mt[e] = -INFINITY;
+            lt[e] = 0.f;
 #pragma unroll
-            for (int w = 0; w < W; ++w) mp = fmaxf(mp, s_mp[r][w]), mt = fmaxf(mt, s_m[r][w]);
-            const float mb = mt == -INFINITY ? 0.f : mt, pb = mp == -INFINITY ? 0.f : mp;
+            for (int w = 0; w < W; ++w) mp[e] = fmaxf(mp[e], s_mp[r][w]), mt[e] = fmaxf(mt[e], s_m[r][w]);
+            const float mb = mt[e] == -INFINITY ? 0.f : mt[e], pb = mp[e] == -INFINITY ? 0.f : mp[e];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-              lt = fmaf(s_l[r][w], ex2(s_m[r][w] - mb), lt);
+              lt[e] = fmaf(s_l[r][w], ex2(s_m[r][w] - mb), lt[e]);
               fac[e][w] = ex2(s_mp[r][w] - pb);
             }
-            // out = O' 2^(m' - m - 14) / l; a row without weight is 0
-            fin[e] = lt == 0.f ? 0.f : __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt);
             if (m == 0 && g == 0) {
-              if (cut)
-                P.stat[static_cast<size_t>(slot) * NQ + r] = make_float4(mp, mt, lt, 0.f);
-              else if (P.lse && r < rows)
-                P.lse[static_cast<size_t>(done.b) * P.Hq + h0 + r] = lt == 0.f ? -INFINITY : (mb + log2f(lt)) * kLn2;
+              if (cut) P.stat[static_cast<size_t>(slot) * NQ + r] = make_float4(mp[e], mt[e], lt[e], 0.f);
+              if (parts > 1) shown_stat[r] = make_float4(mp[e], mt[e], lt[e], 0.f);
             }
           }
         }
@@ -860,14 +938,12 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
           v.z = fmaf(u.z, fac[0][w], v.z);
           v.w = fmaf(u.w, fac[1][w], v.w);
         }
-        if (cut) {
+        if (cut)
           P.part[(static_cast<size_t>(slot) * S::QUADS + quad) * 32 + lane] = v;
-        } else {
-          const int r0 = 8 * t + 2 * c;
-          uint16_t *op = P.out + (static_cast<size_t>(done.b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
-          store_row2(op, fin[0], v.x, v.z, r0 < rows);
-          store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
-        }
+        else if (parts > 1)
+          shown[quad * 32 + lane] = v;
+        else
+          store_quad<D, E4M3>(P, done.b, h0, rows, t, m, v, mp, mt, lt);
       }
       __syncthreads();
     }
@@ -882,14 +958,42 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
             done.head * P.groups + done.group, done.b);
       }
     }
-    if (!cur.more) break;
     first_item = false;
+    if (!cur.more) break;
     if (!kEarlyQ) load_q(cur);
     start_item();
     if (QS) __syncthreads();
   }
   cp_wait<0>();
   if constexpr (!DIRECT) zero_rows();
+  if constexpr (W == 8) {
+    if (parts > 1) {  // join the cluster's blocks: each takes every parts-th quad
+      if (first_item) {  // (nothing came of the loop: an empty part)
+        for (int i = tid; i < S::QUADS * 32; i += THREADS) shown[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (tid < NQ) shown_stat[tid] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+      }
+      cluster_sync();
+      const int h0 = cur.head * P.G + cur.group * NQ, rows = min(NQ, P.G - cur.group * NQ);
+      for (int quad = part + parts * warp; quad < S::QUADS; quad += parts * W) {
+        const int t = quad / MM, m = quad - t * MM, r0 = 8 * t + 2 * c;
+        float4 s[8][2], u[8], v;
+        float mp[2], mt[2], lt[2];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          s[x][0] = s[x][1] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+          u[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (x < parts) {
+            s[x][0] = lds_of(su32(shown_stat + r0), x);
+            s[x][1] = lds_of(su32(shown_stat + r0 + 1), x);
+            u[x] = lds_of(su32(shown + quad * 32 + lane), x);
+          }
+        }
+        add_parts(s, u, v, mp, mt, lt);
+        store_quad<D, E4M3>(P, cur.b, h0, rows, t, m, v, mp, mt, lt);
+      }
+      cluster_sync();  // the others have read this block's
+    }
+  }
 }
 
 // Adds the partial sums of the items that were cut, in the order of their pieces.  The
@@ -932,27 +1036,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AdPara
     const int t = quad / MM, m = quad - t * MM, r0 = 8 * t + 2 * c;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     float mp[2], mt[2], lt[2];
-    // the sum of N parts (statistics s of this lane's two rows, sums u), all at once
-    auto add = [&](const auto &s, const auto &u, auto N) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float np = -INFINITY, nt = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < N.value; ++i) np = fmaxf(np, s[i][x].x), nt = fmaxf(nt, s[i][x].y);
-        const float pb = np == -INFINITY ? 0.f : np, mb = nt == -INFINITY ? 0.f : nt;
-        float a = 0.f, b = 0.f, sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < N.value; ++i) {
-          const float f = ex2(s[i][x].x - pb);
-          a = fmaf(x ? u[i].y : u[i].x, f, a);
-          b = fmaf(x ? u[i].w : u[i].z, f, b);
-          sum = fmaf(s[i][x].z, ex2(s[i][x].y - mb), sum);
-        }
-        (x ? v.y : v.x) = a;
-        (x ? v.w : v.z) = b;
-        mp[x] = np, mt[x] = nt, lt[x] = sum;
-      }
-    };
     const float4 none = make_float4(-INFINITY, -INFINITY, 0.f, 0.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
     mp[0] = mp[1] = mt[0] = mt[1] = -INFINITY;
     lt[0] = lt[1] = 0.f;
@@ -972,7 +1055,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AdPara
         s[kJoinParts][0] = make_float4(mp[0], mt[0], lt[0], 0.f);
         s[kJoinParts][1] = make_float4(mp[1], mt[1], lt[1], 0.f);
         u[kJoinParts] = v;
-        add(s, u, std::integral_constant<int, kJoinParts + 1>());
+        add_parts(s, u, v, mp, mt, lt);
       }
     }
     if (max(sp0, sp1) > 1) {  // (uniform: the block's)
@@ -996,7 +1079,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AdPara
           s[kJoinParts][0] = make_float4(mp[0], mt[0], lt[0], 0.f);
           s[kJoinParts][1] = make_float4(mp[1], mt[1], lt[1], 0.f);
           u[kJoinParts] = v;
-          add(s, u, std::integral_constant<int, kJoinParts + 1>());
+          add_parts(s, u, v, mp, mt, lt);
         }
       }
       __syncthreads();
@@ -1004,17 +1087,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AdPara
     if (in && sub == 0) {
       const int head = me.z / P.groups, group = me.z - head * P.groups;
       const int h0 = head * P.G + group * NQ, rows = min(NQ, P.G - group * NQ);
-      float fin[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float mb = mt[x] == -INFINITY ? 0.f : mt[x], pb = mp[x] == -INFINITY ? 0.f : mp[x];
-        fin[x] = lt[x] == 0.f ? 0.f : exp2f(pb - mb - (E4M3 ? 14.f : 0.f)) / lt[x];
-        if (P.lse && m == 0 && g == 0 && r0 + x < rows)
-          P.lse[static_cast<size_t>(me.w) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
-      }
-      uint16_t *op = P.out + (static_cast<size_t>(me.w) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
-      store_row2(op, fin[0], v.x, v.z, r0 < rows);
-      store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
+      store_quad<D, E4M3>(P, me.w, h0, rows, t, m, v, mp, mt, lt);
     }
   }
 }
@@ -1040,8 +1113,9 @@ AdPlan plan_of(const k3moe_kv_cache &c, int Hq) {
   return p;
 }
 
+// A launch of `blocks` blocks in clusters of `cluster`; 0 blocks: only how many clusters fit the GPU at once.
 template <int D, bool E4M3, int NT, int W, bool DIRECT>
-cudaError_t start(const AdParams &P, long long blocks, cudaStream_t st) {
+cudaError_t start(const AdParams &P, long long blocks, int cluster, cudaStream_t st, int *fit = nullptr) {
   using S = AdShape<D, E4M3, NT, W, DIRECT>;
   static bool attr = false;
   if (!attr) {
@@ -1050,8 +1124,42 @@ cudaError_t start(const AdParams &P, long long blocks, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     attr = true;
   }
-  return launch_pdl(attn_decode_kernel<D, E4M3, NT, W, DIRECT>, dim3(static_cast<unsigned>(blocks)), dim3(W * 32), S::SMEM,
-                    st, P);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks ? blocks : cluster));
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = S::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = cluster;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  if (!blocks) {
+    cfg.attrs = attrs + 1;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(fit, attn_decode_kernel<D, E4M3, NT, W, DIRECT>, &cfg);
+  }
+  return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, E4M3, NT, W, DIRECT>, P);
+}
+
+// Clusters of `parts` (2, 4 or 8) eight-warp blocks that run at once: not all SMs, since a cluster
+// lies within one group of 16 to 20 of them (128 blocks in clusters of 8 took two rounds, 16.3 us, where
+// 64 in clusters of 4 took 10.2).
+template <int D, bool E4M3, int NT>
+int clusters_at_once(const AdParams &P, int parts) {
+  static int known[9];  // + 1
+  if (!known[parts]) {
+    int n = 0;
+    if (start<D, E4M3, NT, 8, true>(P, 0, parts, nullptr, &n) != cudaSuccess) {
+      cudaGetLastError();  // leave no error behind
+      n = 0;
+    }
+    known[parts] = n + 1;
+  }
+  return known[parts] - 1;
 }
 
 template <int D, bool E4M3, int NT>
@@ -1061,15 +1169,21 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
   const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;  // most tokens an item can have
   const long long tokens = P.window > 0 && P.window < visible ? P.window : visible;
   if constexpr (S::ROWB <= 256) {  // (beyond, the stages of eight warps do not fit)
-    if (items <= sm_count() && tokens > S::UNIT && tokens <= kDirectTokens)
-      return start<D, E4M3, NT, 8, true>(P, items, st) == cudaSuccess ? 0 : -1;
+    if (items <= sm_count() && tokens > S::UNIT) {
+      int parts = 1;
+      if (tokens > 4LL * S::UNIT)  // (one more step costs less than a cluster's join up to here)
+        while (parts < 8 && tokens > 2LL * S::UNIT * parts && items <= clusters_at_once<D, E4M3, NT>(P, 2 * parts)) parts *= 2;
+      if (tokens * S::ROWB <= kPartBytes * parts)
+        return start<D, E4M3, NT, 8, true>(P, items * parts, parts, st) == cudaSuccess ? 0 : -1;
+    }
   }
-  if (tokens <= kDirectTokens && items < (1LL << 31)) return start<D, E4M3, NT, 4, true>(P, items, st) == cudaSuccess ? 0 : -1;
+  if (tokens <= kDirectTokens && items < (1LL << 31))
+    return start<D, E4M3, NT, 4, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
   long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;
   if (blocks > kAdMostBlocks) blocks = kAdMostBlocks;
   const long long most = (items * ((tokens + S::RUN + S::UNIT - 2) / S::UNIT * S::UNIT) + kMinTokens - 1) / kMinTokens;
   if (blocks > most) blocks = most;
-  if (start<D, E4M3, NT, 4, false>(P, blocks, st) != cudaSuccess) return -1;
+  if (start<D, E4M3, NT, 4, false>(P, blocks, 1, st) != cudaSuccess) return -1;
   return launch_pdl(attn_join_kernel<D, E4M3, NT>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinWarps * 32), 0, st, P) == cudaSuccess
              ? 0
              : -1;
