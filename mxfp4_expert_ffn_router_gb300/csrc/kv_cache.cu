@@ -6,13 +6,12 @@
 // place.  A negative slot is padding (not written; reads as zeros); one at or past the
 // end sets K3MOE_DEV_BOUNDS and is treated the same.
 //
-// dim / 8 neighbouring lanes hold one vector (a token's key or value of one head), 16
-// bytes of bf16 each; its scale needs one maximum over those lanes.
+// A few neighbouring lanes hold one vector (a token's key or value of one head), 8 or 16 values
+// each; its scale needs one maximum over those lanes.
 //
-// Bound: the bytes, once in and once out.  Four tokens in flight a thread where there are enough
-// of them: reading 16384 tokens of 8 heads of 128 (101 MB) 17.4 us, 5.8 TB/s (one in flight 22.2 us,
-// eight 19.8); writing 4096 tokens (25 MB) 5.5 us, of which about 2 are the launch (6.2 with one);
-// 13 tokens of 96 heads 1.9 us with one in flight, 2.1 with four.
+// Bound: the bytes, once in and once out, with several tokens in flight a thread where there are
+// enough of them: reading 16384 tokens of 8 heads of 128 (101 MB) 17.4 us, 5.8 TB/s (one in flight 22.2
+// us); writing 4096 tokens (25 MB) 4.5 us, of which about 2 are the launch; 13 tokens of 96 heads 1.9 us.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -47,35 +46,50 @@ __device__ __forceinline__ size_t vec_index(const KvView &c, int slot, int head)
 
 // Block (x, y): TOKENS tokens from x TOKENS on, of head y (keys) or y - heads (values): neighbouring
 // tokens mostly have neighbouring slots, so that a block's stores are one stretch of the
-// cache.  A group of D / 8 lanes takes every (256 / L)th of the block's tokens, U in all, loading
-// all of them before the first use.  U = 4 where that leaves two blocks an SM, else 1.
-template <int D, int U_>
+// cache.  A group of L lanes takes every (256 / L)th of the block's tokens, U in all, loading
+// all of them before the first use.
+template <int D, int V_, int U_>
 struct KvTile {
-  static constexpr int L = D / 8, G = 256 / L, U = U_, TOKENS = G * U;
+  static constexpr int V = V_;  // values of a lane
+  static constexpr int L = D / V, G = 256 / L, U = U_, TOKENS = G * U;
+};
+// Values of a lane and tokens in flight (1 where fewer than two blocks an SM would be left).  Quantising
+// shares a maximum, so fewer lanes with 16 values each pay (4.5 against 5.5 us for 4096 tokens); reading back
+// 16 a lane would store two words 32 bytes apart at a time (20.2 against 17.4 us for 16384 tokens).
+template <bool E4M3>
+struct KvWriteWork {
+  static constexpr int V = E4M3 ? 16 : 8, MANY = 2;
+};
+template <bool E4M3>
+struct KvReadWork {
+  static constexpr int V = 8, MANY = 4;
 };
 
 template <int D, bool E4M3, int U>
 __global__ void __launch_bounds__(256)
     kv_write_kernel(KvView c, int n, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, long long k_stride,
                     long long v_stride, const int32_t *__restrict__ slots, int32_t *status) {
-  using K = KvTile<D, U>;
+  using K = KvTile<D, KvWriteWork<E4M3>::V, U>;
   pdl_wait();
   pdl_trigger();
   const int sub = threadIdx.x % K::L;
   const bool val = static_cast<int>(blockIdx.y) >= c.heads;
   const int head = val ? blockIdx.y - c.heads : blockIdx.y;
-  const uint16_t *src = (val ? v : k) + static_cast<size_t>(head) * D + sub * 8;
+  const uint16_t *src = (val ? v : k) + static_cast<size_t>(head) * D + sub * K::V;
   const long long stride = val ? v_stride : k_stride;
   uint8_t *dst = val ? c.v : c.k, *dst_scales = val ? c.vs : c.ks;
   const int t0 = blockIdx.x * K::TOKENS + threadIdx.x / K::L;
   int slot[K::U];
-  uint4 u[K::U];
+  uint4 u[K::U][K::V / 8];
 #pragma unroll
   for (int i = 0; i < K::U; ++i) {
     const int t = t0 + i * K::G;
     slot[i] = t < n ? __ldg(slots + t) : -1;
-    u[i] = make_uint4(0, 0, 0, 0);
-    if (t < n) u[i] = __ldg(reinterpret_cast<const uint4 *>(src + t * stride));
+#pragma unroll
+    for (int h = 0; h < K::V / 8; ++h) {
+      u[i][h] = make_uint4(0, 0, 0, 0);
+      if (t < n) u[i][h] = __ldg(reinterpret_cast<const uint4 *>(src + t * stride) + h);
+    }
   }
 #pragma unroll
   for (int i = 0; i < K::U; ++i) {
@@ -85,22 +99,32 @@ __global__ void __launch_bounds__(256)
     }
     const size_t o = slot[i] >= 0 ? vec_index(c, slot[i], head) : 0;
     if constexpr (!E4M3) {
-      if (slot[i] >= 0) *(reinterpret_cast<uint4 *>(dst + o * (2 * D)) + sub) = u[i];
+      if (slot[i] >= 0) *(reinterpret_cast<uint4 *>(dst + o * (2 * D)) + sub) = u[i][0];
     } else {
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      float f[8];
-      uint32_t m = 0u;
+      // the largest magnitude as a bf16 pattern: two at a time
+      uint32_t m2 = 0u;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        f[2 * q] = __uint_as_float(w[q] << 16);
-        f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
-        m = max(m, max((w[q] << 16) & 0x7FFFFFFFu, w[q] & 0x7FFF0000u));
-      }
+      for (int h = 0; h < 2; ++h)
+        m2 = __vmaxu2(__vmaxu2(m2, __vmaxu2(u[i][h].x & 0x7FFF7FFFu, u[i][h].y & 0x7FFF7FFFu)),
+                      __vmaxu2(u[i][h].z & 0x7FFF7FFFu, u[i][h].w & 0x7FFF7FFFu));
+      uint32_t m = max(m2 << 16, m2 & 0xFFFF0000u);
 #pragma unroll
       for (int off = 1; off < K::L; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
       const uint32_t byte = mx8_scale_byte(m);
+      uint2 q[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w[4] = {u[i][h].x, u[i][h].y, u[i][h].z, u[i][h].w};
+        float f[8];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          f[2 * x] = __uint_as_float(w[x] << 16);
+          f[2 * x + 1] = __uint_as_float(w[x] & 0xFFFF0000u);
+        }
+        q[h] = mx8_codes(f, byte);
+      }
       if (slot[i] >= 0) {
-        *(reinterpret_cast<uint2 *>(dst + o * D) + sub) = mx8_codes(f, byte);
+        *(reinterpret_cast<uint4 *>(dst + o * D) + sub) = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
         if (sub == 0) dst_scales[o] = static_cast<uint8_t>(byte);
       }
     }
@@ -112,7 +136,7 @@ template <int D, bool E4M3, int U>
 __global__ void __launch_bounds__(256)
     kv_read_kernel(KvView c, int n, const int32_t *__restrict__ slots, uint16_t *__restrict__ k_out,
                    uint16_t *__restrict__ v_out, int32_t *status) {
-  using K = KvTile<D, U>;
+  using K = KvTile<D, KvReadWork<E4M3>::V, U>;
   using Word = std::conditional_t<E4M3, uint2, uint4>;  // eight values
   pdl_wait();
   pdl_trigger();
@@ -148,7 +172,7 @@ __global__ void __launch_bounds__(256)
   for (int i = 0; i < K::U; ++i) {
     const int t = t0 + i * K::G;
     if (t >= n) continue;
-    uint4 u;
+    uint4 *to = reinterpret_cast<uint4 *>(out + static_cast<size_t>(t) * c.heads * D + sub * K::V);
     if constexpr (E4M3) {
       const float x = e8m0_to_f32(byte[i]);
       uint32_t h[4], r[4];
@@ -159,32 +183,31 @@ __global__ void __launch_bounds__(256)
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[q]));
         r[q] = bf16x2(f.x * x, f.y * x);
       }
-      u = make_uint4(r[0], r[1], r[2], r[3]);
+      *to = make_uint4(r[0], r[1], r[2], r[3]);
     } else {
-      u = w[i];
+      *to = w[i];
     }
-    *(reinterpret_cast<uint4 *>(out + static_cast<size_t>(t) * c.heads * D) + sub) = u;
   }
 }
 
 namespace {
 
 // Calls f(dim, whether E4M3, U, grid), the first three as types' values.
-template <class F>
+template <template <bool> class Work, class F>
 int kv_dispatch(const k3moe_kv_cache &c, int n, F f) {
-  auto with = [&](auto D, auto E, auto U) {
-    using K = KvTile<decltype(D)::value, decltype(U)::value>;
-    return f(D, E, U, dim3((n + K::TOKENS - 1) / K::TOKENS, 2 * c.heads)) == cudaSuccess ? 0 : -1;
+  auto of_format = [&](auto D, auto E) {
+    using Wk = Work<decltype(E)::value>;
+    auto with = [&](auto U) {
+      constexpr int tokens = KvTile<decltype(D)::value, Wk::V, decltype(U)::value>::TOKENS;
+      const long long blocks = (static_cast<long long>(n) + tokens - 1) / tokens;
+      if (U > 1 && blocks * 2 * c.heads < 2LL * sm_count()) return 1;  // too few
+      return f(D, E, U, dim3(static_cast<unsigned>(blocks), 2 * c.heads)) == cudaSuccess ? 0 : -1;
+    };
+    const int rc = with(std::integral_constant<int, Wk::MANY>());
+    return rc == 1 ? with(std::integral_constant<int, 1>()) : rc;
   };
   auto of_dim = [&](auto D) {
-    constexpr int d = decltype(D)::value, tokens = KvTile<d, 4>::TOKENS;
-    const std::true_type e{};
-    const std::false_type b{};
-    const std::integral_constant<int, 1> one{};
-    const std::integral_constant<int, 4> four{};
-    const bool many = static_cast<long long>((n + tokens - 1) / tokens) * 2 * c.heads >= 2LL * sm_count();
-    if (c.format == K3MOE_KV_E4M3) return many ? with(D, e, four) : with(D, e, one);
-    return many ? with(D, b, four) : with(D, b, one);
+    return c.format == K3MOE_KV_E4M3 ? of_format(D, std::true_type()) : of_format(D, std::false_type());
   };
   if (c.dim == 64) return of_dim(std::integral_constant<int, 64>());
   if (c.dim == 128) return of_dim(std::integral_constant<int, 128>());
@@ -196,7 +219,7 @@ int kv_dispatch(const k3moe_kv_cache &c, int n, F f) {
 
 int launch_kv_write(const k3moe_kv_cache &c, int n, const uint16_t *k, const uint16_t *v, long long k_stride,
                     long long v_stride, const int32_t *slots, int32_t *status, cudaStream_t st) {
-  return kv_dispatch(c, n, [&](auto D, auto E, auto U, dim3 grid) {
+  return kv_dispatch<KvWriteWork>(c, n, [&](auto D, auto E, auto U, dim3 grid) {
     return launch_pdl(kv_write_kernel<decltype(D)::value, decltype(E)::value, decltype(U)::value>, grid, dim3(256), 0, st,
                       view_of(c), n, k, v, k_stride, v_stride, slots, status);
   });
@@ -204,7 +227,7 @@ int launch_kv_write(const k3moe_kv_cache &c, int n, const uint16_t *k, const uin
 
 int launch_kv_read(const k3moe_kv_cache &c, int n, const int32_t *slots, uint16_t *k_out, uint16_t *v_out,
                    int32_t *status, cudaStream_t st) {
-  return kv_dispatch(c, n, [&](auto D, auto E, auto U, dim3 grid) {
+  return kv_dispatch<KvReadWork>(c, n, [&](auto D, auto E, auto U, dim3 grid) {
     return launch_pdl(kv_read_kernel<decltype(D)::value, decltype(E)::value, decltype(U)::value>, grid, dim3(256), 0, st,
                       view_of(c), n, slots, k_out, v_out, status);
   });
