@@ -14,9 +14,10 @@
 //  * Work.  An item is (sequence, key-value head, up to 8 NT of the query heads that
 //    share it); a unit is 64 to 256 of its tokens (8 warps: twice that).  All items' units form one line, cut into
 //    equal pieces, one per block: blocks end together however uneven the lengths are,
-//    and one long sequence fills the GPU.  An item's end costs a block about as much as 1.5 units
+//    and one long sequence fills the GPU.  An item's end costs a block about as much as 1.5 or 3 units
 //    (fitted to the blocks' end times), so it takes that much of the line: 64 sequences of 256 to 16384
-//    tokens took 124.6 us with a weight of 0.25 and 110.9 us with 1.5.  Lengths are read on the
+//    tokens took 124.6 us with a weight of 0.25 and 110.9 us with 1.5; 64 of 125 to 8000 tokens with 16 query heads
+//    a key 88.4 us with 1.5 and 74.2 with 3.  Lengths are read on the
 //    device, so a captured graph follows them.  A piece covers the end of one item, some
 //    whole items and the start of another; only the cut ones leave partial sums in the
 //    workspace, at most two a block, which attn_join_kernel adds in order.
@@ -70,7 +71,7 @@ constexpr int kRun = 16;                 // tokens of a product
 constexpr int kDirectTokens = 1024;      // items that see at most this many are never cut
 constexpr long long kPartBytes = 256 << 10;  // most bytes of keys that one of eight-warp blocks takes
 constexpr int kMinTokens = 256;          // smallest piece of a block
-constexpr int kUnitLen = 4, kItemLen = 6;  // length on the line of a unit, and of an item beside its units
+constexpr int kUnitLen = 4;              // length of a unit on the line
 constexpr int kJoinWarps = 8, kJoinParts = 4;  // warps of a joining block, parts that one adds at once
 constexpr int kAdMostBlocks = 152 * 2;   // pieces (bounds the workspace)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -214,9 +215,9 @@ __device__ __forceinline__ int units_of(const Seen &s) {
 }
 
 // A block's piece [from, to) of the line, and where one warp is in it.  An item that begins at
-// `begin` lies on the line as kItemLen, then kUnitLen for each of its units; a unit belongs
+// `begin` lies on the line as ITEM_LEN, then kUnitLen for each of its units; a unit belongs
 // to the piece in which it begins.
-template <int RUN, int UNIT>
+template <int RUN, int UNIT, int ITEM_LEN>
 struct Walk {
   int b, head, group;    // sequence, key-value head, which of its items
   int n, lo, t0;
@@ -226,7 +227,7 @@ struct Walk {
   __device__ __forceinline__ int units() const { return units_of<UNIT>({n, lo, t0}); }
   // The item's first unit at or past place x of the line.
   __device__ __forceinline__ int unit_at(long long x) const {
-    const long long u = (x - begin - kItemLen + kUnitLen - 1) / kUnitLen;
+    const long long u = (x - begin - ITEM_LEN + kUnitLen - 1) / kUnitLen;
     return u < 0 ? 0 : u > units() ? units() : static_cast<int>(u);
   }
   // Begins the item at `begin`, from its first unit in [from, to) on; first: the warp's place in a unit.
@@ -236,8 +237,8 @@ struct Walk {
   }
   __device__ __forceinline__ void set(const Seen &s) { n = s.n, lo = s.lo, t0 = s.t0; }
   __device__ __forceinline__ void next_item(const AdParams &P, long long from, long long to, int first) {
-    begin += static_cast<long long>(units()) * kUnitLen + kItemLen;
-    more = begin + kItemLen < to;
+    begin += static_cast<long long>(units()) * kUnitLen + ITEM_LEN;
+    more = begin + ITEM_LEN < to;
     if (!more) return;
     if (++group == P.groups) {
       group = 0;
@@ -266,6 +267,8 @@ struct AdShape {
   static constexpr int KB = kRun * ROWB;          // bytes of 16 tokens' keys
   static constexpr int MM = D / 16;               // products (16 dimensions each) of 16 tokens and 8 query heads
   static constexpr int QUADS = MM * NT;           // accumulator quads per lane
+  // What an item's end costs, on the line: 1.5 units, or 3 where there is more to join
+  static constexpr int ITEM_LEN = QUADS <= 8 ? 6 : 12;
   // A warp's step is RR times 16 tokens: 4 to 16 KB, so that what a step costs besides its bytes counts little
   static constexpr int RR = ROWB <= 64 ? 4 : ROWB <= 128 ? 2 : 1;
   static constexpr int RUN = RR * kRun;
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   };
 
   // ---- this block's piece
-  Walk<RUN, UNIT> cur;
+  Walk<RUN, UNIT, S::ITEM_LEN> cur;
   int part = 0, parts = 1;  // of an item that a cluster's blocks share
   long long from = 0, to = 1LL << 62, share = 0;
   if constexpr (DIRECT) {
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     const int b0 = min(P.B, lane * per), b1 = min(P.B, b0 + per);
     auto length = [&](int b, bool report) {  // of an item of sequence b on the line
       const int u = units_of<UNIT>(seen_of<RUN>(P, b, report));
-      return u ? static_cast<long long>(u) * kUnitLen + kItemLen : 0LL;
+      return u ? static_cast<long long>(u) * kUnitLen + S::ITEM_LEN : 0LL;
     };
     long long mine = 0;
     for (int b = b0; b < b1; ++b) mine += length(b, blockIdx.x == 0 && warp == 0);
@@ -494,7 +497,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   const uint32_t vdst = S::KB + lr * S::ROWB + (lx << 4);
   const uint8_t *const klane = P.k + lane * 16, *const vlane = P.v + lane * 16;
   const unsigned place = (1u << P.page_shift) - 1u, page_vecs = static_cast<unsigned>(P.heads) << P.page_shift;
-  Walk<RUN, UNIT> pre = cur;
+  Walk<RUN, UNIT, S::ITEM_LEN> pre = cur;
   uint32_t bad = 0;    // bit st RR + r: a page number outside the cache
   // a run starts at a multiple of RUN and lies in one page if pages are no smaller
   const bool one_page = (RUN - 1u) <= place;
@@ -584,7 +587,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   uint2 raw[D / 16][NT];
   // of query heads 8 t + 2c + x: the scale of a raw score (in powers of two), the running maxima and l
   float sq[NT][2], o[NT][MM][4], mrun[NT][2], m_l[NT][2], l[NT][2];
-  auto load_q = [&](const Walk<RUN, UNIT> &at) {
+  auto load_q = [&](const Walk<RUN, UNIT, S::ITEM_LEN> &at) {
     const int h0 = at.head * P.G + at.group * NQ, rows = min(NQ, P.G - at.group * NQ);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     }
   };
 
-  constexpr bool kEarlyQ = D / 16 * NT <= 8;  // as far as there are registers for it
+  constexpr bool kEarlyQ = D / 16 * NT <= (E4M3 && NT == 2 ? 8 : 16);  // as far as there are registers for it
   bool first_item = true;
   int stage = 0, after = ST - 1;  // the stage in use, and the one that is loaded next
   load_q(cur);
@@ -862,7 +865,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     if (cur.tok < cur.stop) continue;
 
     // ---- the item ends here (or is cut here): join the warps
-    const Walk<RUN, UNIT> done = cur;
+    const Walk<RUN, UNIT, S::ITEM_LEN> done = cur;
     const bool began_before = !DIRECT && done.unit_at(from) > 0, cut = began_before || (!DIRECT && done.unit_at(to) < done.units());
     const int h0 = done.head * P.G + done.group * NQ, rows = min(NQ, P.G - done.group * NQ);
     if (DIRECT)
@@ -949,7 +952,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     }
     if constexpr (!DIRECT) {
       if (tid == 0 && cut) {  // the blocks whose pieces the item covers
-        const long long unit0 = done.begin + kItemLen;
+        const long long unit0 = done.begin + S::ITEM_LEN;
         const int b0 = static_cast<int>(div_small(unit0, share));
         P.meta[2 * blockIdx.x + (began_before ? 0 : 1)] = make_int4(
             // not the first item of its block if the one before has a unit there

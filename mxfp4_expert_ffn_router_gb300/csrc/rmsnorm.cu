@@ -35,18 +35,22 @@ __device__ __forceinline__ uint4 f32x8_to_bf16(const float (&v)[8]) {
   return make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
 }
 
+constexpr int kWarpRows = 8;  // rows of a block where a warp takes one
+
 }  // namespace
 
-// One block per row; a thread holds CH chunks of 8 values (chunk = tid + i * blockDim).
-template <int CH>
+// One block per row, or (WARP) one warp: a thread holds CH chunks of 8 values, tid + i * nth of its row.
+template <int CH, bool WARP>
 __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
-    rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, float eps, int H,
-                   uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
+    rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, float eps, int T,
+                   int H, uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
   __shared__ __align__(16) float part[16];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, nth = blockDim.x, nch = H / 8;
-  const size_t row = static_cast<size_t>(blockIdx.x) * H;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nth = WARP ? 32 : blockDim.x, nch = H / 8;
+  const long long r_at = WARP ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && r_at >= T) return;
+  const size_t row = static_cast<size_t>(r_at) * H;
   float a[CH][8];
   float sum = 0.f;
 #pragma unroll
@@ -66,14 +70,17 @@ __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
-  if (tid < 16 && tid >= nth / 32) part[tid] = 0.f;
-  if ((tid & 31) == 0) part[tid >> 5] = sum;
-  __syncthreads();
-  float4 s[4];
+  float total = sum;
+  if constexpr (!WARP) {
+    if (tid < 16 && tid >= nth / 32) part[tid] = 0.f;
+    if ((tid & 31) == 0) part[tid >> 5] = sum;
+    __syncthreads();
+    float4 s[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s[i] = reinterpret_cast<const float4 *>(part)[i];
-  const float total = (((s[0].x + s[0].y) + (s[0].z + s[0].w)) + ((s[1].x + s[1].y) + (s[1].z + s[1].w))) +
-                      (((s[2].x + s[2].y) + (s[2].z + s[2].w)) + ((s[3].x + s[3].y) + (s[3].z + s[3].w)));
+    for (int i = 0; i < 4; ++i) s[i] = reinterpret_cast<const float4 *>(part)[i];
+    total = (((s[0].x + s[0].y) + (s[0].z + s[0].w)) + ((s[1].x + s[1].y) + (s[1].z + s[1].w))) +
+            (((s[2].x + s[2].y) + (s[2].z + s[2].w)) + ((s[3].x + s[3].y) + (s[3].z + s[3].w)));
+  }
   // m^-1/2 with one Newton step on rsqrtf, 1 - m inv^2 taken from exact products
   const float m = total / static_cast<float>(H) + eps;
   float inv = rsqrtf(m);
@@ -109,17 +116,21 @@ __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
 
 int launch_rmsnorm(int T, int H, const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps,
                    uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales, cudaStream_t st) {
-  const int nch = H / 8;
-  const int ch = nch <= 512 ? 1 : nch <= 1024 ? 2 : 4;  // H <= 16384: 2048 chunks
-  const int nth = ((nch + ch - 1) / ch + 31) / 32 * 32;
-  const dim3 grid(T), block(nth);
+  const int nch = H / 8;  // at most 2048
   cudaError_t err;
-  if (ch == 1)
-    err = launch_pdl(rmsnorm_kernel<1>, grid, block, 0, st, x, residual, weight, eps, H, residual_out, y, codes, scales);
-  else if (ch == 2)
-    err = launch_pdl(rmsnorm_kernel<2>, grid, block, 0, st, x, residual, weight, eps, H, residual_out, y, codes, scales);
-  else
-    err = launch_pdl(rmsnorm_kernel<4>, grid, block, 0, st, x, residual, weight, eps, H, residual_out, y, codes, scales);
+#define K3_RN(CH_, WARP_, GRID_, BLOCK_)                                                                             \
+  err = launch_pdl(rmsnorm_kernel<CH_, WARP_>, dim3(GRID_), dim3(BLOCK_), 0, st, x, residual, weight, eps, T, H, \
+                   residual_out, y, codes, scales)
+  if (nch <= 32) {  // a row is one chunk a lane: 4096 rows of 256 2.5 us, one block each 4.8
+    K3_RN(1, true, (static_cast<unsigned>(T) + kWarpRows - 1) / kWarpRows, 32 * kWarpRows);
+  } else if (nch <= 512) {
+    K3_RN(1, false, T, (nch + 31) / 32 * 32);
+  } else if (nch <= 1024) {
+    K3_RN(2, false, T, ((nch + 1) / 2 + 31) / 32 * 32);
+  } else {
+    K3_RN(4, false, T, ((nch + 3) / 4 + 31) / 32 * 32);
+  }
+#undef K3_RN
   return err == cudaSuccess ? 0 : -1;
 }
 

@@ -67,7 +67,7 @@ def _check(x, r, w, o, eps=EPS):
 
 
 @pytest.mark.parametrize("T,H", [(1, 32), (1, 7168), (3, 64), (2, 160), (37, 7168), (300, 4128), (5, 4096), (4, 8224),
-                                 (3, 16384), (1000, 256), (2, 16352), (700, 2048)])
+                                 (3, 16384), (1000, 256), (13, 224), (2, 16352), (700, 2048)])
 @pytest.mark.parametrize("residual", [True, False])
 def test_rmsnorm(T, H, residual):
     x, r, w = _inputs(T, H, T + H, residual)
