@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll
     for (int r = 0; r < RR; ++r) {
       const unsigned tok = pre.tok + r * kRun;
-      if (r == 0 || !one_page) page[r] = tok < static_cast<unsigned>(pre.n) ? __ldg(row + (tok >> P.page_shift)) : -1;
+      if (r == 0 || !one_page) page[r] = tok < static_cast<unsigned>(pre.n) ? row[tok >> P.page_shift] : -1;
     }
   };
   auto issue = [&](int st) {
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll
         for (int w = 0; w < SP; ++w)
           raw[i * SP + w][t] =
-              r < rows ? __ldg(reinterpret_cast<const uint2 *>(qp + i * (64 / S::ESZ) + 4 * w)) : make_uint2(0, 0);
+              r < rows ? *reinterpret_cast<const uint2 *>(qp + i * (64 / S::ESZ) + 4 * w) : make_uint2(0, 0);
     }
   };
   auto start_item = [&]() {

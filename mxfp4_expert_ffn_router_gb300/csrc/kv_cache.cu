@@ -9,6 +9,9 @@
 // A few neighbouring lanes hold one vector (a token's key or value of one head), 8 or 16 values
 // each; its scale needs one maximum over those lanes.
 //
+// Inputs are read by ordinary loads: a kernel before this one, still running when this one starts, may
+// have written them.
+//
 // Bound: the bytes, once in and once out, with several tokens in flight a thread where there are
 // enough of them: reading 16384 tokens of 8 heads of 128 (101 MB) 17.4 us, 5.8 TB/s (one in flight 22.2
 // us); writing 4096 tokens (25 MB) 4.5 us, of which about 2 are the launch; 13 tokens of 96 heads 1.9 us.
@@ -67,8 +70,8 @@ struct KvReadWork {
 
 template <int D, bool E4M3, int U>
 __global__ void __launch_bounds__(256)
-    kv_write_kernel(KvView c, int n, const uint16_t *__restrict__ k, const uint16_t *__restrict__ v, long long k_stride,
-                    long long v_stride, const int32_t *__restrict__ slots, int32_t *status) {
+    kv_write_kernel(KvView c, int n, const uint16_t *k, const uint16_t *v, long long k_stride,
+                    long long v_stride, const int32_t *slots, int32_t *status) {
   using K = KvTile<D, KvWriteWork<E4M3>::V, U>;
   pdl_wait();
   pdl_trigger();
@@ -84,11 +87,11 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < K::U; ++i) {
     const int t = t0 + i * K::G;
-    slot[i] = t < n ? __ldg(slots + t) : -1;
+    slot[i] = t < n ? slots[t] : -1;
 #pragma unroll
     for (int h = 0; h < K::V / 8; ++h) {
       u[i][h] = make_uint4(0, 0, 0, 0);
-      if (t < n) u[i][h] = __ldg(reinterpret_cast<const uint4 *>(src + t * stride) + h);
+      if (t < n) u[i][h] = *(reinterpret_cast<const uint4 *>(src + t * stride) + h);
     }
   }
 #pragma unroll
@@ -134,8 +137,8 @@ __global__ void __launch_bounds__(256)
 // k_out, v_out: bf16 [n][heads][D].
 template <int D, bool E4M3, int U>
 __global__ void __launch_bounds__(256)
-    kv_read_kernel(KvView c, int n, const int32_t *__restrict__ slots, uint16_t *__restrict__ k_out,
-                   uint16_t *__restrict__ v_out, int32_t *status) {
+    kv_read_kernel(KvView c, int n, const int32_t *slots, uint16_t *k_out,
+                   uint16_t *v_out, int32_t *status) {
   using K = KvTile<D, KvReadWork<E4M3>::V, U>;
   using Word = std::conditional_t<E4M3, uint2, uint4>;  // eight values
   pdl_wait();
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < K::U; ++i) {
     const int t = t0 + i * K::G;
-    slot[i] = t < n ? __ldg(slots + t) : -1;
+    slot[i] = t < n ? slots[t] : -1;
   }
 #pragma unroll
   for (int i = 0; i < K::U; ++i) {

@@ -42,7 +42,7 @@ constexpr int kWarpRows = 8;  // rows of a block where a warp takes one
 // One block per row, or (WARP) one warp: a thread holds CH chunks of 8 values, tid + i * nth of its row.
 template <int CH, bool WARP>
 __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
-    rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *__restrict__ weight, float eps, int T,
+    rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps, int T,
                    int H, uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
   __shared__ __align__(16) float part[16];
   pdl_wait();
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
     if (c < nch) {
       if (residual_out) *(reinterpret_cast<uint4 *>(residual_out + row) + c) = f32x8_to_bf16(a[i]);
       float w[8];
-      bf16x8_to_f32(__ldg(reinterpret_cast<const uint4 *>(weight) + c), w);
+      bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(weight) + c), w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) a[i][q] = a[i][q] * inv * w[q];
       if (y) *(reinterpret_cast<uint4 *>(y + row) + c) = f32x8_to_bf16(a[i]);
