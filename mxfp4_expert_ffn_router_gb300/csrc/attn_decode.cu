@@ -23,7 +23,14 @@
 //    workspace, at most two a block, which attn_join_kernel adds in order.
 //  * Short ones.  The line costs about 10 us whatever the work.  Where no item sees more than
 //    kDirectTokens, a block takes one item and nothing is cut or joined (256 sequences of 900 tokens:
-//    80.9 us against 95.5).  Where there are no more items than SMs, blocks of eight warps take an item
+//    80.9 us against 95.5).  Where items are short and more than such blocks fit the GPU at once, a block is
+//    one warp, eight to an SM: most of the time is starting and ending items, which then overlap, and no
+//    warps are joined.  ONE_WARP is where that stops paying (64 query and 8 key-value heads of 128, E4M3,
+//    128 sequences of 60 tokens: 11.0 us with four warps, 9.4 with one; 250: 20.2 and 18.2; 1000: 50.4 both;
+//    256 of 1000: 87.6 and 111.3, since a warp has two steps in flight at most; 12 query heads a key, 117
+//    sequences of 20: 21.0 and 9.7).  With more query heads a key, or rows of 512 bytes (one block of four
+//    warps to an SM), it pays twice as long (80 sequences of 500 tokens, 64 heads on 8 of 256 in bf16: 60.8
+//    and 55.7).  Where there are no more items than SMs, blocks of eight warps take an item
 //    each, or a cluster of 2, 4 or 8 of them shares it evenly and joins its sums through
 //    distributed shared memory, up to kPartBytes of keys a block (E4M3, 8 heads: 4000 tokens of one
 //    sequence 7.4 us against 11.0 on the line, 16000 14.9 against 15.2, 40000 27.9 against 23.3; 8
@@ -278,8 +285,10 @@ struct AdShape {
   // Stages and blocks per SM: 16 (or 12) warps' loads of 100 to 200 KB in flight per SM.  Blocks of one item
   // each spend more of their time starting and ending, which a third block covers
   static constexpr bool THREE = DIRECT && W == 4 && ROWB <= 256 && NT == 1;
-  static constexpr int STAGES = THREE ? 2 : 3;
-  static constexpr int BLOCKS = THREE ? 3 : ROWB <= 256 && W == 4 ? 2 : 1;
+  static constexpr int STAGES = THREE || W == 1 ? 2 : 3;
+  // Items of at most this many tokens take a warp each (see "Short ones" above)
+  static constexpr int ONE_WARP = (RUN < 32 ? 128 : 256) * NT * (ROWB > 256 ? 2 : 1);
+  static constexpr int BLOCKS = W == 1 ? (ROWB <= 256 ? 8 : 4) : THREE ? 3 : ROWB <= 256 && W == 4 ? 2 : 1;
   // quads that the warps exchange at once where an item ends, each in the stage it has just used
   static constexpr int QR = RR * SUB / 512 < QUADS ? RR * SUB / 512 : QUADS;
   // query fragments: in registers, or from 32 of them on in shared memory (the same for all warps)
@@ -1180,6 +1189,9 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
         return start<D, E4M3, NT, 8, true>(P, items * parts, parts, st) == cudaSuccess ? 0 : -1;
     }
   }
+  if (tokens <= S::ONE_WARP && items < (1LL << 31) &&
+      items > static_cast<long long>(sm_count()) * AdShape<D, E4M3, NT, 4, true>::BLOCKS)
+    return start<D, E4M3, NT, 1, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
   if (tokens <= kDirectTokens && items < (1LL << 31))
     return start<D, E4M3, NT, 4, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
   long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;

@@ -150,6 +150,40 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("fmt", [E4, BF])
+@pytest.mark.parametrize("B,most,Hq,heads,dim,page,window", [
+    (70, 100, 8, 8, 128, 16, 0), (160, 200, 24, 2, 128, 32, 0), (150, 220, 12, 4, 64, 32, 0), (600, 1, 8, 1, 128, 16, 0),
+    (120, 300, 20, 4, 256, 16, 33), (80, 110, 40, 4, 256, 16, 0), (170, 60, 17, 1, 64, 64, 0)])
+def test_many_short_sequences(fmt, B, most, Hq, heads, dim, page, window):
+    """More short items than the GPU holds at once: each is one warp's."""
+    lens = np.random.default_rng(B).integers(0, most + 1, B)
+    lens[:2] = most, 0
+    c = Case(lens.tolist(), Hq, heads, dim, page, fmt, seed=dim + Hq)
+    c.check(*c.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("fmt", [E4, BF])
+def test_many_short_sequences_with_bad_pages(fmt):
+    c = Case([70, 100, 90] + [40] * 120, 8, 4, 128, 16, fmt, seed=21)
+    good, good_lse = c.run()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for bad in (-1, c.cache.pages, 2 ** 31 - 1):
+        table = c.table.copy()
+        table[2, 5] = bad  # its last page: places 80 to 89
+        st.zero_()
+        out, lse = c.run(table=table, status=st)
+        assert int(st.item()) == k3.K3MOE_DEV_BOUNDS
+        short, short_lse = c.run(lens=[70, 100, 80] + [40] * 120)
+        torch.testing.assert_close(out[2].float(), short[2].float(), rtol=2.0 ** -7, atol=1e-3)
+        torch.testing.assert_close(lse[2], short_lse[2], rtol=2.0 ** -18, atol=2.0 ** -18)
+        out[2], lse[2] = good[2], good_lse[2]
+        assert torch.equal(out, good) and torch.equal(lse, good_lse)
+    st.zero_()
+    out, lse = c.run(lens=[-5, 100, 2 ** 31 - 1] + [40] * 120, status=st)
+    assert int(st.item()) == k3.K3MOE_DEV_BOUNDS and not out[0].float().any() and torch.isinf(lse[0]).all()
+    assert torch.equal(out[1], good[1]) and torch.equal(out[3:], good[3:])
+
+
+@pytest.mark.parametrize("fmt", [E4, BF])
 def test_everything_empty(fmt):
     c = Case([0, 0, 0], 8, 2, 128, 16, fmt)
     c.check(*c.run())
