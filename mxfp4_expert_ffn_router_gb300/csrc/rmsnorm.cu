@@ -10,10 +10,10 @@
 // tree: a thread's values in order, a butterfly over the warp, a tree over the warps.
 //
 // Bound: the rows' bytes, 9 of them a value with every output.  A block has one row in registers,
-// read once; four blocks an SM (32 registers a thread) overlap one row's reduction with the others'
-// loads: 4096 rows of 7168 with both outputs (265 MB) 42.5 us, 6.2 TB/s of 6.8 measured for a copy,
+// read once; four blocks an SM (32 registers a thread, many rows) overlap one row's reduction with the others'
+// loads: 4096 rows of 7168 with both outputs (265 MB) 43.4 us, 6.1 TB/s of 6.8 measured for a copy,
 // against 46.2 us at 38 registers (three blocks) and 48 us for a persistent block that loads its next
-// row early.  One row: 2.5 us, the launch and two trips to memory.
+// row early.  One row: 2.3 us, the launch and two trips to memory.
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
@@ -40,8 +40,9 @@ constexpr int kWarpRows = 8;  // rows of a block where a warp takes one
 }  // namespace
 
 // One block per row, or (WARP) one warp: a thread holds CH chunks of 8 values, tid + i * nth of its row.
-template <int CH, bool WARP>
-__global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
+// FEW: at most 4 / CH rows an SM.
+template <int CH, bool WARP, bool FEW>
+__global__ void __launch_bounds__(512, FEW ? 1 : CH <= 2 ? 4 : 2)
     rmsnorm_kernel(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float eps, int T,
                    int H, uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales) {
   __shared__ __align__(16) float part[16];
@@ -53,6 +54,21 @@ __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
   const size_t row = static_cast<size_t>(r_at) * H;
   float a[CH][8];
   float sum = 0.f;
+  // Few rows: the weights are loaded beside x, at 37 to 76 registers a thread (37 rows of 7168 2.55 us against 2.9,
+  // 300 3.3 against 4.0, but 600 7.1 against 6.8).  Many: only brought near (4096 rows of 16384 108.4 us, 110.3 without)
+  constexpr bool kEarly = FEW || WARP;
+  uint4 wr[kEarly ? CH : 1];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * nth;
+    if (c < nch) {
+      const uint4 *const wp = reinterpret_cast<const uint4 *>(weight) + c;
+      if constexpr (kEarly)
+        wr[i] = *wp;
+      else
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(wp));
+    }
+  }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nth;
@@ -96,7 +112,10 @@ __global__ void __launch_bounds__(512, CH <= 2 ? 4 : 2)
     if (c < nch) {
       if (residual_out) *(reinterpret_cast<uint4 *>(residual_out + row) + c) = f32x8_to_bf16(a[i]);
       float w[8];
-      bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(weight) + c), w);
+      if constexpr (kEarly)
+        bf16x8_to_f32(wr[i], w);
+      else
+        bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(weight) + c), w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) a[i][q] = a[i][q] * inv * w[q];
       if (y) *(reinterpret_cast<uint4 *>(y + row) + c) = f32x8_to_bf16(a[i]);
@@ -118,18 +137,24 @@ int launch_rmsnorm(int T, int H, const uint16_t *x, const uint16_t *residual, co
                    uint16_t *residual_out, uint16_t *y, uint8_t *codes, uint8_t *scales, cudaStream_t st) {
   const int nch = H / 8;  // at most 2048
   cudaError_t err;
-#define K3_RN(CH_, WARP_, GRID_, BLOCK_)                                                                             \
-  err = launch_pdl(rmsnorm_kernel<CH_, WARP_>, dim3(GRID_), dim3(BLOCK_), 0, st, x, residual, weight, eps, T, H, \
+#define K3_RN(CH_, WARP_, FEW_, GRID_, BLOCK_)                                                                             \
+  err = launch_pdl(rmsnorm_kernel<CH_, WARP_, FEW_>, dim3(GRID_), dim3(BLOCK_), 0, st, x, residual, weight, eps, T, H, \
                    residual_out, y, codes, scales)
+#define K3_RN_ROW(CH_)                                        \
+  if (T <= 4 / CH_ * sm_count())                              \
+    K3_RN(CH_, false, true, T, ((nch + CH_ - 1) / CH_ + 31) / 32 * 32); \
+  else                                                        \
+    K3_RN(CH_, false, false, T, ((nch + CH_ - 1) / CH_ + 31) / 32 * 32)
   if (nch <= 32) {  // a row is one chunk a lane: 4096 rows of 256 2.5 us, one block each 4.8
-    K3_RN(1, true, (static_cast<unsigned>(T) + kWarpRows - 1) / kWarpRows, 32 * kWarpRows);
+    K3_RN(1, true, false, (static_cast<unsigned>(T) + kWarpRows - 1) / kWarpRows, 32 * kWarpRows);
   } else if (nch <= 512) {
-    K3_RN(1, false, T, (nch + 31) / 32 * 32);
+    K3_RN_ROW(1);
   } else if (nch <= 1024) {
-    K3_RN(2, false, T, ((nch + 1) / 2 + 31) / 32 * 32);
+    K3_RN_ROW(2);
   } else {
-    K3_RN(4, false, T, ((nch + 3) / 4 + 31) / 32 * 32);
+    K3_RN_ROW(4);
   }
+#undef K3_RN_ROW
 #undef K3_RN
   return err == cudaSuccess ? 0 : -1;
 }
