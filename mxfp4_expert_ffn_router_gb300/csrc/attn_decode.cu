@@ -25,16 +25,24 @@
 //    kDirectTokens, a block takes one item and nothing is cut or joined (256 sequences of 900 tokens:
 //    80.9 us against 95.5).  Where items are short and more than such blocks fit the GPU at once, a block is
 //    one warp, eight to an SM: most of the time is starting and ending items, which then overlap, and no
-//    warps are joined.  ONE_WARP is where that stops paying (64 query and 8 key-value heads of 128, E4M3,
+//    warps are joined.  kOneWarp is where that stops paying (64 query and 8 key-value heads of 128, E4M3,
 //    128 sequences of 60 tokens: 11.0 us with four warps, 9.4 with one; 250: 20.2 and 18.2; 1000: 50.4 both;
 //    256 of 1000: 87.6 and 111.3, since a warp has two steps in flight at most; 12 query heads a key, 117
 //    sequences of 20: 21.0 and 9.7).  With more query heads a key, or rows of 512 bytes (one block of four
 //    warps to an SM), it pays twice as long (80 sequences of 500 tokens, 64 heads on 8 of 256 in bf16: 60.8
-//    and 55.7).  Where there are no more items than SMs, blocks of eight warps take an item
+//    and 55.7).  Where there are no more items than SMs, blocks of eight warps (rows of 512 bytes: four) take an item
 //    each, or a cluster of 2, 4 or 8 of them shares it evenly and joins its sums through
 //    distributed shared memory, up to kPartBytes of keys a block (E4M3, 8 heads: 4000 tokens of one
 //    sequence 7.4 us against 11.0 on the line, 16000 14.9 against 15.2, 40000 27.9 against 23.3; 8
-//    sequences of 3000 14.4 against 18.1).
+//    sequences of 3000 14.4 against 18.1; 2 of 2000, 32 heads on 4 of 256 in bf16, 8.5 against 11.9).
+//  * More than 8 query heads a key.  16 of them share an item (NT = 2), so that the cache is read once.  Where
+//    the call is so short that a warp's own chain of instructions is what takes the time, each 8 take an
+//    item of their own and read the keys again through L2: 128 heads on 8, E4M3, one sequence of 60 tokens
+//    5.2 against 3.6 us, of 1000 8.6 and 6.6; 25 sequences of 250 8.8 and 7.2.  That holds as long as the
+//    twice as many items run at once; past kDirectTokens only if their clusters are no smaller (64 heads on 4 of
+//    256, bf16, 4000 tokens: 15.4 and 11.7; 30 sequences of 3000, 16 heads on one of 64: 8.0 and 9.6), and
+//    where 16 heads' items would each have an SM but 8 heads' would not, up to kSplitTokens (15 sequences of
+//    250, 128 heads on 8 of 128: 7.6 and 6.9, of 1000 13.1 and 15.7).
 //  * Loads.  Each warp streams every fourth (eighth) run of 16 RR tokens through a ring
 //    of its own in shared memory with 16-byte cp.async (stages - 1 runs ahead, across items),
 //    so no warp waits for another except where an item ends.  16 tokens from a multiple of
@@ -76,6 +84,7 @@ namespace {
 
 constexpr int kRun = 16;                 // tokens of a product
 constexpr int kDirectTokens = 1024;      // items that see at most this many are never cut
+constexpr int kSplitTokens = 256;        // (see "More than 8 query heads" above)
 constexpr long long kPartBytes = 256 << 10;  // most bytes of keys that one of eight-warp blocks takes
 constexpr int kMinTokens = 256;          // smallest piece of a block
 constexpr int kUnitLen = 4;              // length of a unit on the line
@@ -286,8 +295,6 @@ struct AdShape {
   // each spend more of their time starting and ending, which a third block covers
   static constexpr bool THREE = DIRECT && W == 4 && ROWB <= 256 && NT == 1;
   static constexpr int STAGES = THREE || W == 1 ? 2 : 3;
-  // Items of at most this many tokens take a warp each (see "Short ones" above)
-  static constexpr int ONE_WARP = (RUN < 32 ? 128 : 256) * NT * (ROWB > 256 ? 2 : 1);
   static constexpr int BLOCKS = W == 1 ? (ROWB <= 256 ? 8 : 4) : THREE ? 3 : ROWB <= 256 && W == 4 ? 2 : 1;
   // quads that the warps exchange at once where an item ends, each in the stage it has just used
   static constexpr int QR = RR * SUB / 512 < QUADS ? RR * SUB / 512 : QUADS;
@@ -295,7 +302,8 @@ struct AdShape {
   static constexpr int QREGS = D / 16 * 2 * NT;
   static constexpr int QSMEM = QREGS >= 32 ? QREGS * 32 * 4 : 0;
   // what a cluster's blocks show one another: their sums and statistics
-  static constexpr int SHOWN = W == 8 ? QUADS * 512 + 8 * NT * 16 : 0;
+  static constexpr bool CLUSTER = DIRECT && W == (ROWB <= 256 ? 8 : 4);
+  static constexpr int SHOWN = CLUSTER ? QUADS * 512 + 8 * NT * 16 : 0;
   static constexpr int SMEM = W * STAGES * RR * (SUB + SCALES) + QSMEM + SHOWN + 128;
 };
 
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   int part = 0, parts = 1;  // of an item that a cluster's blocks share
   long long from = 0, to = 1LL << 62, share = 0;
   if constexpr (DIRECT) {
-    if constexpr (W == 8) parts = cluster_size(), part = cluster_rank();
+    if constexpr (S::CLUSTER) parts = cluster_size(), part = cluster_rank();
     const int block = blockIdx.x / parts;
     cur.b = block / items;
     const int item = block - cur.b * items;
@@ -592,7 +600,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   uint32_t qf[QS ? 1 : QN][QW];
   uint4 *const q_sm = reinterpret_cast<uint4 *>(smem + W * ST * RR * (S::SUB + S::SCALES));
   float4 *const shown = reinterpret_cast<float4 *>(smem + W * ST * RR * (S::SUB + S::SCALES) + S::QSMEM);
-  float4 *const shown_stat = shown + S::QUADS * 32;  // (W == 8)
+  float4 *const shown_stat = shown + S::QUADS * 32;  // (CLUSTER)
   uint2 raw[D / 16][NT];
   // of query heads 8 t + 2c + x: the scale of a raw score (in powers of two), the running maxima and l
   float sq[NT][2], o[NT][MM][4], mrun[NT][2], m_l[NT][2], l[NT][2];
@@ -978,7 +986,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   }
   cp_wait<0>();
   if constexpr (!DIRECT) zero_rows();
-  if constexpr (W == 8) {
+  if constexpr (S::CLUSTER) {
     if (parts > 1) {  // join the cluster's blocks: each takes every parts-th quad
       if (first_item) {  // (nothing came of the loop: an empty part)
         for (int i = tid; i < S::QUADS * 32; i += THREADS) shown[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1165,7 +1173,7 @@ int clusters_at_once(const AdParams &P, int parts) {
   static int known[9];  // + 1
   if (!known[parts]) {
     int n = 0;
-    if (start<D, E4M3, NT, 8, true>(P, 0, parts, nullptr, &n) != cudaSuccess) {
+    if (start<D, E4M3, NT, AdShape<D, E4M3, NT, 4, true>::CLUSTER ? 4 : 8, true>(P, 0, parts, nullptr, &n) != cudaSuccess) {
       cudaGetLastError();  // leave no error behind
       n = 0;
     }
@@ -1174,22 +1182,52 @@ int clusters_at_once(const AdParams &P, int parts) {
   return known[parts] - 1;
 }
 
+// Items of at most 8 NT query heads, and the most tokens that one can see.
+long long items_of(const AdParams &P) { return static_cast<long long>(P.B) * P.heads * P.groups; }
+long long tokens_of(const AdParams &P) {
+  const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
+  return P.window > 0 && P.window < visible ? P.window : visible;
+}
+
+// No more items than SMs: how many blocks share one, 0 where there are more or they are too long for that.
+template <int D, bool E4M3, int NT>
+int few_parts(const AdParams &P) {
+  using S = AdShape<D, E4M3, NT, 4, false>;
+  const long long items = items_of(P), tokens = tokens_of(P);
+  if (items > sm_count()) return 0;
+  int parts = 1;
+  if (tokens > 4LL * S::UNIT)  // (one more step costs less than a cluster's join up to here)
+    while (parts < 8 && tokens > 2LL * S::UNIT * parts && items <= clusters_at_once<D, E4M3, NT>(P, 2 * parts)) parts *= 2;
+  return tokens * S::ROWB <= kPartBytes * parts ? parts : 0;
+}
+
+template <int D, bool E4M3, int NT>
+int launch_few(const AdParams &P, int parts, cudaStream_t st) {
+  using S = AdShape<D, E4M3, NT, 4, false>;
+  constexpr int CW = S::ROWB <= 256 ? 8 : 4;  // warps of a cluster's block (rows of 512 bytes: the stages of eight do not fit)
+  const long long items = items_of(P);
+  const cudaError_t e = tokens_of(P) <= S::UNIT ? start<D, E4M3, NT, 4, true>(P, items, 1, st)
+                                                : start<D, E4M3, NT, CW, true>(P, items * parts, parts, st);
+  return e == cudaSuccess ? 0 : -1;
+}
+
 template <int D, bool E4M3, int NT>
 int launch_attn(const AdParams &P, cudaStream_t st) {
   using S = AdShape<D, E4M3, NT, 4, false>;
-  const long long items = static_cast<long long>(P.B) * P.heads * P.groups;
-  const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;  // most tokens an item can have
-  const long long tokens = P.window > 0 && P.window < visible ? P.window : visible;
-  if constexpr (S::ROWB <= 256) {  // (beyond, the stages of eight warps do not fit)
-    if (items <= sm_count() && tokens > S::UNIT) {
-      int parts = 1;
-      if (tokens > 4LL * S::UNIT)  // (one more step costs less than a cluster's join up to here)
-        while (parts < 8 && tokens > 2LL * S::UNIT * parts && items <= clusters_at_once<D, E4M3, NT>(P, 2 * parts)) parts *= 2;
-      if (tokens * S::ROWB <= kPartBytes * parts)
-        return start<D, E4M3, NT, 8, true>(P, items * parts, parts, st) == cudaSuccess ? 0 : -1;
-    }
+  const long long items = items_of(P), tokens = tokens_of(P);
+  const int parts = few_parts<D, E4M3, NT>(P);
+  if constexpr (NT == 2) {
+    AdParams Q = P;
+    Q.groups = (P.G + 7) / 8;
+    const int split = few_parts<D, E4M3, 1>(Q);
+    if (split && (split >= parts || tokens <= kDirectTokens)) return launch_few<D, E4M3, 1>(Q, split, st);
+    if (tokens <= (parts ? kSplitTokens : kDirectTokens) &&
+        items_of(Q) <= static_cast<long long>(sm_count()) * AdShape<D, E4M3, 1, 4, true>::BLOCKS)
+      return start<D, E4M3, 1, 4, true>(Q, items_of(Q), 1, st) == cudaSuccess ? 0 : -1;
   }
-  if (tokens <= S::ONE_WARP && items < (1LL << 31) &&
+  if (parts) return launch_few<D, E4M3, NT>(P, parts, st);
+  constexpr int kOneWarp = (S::RUN < 32 ? 128 : 256) * NT * (S::ROWB > 256 ? 2 : 1);  // most tokens of a warp's item
+  if (tokens <= kOneWarp && items < (1LL << 31) &&
       items > static_cast<long long>(sm_count()) * AdShape<D, E4M3, NT, 4, true>::BLOCKS)
     return start<D, E4M3, NT, 1, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
   if (tokens <= kDirectTokens && items < (1LL << 31))

@@ -152,10 +152,23 @@ def test_many_sequences():
 @pytest.mark.parametrize("fmt", [E4, BF])
 @pytest.mark.parametrize("B,most,Hq,heads,dim,page,window", [
     (70, 100, 8, 8, 128, 16, 0), (160, 200, 24, 2, 128, 32, 0), (150, 220, 12, 4, 64, 32, 0), (600, 1, 8, 1, 128, 16, 0),
-    (120, 300, 20, 4, 256, 16, 33), (80, 110, 40, 4, 256, 16, 0), (170, 60, 17, 1, 64, 64, 0)])
+    (120, 300, 20, 4, 256, 16, 33), (80, 110, 40, 4, 256, 16, 0), (170, 60, 17, 1, 64, 64, 0), (300, 60, 16, 1, 128, 16, 0),
+    (300, 60, 16, 1, 256, 16, 0)])
 def test_many_short_sequences(fmt, B, most, Hq, heads, dim, page, window):
     """More short items than the GPU holds at once: each is one warp's."""
     lens = np.random.default_rng(B).integers(0, most + 1, B)
+    lens[:2] = most, 0
+    c = Case(lens.tolist(), Hq, heads, dim, page, fmt, seed=dim + Hq)
+    c.check(*c.run(window=window), window=window)
+
+
+@pytest.mark.parametrize("fmt", [E4, BF])
+@pytest.mark.parametrize("B,most,Hq,heads,dim,page,window", [
+    (30, 3000, 16, 1, 64, 32, 0), (30, 1500, 11, 1, 256, 16, 0), (4, 1800, 18, 2, 256, 64, 0), (25, 200, 130, 10, 64, 16, 0),
+    (20, 700, 40, 4, 128, 32, 300), (3, 3900, 6, 2, 256, 32, 0), (19, 240, 128, 8, 64, 128, 0), (2, 40, 27, 3, 256, 16, 0)])
+def test_few_sequences_of_shared_heads(fmt, B, most, Hq, heads, dim, page, window):
+    """Up to one item an SM or little more, with more than 8 query heads a key: split by 8 or shared by 16."""
+    lens = np.random.default_rng(B + most).integers(0, most + 1, B)
     lens[:2] = most, 0
     c = Case(lens.tolist(), Hq, heads, dim, page, fmt, seed=dim + Hq)
     c.check(*c.run(window=window), window=window)
