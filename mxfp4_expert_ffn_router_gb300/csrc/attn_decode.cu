@@ -34,7 +34,8 @@
 //    each, or a cluster of 2, 4 or 8 of them shares it evenly and joins its sums through
 //    distributed shared memory, up to kPartBytes of keys a block (E4M3, 8 heads: 4000 tokens of one
 //    sequence 7.4 us against 11.0 on the line, 16000 14.9 against 15.2, 40000 27.9 against 23.3; 8
-//    sequences of 3000 14.4 against 18.1; 2 of 2000, 32 heads on 4 of 256 in bf16, 8.5 against 11.9).
+//    sequences of 3000 14.4 against 18.1; 2 of 2000, 32 heads on 4 of 256 in bf16, 8.5 against 11.9; one of
+//    200, 64 on 8 of 256, 5.7 in clusters of 4 and 6.9 without).
 //  * More than 8 query heads a key.  16 of them share an item (NT = 2), so that the cache is read once.  Where
 //    the call is so short that a warp's own chain of instructions is what takes the time, each 8 take an
 //    item of their own and read the keys again through L2: 128 heads on 8, E4M3, one sequence of 60 tokens
@@ -275,6 +276,10 @@ struct Walk {
   }
 };
 
+// Warps of a block where there are few items (rows of 512 bytes: the stages of eight do not fit)
+template <int D, bool E4M3>
+constexpr int kFewWarps = D * (E4M3 ? 1 : 2) <= 256 ? 8 : 4;
+
 template <int D, bool E4M3, int NT, int W, bool DIRECT>
 struct AdShape {
   static constexpr int ESZ = E4M3 ? 1 : 2;
@@ -302,7 +307,7 @@ struct AdShape {
   static constexpr int QREGS = D / 16 * 2 * NT;
   static constexpr int QSMEM = QREGS >= 32 ? QREGS * 32 * 4 : 0;
   // what a cluster's blocks show one another: their sums and statistics
-  static constexpr bool CLUSTER = DIRECT && W == (ROWB <= 256 ? 8 : 4);
+  static constexpr bool CLUSTER = DIRECT && W == kFewWarps<D, E4M3>;
   static constexpr int SHOWN = CLUSTER ? QUADS * 512 + 8 * NT * 16 : 0;
   static constexpr int SMEM = W * STAGES * RR * (SUB + SCALES) + QSMEM + SHOWN + 128;
 };
@@ -1173,7 +1178,7 @@ int clusters_at_once(const AdParams &P, int parts) {
   static int known[9];  // + 1
   if (!known[parts]) {
     int n = 0;
-    if (start<D, E4M3, NT, AdShape<D, E4M3, NT, 4, true>::CLUSTER ? 4 : 8, true>(P, 0, parts, nullptr, &n) != cudaSuccess) {
+    if (start<D, E4M3, NT, kFewWarps<D, E4M3>, true>(P, 0, parts, nullptr, &n) != cudaSuccess) {
       cudaGetLastError();  // leave no error behind
       n = 0;
     }
@@ -1196,18 +1201,18 @@ int few_parts(const AdParams &P) {
   const long long items = items_of(P), tokens = tokens_of(P);
   if (items > sm_count()) return 0;
   int parts = 1;
-  if (tokens > 4LL * S::UNIT)  // (one more step costs less than a cluster's join up to here)
-    while (parts < 8 && tokens > 2LL * S::UNIT * parts && items <= clusters_at_once<D, E4M3, NT>(P, 2 * parts)) parts *= 2;
+  constexpr long long kStep = S::RUN * kFewWarps<D, E4M3>;  // tokens that a block takes at once
+  if (tokens > 2 * kStep)  // (one more step costs less than a cluster's join up to here)
+    while (parts < 8 && tokens > kStep * parts && items <= clusters_at_once<D, E4M3, NT>(P, 2 * parts)) parts *= 2;
   return tokens * S::ROWB <= kPartBytes * parts ? parts : 0;
 }
 
 template <int D, bool E4M3, int NT>
 int launch_few(const AdParams &P, int parts, cudaStream_t st) {
   using S = AdShape<D, E4M3, NT, 4, false>;
-  constexpr int CW = S::ROWB <= 256 ? 8 : 4;  // warps of a cluster's block (rows of 512 bytes: the stages of eight do not fit)
   const long long items = items_of(P);
   const cudaError_t e = tokens_of(P) <= S::UNIT ? start<D, E4M3, NT, 4, true>(P, items, 1, st)
-                                                : start<D, E4M3, NT, CW, true>(P, items * parts, parts, st);
+                                                : start<D, E4M3, NT, kFewWarps<D, E4M3>, true>(P, items * parts, parts, st);
   return e == cudaSuccess ? 0 : -1;
 }
 
