@@ -26,12 +26,12 @@
 //    80.9 us against 95.5).  Where items are short and more than such blocks fit the GPU at once, a block is
 //    one warp, eight to an SM: most of the time is starting and ending items, which then overlap, and no
 //    warps are joined.  kOneWarp is where that stops paying (64 query and 8 key-value heads of 128, E4M3,
-//    128 sequences of 60 tokens: 11.0 us with four warps, 9.4 with one; 250: 20.2 and 18.2; 1000: 50.4 both;
-//    256 of 1000: 87.6 and 111.3, since a warp has two steps in flight at most; 12 query heads a key, 117
-//    sequences of 20: 21.0 and 9.7).  With more query heads a key, or rows of 512 bytes (one block of four
-//    warps to an SM), it pays twice as long (80 sequences of 500 tokens, 64 heads on 8 of 256 in bf16: 60.8
-//    and 55.7).  Where there are no more items than SMs, blocks of eight warps (rows of 512 bytes: four) take an item
-//    each, or a cluster of 2, 4 or 8 of them shares it evenly and joins its sums through
+//    128 sequences of 60 tokens: 11.0 us with four warps, 9.4 with one; 250: 20.2 and 18.2, but 100 of up to
+//    250 with 96 heads 15.6 and 17.8; 256 of 1000: 87.6 and 111.3, since a warp has two steps in flight at
+//    most).  At rows of 512 bytes, where an SM holds one block of four warps, it pays twice as long (80
+//    sequences of 250 tokens, 64 heads on 8 of 256 in bf16: 38.2 and 31.5).  Where there are no more items
+//    than SMs, blocks of eight warps (rows of 512 bytes: four) take an item each, or a cluster of 2, 4 or 8 of
+//    them shares it evenly and joins its sums through
 //    distributed shared memory, up to kPartBytes of keys a block (E4M3, 8 heads: 4000 tokens of one
 //    sequence 7.4 us against 11.0 on the line, 16000 14.9 against 15.2, 40000 27.9 against 23.3; 8
 //    sequences of 3000 14.4 against 18.1; 2 of 2000, 32 heads on 4 of 256 in bf16, 8.5 against 11.9; one of
@@ -297,8 +297,10 @@ struct AdShape {
   static constexpr int SUB = 2 * KB;              // keys and values of 16 tokens; a multiple of 128: words swizzle by xor
   static constexpr int SCALES = E4M3 ? 32 : 0;    // scale bytes of 16 tokens, after all stages
   // Stages and blocks per SM: 16 (or 12) warps' loads of 100 to 200 KB in flight per SM.  Blocks of one item
-  // each spend more of their time starting and ending, which a third block covers
-  static constexpr bool THREE = DIRECT && W == 4 && ROWB <= 256 && NT == 1;
+  // each spend more of their time starting and ending, which a third block covers (256 sequences of 1000 tokens,
+  // 128 heads on 8, E4M3: 122.8 us with two, 104.3 with three); on the line it costs more in spilled registers and
+  // shorter rings than it brings (32 of 8000 in bf16: 169 and 180)
+  static constexpr bool THREE = DIRECT && W == 4 && ROWB <= 256 && (NT == 1 || D <= 128);
   static constexpr int STAGES = THREE || W == 1 ? 2 : 3;
   static constexpr int BLOCKS = W == 1 ? (ROWB <= 256 ? 8 : 4) : THREE ? 3 : ROWB <= 256 && W == 4 ? 2 : 1;
   // quads that the warps exchange at once where an item ends, each in the stage it has just used
@@ -1231,7 +1233,7 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
       return start<D, E4M3, 1, 4, true>(Q, items_of(Q), 1, st) == cudaSuccess ? 0 : -1;
   }
   if (parts) return launch_few<D, E4M3, NT>(P, parts, st);
-  constexpr int kOneWarp = (S::RUN < 32 ? 128 : 256) * NT * (S::ROWB > 256 ? 2 : 1);  // most tokens of a warp's item
+  constexpr int kOneWarp = S::ROWB > 256 ? 256 : 128;  // most tokens of a warp's item
   if (tokens <= kOneWarp && items < (1LL << 31) &&
       items > static_cast<long long>(sm_count()) * AdShape<D, E4M3, NT, 4, true>::BLOCKS)
     return start<D, E4M3, NT, 1, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;

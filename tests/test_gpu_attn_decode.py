@@ -153,7 +153,7 @@ def test_many_sequences():
 @pytest.mark.parametrize("B,most,Hq,heads,dim,page,window", [
     (70, 100, 8, 8, 128, 16, 0), (160, 200, 24, 2, 128, 32, 0), (150, 220, 12, 4, 64, 32, 0), (600, 1, 8, 1, 128, 16, 0),
     (120, 300, 20, 4, 256, 16, 33), (80, 110, 40, 4, 256, 16, 0), (170, 60, 17, 1, 64, 64, 0), (300, 60, 16, 1, 128, 16, 0),
-    (300, 60, 16, 1, 256, 16, 0)])
+    (300, 60, 16, 1, 256, 16, 0), (250, 60, 17, 1, 64, 64, 0), (250, 100, 24, 2, 128, 16, 0), (240, 100, 12, 4, 64, 16, 50)])
 def test_many_short_sequences(fmt, B, most, Hq, heads, dim, page, window):
     """More short items than the GPU holds at once: each is one warp's."""
     lens = np.random.default_rng(B).integers(0, most + 1, B)
