@@ -388,7 +388,8 @@ int k3moe_kv_read(const k3moe_kv_cache *cache, int32_t n, const int32_t *slots, 
  * not used, whatever it holds.
  *   q           : bf16; sequence b's [Hq][dim] starts q_stride * b values in (q_stride >=
  *                 Hq * dim, a multiple of 8), 16-byte aligned
- *   block_table : int32 [B][max_pages]; entries past a sequence's length are not read
+ *   block_table : int32 [B][max_pages]; entries past a sequence's length, and of pages that
+ *                 lie wholly before its window, are not read
  *   seq_lens    : int32 [B]; negative counts as 0 and more than max_pages * page_size as
  *                 that, both with K3MOE_DEV_BOUNDS
  *   scale       : finite (commonly dim^-1/2)

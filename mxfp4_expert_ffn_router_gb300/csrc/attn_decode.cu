@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   const uint8_t *const klane = P.k + lane * 16, *const vlane = P.v + lane * 16;
   const unsigned place = (1u << P.page_shift) - 1u, page_vecs = static_cast<unsigned>(P.heads) << P.page_shift;
   Walk<RUN, UNIT, S::ITEM_LEN> pre = cur;
-  uint32_t bad = 0;    // bit st RR + r: a page number outside the cache
+  uint32_t bad = 0;    // bit st RR + r: 16 tokens that were not loaded: before the window, or a page outside the cache
   // a run starts at a multiple of RUN and lies in one page if pages are no smaller
   const bool one_page = (RUN - 1u) <= place;
   int page[RR];
@@ -532,7 +532,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll
     for (int r = 0; r < RR; ++r) {
       const unsigned tok = pre.tok + r * kRun;
-      if (r == 0 || !one_page) page[r] = tok < static_cast<unsigned>(pre.n) ? row[tok >> P.page_shift] : -1;
+      // a run that lies in one page begins at most RUN - 1 places before the window, and needs that page.  Tiles that
+      // lie in pages of their own may all be before it: those pages may have been given back, and are not looked up
+      const bool seen = tok < static_cast<unsigned>(pre.n) && (one_page || tok + kRun > static_cast<unsigned>(pre.lo));
+      if (r == 0 || !one_page) page[r] = seen ? row[tok >> P.page_shift] : -1;
     }
   };
   auto issue = [&](int st) {
@@ -565,6 +568,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
           const unsigned tok = pre.tok + r * kRun;
           const int tile = st * RR + r, pg = one_page ? page[0] : page[r];
           if (tok >= static_cast<unsigned>(pre.n)) break;
+          if (tok + kRun <= static_cast<unsigned>(pre.lo)) {
+            bad |= 1u << tile;
+            continue;
+          }
           if (static_cast<unsigned>(pg) >= static_cast<unsigned>(P.pages)) {
             bad |= 1u << tile;
             if (lane == 0) set_status(P.status, K3MOE_DEV_BOUNDS);
@@ -841,7 +848,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         }
       }
       // O^T: rows g and g + 8 of product m are this lane's dimensions 2m and 2m + 1.  16 tokens that are
-      // not seen at all (past the end, or of a bad page) were not loaded and are left out
+      // not seen at all (past the end, before the window, or of a bad page) were not loaded and are left out
 #pragma unroll
       for (int r = 0; r < RR; ++r) {
         if (r > 0 && cur.tok + r * kRun >= static_cast<unsigned>(cur.n)) break;
