@@ -16,6 +16,8 @@ a CUDA graph: tables, lengths and slots are read on the device.
 """
 from __future__ import annotations
 
+from collections import Counter
+
 import torch
 
 from . import (K3MOE_FFN_AUTO, K3MOE_KV_E4M3, K3MOE_OP_BUCKET, K3MOE_OP_EXPERT_FFN, KVCache, Shape, Weights,
@@ -38,14 +40,22 @@ class PageTable:
 
     def append(self, which, count: int = 1) -> torch.Tensor:
         """Make room for ``count`` new tokens of each sequence in ``which``; their slots, int32
-        [len(which) * count], in order.  The lengths include them from here on."""
+        [len(which) * count], in order.  The lengths include them from here on.  RuntimeError where they do
+        not all fit: then nothing has changed, and the call can be made again once pages have come back."""
+        which = list(which)
+        need = 0
+        for b, times in Counter(which).items():
+            pages = -(-(self.lens[b] + count * times) // self.page_size)
+            if pages > self.max_pages:
+                raise RuntimeError(f"sequence {b} would need {pages} pages of at most {self.max_pages}")
+            need += pages - len(self.owned[b])
+        if need > len(self.free):
+            raise RuntimeError(f"no page left: {need} needed, {len(self.free)} free")
         slots = []
         for b in which:
             for _ in range(count):
                 place = self.lens[b] % self.page_size
                 if place == 0:
-                    if not self.free or len(self.owned[b]) == self.max_pages:
-                        raise RuntimeError("no page left")
                     self.owned[b].append(self.free.pop())
                 slots.append(self.owned[b][-1] * self.page_size + place)
                 self.lens[b] += 1
