@@ -400,8 +400,8 @@ def k3moe_rmsnorm(x, weight, eps, residual=None, residual_out=None, y=None, code
     if _fast is not None:
         rc = _fast.rmsnorm(x, weight, eps, residual, residual_out, y, codes, scales,
                            None if stream is None else stream.cuda_stream)
-        if rc == 0:
-            return
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_rmsnorm", rc)
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x: expected a tensor [T, H]")
     shape = x.shape
@@ -456,8 +456,8 @@ def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
     the cache's slots [n] (int32, page * page_size + place; negative = padding)."""
     if _fast is not None:
         rc = _fast.kv_write(cache._addr, k, v, slots, dev_status, None if stream is None else stream.cuda_stream)
-        if rc == 0:
-            return
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_kv_write", rc)
     shape = (slots.numel(), cache.heads, cache.dim)
     kp, ks = _rows(k, shape, "k")
     vp, vs = _rows(v, shape, "v")
@@ -472,8 +472,8 @@ def k3moe_kv_read(cache: KVCache, slots, k, v, dev_status=None, stream=None):
     for a negative slot)."""
     if _fast is not None:
         rc = _fast.kv_read(cache._addr, slots, k, v, dev_status, None if stream is None else stream.cuda_stream)
-        if rc == 0:
-            return
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_kv_read", rc)
     shape = (slots.numel(), cache.heads, cache.dim)
     rc = lib().k3moe_kv_read(cache._ref, shape[0], _in(slots, _I32, shape[:1], "slots"), _in(k, _BF16, shape, "k"),
                              _in(v, _BF16, shape, "v"), _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
@@ -495,8 +495,8 @@ def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, s
         rc = _fast.attn_decode(cache._addr, q, block_table, seq_lens, out, lse,
                                cache.dim ** -0.5 if scale is None else scale, window, ws, dev_status,
                                None if stream is None else stream.cuda_stream)
-        if rc == 0:
-            return
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_attn_decode", rc)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q: expected a tensor [B, Hq, dim]")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
