@@ -506,7 +506,8 @@ def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, s
     qp, qs = _rows(q, shape, "q")
     pages = block_table.shape[1]
     rc = lib().k3moe_attn_decode(cache._ref, B, Hq, qp, qs, _in(block_table, _I32, (B, pages), "block_table"), pages,
-                                 _in(seq_lens, _I32, (B,), "seq_lens"), window,
+                                 # (ctypes would keep the low 32 bits: no length is larger, and no window below 0 is allowed)
+                                 _in(seq_lens, _I32, (B,), "seq_lens"), max(-1, min(window, 0x7FFFFFFF)),
                                  cache.dim ** -0.5 if scale is None else scale, _in(out, _BF16, shape, "out"),
                                  _in(lse, _F32, (B, Hq), "lse"), _ptr(ws, None, "ws"),
                                  ws.nbytes if ws is not None else 0, _ptr(dev_status, torch.int32, "dev_status"),
