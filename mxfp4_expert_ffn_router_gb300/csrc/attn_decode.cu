@@ -322,9 +322,9 @@ __device__ __forceinline__ int quad_dim(int m, int g) {
   return D / PER >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
 }
 
-// Two neighbouring dimensions of a row, times f (0: a row without weight, whatever the sums are).
-__device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float b, bool on) {
-  if (on) *reinterpret_cast<uint32_t *>(p) = f == 0.f ? 0u : pack2<false>(a * f, b * f);
+// Two neighbouring dimensions of a row, times f; zeros for a row without weight, whatever the sums are.
+__device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float b, bool weight, bool on) {
+  if (on) *reinterpret_cast<uint32_t *>(p) = weight ? pack2<false>(a * f, b * f) : 0u;
 }
 
 // Adds N parts of a quad: statistics s (m', m, l) of this lane's two rows, sums u at m'.
@@ -359,14 +359,15 @@ __device__ __forceinline__ void store_quad(const AdParams &P, int b, int h0, int
   float fin[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
-    const float mb = mt[x] == -INFINITY ? 0.f : mt[x], pb = mp[x] == -INFINITY ? 0.f : mp[x];
-    fin[x] = lt[x] == 0.f ? 0.f : __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt[x]);
+    // (no m' beside an m: every value is NaN, and so are the sums)
+    const float mb = mt[x] == -INFINITY ? 0.f : mt[x], pb = mp[x] == -INFINITY ? mb : mp[x];
+    fin[x] = __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt[x]);
     if (P.lse && m == 0 && g == 0 && r0 + x < rows)
       P.lse[static_cast<size_t>(b) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
   }
   uint16_t *op = P.out + (static_cast<size_t>(b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
-  store_row2(op, fin[0], v.x, v.z, r0 < rows);
-  store_row2(op + D, fin[1], v.y, v.w, r0 + 1 < rows);
+  store_row2(op, fin[0], v.x, v.z, lt[0] != 0.f, r0 < rows);
+  store_row2(op + D, fin[1], v.y, v.w, lt[1] != 0.f, r0 + 1 < rows);
 }
 
 // ---- thread-block clusters
