@@ -322,9 +322,9 @@ __device__ __forceinline__ int quad_dim(int m, int g) {
   return D / PER >= 8 ? (g + 8 * (dl / PER)) * PER + dl % PER : g * 8 + dl;
 }
 
-// Two neighbouring dimensions of a row, times f; zeros for a row without weight, whatever the sums are.
-__device__ __forceinline__ void store_row2(uint16_t *p, float f, float a, float b, bool weight, bool on) {
-  if (on) *reinterpret_cast<uint32_t *>(p) = weight ? pack2<false>(a * f, b * f) : 0u;
+// Two neighbouring dimensions of a row, times f and up; zeros for a row without weight, whatever the sums are.
+__device__ __forceinline__ void store_row2(uint16_t *p, float f, float up, float a, float b, bool weight, bool on) {
+  if (on) *reinterpret_cast<uint32_t *>(p) = weight ? pack2<false>(a * f * up, b * f * up) : 0u;
 }
 
 // Adds N parts of a quad: statistics s (m', m, l) of this lane's two rows, sums u at m'.
@@ -351,23 +351,26 @@ __device__ __forceinline__ void add_parts(const float4 (&s)[N][2], const float4 
   }
 }
 
-// Writes a quad of rows that are complete: out = O' 2^(m' - m - 14) / l, and with the first quad lse.
+// Writes a quad of rows that are complete: out = (O' 2^-14 / l) 2^(m' - m), and with the first quad lse.  m' - m is -127
+// to 127, as V's scales are, so that one factor of both would leave fp32's normal numbers where V is tiny (but for
+// the rounding of sums past 2^24, which must not make it infinite).
 template <int D, bool E4M3>
 __device__ __forceinline__ void store_quad(const AdParams &P, int b, int h0, int rows, int t, int m, const float4 &v,
                                            const float (&mp)[2], const float (&mt)[2], const float (&lt)[2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, r0 = 8 * t + 2 * (lane & 3);
-  float fin[2];
+  float fin[2], up[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     // (no m' beside an m: every value is NaN, and so are the sums)
     const float mb = mt[x] == -INFINITY ? 0.f : mt[x], pb = mp[x] == -INFINITY ? mb : mp[x];
-    fin[x] = __fdividef(exp2f(pb - mb - (E4M3 ? 14.f : 0.f)), lt[x]);
+    fin[x] = __fdividef(E4M3 ? 0x1p-14f : 1.f, lt[x]);
+    up[x] = E4M3 ? exp2f(fminf(pb - mb, 127.f)) : 1.f;
     if (P.lse && m == 0 && g == 0 && r0 + x < rows)
       P.lse[static_cast<size_t>(b) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
   }
   uint16_t *op = P.out + (static_cast<size_t>(b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
-  store_row2(op, fin[0], v.x, v.z, lt[0] != 0.f, r0 < rows);
-  store_row2(op + D, fin[1], v.y, v.w, lt[1] != 0.f, r0 + 1 < rows);
+  store_row2(op, fin[0], up[0], v.x, v.z, lt[0] != 0.f, r0 < rows);
+  store_row2(op + D, fin[1], up[1], v.y, v.w, lt[1] != 0.f, r0 + 1 < rows);
 }
 
 // ---- thread-block clusters

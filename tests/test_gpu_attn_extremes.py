@@ -45,3 +45,30 @@ def test_rows_without_weight_stay_zeros(lens):
     _query(c, dim)
     out, lse = c.run(scale=1.0)
     assert not out.float().any() and (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("lens", LENGTHS)
+@pytest.mark.parametrize("power", [-100, -118, -124, 100, 117])
+def test_tiny_and_huge_values(lens, power):
+    """Values of 2^power: within the bound that holds for ordinary ones (it is relative to sum p |V|, plus half a step of
+    the bf16 output, 2^-134 at its smallest).  At 2^-124 a vector's scale is at its least, 2^-127."""
+    n, dim = sum(lens), 128
+    v = np.random.default_rng(2).standard_normal((n, 1, dim)) * 2.0 ** power
+    c = Case(lens, 2, 1, dim, 64, E4, seed=3, kv=(ref.bf16_bits(_keys(n, dim, 3.0)), ref.bf16_bits(v)))
+    _query(c, dim)
+    out, lse = c.run(scale=1.0)
+    c.check(out, lse, scale=1.0)
+
+
+@pytest.mark.parametrize("lens", [[300], [3000], [45000]])
+def test_a_sink_of_tiny_values(lens):
+    """One token far above the rest whose values are near 2^-124, the others' ordinary: the output is the sum of both."""
+    n, dim = sum(lens), 128
+    v = np.random.default_rng(4).standard_normal((n, 1, dim))
+    v[n // 3] *= 2.0 ** -124
+    k = _keys(n, dim, 0.0)
+    k[n // 3, 0, 0] = 90.0
+    c = Case(lens, 2, 1, dim, 64, E4, seed=5, kv=(ref.bf16_bits(k), ref.bf16_bits(v)))
+    _query(c, dim)
+    out, lse = c.run(scale=1.0)
+    c.check(out, lse, scale=1.0)
