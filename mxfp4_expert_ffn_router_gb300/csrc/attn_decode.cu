@@ -77,6 +77,7 @@
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
+#include "per_device.h"
 #include "tc_sm103.cuh"
 
 namespace k3moe {
@@ -1151,17 +1152,23 @@ AdPlan plan_of(const k3moe_kv_cache &c, int Hq) {
   return p;
 }
 
+int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 // A launch of `blocks` blocks in clusters of `cluster`; 0 blocks: only how many clusters fit the GPU at once.
 template <int D, bool E4M3, int NT, int W, bool DIRECT>
 cudaError_t start(const AdParams &P, long long blocks, int cluster, cudaStream_t st, int *fit = nullptr) {
   using S = AdShape<D, E4M3, NT, W, DIRECT>;
-  static bool attr = false;
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, W, DIRECT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static PerDevice raised;  // whether the kernel's limit of shared memory is
+  cudaError_t err = cudaSuccess;
+  raised.get(current_device(), [&] {
+    err = cudaFuncSetAttribute(attn_decode_kernel<D, E4M3, NT, W, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               S::SMEM);
+    return err == cudaSuccess ? 1 : -1;
+  });
+  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks ? blocks : cluster));
   cfg.blockDim = dim3(W * 32);
@@ -1188,16 +1195,13 @@ cudaError_t start(const AdParams &P, long long blocks, int cluster, cudaStream_t
 // 64 in clusters of 4 took 10.2).
 template <int D, bool E4M3, int NT>
 int clusters_at_once(const AdParams &P, int parts) {
-  static int known[9];  // + 1
-  if (!known[parts]) {
+  static PerDevice known[9];
+  return max(0, known[parts].get(current_device(), [&] {
     int n = 0;
-    if (start<D, E4M3, NT, kFewWarps<D, E4M3>, true>(P, 0, parts, nullptr, &n) != cudaSuccess) {
-      cudaGetLastError();  // leave no error behind
-      n = 0;
-    }
-    known[parts] = n + 1;
-  }
-  return known[parts] - 1;
+    if (start<D, E4M3, NT, kFewWarps<D, E4M3>, true>(P, 0, parts, nullptr, &n) == cudaSuccess) return n;
+    cudaGetLastError();  // leave no error behind
+    return -1;
+  }));
 }
 
 // Items of at most 8 NT query heads, and the most tokens that one can see.
