@@ -366,9 +366,9 @@ typedef struct {
  *   k, v  : bf16; token t's vectors are [heads][dim] starting k_stride (v_stride) * t
  *           values in (strides >= heads * dim, multiples of 8; slices of a fused
  *           projection need no copy); 16-byte aligned
- *   slots : int32 [n], distinct where not negative (two tokens on one slot: one of them
- *           remains); negative = padding, not written; past the end: not written and
- *           K3MOE_DEV_BOUNDS */
+ *   slots : int32 [n], distinct where not negative (what two tokens on one slot leave there
+ *           is undefined: a mixture of both); negative = padding, not written; past the
+ *           end: not written and K3MOE_DEV_BOUNDS */
 int k3moe_kv_write(const k3moe_kv_cache *cache, int32_t n, const uint16_t *k, const uint16_t *v, int64_t k_stride,
                    int64_t v_stride, const int32_t *slots, int32_t *dev_status, k3moe_stream_t stream);
 

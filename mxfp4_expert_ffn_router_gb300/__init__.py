@@ -453,7 +453,7 @@ class KVCache:
 
 def k3moe_kv_write(cache: KVCache, k, v, slots, dev_status=None, stream=None):
     """Keys and values k, v [n, heads, dim] (bf16; the first axis may be strided) into
-    the cache's slots [n] (int32, page * page_size + place; negative = padding)."""
+    the cache's slots [n] (int32, page * page_size + place, distinct; negative = padding)."""
     if _fast is not None:
         rc = _fast.kv_write(cache._addr, k, v, slots, dev_status, None if stream is None else stream.cuda_stream)
         if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
