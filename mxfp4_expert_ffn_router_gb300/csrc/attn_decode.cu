@@ -66,7 +66,11 @@
 //    exp2(s_i + e_i - m') with its own running maximum m' of s_i + e_i, times 2^14, rounded to
 //    f16 (11 bits down to 2^-28 of the largest, so that a token with a large score and a tiny
 //    value costs the others nothing), while l sums exp2(s_i - m) in fp32 with m = max s_i.
-//  * bf16.  Q, K and V enter as they are; the weights are rounded to bf16, as V is.
+//  * bf16.  Q, K and V enter as they are.  Both operands of a product are of one type, and bf16's 8 bits are too few for
+//    a weight (the output's error grew from 0.00166 to 0.00188 of its size): it enters as two bf16 numbers, rounded
+//    and what the rounding left, in a product each, 16 bits together.  That costs 0 to 1 % where the cache's bytes
+//    are the time, and 1 to 4 % of a short call (96 heads, 1.51 GB: 232.4 and 234.0 us; window of 1000: 6.7 and 6.9).
+//    E4M3's f16 weights stay in one part: their 11 bits add less than 1 % to the error of the output's own rounding.
 //
 // Measured (GB300, of 6787 GB/s copy): 32 sequences of 63 to 4001 tokens, 96 heads of 128, bf16 (1.51 GB):
 // 225 to 229 us, 6.6 TB/s; 64 sequences of 256 to 16384 tokens, 64 query and 8 key-value heads, E4M3
@@ -840,7 +844,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         }
       }
       // P^T: eight tokens by eight query heads, turned so that a lane has two tokens of one head
-      uint32_t pf[RR][NT][2];
+      uint32_t pf[RR][NT][2], pl[E4M3 ? 1 : RR][NT][2];  // (bf16: and what the rounding left)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const float base[2] = {(mrun[t][0] == -INFINITY ? 0.f : mrun[t][0]) - (E4M3 ? 14.f : 0.f),
@@ -849,7 +853,11 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         for (int j = 0; j < T2; ++j) {
           const float p0 = ex2(sc[t][0][j] - base[0]), p1 = ex2(sc[t][1][j] - base[1]);
           if (!E4M3) l[t][0] += p0, l[t][1] += p1;
-          pf[j >> 1][t][j & 1] = transpose8x8(pack2<E4M3>(p0, p1));
+          const uint32_t hi = pack2<E4M3>(p0, p1);
+          pf[j >> 1][t][j & 1] = transpose8x8(hi);
+          if constexpr (!E4M3)
+            pl[j >> 1][t][j & 1] =
+                transpose8x8(pack2<false>(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u)));
         }
       }
       // O^T: rows g and g + 8 of product m are this lane's dimensions 2m and 2m + 1.  16 tokens that are
@@ -889,7 +897,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
               const uint32_t a0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), a1 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
               const uint32_t a2 = __byte_perm(vw[2][w], vw[3][w], 0x5410), a3 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
 #pragma unroll
-              for (int t = 0; t < NT; ++t) mma16<false>(o[t][i * VW + w], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
+              for (int t = 0; t < NT; ++t) {
+                mma16<false>(o[t][i * VW + w], a0, a1, a2, a3, pf[r][t][0], pf[r][t][1]);
+                mma16<false>(o[t][i * VW + w], a0, a1, a2, a3, pl[r][t][0], pl[r][t][1]);
+              }
             }
           }
         }
