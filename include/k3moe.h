@@ -399,7 +399,8 @@ int k3moe_kv_read(const k3moe_kv_cache *cache, int32_t n, const int32_t *slots, 
  * A page number outside the cache sets K3MOE_DEV_BOUNDS; its places count as not seen.
  * Accumulation: exact products summed in fp32, softmax in fp32; before the product with V
  * the weights are rounded (bf16 cache: to 16 bits, as two bf16 numbers; E4M3 cache: to
- * f16, together with the scale of V).  Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, max_pages >= 1. */
+ * f16, together with the scale of V: 11 bits down to 2^-28 of the row's largest, below that
+ * an error of 2^-39 of it).  Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, max_pages >= 1. */
 size_t k3moe_attn_decode_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t Hq);
 int k3moe_attn_decode(const k3moe_kv_cache *cache, int32_t B, int32_t Hq, const uint16_t *q, int64_t q_stride,
                       const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, float scale,

@@ -21,7 +21,9 @@
 //    device, so a captured graph follows them.  A piece covers the end of one item, some
 //    whole items and the start of another; only the cut ones leave partial sums in the
 //    workspace, at most two a block, which attn_join_kernel adds in order.
-//  * Short ones.  The line costs about 10 us whatever the work.  Where no item sees more than
+//  * Short ones.  The line costs 7 to 10 us whatever the work.  The host does not know the lengths, only the most
+//    that the table's width (and the window) allows: a sequence of 37 tokens takes 3.2 us in a table of 64
+//    places, 4.0 in one of up to 2048 and 6.9, on the line, in a wider one (96 heads, E4M3).  Where no item can see more than
 //    kDirectTokens, a block takes one item and nothing is cut or joined (256 sequences of 900 tokens:
 //    80.9 us against 95.5).  Where items are short and more than such blocks fit the GPU at once, a block is
 //    one warp, eight to an SM: most of the time is starting and ending items, which then overlap, and no
@@ -29,19 +31,19 @@
 //    128 sequences of 60 tokens: 11.0 us with four warps, 9.4 with one; 250: 20.2 and 18.2, but 100 of up to
 //    250 with 96 heads 15.6 and 17.8; 256 of 1000: 87.6 and 111.3, since a warp has two steps in flight at
 //    most).  At rows of 512 bytes, where an SM holds one block of four warps, it pays twice as long (80
-//    sequences of 250 tokens, 64 heads on 8 of 256 in bf16: 38.2 and 31.5).  Where there are no more items
+//    sequences of 250 tokens, 64 heads on 8 of 256 in bf16: 39.9 and 30.7).  Where there are no more items
 //    than SMs, blocks of eight warps (rows of 512 bytes: four) take an item each, or a cluster of 2, 4 or 8 of
 //    them shares it evenly and joins its sums through
 //    distributed shared memory, up to kPartBytes of keys a block (E4M3, 8 heads: 4000 tokens of one
 //    sequence 7.4 us against 11.0 on the line, 16000 14.9 against 15.2, 40000 27.9 against 23.3; 8
-//    sequences of 3000 14.4 against 18.1; 2 of 2000, 32 heads on 4 of 256 in bf16, 8.5 against 11.9; one of
-//    200, 64 on 8 of 256, 5.7 in clusters of 4 and 6.9 without).
+//    sequences of 3000 14.4 against 18.1; 2 of 2000, 32 heads on 4 of 256 in bf16, 9.0 against 13.0; one of
+//    200, 64 on 8 of 256, 5.9 in clusters of 4 and 7.1 without).
 //  * More than 8 query heads a key.  16 of them share an item (NT = 2), so that the cache is read once.  Where
 //    the call is so short that a warp's own chain of instructions is what takes the time, each 8 take an
 //    item of their own and read the keys again through L2: 128 heads on 8, E4M3, one sequence of 60 tokens
 //    5.2 against 3.6 us, of 1000 8.6 and 6.6; 25 sequences of 250 8.8 and 7.2.  That holds as long as the
 //    twice as many items run at once; past kDirectTokens only if their clusters are no smaller (64 heads on 4 of
-//    256, bf16, 4000 tokens: 15.4 and 11.7; 30 sequences of 3000, 16 heads on one of 64: 8.0 and 9.6), and
+//    256, bf16, 4000 tokens: 16.8 and 12.4; 30 sequences of 3000, 16 heads on one of 64, bf16: 8.7 and 10.0), and
 //    where 16 heads' items would each have an SM but 8 heads' would not, up to kSplitTokens (15 sequences of
 //    250, 128 heads on 8 of 128: 7.6 and 6.9, of 1000 13.1 and 15.7).
 //  * Loads.  Each warp streams every fourth (eighth) run of 16 RR tokens through a ring
@@ -72,9 +74,9 @@
 //    are the time, and 1 to 4 % of a short call (96 heads, 1.51 GB: 232.4 and 234.0 us; window of 1000: 6.7 and 6.9).
 //    E4M3's f16 weights stay in one part: their 11 bits add less than 1 % to the error of the output's own rounding.
 //
-// Measured (GB300, of 6787 GB/s copy): 32 sequences of 63 to 4001 tokens, 96 heads of 128, bf16 (1.51 GB):
-// 225 to 229 us, 6.6 TB/s; 64 sequences of 256 to 16384 tokens, 64 query and 8 key-value heads, E4M3
-// (668 MB): 110 us, 6.1 TB/s; one of 131072 tokens (271 MB): 50 us, of which 8 are the start, the
+// Measured (GB300, of 6787 GB/s copy; one GPU and the next differ by 2 %): 32 sequences of 63 to 4001 tokens, 96
+// heads of 128, bf16 (1.51 GB): 232 us, 6.5 TB/s; 64 sequences of 256 to 16384 tokens, 64 query and 8 key-value
+// heads, E4M3 (668 MB): 111 us, 6.0 TB/s; one of 131072 tokens (271 MB): 51 us, of which 8 are the start, the
 // last blocks and the join; 37 tokens of 96 heads: 3.2 us.
 #include <cuda_fp16.h>
 
@@ -295,16 +297,17 @@ struct AdShape {
   static constexpr int QUADS = MM * NT;           // accumulator quads per lane
   // What an item's end costs, on the line: 1.5 units, or 3 where there is more to join
   static constexpr int ITEM_LEN = QUADS <= 8 ? 6 : 12;
-  // A warp's step is RR times 16 tokens: 4 to 16 KB, so that what a step costs besides its bytes counts little
+  // A warp's step is RR times 16 tokens: 8 KB (16 KB at rows of 512 bytes), so that what a step costs besides its
+  // bytes counts little
   static constexpr int RR = ROWB <= 64 ? 4 : ROWB <= 128 ? 2 : 1;
   static constexpr int RUN = RR * kRun;
   static constexpr int UNIT = RUN * W;            // tokens of a block's step
   static constexpr int SUB = 2 * KB;              // keys and values of 16 tokens; a multiple of 128: words swizzle by xor
   static constexpr int SCALES = E4M3 ? 32 : 0;    // scale bytes of 16 tokens, after all stages
-  // Stages and blocks per SM: 16 (or 12) warps' loads of 100 to 200 KB in flight per SM.  Blocks of one item
-  // each spend more of their time starting and ending, which a third block covers (256 sequences of 1000 tokens,
-  // 128 heads on 8, E4M3: 122.8 us with two, 104.3 with three); on the line it costs more in spilled registers and
-  // shorter rings than it brings (32 of 8000 in bf16: 169 and 180)
+  // Stages and blocks per SM: 8 warps (three blocks: 12; rows of 512 bytes: 4) with 64 to 128 KB of loads in flight per
+  // SM.  Blocks of one item each spend more of their time starting and ending, which a third block covers (256
+  // sequences of 1000 tokens, 128 heads on 8, E4M3: 122.8 us with two, 104.3 with three); on the line it costs more in
+  // spilled registers and shorter rings than it brings (32 of 8000, 128 heads on 8, bf16: 172 and 178)
   static constexpr bool THREE = DIRECT && W == 4 && ROWB <= 256 && (NT == 1 || D <= 128);
   static constexpr int STAGES = THREE || W == 1 ? 2 : 3;
   static constexpr int BLOCKS = W == 1 ? (ROWB <= 256 ? 8 : 4) : THREE ? 3 : ROWB <= 256 && W == 4 ? 2 : 1;
@@ -880,7 +883,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
               vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = vw[j][3] = 0u;
             }
           }
-            constexpr int VW = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
+          constexpr int VW = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
 #pragma unroll
           for (int w = 0; w < VW; ++w) {
             if constexpr (E4M3) {

@@ -13,7 +13,8 @@
 // read once; four blocks an SM (32 registers a thread, many rows) overlap one row's reduction with the others'
 // loads: 4096 rows of 7168 with both outputs (265 MB) 43.4 us, 6.1 TB/s of 6.8 measured for a copy,
 // against 46.2 us at 38 registers (three blocks) and 48 us for a persistent block that loads its next
-// row early.  One row: 2.3 us, the launch and two trips to memory.
+// row early.  At 32 registers this kernel (rows of 4128 to 8192) spills 16 bytes; it had none and took 42.8 us before its
+// weights were brought near and its inputs read by ordinary loads.  One row: 2.3 us, the launch and two trips to memory.
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
