@@ -11,10 +11,10 @@
 //
 // Bound: the rows' bytes, 9 of them a value with every output.  A block has one row in registers,
 // read once; four blocks an SM (32 registers a thread, many rows) overlap one row's reduction with the others'
-// loads: 4096 rows of 7168 with both outputs (265 MB) 43.4 us, 6.1 TB/s of 6.8 measured for a copy,
+// loads: 4096 rows of 7168 with both outputs (265 MB) 42.1 us, 6.3 TB/s of 6.8 measured for a copy,
 // against 46.2 us at 38 registers (three blocks) and 48 us for a persistent block that loads its next
-// row early.  At 32 registers this kernel (rows of 4128 to 8192) spills 16 bytes; it had none and took 42.8 us before its
-// weights were brought near and its inputs read by ordinary loads.  One row: 2.3 us, the launch and two trips to memory.
+// row early.  All arrays are indexed by chunks of 8 values from one index, with an index for each at
+// 32 registers 16 bytes spill: 43.4 us (4096 rows of 4096 28.5, now 25.2).  One row: 2.3 us, the launch and two trips to memory.
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
@@ -52,11 +52,12 @@ __global__ void __launch_bounds__(512, FEW ? 1 : CH <= 2 ? 4 : 2)
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, nth = WARP ? 32 : blockDim.x, nch = H / 8;
   const long long r_at = WARP ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && r_at >= T) return;
-  const size_t row = static_cast<size_t>(r_at) * H;
+  const size_t row = static_cast<size_t>(r_at) * nch;  // chunks
   float a[CH][8];
   float sum = 0.f;
-  // Few rows: the weights are loaded beside x, at 37 to 76 registers a thread (37 rows of 7168 2.55 us against 2.9,
-  // 300 3.3 against 4.0, but 600 7.1 against 6.8).  Many: only brought near (4096 rows of 16384 108.4 us, 110.3 without)
+  // Few rows: the weights are loaded beside x, at 37 to 76 registers a thread (37 rows of 7168, all outputs, 2.6 us
+  // against 3.1, 300 3.6 against 5.0, but 600 9.3 against 8.7).  Many: only brought near (4096 rows of 16384 108.1 us,
+  // 110.1 without)
   constexpr bool kEarly = FEW || WARP;
   uint4 wr[kEarly ? CH : 1];
 #pragma unroll
@@ -74,10 +75,10 @@ __global__ void __launch_bounds__(512, FEW ? 1 : CH <= 2 ? 4 : 2)
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * nth;
     if (c < nch) {
-      bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(x + row) + c), a[i]);
+      bf16x8_to_f32(reinterpret_cast<const uint4 *>(x)[row + c], a[i]);
       if (residual) {
         float r[8];
-        bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(residual + row) + c), r);
+        bf16x8_to_f32(reinterpret_cast<const uint4 *>(residual)[row + c], r);
 #pragma unroll
         for (int q = 0; q < 8; ++q) a[i][q] += r[q];
       }
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(512, FEW ? 1 : CH <= 2 ? 4 : 2)
     // the four lanes of a 32-value group are in or out together (H % 32 == 0)
     const unsigned in = __ballot_sync(0xFFFFFFFFu, c < nch);
     if (c < nch) {
-      if (residual_out) *(reinterpret_cast<uint4 *>(residual_out + row) + c) = f32x8_to_bf16(a[i]);
+      if (residual_out) reinterpret_cast<uint4 *>(residual_out)[row + c] = f32x8_to_bf16(a[i]);
       float w[8];
       if constexpr (kEarly)
         bf16x8_to_f32(wr[i], w);
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(512, FEW ? 1 : CH <= 2 ? 4 : 2)
         bf16x8_to_f32(*(reinterpret_cast<const uint4 *>(weight) + c), w);
 #pragma unroll
       for (int q = 0; q < 8; ++q) a[i][q] = a[i][q] * inv * w[q];
-      if (y) *(reinterpret_cast<uint4 *>(y + row) + c) = f32x8_to_bf16(a[i]);
+      if (y) reinterpret_cast<uint4 *>(y)[row + c] = f32x8_to_bf16(a[i]);
       if (codes) {
         uint32_t m = 0u;
 #pragma unroll
@@ -127,8 +128,8 @@ __global__ void __launch_bounds__(512, FEW ? 1 : CH <= 2 ? 4 : 2)
         m = max(m, __shfl_xor_sync(in, m, 1));
         m = max(m, __shfl_xor_sync(in, m, 2));
         const uint32_t byte = mx8_scale_byte(m);
-        *(reinterpret_cast<uint2 *>(codes + row) + c) = mx8_codes(a[i], byte);
-        if ((c & 3) == 0) scales[(row >> 5) + (c >> 2)] = static_cast<uint8_t>(byte);
+        reinterpret_cast<uint2 *>(codes)[row + c] = mx8_codes(a[i], byte);
+        if ((c & 3) == 0) scales[(row + c) >> 2] = static_cast<uint8_t>(byte);
       }
     }
   }
