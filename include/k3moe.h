@@ -406,6 +406,83 @@ int k3moe_attn_decode(const k3moe_kv_cache *cache, int32_t B, int32_t Hq, const 
                       const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, float scale,
                       uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, k3moe_stream_t stream);
 
+/* ---- Several new tokens of a sequence: prompts and drafted tokens --------- */
+
+/* The rotation of positions: dimensions 0 .. dim - 1 of a head's vector (dim a multiple of 16 in
+ * [16, the cache's dim]) are dim / 2 pairs, pair i being (i, i + dim / 2), or (2i, 2i + 1) where
+ * `neighbours` is 1.  At position p pair i turns by the angle a = p * inv_freq[i]:
+ *   (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a)
+ *   turns : int64 [dim / 2] in device memory: inv_freq[i] / 2 pi in units of 2^-64 turns, modulo 2^64
+ *           (8-byte aligned).  p * turns[i] wraps exactly where the angle does, so that a far position's
+ *           angle is as exact as a near one's.
+ *   scale : finite; dimensions past `dim` are neither turned nor scaled */
+typedef struct {
+  int32_t dim, neighbours;
+  float scale;
+  const int64_t *turns;
+} k3moe_rotation;
+
+/* Append n tokens' keys and values to the cache with the rotation of their positions on the
+ * way, and rotate their queries:
+ *   cache[slots[t]] = rotated k[t], v[t] (as k3moe_kv_write; the rotated key is quantised, or
+ *   rounded to bf16, from its fp32 values), q_out[t] = bf16_rne(rotated q[t])
+ *   q, k, v   : bf16; token t's [Hq][dim], [heads][dim], [heads][dim] start q_stride (k_stride,
+ *               v_stride) * t values in (strides at least the rows, multiples of 8); 16-byte aligned
+ *   Hq        : 0 .. 16384 (0: no queries; q and q_out are not looked at)
+ *   slots     : int32 [n] as for k3moe_kv_write; of a token with a negative slot nothing is written,
+ *               q_out included; nor of one past the end (K3MOE_DEV_BOUNDS)
+ *   positions : int32 [n], any
+ *   q_out     : bf16, [Hq][dim] every q_out_stride values; may be q itself (with q's stride),
+ *               and else overlaps none of the inputs */
+int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const uint16_t *q, const uint16_t *k,
+                    const uint16_t *v, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *slots,
+                    const int32_t *positions, const k3moe_rotation *rotation, uint16_t *q_out, int64_t q_out_stride,
+                    int32_t *dev_status, k3moe_stream_t stream);
+
+/* Attention of the new tokens of B sequences over the cache that already holds them (append
+ * them first).  Sequence b has seq_lens[b] = n cached tokens, the last m = q_offsets[b + 1] -
+ * q_offsets[b] of which are its new ones: row q_offsets[b] + i of q is the token at place n - m + i.
+ * The token at place p sees the places
+ *   c <= p with  window == 0  or  c > p - window  or  c < sinks
+ * (a sliding window, and the first `sinks` tokens, which stay visible).  Scores, out and lse
+ * are those of k3moe_attn_decode, whose call with a window this is for m = 1 and no sinks.
+ *   rows        : rows of q, out and lse; those before q_offsets[0] and from q_offsets[B] on are left as they were
+ *   q           : bf16; row r's [Hq][dim] starts q_stride * r values in (q_stride >= Hq * dim, a
+ *                 multiple of 8), 16-byte aligned
+ *   q_offsets   : int32 [B + 1], ascending within 0 .. rows
+ *   max_new     : no sequence has more new tokens (1 .. rows); 1 takes the kernels of single tokens
+ *   block_table, seq_lens, scale, dev_status : as for k3moe_attn_decode; of block_table only the entries
+ *                 of pages that hold a place which some row sees, or lie between two such of one tile of
+ *                 128 places, are read
+ *   out         : uint16 [rows][Hq][dim] bf16, 16-byte aligned
+ *   lse         : float [rows][Hq] or NULL
+ *   ws          : k3moe_attn_extend_workspace_bytes(cache, B, rows, Hq) bytes, 256-byte aligned
+ * A row that sees nothing gives out = 0, lse = -inf.  What lies in places that a row does not
+ * see does not touch it, whatever they hold.  A sequence whose offsets descend, leave 0 .. rows or span
+ * more than max_new rows sets K3MOE_DEV_BOUNDS and its rows are left as they were; one with more new
+ * tokens than cached ones sets it too, and those that have no place see nothing.
+ * Accumulation: exact products summed in fp32, softmax in fp32; the weights are rounded before
+ * the product with V as the comment in attn_extend.cu says.
+ * Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, window and sinks >= 0, max_pages >= 1. */
+size_t k3moe_attn_extend_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq);
+int k3moe_attn_extend(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq, const uint16_t *q,
+                      int64_t q_stride, const int32_t *q_offsets, int32_t max_new, const int32_t *block_table,
+                      int32_t max_pages, const int32_t *seq_lens, int32_t window, int32_t sinks, float scale,
+                      uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, k3moe_stream_t stream);
+
+/* The same for a tree of drafted tokens: the m new tokens of a sequence (at most 64 * words) see
+ * its cached places below n - m, the context, and of one another those that their masks name:
+ *   masks : int64 [rows][words] (8-byte aligned), bit j % 64 of word j / 64 of row i's: its token sees the
+ *           sequence's new token j (its own bit, if it is to see itself, included; bits past m mean nothing)
+ *   words : 1 .. 16
+ * A window counts from the token's position n - m + max(0, s - 1), s being the number of new tokens that it
+ * sees (its ancestors and itself), and with the sinks it limits the context alone. */
+int k3moe_attn_tree(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq, const uint16_t *q,
+                    int64_t q_stride, const int32_t *q_offsets, const int64_t *masks, int32_t words,
+                    const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, int32_t sinks,
+                    float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status,
+                    k3moe_stream_t stream);
+
 /* Self-test of the bounded waits (a test hook, not part of the path): one
  * thread waits, with the iteration bound every mbarrier wait in the tensor-core
  * kernels uses, on a phase that nothing completes, so the wait runs out: the

@@ -9,6 +9,7 @@ library is missing or the device is not sm_103 the calls raise.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -57,6 +58,11 @@ class _KVCacheC(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("format", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class _RotationC(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("neighbours", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("turns", ctypes.c_void_p)]
 
 
 def library_path() -> str:
@@ -120,6 +126,17 @@ def lib():
             L.k3moe_attn_decode_workspace_bytes.argtypes = [kvc, i32, i32]
             L.k3moe_attn_decode.restype = i32
             L.k3moe_attn_decode.argtypes = [kvc, i32, i32, vp, i64, vp, i32, vp, i32, f32, vp, vp, vp, sz, vp, vp]
+            L.k3moe_kv_append.restype = i32
+            L.k3moe_kv_append.argtypes = [kvc, i32, i32, vp, vp, vp, i64, i64, i64, vp, vp, ctypes.POINTER(_RotationC), vp,
+                                          i64, vp, vp]
+            L.k3moe_attn_extend_workspace_bytes.restype = sz
+            L.k3moe_attn_extend_workspace_bytes.argtypes = [kvc, i32, i32, i32]
+            L.k3moe_attn_extend.restype = i32
+            L.k3moe_attn_extend.argtypes = [kvc, i32, i32, i32, vp, i64, vp, i32, vp, i32, vp, i32, i32, f32, vp, vp, vp,
+                                            sz, vp, vp]
+            L.k3moe_attn_tree.restype = i32
+            L.k3moe_attn_tree.argtypes = [kvc, i32, i32, i32, vp, i64, vp, vp, i32, vp, i32, vp, i32, i32, f32, vp, vp, vp,
+                                          sz, vp, vp]
             L.k3moe_selftest_bounded_wait.restype = i32
             L.k3moe_selftest_bounded_wait.argtypes = [vp, vp, vp]
             L.k3moe_status_string.restype = ctypes.c_char_p
@@ -514,3 +531,109 @@ def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, s
                                  _stream(stream))
     if rc:
         _check("k3moe_attn_decode", rc)
+
+
+class Rotation:
+    """The rotation of positions for k3moe_kv_append: the first ``dim`` dimensions of a head's vector (a
+    multiple of 16) are pairs (i, i + dim/2), or (2i, 2i + 1) with ``neighbours``; at position p pair i
+    turns by p * inv_freq[i] and is scaled by ``scale``.  ``inv_freq``: dim/2 numbers (a sequence or a tensor;
+    64 bits keep far positions exact), base ** (-2i / dim) unless given."""
+
+    def __init__(self, dim: int, base: float = 10000.0, inv_freq=None, neighbours: bool = False, scale: float = 1.0,
+                 device="cuda"):
+        if inv_freq is None:
+            inv_freq = [base ** (-2.0 * i / dim) for i in range(dim // 2)]
+        elif isinstance(inv_freq, torch.Tensor):
+            inv_freq = inv_freq.double().tolist()
+        if len(inv_freq) != dim // 2:
+            raise ValueError(f"inv_freq: expected {dim // 2} numbers, got {len(inv_freq)}")
+        if not all(math.isfinite(f) for f in inv_freq):
+            raise ValueError("inv_freq: must be finite")
+        # turns of 2^-64 modulo 2^64, as signed numbers
+        turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
+        self.dim, self.neighbours, self.scale = int(dim), bool(neighbours), float(scale)
+        self.turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self._c = _RotationC(self.dim, int(self.neighbours), self.scale, _ptr(self.turns, torch.int64, "turns"))
+        self._ref, self._addr = ctypes.byref(self._c), ctypes.addressof(self._c)
+
+
+def k3moe_kv_append(cache: KVCache, k, v, slots, positions, rotation: Rotation, q=None, q_out=None, dev_status=None,
+                    stream=None):
+    """Keys and values k, v [n, heads, dim] (bf16; the first axis may be strided) of tokens at ``positions``
+    [n] (int32) into the cache's slots [n] (as k3moe_kv_write), the keys rotated; and the queries q [n, Hq,
+    dim] rotated into q_out (both may be strided; q_out may be q).  Nothing of a token with a negative slot is written."""
+    shape = (slots.numel(), cache.heads, cache.dim)
+    n = shape[0]
+    kp, ks = _rows(k, shape, "k")
+    vp, vs = _rows(v, shape, "v")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out belong together")
+    Hq = qp = qs = op = os_ = 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: expected a tensor [n, Hq, dim]")
+        Hq = q.shape[1]
+        qp, qs = _rows(q, (n, Hq, cache.dim), "q")
+        op, os_ = _rows(q_out, (n, Hq, cache.dim), "q_out")
+    rc = lib().k3moe_kv_append(cache._ref, n, Hq, qp, kp, vp, qs, ks, vs, _in(slots, _I32, (n,), "slots"),
+                               _in(positions, _I32, (n,), "positions"), rotation._ref, op, os_,
+                               _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    if rc:
+        _check("k3moe_kv_append", rc)
+
+
+def k3moe_attn_extend_workspace_bytes(cache: KVCache, batch: int, rows: int, q_heads: int) -> int:
+    """For k3moe_attn_extend and k3moe_attn_tree."""
+    return int(lib().k3moe_attn_extend_workspace_bytes(cache._ref, batch, rows, q_heads))
+
+
+def _most(v):
+    """(ctypes would keep the low 32 bits: no place is larger, and none of these below 0 is allowed)"""
+    return max(-1, min(v, 0x7FFFFFFF))
+
+
+def _extend_args(cache, q, q_offsets, block_table, seq_lens):
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected a tensor [rows, Hq, dim]")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table: expected a tensor [B, max_pages]")
+    (rows, Hq, _), (B, pages) = q.shape, block_table.shape
+    qp, qs = _rows(q, (rows, Hq, cache.dim), "q")
+    return (rows, Hq, B, pages, qp, qs, _in(q_offsets, _I32, (B + 1,), "q_offsets"),
+            _in(block_table, _I32, (B, pages), "block_table"), _in(seq_lens, _I32, (B,), "seq_lens"))
+
+
+def k3moe_attn_extend(cache: KVCache, q, q_offsets, block_table, seq_lens, out, lse=None, scale=None, window: int = 0,
+                      sinks: int = 0, max_new=None, ws=None, dev_status=None, stream=None):
+    """Attention of the newest tokens of each sequence, which the cache already holds: rows q_offsets[b] ..
+    q_offsets[b + 1] - 1 (int32 [B + 1]) of q [rows, Hq, dim] (bf16; the first axis may be strided) are the
+    last ones of the seq_lens[b] cached tokens.  A token sees itself and those before it; with window > 0 of
+    these the last ``window`` and the first ``sinks``.  out [rows, Hq, dim] (bf16), lse [rows, Hq] (fp32); max_new:
+    no sequence has more (1 takes the kernels of single tokens); ws: k3moe_attn_extend_workspace_bytes."""
+    rows, Hq, B, pages, qp, qs, offs, table, lens = _extend_args(cache, q, q_offsets, block_table, seq_lens)
+    rc = lib().k3moe_attn_extend(cache._ref, B, rows, Hq, qp, qs, offs, rows if max_new is None else _most(max_new), table,
+                                 pages, lens, _most(window), _most(sinks), cache.dim ** -0.5 if scale is None else scale,
+                                 _in(out, _BF16, (rows, Hq, cache.dim), "out"), _in(lse, _F32, (rows, Hq), "lse"),
+                                 _ptr(ws, None, "ws"), ws.nbytes if ws is not None else 0,
+                                 _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    if rc:
+        _check("k3moe_attn_extend", rc)
+
+
+def k3moe_attn_tree(cache: KVCache, q, q_offsets, masks, block_table, seq_lens, out, lse=None, scale=None,
+                    window: int = 0, sinks: int = 0, ws=None, dev_status=None, stream=None):
+    """k3moe_attn_extend for drafted tokens: of its sequence's new tokens row r sees those whose bits its mask
+    has (masks [rows, words] int64: bit j % 64 of word j // 64 stands for new token j), and all of the cached
+    ones before them that the window and the sinks leave, the window counting from n - m + (new tokens seen) - 1."""
+    rows, Hq, B, pages, qp, qs, offs, table, lens = _extend_args(cache, q, q_offsets, block_table, seq_lens)
+    if not isinstance(masks, torch.Tensor) or masks.dim() != 2:
+        raise ValueError("masks: expected a tensor [rows, words]")
+    words = masks.shape[1]
+    rc = lib().k3moe_attn_tree(cache._ref, B, rows, Hq, qp, qs, offs, _in(masks, (torch.int64,), (rows, words), "masks"),
+                               words, table, pages, lens, _most(window), _most(sinks),
+                               cache.dim ** -0.5 if scale is None else scale,
+                               _in(out, _BF16, (rows, Hq, cache.dim), "out"), _in(lse, _F32, (rows, Hq), "lse"),
+                               _ptr(ws, None, "ws"), ws.nbytes if ws is not None else 0,
+                               _ptr(dev_status, torch.int32, "dev_status"), _stream(stream))
+    if rc:
+        _check("k3moe_attn_tree", rc)

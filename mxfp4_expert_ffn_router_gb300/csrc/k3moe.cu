@@ -385,6 +385,76 @@ int k3moe_attn_decode(const k3moe_kv_cache *cache, int32_t B, int32_t Hq, const 
                                                 reinterpret_cast<k3moe_stream>(stream)));
 }
 
+int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const uint16_t *q, const uint16_t *k,
+                    const uint16_t *v, int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t *slots,
+                    const int32_t *positions, const k3moe_rotation *rotation, uint16_t *q_out, int64_t q_out_stride,
+                    int32_t *dev_status, k3moe_stream_t stream) {
+  int rc = kv_check(cache);
+  if (rc) return rc;
+  if (!rotation) return K3MOE_ERR_ARG;
+  if (n < 0 || Hq < 0 || Hq > 16384) return K3MOE_ERR_SHAPE;
+  if (rotation->dim < 16 || rotation->dim > cache->dim || rotation->dim % 16) return K3MOE_ERR_SHAPE;
+  if (rotation->neighbours < 0 || rotation->neighbours > 1 || !std::isfinite(rotation->scale)) return K3MOE_ERR_ARG;
+  if (n == 0) return K3MOE_OK;
+  if (!k || !v || !slots || !positions || !rotation->turns || (Hq && (!q || !q_out))) return K3MOE_ERR_ARG;
+  const int64_t row = static_cast<int64_t>(cache->heads) * cache->dim, qrow = static_cast<int64_t>(Hq) * cache->dim;
+  if (k_stride < row || v_stride < row || (Hq && (q_stride < qrow || q_out_stride < qrow))) return K3MOE_ERR_SHAPE;
+  if (Hq && q == q_out && q_stride != q_out_stride) return K3MOE_ERR_ARG;
+  if (!aligned16(k) || !aligned16(v) || k_stride % 8 || v_stride % 8 ||
+      (reinterpret_cast<uintptr_t>(rotation->turns) & 7u) ||
+      (Hq && (!aligned16(q) || !aligned16(q_out) || q_stride % 8 || q_out_stride % 8)))
+    return K3MOE_ERR_ALIGN;
+  if ((rc = abi_check_arch())) return rc;
+  return abi_launched(k3moe::launch_kv_append(*cache, n, Hq, q, k, v, q_stride, k_stride, v_stride, slots, positions,
+                                              *rotation, q_out, q_out_stride, dev_status,
+                                              reinterpret_cast<k3moe_stream>(stream)));
+}
+
+size_t k3moe_attn_extend_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq) {
+  return attn_check(cache, B, Hq) || rows < 0 ? 0 : k3moe::attn_extend_workspace(*cache, B, rows, Hq);
+}
+
+// What k3moe_attn_extend and k3moe_attn_tree check alike; a.c is the cache's where it is not null.
+static int extend_run(const k3moe_kv_cache *cache, k3moe::ExtendArgs &a, size_t ws_bytes, k3moe_stream_t stream) {
+  int rc = attn_check(cache, a.B, a.Hq);
+  if (rc) return rc;
+  a.c = *cache;
+  if (a.rows < 0 || a.max_pages < 1 || a.window < 0 || a.sinks < 0) return K3MOE_ERR_SHAPE;
+  if (static_cast<long long>(a.max_pages) * cache->page_size >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+  if (!std::isfinite(a.scale)) return K3MOE_ERR_ARG;
+  if (a.B == 0 || a.rows == 0) return K3MOE_OK;
+  if (a.max_new < 1) return K3MOE_ERR_SHAPE;
+  if (!a.q || !a.offsets || !a.table || !a.lens || !a.out || (a.words && !a.masks)) return K3MOE_ERR_ARG;
+  if (a.q_stride < static_cast<int64_t>(a.Hq) * cache->dim) return K3MOE_ERR_SHAPE;
+  if (!aligned16(a.q) || a.q_stride % 8 || !aligned16(a.out) || (reinterpret_cast<uintptr_t>(a.masks) & 7u))
+    return K3MOE_ERR_ALIGN;
+  const size_t need = k3moe::attn_extend_workspace(*cache, a.B, a.rows, a.Hq);
+  if (need && (!a.ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(a.ws) & 255u))) return K3MOE_ERR_WORKSPACE;
+  if ((rc = abi_check_arch())) return rc;
+  return abi_launched(k3moe::launch_attn_extend(a, reinterpret_cast<k3moe_stream>(stream)));
+}
+
+int k3moe_attn_extend(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq, const uint16_t *q,
+                      int64_t q_stride, const int32_t *q_offsets, int32_t max_new, const int32_t *block_table,
+                      int32_t max_pages, const int32_t *seq_lens, int32_t window, int32_t sinks, float scale,
+                      uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status, k3moe_stream_t stream) {
+  k3moe::ExtendArgs a = {{}, B, rows, Hq, q, q_stride, q_offsets, max_new < rows ? max_new : rows, nullptr, 0, block_table,
+                         max_pages, seq_lens, window, sinks, scale, out, lse, ws, dev_status};
+  return extend_run(cache, a, ws_bytes, stream);
+}
+
+int k3moe_attn_tree(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq, const uint16_t *q,
+                    int64_t q_stride, const int32_t *q_offsets, const int64_t *masks, int32_t words,
+                    const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, int32_t sinks,
+                    float scale, uint16_t *out, float *lse, void *ws, size_t ws_bytes, int32_t *dev_status,
+                    k3moe_stream_t stream) {
+  if (words < 1 || words > 16) return K3MOE_ERR_SHAPE;
+  k3moe::ExtendArgs a = {{}, B, rows, Hq, q, q_stride, q_offsets, 64 * words < rows ? 64 * words : rows,
+                         reinterpret_cast<const uint64_t *>(masks), words, block_table, max_pages, seq_lens, window,
+                         sinks, scale, out, lse, ws, dev_status};
+  return extend_run(cache, a, ws_bytes, stream);
+}
+
 const char *k3moe_last_cuda_error(void) { return t_last_cuda_error; }
 
 }  // extern "C"
