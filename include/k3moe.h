@@ -451,9 +451,8 @@ int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const ui
  *                 multiple of 8), 16-byte aligned
  *   q_offsets   : int32 [B + 1], ascending within 0 .. rows
  *   max_new     : no sequence has more new tokens (1 .. rows); 1 takes the kernels of single tokens
- *   block_table, seq_lens, scale, dev_status : as for k3moe_attn_decode; of block_table only the entries
- *                 of pages that hold a place which some row sees, or lie between two such of one tile of
- *                 128 places, are read
+ *   block_table, seq_lens, scale, dev_status : as for k3moe_attn_decode (max_pages * page_size at most
+ *                 2^31 - 1024); entries of pages of which no row sees a place may be anything
  *   out         : uint16 [rows][Hq][dim] bf16, 16-byte aligned
  *   lse         : float [rows][Hq] or NULL
  *   ws          : k3moe_attn_extend_workspace_bytes(cache, B, rows, Hq) bytes, 256-byte aligned
@@ -463,7 +462,8 @@ int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const ui
  * tokens than cached ones sets it too, and those that have no place see nothing.
  * Accumulation: exact products summed in fp32, softmax in fp32; the weights are rounded before
  * the product with V as the comment in attn_extend.cu says.
- * Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, window and sinks >= 0, max_pages >= 1. */
+ * Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, window and sinks >= 0, max_pages >= 1, rows * Hq / heads
+ * below 2^31. */
 size_t k3moe_attn_extend_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq);
 int k3moe_attn_extend(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq, const uint16_t *q,
                       int64_t q_stride, const int32_t *q_offsets, int32_t max_new, const int32_t *block_table,

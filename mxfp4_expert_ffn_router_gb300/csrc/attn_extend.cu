@@ -4,10 +4,27 @@
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
 #include "mx8_quant.cuh"
+#include "per_device.h"
+#include "tc_sm103.cuh"
 
 namespace k3moe {
 
 namespace {
+
+constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 MMA, 9 loads, 12-15 values
+constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
+constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrowth = 8.f;     // a row's sums are rescaled once its maximum has grown by 2^8
+
+struct AxStart {  // where a block's piece of the line begins
+  long long begin;  // of the item that it begins in
+  int b, head, t, pad;
+};
+struct AxPlan {
+  long long total, share;
+};
 
 struct AxParams {
   const uint8_t *k, *v, *ks, *vs;
@@ -27,6 +44,14 @@ struct AxParams {
   uint16_t *out;
   float *lse;
   int32_t *status;
+  AxPlan *plan;
+  AxStart *start;
+  int4 *meta;        // [blocks]: {sequence, head, tile, parts} of the item that begins in the block's piece and goes on
+  int *first_entry;  // [B + 1]
+  long long *prefix; // [entries + 1]
+  float2 *stat;      // [2 blocks][rows of a tile]
+  float *part;       // [2 blocks][dim][rows of a tile]
+  int blocks, entries;  // pieces; room for the tiles of query rows
 };
 
 struct Seq {
@@ -51,68 +76,1077 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
   return s;
 }
 
-}  // namespace
-
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(256) attn_extend_simple(const AxParams P) {
-  const int b = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  const Seq s = seq_of(P, b, h == 0 && blockIdx.z == 0 && threadIdx.x == 0);
-  const int g = h / P.G;
-  for (int i = blockIdx.z * 8 + warp; i < s.m; i += 8 * gridDim.z) {
-    const size_t row = s.first + i;
-    const uint16_t *q = P.q + static_cast<long long>(row) * P.q_stride + static_cast<size_t>(h) * D;
-    float qv[D / 32], o[D / 32], m = -INFINITY, l = 0.f;
-    for (int x = 0; x < D / 32; ++x) qv[x] = bf16_bits_to_f32(q[x * 32 + lane]), o[x] = 0.f;
-    int pos = s.ctx + i;
-    if (P.masks) {
-      int seen = 0;
-      for (int j = 0; j < s.m; ++j) seen += (P.masks[row * P.words + j / 64] >> (j % 64)) & 1;
-      pos = s.ctx + max(0, seen - 1);
-    }
-    for (int c = 0; c < s.n; ++c) {
-      bool see;
-      if (P.masks && c >= s.ctx) {
-        const int j = c - s.ctx;
-        see = (P.masks[row * P.words + j / 64] >> (j % 64)) & 1;
-      } else {
-        see = (P.masks || c <= pos) && (P.window == 0 || c > static_cast<long long>(pos) - P.window || c < P.sinks);
-      }
-      if (!see) continue;
-      const int page = P.table[static_cast<size_t>(b) * P.max_pages + (c >> P.page_shift)];
-      if (page < 0 || page >= P.pages) {
-        if (lane == 0) set_status(P.status, K3MOE_DEV_BOUNDS);
-        continue;
-      }
-      const size_t vec = ((static_cast<size_t>(page) * P.heads + g) << P.page_shift) + (c & ((1 << P.page_shift) - 1));
-      float kv[D / 32], vv[D / 32], dot = 0.f;
-      for (int x = 0; x < D / 32; ++x) {
-        if (E4M3) {
-          uint32_t a, z;
-          e4m3x4_to_f16x2(P.k[vec * D + x * 32 + lane], a, z);
-          kv[x] = __half2float(__ushort_as_half(a & 0xFFFF)) * e8m0_to_f32(P.ks[vec]);
-          e4m3x4_to_f16x2(P.v[vec * D + x * 32 + lane], a, z);
-          vv[x] = __half2float(__ushort_as_half(a & 0xFFFF)) * e8m0_to_f32(P.vs[vec]);
-        } else {
-          kv[x] = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.k)[vec * D + x * 32 + lane]);
-          vv[x] = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x * 32 + lane]);
+struct AxShape {
+  static constexpr int TN = D == 256 ? 64 : 128;   // places of a tile
+  static constexpr int NS = D == 256 ? 1 : 2;      // streams: 128 query rows with sums of their own
+  static constexpr int ROWS = 128 * NS;            // query rows of an item
+  static constexpr int QB = 128 * D * 2;           // bytes of a stream's queries
+  static constexpr int TILE = TN * D * 2;          // bytes of a tile's keys or values as operands
+  static constexpr int RAW = E4M3 ? TN * D : 0;    // as codes
+  static constexpr int NK = D == 64 ? (E4M3 ? 3 : 4) : E4M3 ? 2 : 3;
+  static constexpr int NV = D == 64 ? (E4M3 ? 3 : 4) : 2;
+  static constexpr int NR = E4M3 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int RAWB = RAW + (E4M3 ? 128 : 0);  // codes and scales
+  static constexpr int OFF_K = NS * QB, OFF_V = OFF_K + NK * TILE, OFF_R = OFF_V + NV * TILE;
+  static constexpr int SMEM = OFF_R + NR * RAWB;
+  static constexpr int S_COLS = TN;                // columns of a score buffer
+  static constexpr int O_COL = 256, O_COLS = D == 256 ? 256 : 128;
+};
+
+// ---- which places the rows of an item see
+struct Tiles {
+  int pmin, pmax;    // positions of its first and last row
+  int lo, sinks;     // seen by any of them: lo .. pmax and 0 .. sinks - 1
+  int sink_tiles, t0, units;
+  __device__ __forceinline__ int tile(int u) const { return u < sink_tiles ? u : u - sink_tiles + t0; }
+  // Whether some row sees some of the `run` places from `place` on (pages that none sees may have been given back)
+  __device__ __forceinline__ bool needs(const Seq &s, int place, int run) const {
+    return place < s.n && (place + run > lo || place < sinks);
+  }
+};
+template <int TN>
+__device__ __forceinline__ Tiles tiles_of(const AxParams &P, const Seq &s, int r0, int rows) {
+  Tiles t;
+  if (P.masks) {
+    t.pmin = s.ctx;
+    t.pmax = s.n - 1;
+  } else {
+    t.pmin = s.ctx + r0 / P.G;
+    t.pmax = s.ctx + (r0 + rows - 1) / P.G;
+  }
+  t.lo = P.window > 0 && t.pmin >= P.window ? t.pmin - P.window + 1 : 0;
+  t.t0 = t.lo / TN;
+  const int t1 = t.pmax >= 0 ? t.pmax / TN + 1 : 0;
+  t.sinks = P.window > 0 ? min(P.sinks, t.pmax + 1) : 0;
+  t.sink_tiles = t.sinks > 0 ? min((t.sinks - 1) / TN + 1, t.t0) : 0;
+  t.units = max(1, t.sink_tiles + t1 - t.t0);
+  return t;
+}
+// Whether some row does not see some place of the tile.
+template <int TN>
+__device__ __forceinline__ bool masked(const AxParams &P, const Seq &s, const Tiles &t, int tile) {
+  const int c0 = tile * TN, c1 = c0 + TN;
+  const int all = P.masks ? s.ctx : t.pmin + 1;  // places below are seen, the window aside
+  return c1 > all || (P.window > 0 && c1 > P.sinks && c0 <= t.pmax - P.window);
+}
+
+// The page of a place; whether the cache has it.
+__device__ __forceinline__ int page_of(const AxParams &P, int b, int place) {
+  return P.table[static_cast<size_t>(b) * P.max_pages + (place >> P.page_shift)];
+}
+__device__ __forceinline__ bool is_page(const AxParams &P, int page) {
+  return static_cast<unsigned>(page) < static_cast<unsigned>(P.pages);
+}
+// Whether the 16 places from `place` on are needed, but lie in no page of the cache.
+__device__ __forceinline__ bool lost16(const AxParams &P, const Seq &s, const Tiles &t, int b, int place) {
+  return t.needs(s, place, 16) && !is_page(P, page_of(P, b, place));
+}
+// Whether any of the tiles u0 .. u1 - 1 has such places (asked by a whole warp).
+template <int TN>
+__device__ __forceinline__ bool any_lost(const AxParams &P, const Seq &s, const Tiles &t, int b, int u0, int u1) {
+  bool bad = false;
+  for (int x = threadIdx.x & 31; x < (u1 - u0) * (TN / 16); x += 32)
+    bad |= lost16(P, s, t, b, t.tile(u0 + x / (TN / 16)) * TN + x % (TN / 16) * 16);
+  return __any_sync(0xFFFFFFFFu, bad);
+}
+
+// A block's piece of the line, item by item.
+template <int TN, int ROWS>
+struct Walk {
+  long long from, to, begin;
+  int b, head, t, tiles;
+  Seq s;
+  int r0, rows;  // query rows of the item
+  Tiles list;
+  int weight;    // of a tile on the line
+  int u0, u1;    // the item's tiles that are this piece's
+  bool more;
+
+  __device__ __forceinline__ void measure(const AxParams &P) {
+    r0 = t * ROWS;
+    rows = min(ROWS, s.m * P.G - r0);
+    list = tiles_of<TN>(P, s, r0, rows);
+    weight = rows > 128 ? 2 : 1;
+  }
+  __device__ __forceinline__ void set_seq(const AxParams &P) {
+    s = seq_of(P, b, false);
+    tiles = P.first_entry[b + 1] - P.first_entry[b];
+  }
+  __device__ __forceinline__ int unit_at(long long x) const {
+    const long long u = (x - begin - kItemLen + weight - 1) / weight;
+    return u < 0 ? 0 : u > list.units ? list.units : static_cast<int>(u);
+  }
+  __device__ __forceinline__ void enter() { u0 = unit_at(from), u1 = unit_at(to); }
+  __device__ __forceinline__ long long length() const { return kItemLen + static_cast<long long>(list.units) * weight; }
+  __device__ __forceinline__ void init(const AxParams &P, int block) {
+    const long long total = P.plan->total, share = P.plan->share;
+    from = block * share;
+    to = min(total, from + share);
+    more = from < to;
+    if (!more) return;
+    const AxStart st = P.start[block];
+    begin = st.begin, b = st.b, head = st.head, t = st.t;
+    set_seq(P);
+    measure(P);
+    enter();
+    if (u0 >= u1) next(P);
+  }
+  __device__ __forceinline__ void next(const AxParams &P) {
+    do {
+      begin += length();
+      more = begin + kItemLen < to;
+      if (!more) return;
+      if (++t == tiles) {
+        t = 0;
+        if (++head == P.heads) {
+          head = 0;
+          do {
+            if (++b >= P.B) {
+              more = false;
+              return;
+            }
+            set_seq(P);
+          } while (tiles == 0);
         }
-        dot += qv[x] * kv[x];
       }
-      for (int off = 16; off; off >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, off);
-      const float sc = dot * P.scale, mn = fmaxf(m, sc), base = mn == -INFINITY ? 0.f : mn;
-      const float f = __expf(m - base), p = expf(sc - base);
-      l = l * f + p;
-      for (int x = 0; x < D / 32; ++x) o[x] = o[x] * f + p * vv[x];
-      m = mn;
+      measure(P);
+      enter();
+    } while (u0 >= u1);
+  }
+  __device__ __forceinline__ bool cut() const { return u0 > 0 || u1 < list.units; }
+};
+
+// ---- small device functions
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// A wait of a whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mb_wait(bar, parity));
+}
+__device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u; }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(su32(bar))
+               : "memory");
+}
+
+// Instruction descriptor, kind::f16: bf16 A and B, fp32 sums; B along K (keys) or along N (values).
+__device__ __forceinline__ uint32_t idesc(int N, bool b_along_n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (b_along_n ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+// Values [place][64 dimensions], 128-byte swizzle, along N: blocks of 64 dimensions `block` bytes
+// apart, groups of eight places 1024 bytes.
+__device__ __forceinline__ uint64_t values_desc(uint32_t saddr, uint32_t block) {
+  return static_cast<uint64_t>((saddr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+               "l"(a), "l"(b), "r"(id), "r"(acc)
+               : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+                   d),
+               "r"(a), "l"(b), "r"(id), "r"(acc)
+               : "memory");
+}
+// 32 columns of this thread's lane; the values are there after tc_wait_ld.
+__device__ __forceinline__ void tc_ld32(uint32_t taddr, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]),
+        "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]),
+        "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(float (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // (uses stay behind the wait)
+}
+__device__ __forceinline__ void tc_st16r(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32r(uint32_t taddr, const float *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+      "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+      "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
+      "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two codes of `w` (bytes 0 and 1 of the selection) to bf16 patterns of their values times 2^-120: exponent and
+// mantissa move to their places, subnormal codes to subnormal numbers.  (A NaN's code is not seen.)
+__device__ __forceinline__ uint32_t codes_up(uint32_t w, uint32_t sel) {
+  const uint32_t x = __byte_perm(w, 0u, sel);
+  return ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+}
+
+// What a row sees of a tile, bit x for place c0 + x.
+struct Row {
+  int hi, lo;            // (causal) last place seen; first of the window
+  const uint32_t *mask;  // (drafted) its words
+  bool on;               // a row of the item
+};
+template <int TN>
+__device__ __forceinline__ void sees(const AxParams &P, const Seq &s, const Row &row, int c0, uint32_t (&vis)[TN / 32]) {
+#pragma unroll
+  for (int w = 0; w < TN / 32; ++w) {
+    const int c = c0 + 32 * w;
+    const uint32_t win = P.window > 0 ? ~below(row.lo - c) | below(P.sinks - c) : 0xFFFFFFFFu;
+    if (P.masks) {
+      uint32_t v = below(s.ctx - c) & win;
+      const int j = c - s.ctx;  // the new token that bit 0 stands for
+      if (j > -32 && j < s.m) {
+        const int at = j >> 5, sh = j & 31, most = 2 * P.words;
+        const uint32_t w0 = at >= 0 && at < most ? row.mask[at] : 0u;
+        const uint32_t w1 = at + 1 >= 0 && at + 1 < most ? row.mask[at + 1] : 0u;
+        v |= __funnelshift_r(w0, w1, sh) & below(s.m - j) & ~below(-c);
+      }
+      vis[w] = v;
+    } else {
+      vis[w] = below(row.hi + 1 - c) & win;
     }
-    for (int x = 0; x < D / 32; ++x)
-      P.out[(row * P.Hq + h) * D + x * 32 + lane] = l == 0.f ? 0 : f32_to_bf16_rne(o[x] / l);
-    if (P.lse && lane == 0) P.lse[row * P.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
   }
 }
 
-size_t attn_extend_workspace(const k3moe_kv_cache &, int, int, int) { return 0; }
+}  // namespace
+
+// The pieces of the line: one block.
+template <int TN, int ROWS>
+__global__ void __launch_bounds__(1024) attn_plan_kernel(const AxParams P) {
+  __shared__ long long s_scan[32];
+  __shared__ long long s_carry;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  auto scan = [&](long long v, long long &before) {  // exclusive over the block, plus the carry; the carry grows
+    long long incl = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long w = s_scan[lane], wi = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long o = __shfl_up_sync(0xFFFFFFFFu, wi, off);
+      if (lane >= off) wi += o;
+    }
+    const long long warps_before = __shfl_sync(0xFFFFFFFFu, wi - w, warp), all = __shfl_sync(0xFFFFFFFFu, wi, 31);
+    before = s_carry + warps_before + incl - v;
+    __syncthreads();
+    if (tid == 0) s_carry += all;
+    __syncthreads();
+  };
+  if (tid == 0) s_carry = 0;
+  __syncthreads();
+  for (int b0 = 0; b0 < P.B; b0 += 1024) {
+    const int b = b0 + tid;
+    long long tiles = 0, before;
+    if (b < P.B) {
+      const Seq s = seq_of(P, b, true);
+      tiles = (static_cast<long long>(s.m) * P.G + ROWS - 1) / ROWS;
+    }
+    scan(tiles, before);
+    if (b < P.B) P.first_entry[b] = static_cast<int>(min(before, static_cast<long long>(P.entries)));
+  }
+  // (there is room for all unless the offsets descend, and sequences share rows)
+  const int entries = static_cast<int>(min(s_carry, static_cast<long long>(P.entries)));
+  if (tid == 0) P.first_entry[P.B] = entries;
+  __syncthreads();
+  if (tid == 0) s_carry = 0;
+  __syncthreads();
+  // the last sequence whose first entry is at most e
+  auto seq_at = [&](auto at_most) {
+    int lo = 0, hi = P.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at_most(mid))
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  };
+  for (int e0 = 0; e0 < entries; e0 += 1024) {
+    const int e = e0 + tid;
+    long long len = 0, before;
+    if (e < entries) {
+      const int b = seq_at([&](int x) { return P.first_entry[x] <= e; });
+      Walk<TN, ROWS> w;
+      w.s = seq_of(P, b, false);
+      w.t = e - P.first_entry[b];
+      w.measure(P);
+      len = w.length();
+    }
+    scan(len, before);
+    if (e < entries) P.prefix[e] = before;
+  }
+  if (tid == 0) P.prefix[entries] = s_carry;
+  __syncthreads();
+  const long long total = s_carry * P.heads, share = max(8LL, (total + P.blocks - 1) / P.blocks);
+  if (tid == 0) *P.plan = {total, share};
+  if (tid < P.blocks) {
+    P.meta[tid] = make_int4(0, 0, 0, 0);
+    const long long x = tid * share;
+    if (x < total) {
+      const int b = seq_at([&](int y) { return P.prefix[P.first_entry[y]] * P.heads <= x; });
+      const int f0 = P.first_entry[b], f1 = P.first_entry[b + 1];
+      const long long p0 = P.prefix[f0], len = P.prefix[f1] - p0, base = p0 * P.heads;
+      const int head = static_cast<int>((x - base) / len);
+      const long long at = x - base - head * len + p0;
+      int lo = f0, hi = f1 - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (P.prefix[mid] <= at)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      P.start[tid] = {base + head * len + P.prefix[lo] - p0, b, head, lo - f0, 0};
+    }
+  }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kAxThreads, 1)
+    attn_extend_kernel(const AxParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using S = AxShape<D, E4M3>;
+  constexpr int TN = S::TN, NS = S::NS, ROWS = S::ROWS, NK = S::NK, NV = S::NV, NR = S::NR > 0 ? S::NR : 1;
+  using W = Walk<TN, ROWS>;
+  extern __shared__ __align__(1024) uint8_t ax_smem[];
+  __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_ready[NV], v_empty[NV], r_full[NR], r_empty[NR];
+  __shared__ uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], o_done;
+  __shared__ uint32_t tmem_holder;
+  __shared__ uint64_t j_free, j_shown, j_read;  // the streams' joint: queries not needed, sums shown, sums read
+  __shared__ int s_odd[16];         // whether values that are not finite were left out of an item's products
+  __shared__ float2 s_other[128];  // the second stream's statistics
+  uint8_t *smem = ax_smem;
+  const uint32_t sbase = su32(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < NK; ++i) mb_init(&k_full[i], E4M3 ? 4 : 1), mb_init(&k_empty[i], 1);
+    for (int i = 0; i < NV; ++i) mb_init(&v_full[i], 1), mb_init(&v_ready[i], 4), mb_init(&v_empty[i], 1);
+    for (int i = 0; i < NR; ++i) mb_init(&r_full[i], 1), mb_init(&r_empty[i], 4);
+    for (int i = 0; i < 2; ++i) mb_init(&s_full[i], 1), mb_init(&p_ready[i], 4), mb_init(&o_full[i], 1), mb_init(&q_ready[i], 4);
+    mb_init(&o_done, 1), mb_init(&j_free, 4), mb_init(&j_shown, 4), mb_init(&j_read, 4);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < 16; ++i) s_odd[i] = 0;
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_holder)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  bool timeout = false;
+  pdl_wait();
+  pdl_trigger();
+
+  W it;
+  it.init(P, blockIdx.x);
+  // steps of an item: both streams at every tile, or where it has rows for one stream only, the streams in turn
+  auto both_of = [&](const W &w) { return NS == 2 && w.rows > 128; };
+
+  if (warp < 8) {
+    regs_up<176>();
+    const int st = warp >> 2;  // stream
+    const int lrow = 32 * (warp & 3) + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
+    const float c = flat ? 1.f : fabsf(P.scale) * kLog2e;
+    const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = flat ? 0u : 0xFFFFFFFFu;
+    uint32_t steps_done[2] = {0, 0};  // of each score buffer
+    uint32_t items = 0, finals = 0, pv = 0, joins = 0;
+    for (; it.more && st < NS && !timeout; it.next(P), ++items) {
+      const bool both = both_of(it);
+      const int r = (both ? 128 * st : 0) + lrow;  // row of the item
+      Row row;
+      row.on = r < it.rows;
+      const int i = min((it.r0 + r) / P.G, it.s.m - 1), g = (it.r0 + r) - (it.r0 + r) / P.G * P.G;
+      const long long grow = static_cast<long long>(it.s.first) + i;
+      // ---- queries
+      {
+        const int base = both ? 128 * st : 0;
+        constexpr int CH = D / 8;
+        for (int x = tid & 127; x < 128 * CH; x += 128) {
+          const int rr = x / CH, ch = x % CH, ir = it.r0 + base + rr;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (base + rr < it.rows) {
+            const int ii = ir / P.G, gg = ir - ii * P.G;
+            u = *reinterpret_cast<const uint4 *>(P.q + (static_cast<long long>(it.s.first) + ii) * P.q_stride +
+                                                 static_cast<size_t>(it.head * P.G + gg) * D + ch * 8);
+            u.x = (u.x ^ flip) & keep, u.y = (u.y ^ flip) & keep, u.z = (u.z ^ flip) & keep, u.w = (u.w ^ flip) & keep;
+          }
+          *reinterpret_cast<uint4 *>(smem + st * S::QB + (ch / 8) * (128 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u;
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&q_ready[st]);
+      }
+      int pos = it.s.ctx + i;
+      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? grow * P.words : 0));
+      if (P.masks) {
+        int seen = 0;
+        for (int w = 0; 32 * w < it.s.m; ++w) seen += __popc(row.mask[w] & below(it.s.m - 32 * w));
+        pos = it.s.ctx + max(0, seen - 1);
+      }
+      row.hi = pos;
+      row.lo = P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
+      const bool any_bad = any_lost<TN>(P, it.s, it.list, it.b, it.u0, it.u1);
+      const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < it.rows;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      const int T = it.u1 - it.u0, K = both ? 2 * T : T;
+      for (int k = NS == 2 ? st : 0; k < K; k += NS) {
+        const int sb = k & 1, tile = it.list.tile(it.u0 + (both ? k >> 1 : k));
+        if (!warp_wait(&s_full[sb], steps_done[sb] & 1u)) {
+          timeout = true;
+          break;
+        }
+        ++steps_done[sb];
+        tc_fence_after();
+        if (warp_on) {
+          float sc[TN];
+          const uint32_t sa = tmem + lane_addr + sb * S::S_COLS;
+#pragma unroll
+          for (int x = 0; x < TN; x += 32) tc_ld32(sa + x, sc + x);
+          tc_wait_ld(sc);
+          if (any_bad || masked<TN>(P, it.s, it.list, tile)) {
+            uint32_t vis[TN / 32];
+            sees<TN>(P, it.s, row, tile * TN, vis);
+            if (any_bad) {
+#pragma unroll
+              for (int x = 0; x < TN / 16; ++x)
+                if (lost16(P, it.s, it.list, it.b, tile * TN + 16 * x)) vis[x / 2] &= ~(0xFFFFu << (16 * (x & 1)));
+            }
+#pragma unroll
+            for (int x = 0; x < TN; ++x)
+              if (!((vis[x >> 5] >> (x & 31)) & 1u)) sc[x] = -INFINITY;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < TN; ++x) mx[x & 3] = fmaxf(mx[x & 3], sc[x]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (first) {
+            m = top;
+          } else {
+            const bool grows = (top - m) * c > kGrowth;
+            if (__any_sync(0xFFFFFFFFu, grows)) {
+              if (NS == 1 && !warp_wait(&o_done, (pv - 1) & 1u)) timeout = true;
+              tc_fence_after();
+              const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
+              m = mn;
+              l *= f;
+#pragma unroll 1
+              for (int x = 0; x < D; x += 32) {
+                float o[32];
+                const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS + x;
+                tc_ld32(oa, o);
+                tc_wait_ld(o);
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] *= f;
+                tc_st32r(oa, o);
+              }
+              tc_wait_st();
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : m * c;
+          float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < TN; x += 16) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int y = 0; y < 16; y += 2) {
+              const float p0 = ex2(fmaf(sc[x + y], c, -base)), p1 = ex2(fmaf(sc[x + y + 1], c, -base));
+              add[y & 3] += p0, add[(y & 3) + 1] += p1;
+              const uint32_t hi = bf16x2(p0, p1);
+              pk[y / 2] = hi;
+              pk[8 + y / 2] = bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+            }
+            tc_st16r(sa + x, pk);
+          }
+          l += (add[0] + add[1]) + (add[2] + add[3]);
+          tc_wait_st();
+        }
+        first = false;
+        ++pv;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&p_ready[sb]);
+      }
+      if (timeout) break;
+      // ---- the item's end
+      const bool had = !first;  // whether this stream had a step
+      if (had) {
+        if (!warp_wait(&o_full[st], finals & 1u)) {
+          timeout = true;
+          break;
+        }
+        ++finals;
+        tc_fence_after();
+      }
+      const bool odd = (s_odd[items & 15] & 1) != 0;
+      auto left_out = [&](float (&o)[32], int x0) {  // values that were left out of the products, added to rows that see them
+        for (int u = it.u0; u < it.u1; ++u) {
+          if (!both && NS == 2 && ((u - it.u0) & 1) != st) continue;
+          const int tile = it.list.tile(u);
+          if (!any_bad && !masked<TN>(P, it.s, it.list, tile)) continue;
+          uint32_t vis[TN / 32];
+          sees<TN>(P, it.s, row, tile * TN, vis);
+          for (int x = 0; x < TN; ++x) {
+            const int place = tile * TN + x;
+            if (!((vis[x >> 5] >> (x & 31)) & 1u) || place >= it.s.n) continue;
+            const int page = page_of(P, it.b, place);
+            if (!is_page(P, page)) continue;
+            const size_t vec = ((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) +
+                               (place & ((1 << P.page_shift) - 1));
+#pragma unroll
+            for (int y = 0; y < 32; ++y) {
+              float v;
+              if (E4M3) {
+                const uint32_t code = P.v[vec * D + x0 + y];
+                v = (code & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.f;
+                if (P.vs[vec] == 255) v = __uint_as_float(0x7FC00000u);
+                // (a product past the largest number: an infinity)
+                uint32_t a, z;
+                e4m3x4_to_f16x2(code, a, z);
+                const float w = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
+                if (isinf(w)) v = w;
+              } else {
+                v = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
+              }
+              if (!isfinite(v)) o[y] += v;
+            }
+          }
+        }
+      };
+      const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+      float mb = m == -INFINITY ? -INFINITY : m * c;
+      if (NS == 2 && !both) {  // join the streams: the second shows its sums where the queries were
+        float *shown = reinterpret_cast<float *>(smem);
+        if (st == 0) {
+          if (lane == 0) mb_arrive(&j_free);  // (all of this stream's products are complete)
+        } else {
+          if (!warp_wait(&j_free, joins & 1u)) {
+            timeout = true;
+            break;
+          }
+          s_other[lrow] = make_float2(mb, l);
+          if (had && warp_on) {
+#pragma unroll 1
+            for (int x = 0; x < D; x += 32) {
+              float o[32];
+              __syncwarp();
+              tc_ld32(oa + x, o);
+              tc_wait_ld(o);
+              if (odd && row.on) left_out(o, x);
+#pragma unroll
+              for (int y = 0; y < 32; ++y) shown[(x + y) * 128 + lrow] = o[y];
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mb_arrive(&j_shown);
+        }
+        if (st == 0 && !warp_wait(&j_shown, joins & 1u)) {
+          timeout = true;
+          break;
+        }
+      }
+      if (!(NS == 2 && !both && st == 1) && warp_on) {
+        float f0 = 1.f, f1 = 0.f;
+        const float *shown = reinterpret_cast<const float *>(smem);
+        const bool join = NS == 2 && !both && K > 1;
+        if (join) {
+          const float2 o = s_other[lrow];
+          const float mm = fmaxf(mb, o.x), base = mm == -INFINITY ? 0.f : mm;
+          f0 = ex2(mb - base), f1 = ex2(o.x - base);
+          l = l * f0 + o.y * f1;
+          mb = mm;
+        }
+        const bool cut = it.cut();
+        const int slot = 2 * blockIdx.x + (it.u0 > 0 ? 0 : 1);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t orow = static_cast<size_t>(grow) * P.Hq + it.head * P.G + g;
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+          float o[32];
+          __syncwarp();
+          tc_ld32(oa + x, o);
+          tc_wait_ld(o);
+          if (odd && row.on) left_out(o, x);
+          if (join) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = o[y] * f0 + shown[(x + y) * 128 + lrow] * f1;
+          }
+          if (row.on && cut) {
+            float *to = P.part + (static_cast<size_t>(slot) * D + x) * ROWS + r;
+#pragma unroll
+            for (int y = 0; y < 32; ++y) to[y * ROWS] = o[y];
+          } else if (row.on) {
+            uint4 *to = reinterpret_cast<uint4 *>(P.out + orow * D + x);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              uint32_t w[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                w[z] = l == 0.f ? 0u : bf16x2(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
+              to[y] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (row.on) {
+          if (cut)
+            P.stat[static_cast<size_t>(slot) * ROWS + r] = make_float2(mb, l);
+          else if (P.lse)
+            P.lse[orow] = l == 0.f ? -INFINITY : (mb + log2f(l)) * kLn2;
+        }
+      }
+      if (NS == 2 && !both) {  // the sums have been read: queries may come
+        __syncwarp();
+        if (st == 0 && lane == 0) mb_arrive(&j_read);
+        if (!warp_wait(&j_read, joins & 1u)) {
+          timeout = true;
+          break;
+        }
+        ++joins;
+      }
+      if (st == 0 && tid == 0 && it.u0 == 0 && it.u1 < it.list.units) {
+        const long long last = it.begin + kItemLen + static_cast<long long>(it.list.units - 1) * it.weight;
+        P.meta[blockIdx.x] = make_int4(it.b, it.head, it.t, static_cast<int>(last / P.plan->share) - blockIdx.x + 1);
+      }
+    }
+  } else if (warp < 12) {
+    regs_down<80>();
+    if (warp == 8 && lane == 0) {
+      // ---- products
+      uint32_t kt = 0, vt = 0, used[2] = {0, 0}, items = 0;
+      const uint32_t id_s = idesc(TN, false), id_o = idesc(D, true);
+      for (; it.more && !timeout; it.next(P), ++items) {
+        const bool both = both_of(it);
+        const int T = it.u1 - it.u0, K = both ? 2 * T : T;
+        const uint32_t k0 = kt, v0 = vt;
+        for (int s = 0; s < NS; ++s)
+          if (!mb_wait(&q_ready[s], items & 1u)) timeout = true;
+        if (timeout) break;
+        tc_fence_after();
+        auto scores = [&](int k) {
+          const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
+          const uint32_t t = k0 + (both ? k >> 1 : k), slot = t % NK;
+          if (!both || !(k & 1)) {
+            if (!mb_wait(&k_full[slot], (t / NK) & 1u)) return false;
+            tc_fence_after();
+          }
+          const uint32_t qa = sbase + st * S::QB, ka = sbase + S::OFF_K + slot * S::TILE;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x)
+            mma_ss(tmem + sb * S::S_COLS, smem_desc_sw128(qa + (x / 4) * (128 * 128) + (x % 4) * 32),
+                   smem_desc_sw128(ka + (x / 4) * (TN * 128) + (x % 4) * 32), id_s, x > 0);
+          if (!both || (k & 1)) tc_commit(&k_empty[slot]);
+          tc_commit(&s_full[sb]);
+          return true;
+        };
+        bool ok = scores(0) && (K < 2 || scores(1));
+        for (int k = 0; ok && k < K; ++k) {
+          const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
+          const uint32_t t = v0 + (both ? k >> 1 : k), slot = t % NV;
+          ok = mb_wait(&p_ready[sb], used[sb] & 1u);
+          if (!ok) break;
+          ++used[sb];
+          if (!both || !(k & 1)) ok = mb_wait(&v_ready[slot], (t / NV) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t va = sbase + S::OFF_V + slot * S::TILE, pa = tmem + sb * S::S_COLS;
+          const uint32_t oa = tmem + S::O_COL + st * S::O_COLS;
+          const bool begun = k >= NS;
+#pragma unroll
+          for (int x = 0; x < TN / 16; ++x) {
+            const uint64_t vd = values_desc(va + x * 2048, TN * 128);
+            mma_ts(oa, pa + x * 16, vd, id_o, x > 0 || begun);
+            mma_ts(oa, pa + x * 16 + 8, vd, id_o, 1);
+          }
+          if (!both || (k & 1)) tc_commit(&v_empty[slot]);
+          if (NS == 1) tc_commit(&o_done);
+          if (k + NS >= K) tc_commit(&o_full[st]);
+          if (k + 2 < K) ok = scores(k + 2);
+        }
+        if (!ok) timeout = true;
+        kt += T, vt += T;
+      }
+    } else if (warp == 9) {
+      // ---- loads
+      uint32_t kt = 0, vt = 0, rt = 0;
+      const int page_size = 1 << P.page_shift, run = min(page_size, TN), runs = TN / run;
+      constexpr int EB = E4M3 ? 1 : 2, BOX = D * EB < 128 ? D * EB : 128, BOXES = D * EB / BOX;  // bytes of a box's rows
+      for (; it.more && !timeout; it.next(P)) {
+        for (int u = it.u0; u < it.u1 && !timeout; ++u) {
+          const int tile = it.list.tile(u);
+          int page = P.pages;  // (past the end: the copy fills in zeros)
+          if (lane < runs) {
+            const int place = tile * TN + lane * run;
+            if (it.list.needs(it.s, place, run)) {
+              page = page_of(P, it.b, place);
+              if (!is_page(P, page)) {
+                set_status(P.status, K3MOE_DEV_BOUNDS);
+                page = P.pages;
+              }
+            }
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            uint64_t *full;
+            uint32_t dst;
+            bool ok = true;
+            if constexpr (E4M3) {
+              const uint32_t slot = rt % NR;
+              if (lane == 0) ok = mb_wait(&r_empty[slot], ((rt / NR) & 1u) ^ 1u);
+              full = &r_full[slot], dst = sbase + S::OFF_R + slot * S::RAWB;
+              ++rt;
+            } else if (kv == 0) {
+              const uint32_t slot = kt % NK;
+              if (lane == 0) ok = mb_wait(&k_empty[slot], ((kt / NK) & 1u) ^ 1u);
+              full = &k_full[slot], dst = sbase + S::OFF_K + slot * S::TILE;
+              ++kt;
+            } else {
+              const uint32_t slot = vt % NV;
+              if (lane == 0) ok = mb_wait(&v_empty[slot], ((vt / NV) & 1u) ^ 1u);
+              full = &v_full[slot], dst = sbase + S::OFF_V + slot * S::TILE;
+              ++vt;
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (!ok) {
+              timeout = true;
+              break;
+            }
+            const bool scales = E4M3 && page < P.pages;
+            const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, lane < runs && scales));
+            if (lane == 0) mb_arrive_tx(full, TN * D * EB + (E4M3 ? scaled * run : 0));
+            __syncwarp();
+            if (lane < runs) {
+              const int at = (tile * TN + lane * run) & (page_size - 1);
+#pragma unroll
+              for (int x = 0; x < BOXES; ++x)
+                tma_load_4d(dst + x * (TN * BOX) + lane * (run * BOX), kv ? &vmap : &kmap, x * (BOX / EB), at, it.head, page, full);
+              if (scales)
+                bulk_load(dst + S::RAW + lane * run,
+                          (kv ? P.vs : P.ks) + (((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) + at), run, full);
+            }
+          }
+        }
+      }
+      // every copy has landed before the block can leave
+      if (timeout && lane == 0) {
+        if constexpr (E4M3) {
+          for (uint32_t i = rt < NR ? 0 : rt - NR; i < rt; ++i) mb_wait(&r_full[i % NR], (i / NR) & 1u);
+        } else {
+          for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&k_full[i % NK], (i / NK) & 1u);
+          for (uint32_t i = vt < NV ? 0 : vt - NV; i < vt; ++i) mb_wait(&v_full[i % NV], (i / NV) & 1u);
+        }
+      }
+    }
+  } else {
+    regs_down<80>();
+    // ---- codes become operands; values that a row does not see must not be other than finite
+    const int t128 = tid - 384;
+    uint32_t kt = 0, vt = 0, rt = 0, items = 0;
+    for (; it.more && !timeout; it.next(P), ++items) {
+      if (t128 == 0) s_odd[(items + 8) & 15] = 0;
+      const bool any_bad = any_lost<TN>(P, it.s, it.list, it.b, it.u0, it.u1);
+      auto there = [&](int place) {
+        return it.list.needs(it.s, place & ~15, 16) && place < it.s.n && is_page(P, page_of(P, it.b, place));
+      };
+      for (int u = it.u0; u < it.u1 && !timeout; ++u) {
+        const int tile = it.list.tile(u);
+        const bool check = any_bad || masked<TN>(P, it.s, it.list, tile);
+#pragma unroll
+        for (int kv = E4M3 ? 0 : 1; kv < 2; ++kv) {
+          uint32_t op;
+          uint64_t *ready;
+          if constexpr (E4M3) {
+            const uint32_t rs = rt % NR;
+            if (!warp_wait(&r_full[rs], (rt / NR) & 1u)) timeout = true;
+            const uint32_t slot = kv ? vt % NV : kt % NK;
+            uint64_t *empty = kv ? &v_empty[slot] : &k_empty[slot];
+            if (!warp_wait(empty, (((kv ? vt / NV : kt / NK)) & 1u) ^ 1u)) timeout = true;
+            if (timeout) break;
+            ready = kv ? &v_ready[slot] : &k_full[slot];
+            op = (kv ? S::OFF_V : S::OFF_K) + slot * S::TILE;
+            const uint8_t *raw = smem + S::OFF_R + rs * S::RAWB, *scales = raw + S::RAW;
+            constexpr int BOX = D < 128 ? D : 128, CH = D / 16;  // chunks of 16 codes in a row
+            for (int x = t128; x < TN * CH; x += 128) {
+              const int rr = x / CH, ch = x % CH;
+              uint4 u4 = *reinterpret_cast<const uint4 *>(raw + (ch * 16 / BOX) * (TN * BOX) + rr * BOX + (ch * 16) % BOX);
+              uint32_t in[4] = {u4.x, u4.y, u4.z, u4.w}, h[8];
+              const int place = tile * TN + rr;
+              uint32_t byte = scales[rr];
+              if (check) {
+                if (!there(place)) byte = 127u, in[0] = in[1] = in[2] = in[3] = 0u;
+              }
+              // 2^(byte - 127 + 120) in two factors
+              const int e = static_cast<int>(byte) - 127, e1 = min(e, 7) + 120, e2 = e - min(e, 7);
+              uint32_t f1 = static_cast<uint32_t>(e1 + 127) << 7, f2 = static_cast<uint32_t>(e2 + 127) << 7;
+              if (byte == 255u) f1 = 0x7FC0u, f2 = 0x3F80u;
+              f1 |= f1 << 16, f2 |= f2 << 16;
+              uint32_t nan = 0;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                nan |= (in[y] & 0x7F7F7F7Fu) + 0x01010101u;
+                h[2 * y] = mul_bf16x2(codes_up(in[y], 0x1404), f1);
+                h[2 * y + 1] = mul_bf16x2(codes_up(in[y], 0x3424), f1);
+              }
+              if (e2 > 0 && byte != 255u) {
+#pragma unroll
+                for (int y = 0; y < 8; ++y) h[y] = mul_bf16x2(h[y], f2);
+              }
+              if (nan & 0x80808080u) {
+#pragma unroll
+                for (int y = 0; y < 16; ++y)
+                  if (((in[y / 4] >> (8 * (y & 3))) & 0x7Fu) == 0x7Fu)
+                    h[y / 2] = (h[y / 2] & (y & 1 ? 0xFFFFu : 0xFFFF0000u)) | (y & 1 ? 0x7FC00000u : 0x7FC0u);
+              }
+              if (kv && check) {
+                bool odd = false;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) {
+                  if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
+                  if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
+                }
+                if (odd) atomicOr(&s_odd[items & 15], 1);
+              }
+              uint8_t *to = smem + op + (ch / 4) * (TN * 128) + rr * 128;
+              const int c0 = (2 * ch) & 7, sw = (ch >> 2) & 1;
+              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+              *reinterpret_cast<uint4 *>(to + (((c0 + sw) ^ (rr & 7)) << 4)) = sw ? hi : lo;
+              *reinterpret_cast<uint4 *>(to + (((c0 + 1 - sw) ^ (rr & 7)) << 4)) = sw ? lo : hi;
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&r_empty[rs]);
+            ++rt;
+            kv ? ++vt : ++kt;
+          } else {
+            const uint32_t slot = vt % NV;
+            if (!warp_wait(&v_full[slot], (vt / NV) & 1u)) {
+              timeout = true;
+              break;
+            }
+            ready = &v_ready[slot];
+            op = S::OFF_V + slot * S::TILE;
+            ++vt;
+            if (check) {
+              constexpr int CH = D / 8;
+              for (int x = t128; x < TN * CH; x += 128) {
+                const int rr = x / CH, ch = x % CH, place = tile * TN + rr;
+                uint4 *at = reinterpret_cast<uint4 *>(smem + op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+                if (!there(place)) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                uint4 u4 = *at;
+                uint32_t h[4] = {u4.x, u4.y, u4.z, u4.w};
+                bool odd = false;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
+                  if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
+                }
+                if (odd) {
+                  *at = make_uint4(h[0], h[1], h[2], h[3]);
+                  atomicOr(&s_odd[items & 15], 1);
+                }
+              }
+              fence_async();
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mb_arrive(ready);
+        }
+      }
+    }
+  }
+  if (timeout) set_status(P.status, K3MOE_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+// Adds the parts of an item that was cut, in the order of their pieces: block (x, y) joins 32 rows of the item that
+// begins in piece x.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const int4 me = P.meta[blockIdx.x];
+  if (me.w < 2) return;
+  const Seq s = seq_of(P, me.x, false);
+  const int r0 = me.z * ROWS, rows = min(ROWS, s.m * P.G - r0), r = 32 * blockIdx.y + lane;
+  if (32 * static_cast<int>(blockIdx.y) >= rows) return;
+  auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
+  float mm = -INFINITY, l = 0.f;
+  for (int p = 0; p < me.w; ++p) mm = fmaxf(mm, P.stat[slot_of(p) * ROWS + r].x);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  for (int p = 0; p < me.w; ++p) {
+    const float2 st = P.stat[slot_of(p) * ROWS + r];
+    l = fmaf(st.y, ex2(st.x - base), l);
+  }
+  const int i = (r0 + r) / P.G, g = r0 + r - i * P.G;
+  const size_t row = (static_cast<size_t>(s.first) + i) * P.Hq + me.y * P.G + g;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int x = 8 * warp; x < D; x += 32) {
+    float o[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) o[y] = 0.f;
+    for (int p = 0; p < me.w; ++p) {
+      const size_t slot = slot_of(p);
+      const float f = ex2(P.stat[slot * ROWS + r].x - base);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] = fmaf(P.part[(slot * D + x + y) * ROWS + r], f, o[y]);
+    }
+    if (r < rows) {
+      uint32_t w[4];
+#pragma unroll
+      for (int z = 0; z < 4; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+      *reinterpret_cast<uint4 *>(P.out + row * D + x) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (P.lse && warp == 0 && r < rows) P.lse[row] = l == 0.f ? -INFINITY : (mm + log2f(l)) * kLn2;
+}
+
+namespace {
+
+int entries_of(int item, int B, int rows, int G) {
+  return static_cast<int>(static_cast<long long>(rows) * G / item + B);
+}
+size_t aligned256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+struct AxSpace {
+  size_t plan, start, meta, first_entry, prefix, stat, part, bytes;
+};
+AxSpace space_of(const k3moe_kv_cache &c, int B, int rows, int Hq) {
+  const int item = c.dim == 256 ? 128 : 256;
+  const size_t entries = static_cast<size_t>(entries_of(item, B, rows, Hq / c.heads)) + 1;
+  AxSpace s;
+  s.plan = 0;
+  s.start = 256;
+  s.meta = s.start + aligned256(kAxMostBlocks * sizeof(AxStart));
+  s.first_entry = s.meta + aligned256(kAxMostBlocks * sizeof(int4));
+  s.prefix = s.first_entry + aligned256((static_cast<size_t>(B) + 1) * 4);
+  s.stat = s.prefix + aligned256(entries * 8);
+  s.part = s.stat + aligned256(2 * kAxMostBlocks * item * sizeof(float2));
+  s.bytes = s.part + static_cast<size_t>(2) * kAxMostBlocks * item * c.dim * 4;
+  return s;
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static const EncodeTiledFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &st) != cudaSuccess ||
+        st != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// Boxes of 128 bytes (or a row) by min(page_size, TN) places of one head of a page.
+bool cache_map(CUtensorMap *m, const k3moe_kv_cache &c, void *base, int TN) {
+  const EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const bool e = c.format == K3MOE_KV_E4M3;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.dim) * (e ? 1 : 2);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t strides[3] = {row, row * c.page_size, row * c.page_size * c.heads};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(e ? (c.dim < 128 ? c.dim : 128) : 64),
+                             static_cast<cuuint32_t>(c.page_size < TN ? c.page_size : TN), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return fn(m, e ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, e ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+template <int D, bool E4M3>
+int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
+  using S = AxShape<D, E4M3>;
+  static_assert(S::SMEM <= 232448 - 2048, "shared memory of a block");
+  CUtensorMap kmap, vmap;
+  if (!cache_map(&kmap, c, c.k, S::TN) || !cache_map(&vmap, c, c.v, S::TN)) return -1;
+  static PerDevice raised;
+  cudaError_t err = cudaSuccess;
+  raised.get(current_device(), [&] {
+    err = cudaFuncSetAttribute(attn_extend_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    return err == cudaSuccess ? 1 : -1;
+  });
+  if (err != cudaSuccess) return -1;
+  P.blocks = min(sm_count(), kAxMostBlocks);
+  P.entries = entries_of(S::ROWS, P.B, P.rows, P.G);
+  if (launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
+  if (launch_pdl(attn_extend_kernel<D, E4M3>, dim3(P.blocks), dim3(kAxThreads), S::SMEM, st, P, kmap, vmap) != cudaSuccess)
+    return -1;
+  return launch_pdl(attn_extend_join_kernel<D, S::ROWS>, dim3(P.blocks, S::ROWS / 32), dim3(128), 0, st, P) == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq) { return space_of(c, B, rows, Hq).bytes; }
 
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   AxParams P;
@@ -124,14 +1158,16 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   P.q = a.q, P.q_stride = a.q_stride, P.offsets = a.offsets, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
   P.table = a.table, P.max_pages = a.max_pages, P.lens = a.lens, P.window = a.window, P.sinks = a.sinks;
   P.scale = a.scale, P.out = a.out, P.lse = a.lse, P.status = a.status;
-  const dim3 grid(a.B, a.Hq, a.max_new > 64 ? 32 : 1);
+  const AxSpace s = space_of(c, a.B, a.rows, a.Hq);
+  uint8_t *w = static_cast<uint8_t *>(a.ws);
+  P.plan = reinterpret_cast<AxPlan *>(w + s.plan), P.start = reinterpret_cast<AxStart *>(w + s.start);
+  P.meta = reinterpret_cast<int4 *>(w + s.meta), P.first_entry = reinterpret_cast<int *>(w + s.first_entry);
+  P.prefix = reinterpret_cast<long long *>(w + s.prefix), P.stat = reinterpret_cast<float2 *>(w + s.stat);
+  P.part = reinterpret_cast<float *>(w + s.part);
   const bool e = c.format == K3MOE_KV_E4M3;
-#define K3_AX(D_)                                                                                              \
-  if (c.dim == D_)                                                                                             \
-    return launch_pdl(e ? attn_extend_simple<D_, true> : attn_extend_simple<D_, false>, grid, dim3(256), 0, st, P) == \
-                   cudaSuccess ? 0 : -1;
-  K3_AX(64) K3_AX(128) K3_AX(256)
-#undef K3_AX
+  if (c.dim == 64) return e ? launch_extend<64, true>(c, P, st) : launch_extend<64, false>(c, P, st);
+  if (c.dim == 128) return e ? launch_extend<128, true>(c, P, st) : launch_extend<128, false>(c, P, st);
+  if (c.dim == 256) return e ? launch_extend<256, true>(c, P, st) : launch_extend<256, false>(c, P, st);
   return -1;
 }
 

@@ -411,7 +411,8 @@ int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const ui
 }
 
 size_t k3moe_attn_extend_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq) {
-  return attn_check(cache, B, Hq) || rows < 0 ? 0 : k3moe::attn_extend_workspace(*cache, B, rows, Hq);
+  if (attn_check(cache, B, Hq) || rows < 0 || static_cast<long long>(rows) * (Hq / cache->heads) >= (1LL << 31)) return 0;
+  return k3moe::attn_extend_workspace(*cache, B, rows, Hq);
 }
 
 // What k3moe_attn_extend and k3moe_attn_tree check alike; a.c is the cache's where it is not null.
@@ -420,7 +421,8 @@ static int extend_run(const k3moe_kv_cache *cache, k3moe::ExtendArgs &a, size_t 
   if (rc) return rc;
   a.c = *cache;
   if (a.rows < 0 || a.max_pages < 1 || a.window < 0 || a.sinks < 0) return K3MOE_ERR_SHAPE;
-  if (static_cast<long long>(a.max_pages) * cache->page_size >= (1LL << 31)) return K3MOE_ERR_SHAPE;
+  if (static_cast<long long>(a.max_pages) * cache->page_size > (1LL << 31) - 1024) return K3MOE_ERR_SHAPE;
+  if (static_cast<long long>(a.rows) * (a.Hq / cache->heads) >= (1LL << 31)) return K3MOE_ERR_SHAPE;
   if (!std::isfinite(a.scale)) return K3MOE_ERR_ARG;
   if (a.B == 0 || a.rows == 0) return K3MOE_OK;
   if (a.max_new < 1) return K3MOE_ERR_SHAPE;
