@@ -223,20 +223,29 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
 // A wait of a whole warp, with one answer.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mb_wait(bar, parity));
 }
 __device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u; }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
@@ -261,16 +270,32 @@ __device__ __forceinline__ uint64_t values_desc(uint32_t saddr, uint32_t block) 
   return static_cast<uint64_t>((saddr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-               "l"(a), "l"(b), "r"(id), "r"(acc)
-               : "memory");
+// Four products of 16 dimensions each: descriptors 32 bytes further each; the first one adds where `acc` is not 0.
+__device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %3, %3;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
+      "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
-                   d),
-               "r"(a), "l"(b), "r"(id), "r"(acc)
-               : "memory");
+// Weights of 32 places (as two numbers, 8 columns each by 16 places) with their values, 2048 bytes each 16.
+__device__ __forceinline__ void mma4_values(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %3, %3;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u64 b1, %2, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, q;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b1, %3, q;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %3, q;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
 }
 // 32 columns of this thread's lane; the values are there after tc_wait_ld.
 __device__ __forceinline__ void tc_ld32(uint32_t taddr, float *v) {
@@ -289,14 +314,6 @@ __device__ __forceinline__ void tc_wait_ld(float (&v)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));  // (uses stay behind the wait)
 }
-__device__ __forceinline__ void tc_st16r(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tc_st32r(uint32_t taddr, const float *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -306,6 +323,12 @@ __device__ __forceinline__ void tc_st32r(uint32_t taddr, const float *r) {
       "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
       "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
       : "memory");
+}
+__device__ __forceinline__ void tc_st32u(uint32_t taddr, const uint32_t (&r)[32]) {
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+  tc_st32r(taddr, f);
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -321,32 +344,25 @@ __device__ __forceinline__ uint32_t codes_up(uint32_t w, uint32_t sel) {
   return ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
 }
 
-// What a row sees of a tile, bit x for place c0 + x.
+// What a row sees.
 struct Row {
   int hi, lo;            // (causal) last place seen; first of the window
   const uint32_t *mask;  // (drafted) its words
   bool on;               // a row of the item
 };
-template <int TN>
-__device__ __forceinline__ void sees(const AxParams &P, const Seq &s, const Row &row, int c0, uint32_t (&vis)[TN / 32]) {
-#pragma unroll
-  for (int w = 0; w < TN / 32; ++w) {
-    const int c = c0 + 32 * w;
-    const uint32_t win = P.window > 0 ? ~below(row.lo - c) | below(P.sinks - c) : 0xFFFFFFFFu;
-    if (P.masks) {
-      uint32_t v = below(s.ctx - c) & win;
-      const int j = c - s.ctx;  // the new token that bit 0 stands for
-      if (j > -32 && j < s.m) {
-        const int at = j >> 5, sh = j & 31, most = 2 * P.words;
-        const uint32_t w0 = at >= 0 && at < most ? row.mask[at] : 0u;
-        const uint32_t w1 = at + 1 >= 0 && at + 1 < most ? row.mask[at + 1] : 0u;
-        v |= __funnelshift_r(w0, w1, sh) & below(s.m - j) & ~below(-c);
-      }
-      vis[w] = v;
-    } else {
-      vis[w] = below(row.hi + 1 - c) & win;
-    }
+// The 32 places from c on, of which bit x stands for c + x.
+__device__ __forceinline__ uint32_t sees(const AxParams &P, const Seq &s, const Row &row, int c) {
+  const uint32_t win = P.window > 0 ? ~below(row.lo - c) | below(P.sinks - c) : 0xFFFFFFFFu;
+  if (!P.masks) return below(row.hi + 1 - c) & win;
+  uint32_t v = below(s.ctx - c) & win;
+  const int j = c - s.ctx;  // the new token that bit 0 stands for
+  if (j > -32 && j < s.m) {
+    const int at = j >> 5, most = 2 * P.words;
+    const uint32_t w0 = at >= 0 && at < most ? row.mask[at] : 0u;
+    const uint32_t w1 = at + 1 >= 0 && at + 1 < most ? row.mask[at + 1] : 0u;
+    v |= __funnelshift_r(w0, w1, j & 31) & below(s.m - j);
   }
+  return v;
 }
 
 }  // namespace
@@ -494,7 +510,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
   auto both_of = [&](const W &w) { return NS == 2 && w.rows > 128; };
 
   if (warp < 8) {
-    regs_up<176>();
     const int st = warp >> 2;  // stream
     const int lrow = 32 * (warp & 3) + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -552,27 +567,31 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         ++steps_done[sb];
         tc_fence_after();
         if (warp_on) {
-          float sc[TN];
           const uint32_t sa = tmem + lane_addr + sb * S::S_COLS;
+          float sc[32];
+          float top = -INFINITY;
+          const bool some = any_bad || masked<TN>(P, it.s, it.list, tile);
+#pragma unroll 1
+          for (int x = 0; x < TN; x += 32) {
+            tc_ld32(sa + x, sc);
+            tc_wait_ld(sc);
+            if (some) {
+              uint32_t vis = sees(P, it.s, row, tile * TN + x);
+              if (any_bad) {
+                if (lost16(P, it.s, it.list, it.b, tile * TN + x)) vis &= 0xFFFF0000u;
+                if (lost16(P, it.s, it.list, it.b, tile * TN + x + 16)) vis &= 0xFFFFu;
+              }
 #pragma unroll
-          for (int x = 0; x < TN; x += 32) tc_ld32(sa + x, sc + x);
-          tc_wait_ld(sc);
-          if (any_bad || masked<TN>(P, it.s, it.list, tile)) {
-            uint32_t vis[TN / 32];
-            sees<TN>(P, it.s, row, tile * TN, vis);
-            if (any_bad) {
-#pragma unroll
-              for (int x = 0; x < TN / 16; ++x)
-                if (lost16(P, it.s, it.list, it.b, tile * TN + 16 * x)) vis[x / 2] &= ~(0xFFFFu << (16 * (x & 1)));
+              for (int y = 0; y < 32; ++y)
+                if (!((vis >> y) & 1u)) sc[y] = -INFINITY;
+              tc_st32r(sa + x, sc);
             }
+            float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int x = 0; x < TN; ++x)
-              if (!((vis[x >> 5] >> (x & 31)) & 1u)) sc[x] = -INFINITY;
+            for (int y = 0; y < 32; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(sc[y], sc[y + 1]), mx[(y / 2) & 3]);
+            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int x = 0; x < TN; ++x) mx[x & 3] = fmaxf(mx[x & 3], sc[x]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          if (some) tc_wait_st();
           if (first) {
             m = top;
           } else {
@@ -593,25 +612,29 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                 for (int y = 0; y < 32; ++y) o[y] *= f;
                 tc_st32r(oa, o);
               }
-              tc_wait_st();
             }
           }
           const float base = m == -INFINITY ? 0.f : m * c;
-          float add[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int x = 0; x < TN; x += 32) {
+            tc_ld32(sa + x, sc);
+            tc_wait_ld(sc);
+            uint32_t pk[32];
 #pragma unroll
-          for (int x = 0; x < TN; x += 16) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int y = 0; y < 16; y += 2) {
-              const float p0 = ex2(fmaf(sc[x + y], c, -base)), p1 = ex2(fmaf(sc[x + y + 1], c, -base));
-              add[y & 3] += p0, add[(y & 3) + 1] += p1;
-              const uint32_t hi = bf16x2(p0, p1);
-              pk[y / 2] = hi;
-              pk[8 + y / 2] = bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+            for (int y = 0; y < 32; y += 2) {
+              const float2 e = fma2(make_float2(sc[y], sc[y + 1]), c2, b2), p = make_float2(ex2(e.x), ex2(e.y));
+              add[(y / 2) & 1] = add2(add[(y / 2) & 1], p);
+              const uint32_t hi = bf16x2(p.x, p.y);
+              const float2 r = add2(p, make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u)));
+              const int at = (y & 16) + (y & 15) / 2;
+              pk[at] = hi;
+              pk[at + 8] = bf16x2(r.x, r.y);
             }
-            tc_st16r(sa + x, pk);
+            tc_st32u(sa + x, pk);
           }
-          l += (add[0] + add[1]) + (add[2] + add[3]);
+          l += (add[0].x + add[0].y) + (add[1].x + add[1].y);
           tc_wait_st();
         }
         first = false;
@@ -631,42 +654,47 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         ++finals;
         tc_fence_after();
       }
-      const bool odd = (s_odd[items & 15] & 1) != 0;
-      auto left_out = [&](float (&o)[32], int x0) {  // values that were left out of the products, added to rows that see them
-        for (int u = it.u0; u < it.u1; ++u) {
-          if (!both && NS == 2 && ((u - it.u0) & 1) != st) continue;
-          const int tile = it.list.tile(u);
-          if (!any_bad && !masked<TN>(P, it.s, it.list, tile)) continue;
-          uint32_t vis[TN / 32];
-          sees<TN>(P, it.s, row, tile * TN, vis);
-          for (int x = 0; x < TN; ++x) {
-            const int place = tile * TN + x;
-            if (!((vis[x >> 5] >> (x & 31)) & 1u) || place >= it.s.n) continue;
-            const int page = page_of(P, it.b, place);
-            if (!is_page(P, page)) continue;
-            const size_t vec = ((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) +
-                               (place & ((1 << P.page_shift) - 1));
+      const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+      if ((s_odd[items & 15] & 1) && had && warp_on) {
+        // values that were left out of the products are added to the rows that see them
+#pragma unroll 1
+        for (int x0 = 0; x0 < D; x0 += 32) {
+          float o[32];
+          __syncwarp();
+          tc_ld32(oa + x0, o);
+          tc_wait_ld(o);
+#pragma unroll 1
+          for (int u = it.u0; u < it.u1; ++u) {
+            const int tile = it.list.tile(u);
+            if ((!both && NS == 2 && ((u - it.u0) & 1) != st) || !row.on) continue;
+            if (!any_bad && !masked<TN>(P, it.s, it.list, tile)) continue;
+#pragma unroll 1
+            for (int x = 0; x < TN; ++x) {
+              const int place = tile * TN + x;
+              if (!(sees(P, it.s, row, place) & 1u) || place >= it.s.n) continue;
+              const int page = page_of(P, it.b, place);
+              if (!is_page(P, page)) continue;
+              const size_t vec = ((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) +
+                                 (place & ((1 << P.page_shift) - 1));
 #pragma unroll
-            for (int y = 0; y < 32; ++y) {
-              float v;
-              if (E4M3) {
-                const uint32_t code = P.v[vec * D + x0 + y];
-                v = (code & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.f;
-                if (P.vs[vec] == 255) v = __uint_as_float(0x7FC00000u);
-                // (a product past the largest number: an infinity)
-                uint32_t a, z;
-                e4m3x4_to_f16x2(code, a, z);
-                const float w = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
-                if (isinf(w)) v = w;
-              } else {
-                v = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
+              for (int y = 0; y < 32; ++y) {
+                float v;
+                if (E4M3) {
+                  uint32_t a, z;
+                  e4m3x4_to_f16x2(P.v[vec * D + x0 + y], a, z);
+                  v = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
+                } else {
+                  v = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
+                }
+                if (!isfinite(v)) o[y] += v;
               }
-              if (!isfinite(v)) o[y] += v;
             }
           }
+          __syncwarp();
+          tc_st32r(oa + x0, o);
         }
-      };
-      const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+        tc_wait_st();
+      }
       float mb = m == -INFINITY ? -INFINITY : m * c;
       if (NS == 2 && !both) {  // join the streams: the second shows its sums where the queries were
         float *shown = reinterpret_cast<float *>(smem);
@@ -685,7 +713,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               __syncwarp();
               tc_ld32(oa + x, o);
               tc_wait_ld(o);
-              if (odd && row.on) left_out(o, x);
 #pragma unroll
               for (int y = 0; y < 32; ++y) shown[(x + y) * 128 + lrow] = o[y];
             }
@@ -719,7 +746,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           __syncwarp();
           tc_ld32(oa + x, o);
           tc_wait_ld(o);
-          if (odd && row.on) left_out(o, x);
           if (join) {
 #pragma unroll
             for (int y = 0; y < 32; ++y) o[y] = o[y] * f0 + shown[(x + y) * 128 + lrow] * f1;
@@ -762,7 +788,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       }
     }
   } else if (warp < 12) {
-    regs_down<80>();
     if (warp == 8 && lane == 0) {
       // ---- products
       uint32_t kt = 0, vt = 0, used[2] = {0, 0}, items = 0;
@@ -783,10 +808,10 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             tc_fence_after();
           }
           const uint32_t qa = sbase + st * S::QB, ka = sbase + S::OFF_K + slot * S::TILE;
+          const uint64_t qd = smem_desc_sw128(qa), kd = smem_desc_sw128(ka);
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x)
-            mma_ss(tmem + sb * S::S_COLS, smem_desc_sw128(qa + (x / 4) * (128 * 128) + (x % 4) * 32),
-                   smem_desc_sw128(ka + (x / 4) * (TN * 128) + (x % 4) * 32), id_s, x > 0);
+          for (int x = 0; x < D / 64; ++x)
+            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
           if (!both || (k & 1)) tc_commit(&k_empty[slot]);
           tc_commit(&s_full[sb]);
           return true;
@@ -804,12 +829,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           const uint32_t va = sbase + S::OFF_V + slot * S::TILE, pa = tmem + sb * S::S_COLS;
           const uint32_t oa = tmem + S::O_COL + st * S::O_COLS;
           const bool begun = k >= NS;
+          const uint64_t vd = values_desc(va, TN * 128);
 #pragma unroll
-          for (int x = 0; x < TN / 16; ++x) {
-            const uint64_t vd = values_desc(va + x * 2048, TN * 128);
-            mma_ts(oa, pa + x * 16, vd, id_o, x > 0 || begun);
-            mma_ts(oa, pa + x * 16 + 8, vd, id_o, 1);
-          }
+          for (int x = 0; x < TN / 32; ++x) mma4_values(oa, pa + x * 32, vd + x * (4096 / 16), id_o, x > 0 || begun);
           if (!both || (k & 1)) tc_commit(&v_empty[slot]);
           if (NS == 1) tc_commit(&o_done);
           if (k + NS >= K) tc_commit(&o_full[st]);
@@ -890,7 +912,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       }
     }
   } else {
-    regs_down<80>();
     // ---- codes become operands; values that a row does not see must not be other than finite
     const int t128 = tid - 384;
     uint32_t kt = 0, vt = 0, rt = 0, items = 0;
