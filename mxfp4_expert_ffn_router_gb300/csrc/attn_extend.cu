@@ -16,7 +16,7 @@ constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
 constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrowth = 8.f;     // a row's sums are rescaled once its maximum has grown by 2^8
+constexpr float kGrowth = 16.f;    // a row's reference moves once a weight would pass 2^16
 
 struct AxStart {  // where a block's piece of the line begins
   long long begin;  // of the item that it begins in
@@ -568,66 +568,84 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         tc_fence_after();
         if (warp_on) {
           const uint32_t sa = tmem + lane_addr + sb * S::S_COLS;
-          float sc[32];
-          float top = -INFINITY;
           const bool some = any_bad || masked<TN>(P, it.s, it.list, tile);
+          float base = m == -INFINITY ? 0.f : m * c;
+          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // the row's reference moves up to mx: sums, and the weights of the x places before, by the quotient
+          auto grow = [&](float mx, int x) {
+            const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
+            m = mn;
+            base = m == -INFINITY ? 0.f : m * c;
+            l *= f;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) add[y].x *= f, add[y].y *= f;
+            float o[32];
 #pragma unroll 1
-          for (int x = 0; x < TN; x += 32) {
-            tc_ld32(sa + x, sc);
-            tc_wait_ld(sc);
-            if (some) {
+            for (int y = 0; y < x; y += 32) {
+              tc_ld32(sa + y, o);
+              tc_wait_ld(o);
+#pragma unroll
+              for (int z = 0; z < 32; z = z % 16 == 7 ? z + 9 : z + 1) {
+                const uint32_t hi = __float_as_uint(o[z]), lo = __float_as_uint(o[z + 8]);
+                const float p0 = (__uint_as_float(hi << 16) + __uint_as_float(lo << 16)) * f;
+                const float p1 = (__uint_as_float(hi & 0xFFFF0000u) + __uint_as_float(lo & 0xFFFF0000u)) * f;
+                const uint32_t h = bf16x2(p0, p1);
+                o[z] = __uint_as_float(h);
+                o[z + 8] = __uint_as_float(bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u)));
+              }
+              tc_st32r(sa + y, o);
+            }
+            if (!first) {
+              if (NS == 1 && !warp_wait(&o_done, (pv - 1) & 1u)) timeout = true;
+              tc_fence_after();
+              const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+#pragma unroll 1
+              for (int y = 0; y < D; y += 32) {
+                tc_ld32(oa + y, o);
+                tc_wait_ld(o);
+#pragma unroll
+                for (int z = 0; z < 32; ++z) o[z] *= f;
+                tc_st32r(oa + y, o);
+              }
+            }
+            tc_wait_st();
+          };
+          float v[32];
+          if (some) {
+#pragma unroll 1
+            for (int x = 0; x < TN; x += 32) {
+              tc_ld32(sa + x, v);
               uint32_t vis = sees(P, it.s, row, tile * TN + x);
               if (any_bad) {
                 if (lost16(P, it.s, it.list, it.b, tile * TN + x)) vis &= 0xFFFF0000u;
                 if (lost16(P, it.s, it.list, it.b, tile * TN + x + 16)) vis &= 0xFFFFu;
               }
+              tc_wait_ld(v);
 #pragma unroll
               for (int y = 0; y < 32; ++y)
-                if (!((vis >> y) & 1u)) sc[y] = -INFINITY;
-              tc_st32r(sa + x, sc);
+                if (!((vis >> y) & 1u)) v[y] = -INFINITY;
+              tc_st32r(sa + x, v);
             }
-            float mx[4] = {top, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int y = 0; y < 32; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(sc[y], sc[y + 1]), mx[(y / 2) & 3]);
-            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            tc_wait_st();
           }
-          if (some) tc_wait_st();
-          if (first) {
-            m = top;
-          } else {
-            const bool grows = (top - m) * c > kGrowth;
-            if (__any_sync(0xFFFFFFFFu, grows)) {
-              if (NS == 1 && !warp_wait(&o_done, (pv - 1) & 1u)) timeout = true;
-              tc_fence_after();
-              const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
-              m = mn;
-              l *= f;
-#pragma unroll 1
-              for (int x = 0; x < D; x += 32) {
-                float o[32];
-                const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS + x;
-                tc_ld32(oa, o);
-                tc_wait_ld(o);
-#pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] *= f;
-                tc_st32r(oa, o);
-              }
-            }
-          }
-          const float base = m == -INFINITY ? 0.f : m * c;
-          const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // 32 places at a time: scores in, weights out (in place)
 #pragma unroll 1
           for (int x = 0; x < TN; x += 32) {
-            tc_ld32(sa + x, sc);
-            tc_wait_ld(sc);
+            tc_ld32(sa + x, v);
+            tc_wait_ld(v);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(v[y], v[y + 1]), mx[(y / 2) & 3]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            if (__any_sync(0xFFFFFFFFu, (top - m) * c > kGrowth)) grow(top, x);
+            const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base), less = make_float2(-1.f, -1.f);
             uint32_t pk[32];
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
-              const float2 e = fma2(make_float2(sc[y], sc[y + 1]), c2, b2), p = make_float2(ex2(e.x), ex2(e.y));
+              const float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2), p = make_float2(ex2(e.x), ex2(e.y));
               add[(y / 2) & 1] = add2(add[(y / 2) & 1], p);
               const uint32_t hi = bf16x2(p.x, p.y);
-              const float2 r = add2(p, make_float2(-__uint_as_float(hi << 16), -__uint_as_float(hi & 0xFFFF0000u)));
+              const float2 r = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), less, p);
               const int at = (y & 16) + (y & 15) / 2;
               pk[at] = hi;
               pk[at + 8] = bf16x2(r.x, r.y);
