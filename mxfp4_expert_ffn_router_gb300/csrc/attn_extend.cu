@@ -270,31 +270,44 @@ __device__ __forceinline__ uint64_t values_desc(uint32_t saddr, uint32_t block) 
   return static_cast<uint64_t>((saddr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
+// The products are issued by one elected thread of a warp that runs converged, so that the operands' addresses stay in
+// uniform registers: issued from a branch of lane 0 they cost about ten instructions a product, and the tensor
+// cores waited for those.
+//
 // Four products of 16 dimensions each: descriptors 32 bytes further each; the first one adds where `acc` is not 0.
 __device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %3, %3;\n\t"
       "add.u64 a1, %1, 2;\n\tadd.u64 a2, %1, 4;\n\tadd.u64 a3, %1, 6;\n\t"
       "add.u64 b1, %2, 2;\n\tadd.u64 b2, %2, 4;\n\tadd.u64 b3, %2, 6;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 // Weights of 32 places (as two numbers, 8 columns each by 16 places) with their values, 2048 bytes each 16.
 __device__ __forceinline__ void mma4_values(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %3, %3;\n\t"
       "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u64 b1, %2, 128;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, q;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b1, %3, q;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %3, q;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %3, q;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// tc_commit from the elected thread of a converged warp.
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(su32(bar))
       : "memory");
 }
 // 32 columns of this thread's lane; the values are there after tc_wait_ld.
@@ -806,7 +819,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       }
     }
   } else if (warp < 12) {
-    if (warp == 8 && lane == 0) {
+    if (warp == 8) {
       // ---- products
       uint32_t kt = 0, vt = 0, used[2] = {0, 0}, items = 0;
       const uint32_t id_s = idesc(TN, false), id_o = idesc(D, true);
@@ -815,14 +828,14 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         const int T = it.u1 - it.u0, K = both ? 2 * T : T;
         const uint32_t k0 = kt, v0 = vt;
         for (int s = 0; s < NS; ++s)
-          if (!mb_wait(&q_ready[s], items & 1u)) timeout = true;
+          if (!warp_wait(&q_ready[s], items & 1u)) timeout = true;
         if (timeout) break;
         tc_fence_after();
         auto scores = [&](int k) {
           const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
           const uint32_t t = k0 + (both ? k >> 1 : k), slot = t % NK;
           if (!both || !(k & 1)) {
-            if (!mb_wait(&k_full[slot], (t / NK) & 1u)) return false;
+            if (!warp_wait(&k_full[slot], (t / NK) & 1u)) return false;
             tc_fence_after();
           }
           const uint32_t qa = sbase + st * S::QB, ka = sbase + S::OFF_K + slot * S::TILE;
@@ -830,18 +843,18 @@ __global__ void __launch_bounds__(kAxThreads, 1)
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
             mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
-          if (!both || (k & 1)) tc_commit(&k_empty[slot]);
-          tc_commit(&s_full[sb]);
+          if (!both || (k & 1)) commit(&k_empty[slot]);
+          commit(&s_full[sb]);
           return true;
         };
         bool ok = scores(0) && (K < 2 || scores(1));
         for (int k = 0; ok && k < K; ++k) {
           const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
           const uint32_t t = v0 + (both ? k >> 1 : k), slot = t % NV;
-          ok = mb_wait(&p_ready[sb], used[sb] & 1u);
+          ok = warp_wait(&p_ready[sb], used[sb] & 1u);
           if (!ok) break;
           ++used[sb];
-          if (!both || !(k & 1)) ok = mb_wait(&v_ready[slot], (t / NV) & 1u);
+          if (!both || !(k & 1)) ok = warp_wait(&v_ready[slot], (t / NV) & 1u);
           if (!ok) break;
           tc_fence_after();
           const uint32_t va = sbase + S::OFF_V + slot * S::TILE, pa = tmem + sb * S::S_COLS;
@@ -850,9 +863,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           const uint64_t vd = values_desc(va, TN * 128);
 #pragma unroll
           for (int x = 0; x < TN / 32; ++x) mma4_values(oa, pa + x * 32, vd + x * (4096 / 16), id_o, x > 0 || begun);
-          if (!both || (k & 1)) tc_commit(&v_empty[slot]);
-          if (NS == 1) tc_commit(&o_done);
-          if (k + NS >= K) tc_commit(&o_full[st]);
+          if (!both || (k & 1)) commit(&v_empty[slot]);
+          if (NS == 1) commit(&o_done);
+          if (k + NS >= K) commit(&o_full[st]);
           if (k + 2 < K) ok = scores(k + 2);
         }
         if (!ok) timeout = true;
