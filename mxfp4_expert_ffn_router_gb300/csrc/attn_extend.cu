@@ -11,7 +11,7 @@ namespace k3moe {
 
 namespace {
 
-constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 MMA, 9 loads, 12-15 values
+constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 scores, 9 loads, 10 sums, 12-15 values
 constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
 constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
 constexpr float kLog2e = 1.4426950408889634f;
@@ -49,9 +49,10 @@ struct AxParams {
   int4 *meta;        // [blocks]: {sequence, head, tile, parts} of the item that begins in the block's piece and goes on
   int *first_entry;  // [B + 1]
   long long *prefix; // [entries + 1]
-  float2 *stat;      // [2 blocks][rows of a tile]
+  float4 *stat;      // [2 blocks][rows of a tile]: reference, sum of the weights, of the rounded ones
   float *part;       // [2 blocks][dim][rows of a tile]
   int blocks, entries;  // pieces; room for the tiles of query rows
+  uint32_t per_head;    // ceil(2^32 / G) (token_of)
 };
 
 struct Seq {
@@ -76,6 +77,19 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
   return s;
 }
 
+// What a block's warps share besides the tiles.
+template <int NK, int NV, int NR>
+struct AxShared {
+  uint64_t k_full[NK], k_empty[NK], v_full[NV], v_ready[NV], v_empty[NV], r_full[NR], r_empty[NR];
+  uint64_t s_full[2], p_ready[2], pv_done[2], q_ready[2];
+  uint64_t j_shown, j_read;  // the streams' joint: sums shown, sums read
+  float2 stat[2][128];       // the streams' statistics: reference, sum of the rounded weights
+  float sum1[128];           // the second stream's sum of the weights
+  uint8_t lost[16];  // of a tile: bit x for the 16 places from 16 x on that lie in no page of the cache
+  uint32_t odd;      // bit x: values that are not finite were left out of item x's products
+  uint32_t tmem;
+};
+
 template <int D, bool E4M3>
 struct AxShape {
   static constexpr int TN = D == 256 ? 64 : 128;   // places of a tile
@@ -89,7 +103,9 @@ struct AxShape {
   static constexpr int NR = E4M3 ? (D == 64 ? 4 : 2) : 0;
   static constexpr int RAWB = RAW + (E4M3 ? 128 : 0);  // codes and scales
   static constexpr int OFF_K = NS * QB, OFF_V = OFF_K + NK * TILE, OFF_R = OFF_V + NV * TILE;
-  static constexpr int SMEM = OFF_R + NR * RAWB;
+  using Shared = AxShared<NK, NV, NR ? NR : 1>;
+  static constexpr int OFF_S = OFF_R + NR * RAWB;
+  static constexpr int SMEM = OFF_S + sizeof(Shared);
   static constexpr int S_COLS = TN;                // columns of a score buffer
   static constexpr int O_COL = 256, O_COLS = D == 256 ? 256 : 128;
 };
@@ -131,6 +147,10 @@ __device__ __forceinline__ bool masked(const AxParams &P, const Seq &s, const Ti
   return c1 > all || (P.window > 0 && c1 > P.sinks && c0 <= t.pmax - P.window);
 }
 
+// n / G for 0 <= n < 2^16.
+__device__ __forceinline__ int token_of(const AxParams &P, int n) {
+  return P.G == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), P.per_head));
+}
 // The page of a place; whether the cache has it.
 __device__ __forceinline__ int page_of(const AxParams &P, int b, int place) {
   return P.table[static_cast<size_t>(b) * P.max_pages + (place >> P.page_shift)];
@@ -138,19 +158,6 @@ __device__ __forceinline__ int page_of(const AxParams &P, int b, int place) {
 __device__ __forceinline__ bool is_page(const AxParams &P, int page) {
   return static_cast<unsigned>(page) < static_cast<unsigned>(P.pages);
 }
-// Whether the 16 places from `place` on are needed, but lie in no page of the cache.
-__device__ __forceinline__ bool lost16(const AxParams &P, const Seq &s, const Tiles &t, int b, int place) {
-  return t.needs(s, place, 16) && !is_page(P, page_of(P, b, place));
-}
-// Whether any of the tiles u0 .. u1 - 1 has such places (asked by a whole warp).
-template <int TN>
-__device__ __forceinline__ bool any_lost(const AxParams &P, const Seq &s, const Tiles &t, int b, int u0, int u1) {
-  bool bad = false;
-  for (int x = threadIdx.x & 31; x < (u1 - u0) * (TN / 16); x += 32)
-    bad |= lost16(P, s, t, b, t.tile(u0 + x / (TN / 16)) * TN + x % (TN / 16) * 16);
-  return __any_sync(0xFFFFFFFFu, bad);
-}
-
 // A block's piece of the line, item by item.
 template <int TN, int ROWS>
 struct Walk {
@@ -289,17 +296,18 @@ __device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t a, uint64_t b, 
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-// Weights of 32 places (as two numbers, 8 columns each by 16 places) with their values, 2048 bytes each 16.
+// Weights of 64 places (8 columns each by 16 places) with their values, 2048 bytes each 16.
 __device__ __forceinline__ void mma4_values(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1;\n\t"
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b32 a1, a2, a3;\n\t.reg .b64 b1, b2, b3;\n\t"
       "elect.sync _|e, 0xFFFFFFFF;\n\t"
       "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %3, %3;\n\t"
-      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u64 b1, %2, 128;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "add.u64 b1, %2, 128;\n\tadd.u64 b2, %2, 256;\n\tadd.u64 b3, %2, 384;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b1, %3, q;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %3, q;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
@@ -321,6 +329,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t taddr, float *v) {
         "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tc_ld16f(uint32_t taddr, float (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+        "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(taddr));
+}
 template <int N>
 __device__ __forceinline__ void tc_wait_ld(float (&v)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -337,11 +352,13 @@ __device__ __forceinline__ void tc_st32r(uint32_t taddr, const float *r) {
       "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tc_st32u(uint32_t taddr, const uint32_t (&r)[32]) {
-  float f[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-  tc_st32r(taddr, f);
+__device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -486,33 +503,28 @@ __global__ void __launch_bounds__(kAxThreads, 1)
   constexpr int TN = S::TN, NS = S::NS, ROWS = S::ROWS, NK = S::NK, NV = S::NV, NR = S::NR > 0 ? S::NR : 1;
   using W = Walk<TN, ROWS>;
   extern __shared__ __align__(1024) uint8_t ax_smem[];
-  __shared__ uint64_t k_full[NK], k_empty[NK], v_full[NV], v_ready[NV], v_empty[NV], r_full[NR], r_empty[NR];
-  __shared__ uint64_t s_full[2], p_ready[2], o_full[2], q_ready[2], o_done;
-  __shared__ uint32_t tmem_holder;
-  __shared__ uint64_t j_free, j_shown, j_read;  // the streams' joint: queries not needed, sums shown, sums read
-  __shared__ int s_odd[16];         // whether values that are not finite were left out of an item's products
-  __shared__ float2 s_other[128];  // the second stream's statistics
   uint8_t *smem = ax_smem;
+  typename S::Shared &sh = *reinterpret_cast<typename S::Shared *>(smem + S::OFF_S);
   const uint32_t sbase = su32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < NK; ++i) mb_init(&k_full[i], E4M3 ? 4 : 1), mb_init(&k_empty[i], 1);
-    for (int i = 0; i < NV; ++i) mb_init(&v_full[i], 1), mb_init(&v_ready[i], 4), mb_init(&v_empty[i], 1);
-    for (int i = 0; i < NR; ++i) mb_init(&r_full[i], 1), mb_init(&r_empty[i], 4);
-    for (int i = 0; i < 2; ++i) mb_init(&s_full[i], 1), mb_init(&p_ready[i], 4), mb_init(&o_full[i], 1), mb_init(&q_ready[i], 4);
-    mb_init(&o_done, 1), mb_init(&j_free, 4), mb_init(&j_shown, 4), mb_init(&j_read, 4);
+    for (int i = 0; i < NK; ++i) mb_init(&sh.k_full[i], E4M3 ? 4 : 1), mb_init(&sh.k_empty[i], 1);
+    for (int i = 0; i < NV; ++i) mb_init(&sh.v_full[i], 1), mb_init(&sh.v_ready[i], 4), mb_init(&sh.v_empty[i], 1);
+    for (int i = 0; i < NR; ++i) mb_init(&sh.r_full[i], 1), mb_init(&sh.r_empty[i], 4);
+    for (int i = 0; i < 2; ++i) mb_init(&sh.s_full[i], 1), mb_init(&sh.p_ready[i], 4), mb_init(&sh.pv_done[i], 1), mb_init(&sh.q_ready[i], 4);
+    mb_init(&sh.j_shown, 8), mb_init(&sh.j_read, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    for (int i = 0; i < 16; ++i) s_odd[i] = 0;
+    sh.odd = 0;
   }
   if (warp == 8) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&tmem_holder)), "r"(512)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_holder;
+  const uint32_t tmem = sh.tmem;
   bool timeout = false;
   pdl_wait();
   pdl_trigger();
@@ -529,36 +541,49 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
     const float c = flat ? 1.f : fabsf(P.scale) * kLog2e;
     const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = flat ? 0u : 0xFFFFFFFFu;
-    uint32_t steps_done[2] = {0, 0};  // of each score buffer
-    uint32_t items = 0, finals = 0, pv = 0, joins = 0;
-    for (; it.more && st < NS && !timeout; it.next(P), ++items) {
+    // this stream's queries of an item into shared memory
+    auto load_q = [&](const W &w) {
+      constexpr int CH = D / 8, N = 8;
+      const int base = w.r0 + (both_of(w) ? 128 * st : 0), left = w.r0 + w.rows - base;
+      const int i0 = base / P.G, g0 = base - i0 * P.G, ch = tid % CH, first = (tid & 127) / CH;
+      const uint16_t *q = P.q + (static_cast<long long>(w.s.first) + i0) * P.q_stride + static_cast<size_t>(w.head) * P.G * D + ch * 8;
+      uint8_t *to = smem + st * S::QB + (ch / 8) * (128 * 128);
+#pragma unroll
+      for (int j = 0; j < CH; j += N) {
+        uint4 u[N];
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          const int rr = first + (j + x) * (128 / CH), at = g0 + rr;
+          const int ii = token_of(P, at), gg = at - ii * P.G;
+          u[x] = make_uint4(0, 0, 0, 0);
+          if (rr < left) u[x] = *reinterpret_cast<const uint4 *>(q + ii * P.q_stride + gg * D);
+        }
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+          const int rr = first + (j + x) * (128 / CH);
+          u[x].x = (u[x].x ^ flip) & keep, u[x].y = (u[x].y ^ flip) & keep;
+          u[x].z = (u[x].z ^ flip) & keep, u[x].w = (u[x].w ^ flip) & keep;
+          *reinterpret_cast<uint4 *>(to + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u[x];
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mb_arrive(&sh.q_ready[st]);
+    };
+    uint32_t uses[2] = {0, 0};  // steps of each score buffer
+    uint32_t items = 0, joins = 0, tiles_before = 0;
+    if (st < NS && it.more) load_q(it);
+    while (it.more && st < NS) {
       const bool both = both_of(it);
       const int r = (both ? 128 * st : 0) + lrow;  // row of the item
       Row row;
       row.on = r < it.rows;
-      const int i = min((it.r0 + r) / P.G, it.s.m - 1), g = (it.r0 + r) - (it.r0 + r) / P.G * P.G;
-      const long long grow = static_cast<long long>(it.s.first) + i;
-      // ---- queries
-      {
-        const int base = both ? 128 * st : 0;
-        constexpr int CH = D / 8;
-        for (int x = tid & 127; x < 128 * CH; x += 128) {
-          const int rr = x / CH, ch = x % CH, ir = it.r0 + base + rr;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (base + rr < it.rows) {
-            const int ii = ir / P.G, gg = ir - ii * P.G;
-            u = *reinterpret_cast<const uint4 *>(P.q + (static_cast<long long>(it.s.first) + ii) * P.q_stride +
-                                                 static_cast<size_t>(it.head * P.G + gg) * D + ch * 8);
-            u.x = (u.x ^ flip) & keep, u.y = (u.y ^ flip) & keep, u.z = (u.z ^ flip) & keep, u.w = (u.w ^ flip) & keep;
-          }
-          *reinterpret_cast<uint4 *>(smem + st * S::QB + (ch / 8) * (128 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u;
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0) mb_arrive(&q_ready[st]);
-      }
+      const int i0 = it.r0 / P.G, at = it.r0 - i0 * P.G + r;
+      const int di = token_of(P, at), g = at - di * P.G;
+      const int i = min(i0 + di, it.s.m - 1);
+      const long long grow_ = static_cast<long long>(it.s.first) + i;
       int pos = it.s.ctx + i;
-      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? grow * P.words : 0));
+      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? grow_ * P.words : 0));
       if (P.masks) {
         int seen = 0;
         for (int w = 0; 32 * w < it.s.m; ++w) seen += __popc(row.mask[w] & below(it.s.m - 32 * w));
@@ -566,73 +591,35 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       }
       row.hi = pos;
       row.lo = P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
-      const bool any_bad = any_lost<TN>(P, it.s, it.list, it.b, it.u0, it.u1);
       const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < it.rows;
-      float m = -INFINITY, l = 0.f;
+      // the reference in scores; sums of the weights, and of the weights as they are rounded, which the outputs are
+      // divided by
+      float m = -INFINITY, l = 0.f, lw = 0.f;
       bool first = true;
       const int T = it.u1 - it.u0, K = both ? 2 * T : T;
+      int sb = st;
       for (int k = NS == 2 ? st : 0; k < K; k += NS) {
-        const int sb = k & 1, tile = it.list.tile(it.u0 + (both ? k >> 1 : k));
-        if (!warp_wait(&s_full[sb], steps_done[sb] & 1u)) {
+        sb = k & 1;
+        const int u = both ? k >> 1 : k, tile = it.list.tile(it.u0 + u);
+        if (!warp_wait(&sh.s_full[sb], uses[sb] & 1u)) {
           timeout = true;
           break;
         }
-        ++steps_done[sb];
+        ++uses[sb];
         tc_fence_after();
         if (warp_on) {
           const uint32_t sa = tmem + lane_addr + sb * S::S_COLS;
-          const bool some = any_bad || masked<TN>(P, it.s, it.list, tile);
+          const uint32_t lost = sh.lost[(tiles_before + u) & 15];
           float base = m == -INFINITY ? 0.f : m * c;
-          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // the row's reference moves up to mx: sums, and the weights of the x places before, by the quotient
-          auto grow = [&](float mx, int x) {
-            const float mn = fmaxf(m, mx), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
-            m = mn;
-            base = m == -INFINITY ? 0.f : m * c;
-            l *= f;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) add[y].x *= f, add[y].y *= f;
-            float o[32];
-#pragma unroll 1
-            for (int y = 0; y < x; y += 32) {
-              tc_ld32(sa + y, o);
-              tc_wait_ld(o);
-#pragma unroll
-              for (int z = 0; z < 32; z = z % 16 == 7 ? z + 9 : z + 1) {
-                const uint32_t hi = __float_as_uint(o[z]), lo = __float_as_uint(o[z + 8]);
-                const float p0 = (__uint_as_float(hi << 16) + __uint_as_float(lo << 16)) * f;
-                const float p1 = (__uint_as_float(hi & 0xFFFF0000u) + __uint_as_float(lo & 0xFFFF0000u)) * f;
-                const uint32_t h = bf16x2(p0, p1);
-                o[z] = __uint_as_float(h);
-                o[z + 8] = __uint_as_float(bf16x2(p0 - __uint_as_float(h << 16), p1 - __uint_as_float(h & 0xFFFF0000u)));
-              }
-              tc_st32r(sa + y, o);
-            }
-            if (!first) {
-              if (NS == 1 && !warp_wait(&o_done, (pv - 1) & 1u)) timeout = true;
-              tc_fence_after();
-              const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
-#pragma unroll 1
-              for (int y = 0; y < D; y += 32) {
-                tc_ld32(oa + y, o);
-                tc_wait_ld(o);
-#pragma unroll
-                for (int z = 0; z < 32; ++z) o[z] *= f;
-                tc_st32r(oa + y, o);
-              }
-            }
-            tc_wait_st();
-          };
+          float2 add = make_float2(0.f, 0.f), addw = make_float2(0.f, 0.f);
           float v[32];
-          if (some) {
+          if (lost || masked<TN>(P, it.s, it.list, tile)) {
 #pragma unroll 1
             for (int x = 0; x < TN; x += 32) {
               tc_ld32(sa + x, v);
               uint32_t vis = sees(P, it.s, row, tile * TN + x);
-              if (any_bad) {
-                if (lost16(P, it.s, it.list, it.b, tile * TN + x)) vis &= 0xFFFF0000u;
-                if (lost16(P, it.s, it.list, it.b, tile * TN + x + 16)) vis &= 0xFFFFu;
-              }
+              if (lost >> (x / 16) & 1u) vis &= 0xFFFF0000u;
+              if (lost >> (x / 16) & 2u) vis &= 0xFFFFu;
               tc_wait_ld(v);
 #pragma unroll
               for (int y = 0; y < 32; ++y)
@@ -641,7 +628,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             tc_wait_st();
           }
-          // 32 places at a time: scores in, weights out (in place)
+          // 32 places at a time: scores in, weights out (in place: their 16 columns lie behind what was read)
 #pragma unroll 1
           for (int x = 0; x < TN; x += 32) {
             tc_ld32(sa + x, v);
@@ -650,43 +637,78 @@ __global__ void __launch_bounds__(kAxThreads, 1)
 #pragma unroll
             for (int y = 0; y < 32; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(v[y], v[y + 1]), mx[(y / 2) & 3]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (__any_sync(0xFFFFFFFFu, (top - m) * c > kGrowth)) grow(top, x);
-            const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base), less = make_float2(-1.f, -1.f);
-            uint32_t pk[32];
+            if (__any_sync(0xFFFFFFFFu, (top - m) * c > kGrowth)) {
+              // the row's reference moves up: sums, and the weights of the x places before, by the quotient
+              const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
+              m = mn;
+              base = m == -INFINITY ? 0.f : m * c;
+              l *= f, lw *= f;
+              add.x *= f, add.y *= f, addw.x *= f, addw.y *= f;
+              float o[16];
+#pragma unroll 1
+              for (int y = 0; y < x / 2; y += 16) {
+                tc_ld16f(sa + y, o);
+                tc_wait_ld(o);
+                uint32_t h[16];
+#pragma unroll
+                for (int z = 0; z < 16; ++z)
+                  h[z] = bf16x2(__uint_as_float(__float_as_uint(o[z]) << 16) * f,
+                                __uint_as_float(__float_as_uint(o[z]) & 0xFFFF0000u) * f);
+                tc_st16u(sa + y, h);
+              }
+              if (!first) {
+                if (NS == 1) {
+                  if (!warp_wait(&sh.pv_done[sb ^ 1], (uses[sb ^ 1] - 1) & 1u)) timeout = true;
+                  tc_fence_after();
+                }
+                const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+#pragma unroll 1
+                for (int y = 0; y < D; y += 16) {
+                  tc_ld16f(oa + y, o);
+                  tc_wait_ld(o);
+                  uint32_t h[16];
+#pragma unroll
+                  for (int z = 0; z < 16; ++z) h[z] = __float_as_uint(o[z] * f);
+                  tc_st16u(oa + y, h);
+                }
+              }
+              tc_wait_st();
+            }
+            const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
+            uint32_t pk[16];
 #pragma unroll
             for (int y = 0; y < 32; y += 2) {
-              const float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2), p = make_float2(ex2(e.x), ex2(e.y));
-              add[(y / 2) & 1] = add2(add[(y / 2) & 1], p);
-              const uint32_t hi = bf16x2(p.x, p.y);
-              const float2 r = fma2(make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), less, p);
-              const int at = (y & 16) + (y & 15) / 2;
-              pk[at] = hi;
-              pk[at + 8] = bf16x2(r.x, r.y);
+              const float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2);
+              const float2 w = make_float2(ex2(e.x), ex2(e.y));
+              const uint32_t h = pk[y / 2] = bf16x2(w.x, w.y);
+              add = add2(add, w);
+              addw = add2(addw, make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)));
             }
-            tc_st32u(sa + x, pk);
+            tc_st16u(sa + x / 2, pk);
           }
-          l += (add[0].x + add[0].y) + (add[1].x + add[1].y);
+          l += add.x + add.y, lw += addw.x + addw.y;
           tc_wait_st();
         }
         first = false;
-        ++pv;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mb_arrive(&p_ready[sb]);
+        if (lane == 0) mb_arrive(&sh.p_ready[sb]);
       }
       if (timeout) break;
-      // ---- the item's end
+      // ---- the item's end: the next one's queries, then this one's sums
       const bool had = !first;  // whether this stream had a step
-      if (had) {
-        if (!warp_wait(&o_full[st], finals & 1u)) {
+      W nx = it;
+      nx.next(P);
+      if (had) {  // (the last scores are there: its queries are not read any more)
+        if (nx.more) load_q(nx);
+        if (!warp_wait(&sh.pv_done[sb], (uses[sb] - 1) & 1u)) {
           timeout = true;
           break;
         }
-        ++finals;
         tc_fence_after();
       }
       const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
-      if ((s_odd[items & 15] & 1) && had && warp_on) {
+      if ((*reinterpret_cast<volatile uint32_t *>(&sh.odd) >> (items & 31) & 1u) && had && warp_on) {
         // values that were left out of the products are added to the rows that see them
 #pragma unroll 1
         for (int x0 = 0; x0 < D; x0 += 32) {
@@ -698,7 +720,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           for (int u = it.u0; u < it.u1; ++u) {
             const int tile = it.list.tile(u);
             if ((!both && NS == 2 && ((u - it.u0) & 1) != st) || !row.on) continue;
-            if (!any_bad && !masked<TN>(P, it.s, it.list, tile)) continue;
+            if (!sh.lost[(tiles_before + u - it.u0) & 15] && !masked<TN>(P, it.s, it.list, tile)) continue;
 #pragma unroll 1
             for (int x = 0; x < TN; ++x) {
               const int place = tile * TN + x;
@@ -709,15 +731,15 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                                  (place & ((1 << P.page_shift) - 1));
 #pragma unroll
               for (int y = 0; y < 32; ++y) {
-                float v;
+                float w;
                 if (E4M3) {
                   uint32_t a, z;
                   e4m3x4_to_f16x2(P.v[vec * D + x0 + y], a, z);
-                  v = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
+                  w = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
                 } else {
-                  v = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
+                  w = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
                 }
-                if (!isfinite(v)) o[y] += v;
+                if (!isfinite(w)) o[y] += w;
               }
             }
           }
@@ -726,60 +748,49 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
         tc_wait_st();
       }
-      float mb = m == -INFINITY ? -INFINITY : m * c;
-      if (NS == 2 && !both) {  // join the streams: the second shows its sums where the queries were
-        float *shown = reinterpret_cast<float *>(smem);
-        if (st == 0) {
-          if (lane == 0) mb_arrive(&j_free);  // (all of this stream's products are complete)
-        } else {
-          if (!warp_wait(&j_free, joins & 1u)) {
-            timeout = true;
-            break;
-          }
-          s_other[lrow] = make_float2(mb, l);
-          if (had && warp_on) {
-#pragma unroll 1
-            for (int x = 0; x < D; x += 32) {
-              float o[32];
-              __syncwarp();
-              tc_ld32(oa + x, o);
-              tc_wait_ld(o);
-#pragma unroll
-              for (int y = 0; y < 32; ++y) shown[(x + y) * 128 + lrow] = o[y];
-            }
-          }
-          __syncwarp();
-          if (lane == 0) mb_arrive(&j_shown);
-        }
-        if (st == 0 && !warp_wait(&j_shown, joins & 1u)) {
+      float mb = m == -INFINITY ? -INFINITY : m * c, f0 = 1.f, f1 = 0.f;
+      const bool split = NS == 2 && !both;  // the streams share the rows: each writes half of the dimensions
+      if (split) {
+        sh.stat[st][lrow] = make_float2(mb, lw);
+        if (st == 1) sh.sum1[lrow] = l;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mb_arrive(&sh.j_shown);
+        if (!warp_wait(&sh.j_shown, joins & 1u)) {
           timeout = true;
           break;
         }
-      }
-      if (!(NS == 2 && !both && st == 1) && warp_on) {
-        float f0 = 1.f, f1 = 0.f;
-        const float *shown = reinterpret_cast<const float *>(smem);
-        const bool join = NS == 2 && !both && K > 1;
-        if (join) {
-          const float2 o = s_other[lrow];
-          const float mm = fmaxf(mb, o.x), base = mm == -INFINITY ? 0.f : mm;
-          f0 = ex2(mb - base), f1 = ex2(o.x - base);
-          l = l * f0 + o.y * f1;
-          mb = mm;
+        tc_fence_after();
+        if (K > 1) {
+          const float2 a = sh.stat[0][lrow], b = sh.stat[1][lrow];
+          mb = fmaxf(a.x, b.x);
+          const float base = mb == -INFINITY ? 0.f : mb;
+          f0 = ex2(a.x - base), f1 = ex2(b.x - base);
+          lw = a.y * f0 + b.y * f1;
+          if (st == 0) l = l * f0 + sh.sum1[lrow] * f1;
+        } else {
+          mb = sh.stat[0][lrow].x, lw = sh.stat[0][lrow].y;
         }
+      }
+      if (warp_on) {
         const bool cut = it.cut();
         const int slot = 2 * blockIdx.x + (it.u0 > 0 ? 0 : 1);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t orow = static_cast<size_t>(grow) * P.Hq + it.head * P.G + g;
+        const float inv = lw == 0.f ? 0.f : 1.f / lw;
+        const size_t orow = static_cast<size_t>(grow_) * P.Hq + it.head * P.G + g;
+        const int x0 = split ? st * (D / 2) : 0, x1 = split ? x0 + D / 2 : D;
+        const uint32_t o0 = tmem + lane_addr + S::O_COL + (split ? 0 : st * S::O_COLS), o1 = o0 + S::O_COLS;
 #pragma unroll 1
-        for (int x = 0; x < D; x += 32) {
+        for (int x = x0; x < x1; x += 32) {
           float o[32];
           __syncwarp();
-          tc_ld32(oa + x, o);
+          tc_ld32(o0 + x, o);
           tc_wait_ld(o);
-          if (join) {
+          if (split && K > 1) {
+            float z[32];
+            tc_ld32(o1 + x, z);
+            tc_wait_ld(z);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = o[y] * f0 + shown[(x + y) * 128 + lrow] * f1;
+            for (int y = 0; y < 32; ++y) o[y] = o[y] * f0 + z[y] * f1;
           }
           if (row.on && cut) {
             float *to = P.part + (static_cast<size_t>(slot) * D + x) * ROWS + r;
@@ -792,22 +803,24 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                w[z] = l == 0.f ? 0u : bf16x2(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
+                w[z] = lw == 0.f ? 0u : bf16x2(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
               to[y] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
-        if (row.on) {
+        if (row.on && !(split && st)) {
           if (cut)
-            P.stat[static_cast<size_t>(slot) * ROWS + r] = make_float2(mb, l);
+            P.stat[static_cast<size_t>(slot) * ROWS + r] = make_float4(mb, l, lw, 0.f);
           else if (P.lse)
             P.lse[orow] = l == 0.f ? -INFINITY : (mb + log2f(l)) * kLn2;
         }
       }
-      if (NS == 2 && !both) {  // the sums have been read: queries may come
+      if (split) {  // the sums have been read: the next item's may come
+        tc_fence_before();
         __syncwarp();
-        if (st == 0 && lane == 0) mb_arrive(&j_read);
-        if (!warp_wait(&j_read, joins & 1u)) {
+        if (lane == 0) mb_arrive(&sh.j_read);
+        if (!had && nx.more) load_q(nx);
+        if (!warp_wait(&sh.j_read, joins & 1u)) {
           timeout = true;
           break;
         }
@@ -817,68 +830,77 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         const long long last = it.begin + kItemLen + static_cast<long long>(it.list.units - 1) * it.weight;
         P.meta[blockIdx.x] = make_int4(it.b, it.head, it.t, static_cast<int>(last / P.plan->share) - blockIdx.x + 1);
       }
+      tiles_before += T;
+      ++items;
+      it = nx;
     }
   } else if (warp < 12) {
     if (warp == 8) {
-      // ---- products
-      uint32_t kt = 0, vt = 0, used[2] = {0, 0}, items = 0;
-      const uint32_t id_s = idesc(TN, false), id_o = idesc(D, true);
+      // ---- scores
+      uint32_t kt = 0, uses[2] = {0, 0}, items = 0;
+      const uint32_t id = idesc(TN, false);
       for (; it.more && !timeout; it.next(P), ++items) {
         const bool both = both_of(it);
         const int T = it.u1 - it.u0, K = both ? 2 * T : T;
-        const uint32_t k0 = kt, v0 = vt;
-        for (int s = 0; s < NS; ++s)
-          if (!warp_wait(&q_ready[s], items & 1u)) timeout = true;
-        if (timeout) break;
-        tc_fence_after();
-        auto scores = [&](int k) {
+        for (int x = 0; x < NS; ++x)
+          if (!warp_wait(&sh.q_ready[x], items & 1u)) timeout = true;
+        for (int k = 0; k < K && !timeout; ++k) {
           const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
-          const uint32_t t = k0 + (both ? k >> 1 : k), slot = t % NK;
-          if (!both || !(k & 1)) {
-            if (!warp_wait(&k_full[slot], (t / NK) & 1u)) return false;
-            tc_fence_after();
+          const uint32_t t = kt + (both ? k >> 1 : k), slot = t % NK;
+          // the buffer's weights have been used
+          bool ok = uses[sb] == 0 || warp_wait(&sh.pv_done[sb], (uses[sb] - 1) & 1u);
+          if (!both || !(k & 1)) ok = ok && warp_wait(&sh.k_full[slot], (t / NK) & 1u);
+          if (!ok) {
+            timeout = true;
+            break;
           }
-          const uint32_t qa = sbase + st * S::QB, ka = sbase + S::OFF_K + slot * S::TILE;
-          const uint64_t qd = smem_desc_sw128(qa), kd = smem_desc_sw128(ka);
+          ++uses[sb];
+          tc_fence_after();
+          const uint64_t qd = smem_desc_sw128(sbase + st * S::QB), kd = smem_desc_sw128(sbase + S::OFF_K + slot * S::TILE);
 #pragma unroll
           for (int x = 0; x < D / 64; ++x)
-            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
-          if (!both || (k & 1)) commit(&k_empty[slot]);
-          commit(&s_full[sb]);
-          return true;
-        };
-        bool ok = scores(0) && (K < 2 || scores(1));
-        for (int k = 0; ok && k < K; ++k) {
-          const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
-          const uint32_t t = v0 + (both ? k >> 1 : k), slot = t % NV;
-          ok = warp_wait(&p_ready[sb], used[sb] & 1u);
-          if (!ok) break;
-          ++used[sb];
-          if (!both || !(k & 1)) ok = warp_wait(&v_ready[slot], (t / NV) & 1u);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t va = sbase + S::OFF_V + slot * S::TILE, pa = tmem + sb * S::S_COLS;
-          const uint32_t oa = tmem + S::O_COL + st * S::O_COLS;
-          const bool begun = k >= NS;
-          const uint64_t vd = values_desc(va, TN * 128);
-#pragma unroll
-          for (int x = 0; x < TN / 32; ++x) mma4_values(oa, pa + x * 32, vd + x * (4096 / 16), id_o, x > 0 || begun);
-          if (!both || (k & 1)) commit(&v_empty[slot]);
-          if (NS == 1) commit(&o_done);
-          if (k + NS >= K) commit(&o_full[st]);
-          if (k + 2 < K) ok = scores(k + 2);
+            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id, x > 0);
+          commit(&sh.s_full[sb]);
+          if (!both || (k & 1)) commit(&sh.k_empty[slot]);
         }
-        if (!ok) timeout = true;
-        kt += T, vt += T;
+        kt += T;
+      }
+    } else if (warp == 10) {
+      // ---- weights with values
+      uint32_t vt = 0, uses[2] = {0, 0};
+      const uint32_t id = idesc(D, true);
+      for (; it.more && !timeout; it.next(P)) {
+        const bool both = both_of(it);
+        const int T = it.u1 - it.u0, K = both ? 2 * T : T;
+        for (int k = 0; k < K; ++k) {
+          const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
+          const uint32_t t = vt + (both ? k >> 1 : k), slot = t % NV;
+          bool ok = both && (k & 1) ? true : warp_wait(&sh.v_ready[slot], (t / NV) & 1u);
+          ok = ok && warp_wait(&sh.p_ready[sb], uses[sb] & 1u);
+          if (!ok) {
+            timeout = true;
+            break;
+          }
+          ++uses[sb];
+          tc_fence_after();
+          const uint64_t vd = values_desc(sbase + S::OFF_V + slot * S::TILE, TN * 128);
+#pragma unroll
+          for (int x = 0; x < TN / 64; ++x)
+            mma4_values(tmem + S::O_COL + st * S::O_COLS, tmem + sb * S::S_COLS + x * 32, vd + x * (8192 / 16), id, x > 0 || k >= NS);
+          commit(&sh.pv_done[sb]);
+          if (!both || (k & 1)) commit(&sh.v_empty[slot]);
+        }
+        vt += T;
       }
     } else if (warp == 9) {
       // ---- loads
-      uint32_t kt = 0, vt = 0, rt = 0;
+      uint32_t kt = 0, vt = 0, rt = 0, seq = 0;
       const int page_size = 1 << P.page_shift, run = min(page_size, TN), runs = TN / run;
       constexpr int EB = E4M3 ? 1 : 2, BOX = D * EB < 128 ? D * EB : 128, BOXES = D * EB / BOX;  // bytes of a box's rows
       for (; it.more && !timeout; it.next(P)) {
-        for (int u = it.u0; u < it.u1 && !timeout; ++u) {
+        for (int u = it.u0; u < it.u1 && !timeout; ++u, ++seq) {
           const int tile = it.list.tile(u);
+          uint32_t lost = 0;
           int page = P.pages;  // (past the end: the copy fills in zeros)
           if (lane < runs) {
             const int place = tile * TN + lane * run;
@@ -887,9 +909,11 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               if (!is_page(P, page)) {
                 set_status(P.status, K3MOE_DEV_BOUNDS);
                 page = P.pages;
+                lost = below(run / 16) << (lane * run / 16);
               }
             }
           }
+          lost = __reduce_or_sync(0xFFFFFFFFu, lost);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             uint64_t *full;
@@ -897,18 +921,18 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             bool ok = true;
             if constexpr (E4M3) {
               const uint32_t slot = rt % NR;
-              if (lane == 0) ok = mb_wait(&r_empty[slot], ((rt / NR) & 1u) ^ 1u);
-              full = &r_full[slot], dst = sbase + S::OFF_R + slot * S::RAWB;
+              if (lane == 0) ok = mb_wait(&sh.r_empty[slot], ((rt / NR) & 1u) ^ 1u);
+              full = &sh.r_full[slot], dst = sbase + S::OFF_R + slot * S::RAWB;
               ++rt;
             } else if (kv == 0) {
               const uint32_t slot = kt % NK;
-              if (lane == 0) ok = mb_wait(&k_empty[slot], ((kt / NK) & 1u) ^ 1u);
-              full = &k_full[slot], dst = sbase + S::OFF_K + slot * S::TILE;
+              if (lane == 0) ok = mb_wait(&sh.k_empty[slot], ((kt / NK) & 1u) ^ 1u);
+              full = &sh.k_full[slot], dst = sbase + S::OFF_K + slot * S::TILE;
               ++kt;
             } else {
               const uint32_t slot = vt % NV;
-              if (lane == 0) ok = mb_wait(&v_empty[slot], ((vt / NV) & 1u) ^ 1u);
-              full = &v_full[slot], dst = sbase + S::OFF_V + slot * S::TILE;
+              if (lane == 0) ok = mb_wait(&sh.v_empty[slot], ((vt / NV) & 1u) ^ 1u);
+              full = &sh.v_full[slot], dst = sbase + S::OFF_V + slot * S::TILE;
               ++vt;
             }
             ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -918,6 +942,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             const bool scales = E4M3 && page < P.pages;
             const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, lane < runs && scales));
+            if (lane == 0 && kv == 0) sh.lost[seq & 15] = lost;
             if (lane == 0) mb_arrive_tx(full, TN * D * EB + (E4M3 ? scaled * run : 0));
             __syncwarp();
             if (lane < runs) {
@@ -935,38 +960,39 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       // every copy has landed before the block can leave
       if (timeout && lane == 0) {
         if constexpr (E4M3) {
-          for (uint32_t i = rt < NR ? 0 : rt - NR; i < rt; ++i) mb_wait(&r_full[i % NR], (i / NR) & 1u);
+          for (uint32_t i = rt < NR ? 0 : rt - NR; i < rt; ++i) mb_wait(&sh.r_full[i % NR], (i / NR) & 1u);
         } else {
-          for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&k_full[i % NK], (i / NK) & 1u);
-          for (uint32_t i = vt < NV ? 0 : vt - NV; i < vt; ++i) mb_wait(&v_full[i % NV], (i / NV) & 1u);
+          for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&sh.k_full[i % NK], (i / NK) & 1u);
+          for (uint32_t i = vt < NV ? 0 : vt - NV; i < vt; ++i) mb_wait(&sh.v_full[i % NV], (i / NV) & 1u);
         }
       }
     }
   } else {
     // ---- codes become operands; values that a row does not see must not be other than finite
     const int t128 = tid - 384;
-    uint32_t kt = 0, vt = 0, rt = 0, items = 0;
+    uint32_t kt = 0, vt = 0, rt = 0, seq = 0, items = 0;
     for (; it.more && !timeout; it.next(P), ++items) {
-      if (t128 == 0) s_odd[(items + 8) & 15] = 0;
-      const bool any_bad = any_lost<TN>(P, it.s, it.list, it.b, it.u0, it.u1);
-      auto there = [&](int place) {
-        return it.list.needs(it.s, place & ~15, 16) && place < it.s.n && is_page(P, page_of(P, it.b, place));
-      };
-      for (int u = it.u0; u < it.u1 && !timeout; ++u) {
+      if (t128 == 0) atomicAnd(&sh.odd, ~(1u << ((items + 16) & 31)));
+      for (int u = it.u0; u < it.u1 && !timeout; ++u, ++seq) {
         const int tile = it.list.tile(u);
-        const bool check = any_bad || masked<TN>(P, it.s, it.list, tile);
+        uint32_t lost = 0;
+        bool check = masked<TN>(P, it.s, it.list, tile);
+        auto there = [&](int place) {  // whether a row may see it
+          return it.list.needs(it.s, place & ~15, 16) && place < it.s.n && !(lost >> ((place % TN) / 16) & 1u);
+        };
 #pragma unroll
         for (int kv = E4M3 ? 0 : 1; kv < 2; ++kv) {
           uint32_t op;
           uint64_t *ready;
           if constexpr (E4M3) {
             const uint32_t rs = rt % NR;
-            if (!warp_wait(&r_full[rs], (rt / NR) & 1u)) timeout = true;
+            if (!warp_wait(&sh.r_full[rs], (rt / NR) & 1u)) timeout = true;
             const uint32_t slot = kv ? vt % NV : kt % NK;
-            uint64_t *empty = kv ? &v_empty[slot] : &k_empty[slot];
+            uint64_t *empty = kv ? &sh.v_empty[slot] : &sh.k_empty[slot];
             if (!warp_wait(empty, (((kv ? vt / NV : kt / NK)) & 1u) ^ 1u)) timeout = true;
             if (timeout) break;
-            ready = kv ? &v_ready[slot] : &k_full[slot];
+            lost = sh.lost[seq & 15], check = check || lost;
+            ready = kv ? &sh.v_ready[slot] : &sh.k_full[slot];
             op = (kv ? S::OFF_V : S::OFF_K) + slot * S::TILE;
             const uint8_t *raw = smem + S::OFF_R + rs * S::RAWB, *scales = raw + S::RAW;
             constexpr int BOX = D < 128 ? D : 128, CH = D / 16;  // chunks of 16 codes in a row
@@ -1008,7 +1034,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                   if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
                   if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
                 }
-                if (odd) atomicOr(&s_odd[items & 15], 1);
+                if (odd) atomicOr(&sh.odd, 1u << (items & 31));
               }
               uint8_t *to = smem + op + (ch / 4) * (TN * 128) + rr * 128;
               const int c0 = (2 * ch) & 7, sw = (ch >> 2) & 1;
@@ -1018,16 +1044,17 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) mb_arrive(&r_empty[rs]);
+            if (lane == 0) mb_arrive(&sh.r_empty[rs]);
             ++rt;
             kv ? ++vt : ++kt;
           } else {
             const uint32_t slot = vt % NV;
-            if (!warp_wait(&v_full[slot], (vt / NV) & 1u)) {
+            if (!warp_wait(&sh.v_full[slot], (vt / NV) & 1u)) {
               timeout = true;
               break;
             }
-            ready = &v_ready[slot];
+            lost = sh.lost[seq & 15], check = check || lost;
+            ready = &sh.v_ready[slot];
             op = S::OFF_V + slot * S::TILE;
             ++vt;
             if (check) {
@@ -1049,7 +1076,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                 }
                 if (odd) {
                   *at = make_uint4(h[0], h[1], h[2], h[3]);
-                  atomicOr(&s_odd[items & 15], 1);
+                  atomicOr(&sh.odd, 1u << (items & 31));
                 }
               }
               fence_async();
@@ -1083,16 +1110,17 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
   const int r0 = me.z * ROWS, rows = min(ROWS, s.m * P.G - r0), r = 32 * blockIdx.y + lane;
   if (32 * static_cast<int>(blockIdx.y) >= rows) return;
   auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
-  float mm = -INFINITY, l = 0.f;
+  float mm = -INFINITY, l = 0.f, lw = 0.f;
   for (int p = 0; p < me.w; ++p) mm = fmaxf(mm, P.stat[slot_of(p) * ROWS + r].x);
   const float base = mm == -INFINITY ? 0.f : mm;
   for (int p = 0; p < me.w; ++p) {
-    const float2 st = P.stat[slot_of(p) * ROWS + r];
-    l = fmaf(st.y, ex2(st.x - base), l);
+    const float4 st = P.stat[slot_of(p) * ROWS + r];
+    const float f = ex2(st.x - base);
+    l = fmaf(st.y, f, l), lw = fmaf(st.z, f, lw);
   }
   const int i = (r0 + r) / P.G, g = r0 + r - i * P.G;
   const size_t row = (static_cast<size_t>(s.first) + i) * P.Hq + me.y * P.G + g;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = lw == 0.f ? 0.f : 1.f / lw;
   for (int x = 8 * warp; x < D; x += 32) {
     float o[8];
 #pragma unroll
@@ -1106,7 +1134,7 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
     if (r < rows) {
       uint32_t w[4];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+      for (int z = 0; z < 4; ++z) w[z] = lw == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
       *reinterpret_cast<uint4 *>(P.out + row * D + x) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
@@ -1133,7 +1161,7 @@ AxSpace space_of(const k3moe_kv_cache &c, int B, int rows, int Hq) {
   s.first_entry = s.meta + aligned256(kAxMostBlocks * sizeof(int4));
   s.prefix = s.first_entry + aligned256((static_cast<size_t>(B) + 1) * 4);
   s.stat = s.prefix + aligned256(entries * 8);
-  s.part = s.stat + aligned256(2 * kAxMostBlocks * item * sizeof(float2));
+  s.part = s.stat + aligned256(2 * kAxMostBlocks * item * sizeof(float4));
   s.bytes = s.part + static_cast<size_t>(2) * kAxMostBlocks * item * c.dim * 4;
   return s;
 }
@@ -1178,7 +1206,7 @@ int current_device() {
 template <int D, bool E4M3>
 int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   using S = AxShape<D, E4M3>;
-  static_assert(S::SMEM <= 232448 - 2048, "shared memory of a block");
+  static_assert(S::SMEM <= 232448, "shared memory of a block");
   CUtensorMap kmap, vmap;
   if (!cache_map(&kmap, c, c.k, S::TN) || !cache_map(&vmap, c, c.v, S::TN)) return -1;
   static PerDevice raised;
@@ -1190,6 +1218,7 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   if (err != cudaSuccess) return -1;
   P.blocks = min(sm_count(), kAxMostBlocks);
   P.entries = entries_of(S::ROWS, P.B, P.rows, P.G);
+  P.per_head = static_cast<uint32_t>(((1ULL << 32) + P.G - 1) / P.G);
   if (launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
   if (launch_pdl(attn_extend_kernel<D, E4M3>, dim3(P.blocks), dim3(kAxThreads), S::SMEM, st, P, kmap, vmap) != cudaSuccess)
     return -1;
@@ -1214,7 +1243,7 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   uint8_t *w = static_cast<uint8_t *>(a.ws);
   P.plan = reinterpret_cast<AxPlan *>(w + s.plan), P.start = reinterpret_cast<AxStart *>(w + s.start);
   P.meta = reinterpret_cast<int4 *>(w + s.meta), P.first_entry = reinterpret_cast<int *>(w + s.first_entry);
-  P.prefix = reinterpret_cast<long long *>(w + s.prefix), P.stat = reinterpret_cast<float2 *>(w + s.stat);
+  P.prefix = reinterpret_cast<long long *>(w + s.prefix), P.stat = reinterpret_cast<float4 *>(w + s.stat);
   P.part = reinterpret_cast<float *>(w + s.part);
   const bool e = c.format == K3MOE_KV_E4M3;
   if (c.dim == 64) return e ? launch_extend<64, true>(c, P, st) : launch_extend<64, false>(c, P, st);
