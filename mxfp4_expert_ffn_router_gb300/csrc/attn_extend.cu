@@ -181,7 +181,7 @@ struct Walk {
     tiles = P.first_entry[b + 1] - P.first_entry[b];
   }
   __device__ __forceinline__ int unit_at(long long x) const {
-    const long long u = (x - begin - kItemLen + weight - 1) / weight;
+    const long long u = (x - begin - kItemLen + weight - 1) >> (weight - 1);
     return u < 0 ? 0 : u > list.units ? list.units : static_cast<int>(u);
   }
   __device__ __forceinline__ void enter() { u0 = unit_at(from), u1 = unit_at(to); }
@@ -849,6 +849,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           const uint32_t t = kt + (both ? k >> 1 : k), slot = t % NK;
           // the buffer's weights have been used
           bool ok = uses[sb] == 0 || warp_wait(&sh.pv_done[sb], (uses[sb] - 1) & 1u);
+          // of a longer item the second stream starts half a step behind, so that one's products meet the other's softmax
+          if (k == 1 && K > 8 && NS == 2) ok = ok && warp_wait(&sh.p_ready[0], (uses[0] - 1) & 1u);
           if (!both || !(k & 1)) ok = ok && warp_wait(&sh.k_full[slot], (t / NK) & 1u);
           if (!ok) {
             timeout = true;
