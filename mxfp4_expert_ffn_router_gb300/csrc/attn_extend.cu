@@ -11,7 +11,7 @@ namespace k3moe {
 
 namespace {
 
-constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 scores, 9 loads, 10 sums, 12-15 values
+constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 and 10 products, 9 loads, 12-15 values
 constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
 constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
 constexpr float kLog2e = 1.4426950408889634f;
@@ -49,7 +49,7 @@ struct AxParams {
   int4 *meta;        // [blocks]: {sequence, head, tile, parts} of the item that begins in the block's piece and goes on
   int *first_entry;  // [B + 1]
   long long *prefix; // [entries + 1]
-  float4 *stat;      // [2 blocks][rows of a tile]: reference, sum of the weights, of the rounded ones
+  float2 *stat;      // [2 blocks][rows of a tile]: reference, sum of the weights
   float *part;       // [2 blocks][dim][rows of a tile]
   int blocks, entries;  // pieces; room for the tiles of query rows
   uint32_t per_head;    // ceil(2^32 / G) (token_of)
@@ -81,10 +81,10 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
 template <int NK, int NV, int NR>
 struct AxShared {
   uint64_t k_full[NK], k_empty[NK], v_full[NV], v_ready[NV], v_empty[NV], r_full[NR], r_empty[NR];
-  uint64_t s_full[2], p_ready[2], pv_done[2], q_ready[2];
+  uint64_t s_full[2], p_half[2], half_done[2], p_ready[2], pv_done[2], q_ready[2];
+  uint64_t go;               // the second stream may start
   uint64_t j_shown, j_read;  // the streams' joint: sums shown, sums read
-  float2 stat[2][128];       // the streams' statistics: reference, sum of the rounded weights
-  float sum1[128];           // the second stream's sum of the weights
+  float2 stat[2][128];       // the streams' statistics: reference, sum of the weights
   uint8_t lost[16];  // of a tile: bit x for the 16 places from 16 x on that lie in no page of the cache
   uint32_t odd;      // bit x: values that are not finite were left out of item x's products
   uint32_t tmem;
@@ -360,6 +360,12 @@ __device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16]
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tc_st32u(uint32_t taddr, const uint32_t (&r)[32]) {
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
+  tc_st32r(taddr, f);
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -508,11 +514,11 @@ __global__ void __launch_bounds__(kAxThreads, 1)
   const uint32_t sbase = su32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < NK; ++i) mb_init(&sh.k_full[i], E4M3 ? 4 : 1), mb_init(&sh.k_empty[i], 1);
-    for (int i = 0; i < NV; ++i) mb_init(&sh.v_full[i], 1), mb_init(&sh.v_ready[i], 4), mb_init(&sh.v_empty[i], 1);
+    for (int i = 0; i < NK; ++i) mb_init(&sh.k_full[i], E4M3 ? 4 : 1), mb_init(&sh.k_empty[i], NS);
+    for (int i = 0; i < NV; ++i) mb_init(&sh.v_full[i], 1), mb_init(&sh.v_ready[i], 4), mb_init(&sh.v_empty[i], NS);
     for (int i = 0; i < NR; ++i) mb_init(&sh.r_full[i], 1), mb_init(&sh.r_empty[i], 4);
-    for (int i = 0; i < 2; ++i) mb_init(&sh.s_full[i], 1), mb_init(&sh.p_ready[i], 4), mb_init(&sh.pv_done[i], 1), mb_init(&sh.q_ready[i], 4);
-    mb_init(&sh.j_shown, 8), mb_init(&sh.j_read, 8);
+    for (int i = 0; i < 2; ++i) mb_init(&sh.s_full[i], 1), mb_init(&sh.p_half[i], 4), mb_init(&sh.half_done[i], 1), mb_init(&sh.p_ready[i], 4), mb_init(&sh.pv_done[i], 1), mb_init(&sh.q_ready[i], 4);
+    mb_init(&sh.go, 1), mb_init(&sh.j_shown, 8), mb_init(&sh.j_read, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.odd = 0;
   }
@@ -571,8 +577,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       if (lane == 0) mb_arrive(&sh.q_ready[st]);
     };
     uint32_t uses[2] = {0, 0};  // steps of each score buffer
-    uint32_t items = 0, joins = 0, tiles_before = 0;
-    if (st < NS && it.more) load_q(it);
+    uint32_t items = 0, joins = 0, finals = 0, tiles_before = 0;
+    auto has_steps = [&](const W &w) { return st == 0 || both_of(w) || w.u1 - w.u0 > 1; };
+    if (st < NS && it.more && has_steps(it)) load_q(it);
     while (it.more && st < NS) {
       const bool both = both_of(it);
       const int r = (both ? 128 * st : 0) + lrow;  // row of the item
@@ -592,9 +599,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       row.hi = pos;
       row.lo = P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
       const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < it.rows;
-      // the reference in scores; sums of the weights, and of the weights as they are rounded, which the outputs are
-      // divided by
-      float m = -INFINITY, l = 0.f, lw = 0.f;
+      float m = -INFINITY, l = 0.f;  // the reference, in scores; the weights' sum
       bool first = true;
       const int T = it.u1 - it.u0, K = both ? 2 * T : T;
       int sb = st;
@@ -611,8 +616,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           const uint32_t sa = tmem + lane_addr + sb * S::S_COLS;
           const uint32_t lost = sh.lost[(tiles_before + u) & 15];
           float base = m == -INFINITY ? 0.f : m * c;
-          float2 add = make_float2(0.f, 0.f), addw = make_float2(0.f, 0.f);
-          float v[32];
+          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float v[64];
           if (lost || masked<TN>(P, it.s, it.list, tile)) {
 #pragma unroll 1
             for (int x = 0; x < TN; x += 32) {
@@ -628,40 +633,33 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             tc_wait_st();
           }
-          // 32 places at a time: scores in, weights out (in place: their 16 columns lie behind what was read)
+          // 64 places at a time: scores in, weights out (in place: their 32 columns lie behind what was read)
 #pragma unroll 1
-          for (int x = 0; x < TN; x += 32) {
+          for (int x = 0; x < TN; x += 64) {
             tc_ld32(sa + x, v);
+            tc_ld32(sa + x + 32, v + 32);
             tc_wait_ld(v);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int y = 0; y < 32; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(v[y], v[y + 1]), mx[(y / 2) & 3]);
+            for (int y = 0; y < 64; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(v[y], v[y + 1]), mx[(y / 2) & 3]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             if (__any_sync(0xFFFFFFFFu, (top - m) * c > kGrowth)) {
-              // the row's reference moves up: sums, and the weights of the x places before, by the quotient
+              // the row's reference moves up: sums by the quotient
               const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
               m = mn;
               base = m == -INFINITY ? 0.f : m * c;
-              l *= f, lw *= f;
-              add.x *= f, add.y *= f, addw.x *= f, addw.y *= f;
-              float o[16];
-#pragma unroll 1
-              for (int y = 0; y < x / 2; y += 16) {
-                tc_ld16f(sa + y, o);
-                tc_wait_ld(o);
-                uint32_t h[16];
+              l *= f;
 #pragma unroll
-                for (int z = 0; z < 16; ++z)
-                  h[z] = bf16x2(__uint_as_float(__float_as_uint(o[z]) << 16) * f,
-                                __uint_as_float(__float_as_uint(o[z]) & 0xFFFF0000u) * f);
-                tc_st16u(sa + y, h);
-              }
-              if (!first) {
-                if (NS == 1) {
+              for (int y = 0; y < 2; ++y) add[y].x *= f, add[y].y *= f;
+              if (!first || x > 0) {
+                if (x > 0) {  // the products of the places before
+                  if (!warp_wait(&sh.half_done[sb], (uses[sb] - 1) & 1u)) timeout = true;
+                } else if (NS == 1) {  // of the step before (else its columns' next scores say so)
                   if (!warp_wait(&sh.pv_done[sb ^ 1], (uses[sb ^ 1] - 1) & 1u)) timeout = true;
-                  tc_fence_after();
                 }
+                tc_fence_after();
                 const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+                float o[16];
 #pragma unroll 1
                 for (int y = 0; y < D; y += 16) {
                   tc_ld16f(oa + y, o);
@@ -675,19 +673,25 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               tc_wait_st();
             }
             const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-            uint32_t pk[16];
+            uint32_t pk[32];
 #pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              const float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2);
-              const float2 w = make_float2(ex2(e.x), ex2(e.y));
-              const uint32_t h = pk[y / 2] = bf16x2(w.x, w.y);
-              add = add2(add, w);
-              addw = add2(addw, make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)));
+            for (int y = 0; y < 64; y += 2) {
+              const float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2), w = make_float2(ex2(e.x), ex2(e.y));
+              pk[y / 2] = bf16x2(w.x, w.y);
+              add[(y / 2) & 1] = add2(add[(y / 2) & 1], w);
             }
-            tc_st16u(sa + x / 2, pk);
+            tc_st32u(sa + x / 2, pk);
+            if (x + 64 < TN) {  // these can be multiplied while the others are computed
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mb_arrive(&sh.p_half[sb]);
+            }
           }
-          l += add.x + add.y, lw += addw.x + addw.y;
+          l += (add[0].x + add[0].y) + (add[1].x + add[1].y);
           tc_wait_st();
+        } else if (TN > 64 && lane == 0) {
+          mb_arrive(&sh.p_half[sb]);
         }
         first = false;
         tc_fence_before();
@@ -699,12 +703,13 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       const bool had = !first;  // whether this stream had a step
       W nx = it;
       nx.next(P);
-      if (had) {  // (the last scores are there: its queries are not read any more)
-        if (nx.more) load_q(nx);
-        if (!warp_wait(&sh.pv_done[sb], (uses[sb] - 1) & 1u)) {
+      if (nx.more && has_steps(nx)) load_q(nx);  // (the last scores are there: this one's are not read any more)
+      if (had) {
+        if (!warp_wait(&sh.pv_done[sb], (NS == 2 ? finals : uses[sb] - 1) & 1u)) {
           timeout = true;
           break;
         }
+        ++finals;
         tc_fence_after();
       }
       const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
@@ -751,8 +756,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       float mb = m == -INFINITY ? -INFINITY : m * c, f0 = 1.f, f1 = 0.f;
       const bool split = NS == 2 && !both;  // the streams share the rows: each writes half of the dimensions
       if (split) {
-        sh.stat[st][lrow] = make_float2(mb, lw);
-        if (st == 1) sh.sum1[lrow] = l;
+        sh.stat[st][lrow] = make_float2(mb, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mb_arrive(&sh.j_shown);
@@ -766,16 +770,15 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           mb = fmaxf(a.x, b.x);
           const float base = mb == -INFINITY ? 0.f : mb;
           f0 = ex2(a.x - base), f1 = ex2(b.x - base);
-          lw = a.y * f0 + b.y * f1;
-          if (st == 0) l = l * f0 + sh.sum1[lrow] * f1;
+          l = a.y * f0 + b.y * f1;
         } else {
-          mb = sh.stat[0][lrow].x, lw = sh.stat[0][lrow].y;
+          mb = sh.stat[0][lrow].x, l = sh.stat[0][lrow].y;
         }
       }
       if (warp_on) {
         const bool cut = it.cut();
         const int slot = 2 * blockIdx.x + (it.u0 > 0 ? 0 : 1);
-        const float inv = lw == 0.f ? 0.f : 1.f / lw;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t orow = static_cast<size_t>(grow_) * P.Hq + it.head * P.G + g;
         const int x0 = split ? st * (D / 2) : 0, x1 = split ? x0 + D / 2 : D;
         const uint32_t o0 = tmem + lane_addr + S::O_COL + (split ? 0 : st * S::O_COLS), o1 = o0 + S::O_COLS;
@@ -803,14 +806,14 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               uint32_t w[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
-                w[z] = lw == 0.f ? 0u : bf16x2(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
+                w[z] = l == 0.f ? 0u : bf16x2(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
               to[y] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
         if (row.on && !(split && st)) {
           if (cut)
-            P.stat[static_cast<size_t>(slot) * ROWS + r] = make_float4(mb, l, lw, 0.f);
+            P.stat[static_cast<size_t>(slot) * ROWS + r] = make_float2(mb, l);
           else if (P.lse)
             P.lse[orow] = l == 0.f ? -INFINITY : (mb + log2f(l)) * kLn2;
         }
@@ -819,7 +822,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mb_arrive(&sh.j_read);
-        if (!had && nx.more) load_q(nx);
         if (!warp_wait(&sh.j_read, joins & 1u)) {
           timeout = true;
           break;
@@ -835,64 +837,82 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       it = nx;
     }
   } else if (warp < 12) {
-    if (warp == 8) {
-      // ---- scores
-      uint32_t kt = 0, uses[2] = {0, 0}, items = 0;
-      const uint32_t id = idesc(TN, false);
-      for (; it.more && !timeout; it.next(P), ++items) {
-        const bool both = both_of(it);
-        const int T = it.u1 - it.u0, K = both ? 2 * T : T;
-        for (int x = 0; x < NS; ++x)
-          if (!warp_wait(&sh.q_ready[x], items & 1u)) timeout = true;
-        for (int k = 0; k < K && !timeout; ++k) {
-          const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
-          const uint32_t t = kt + (both ? k >> 1 : k), slot = t % NK;
-          // the buffer's weights have been used
-          bool ok = uses[sb] == 0 || warp_wait(&sh.pv_done[sb], (uses[sb] - 1) & 1u);
-          // of a longer item the second stream starts half a step behind, so that one's products meet the other's softmax
-          if (k == 1 && K > 8 && NS == 2) ok = ok && warp_wait(&sh.p_ready[0], (uses[0] - 1) & 1u);
-          if (!both || !(k & 1)) ok = ok && warp_wait(&sh.k_full[slot], (t / NK) & 1u);
-          if (!ok) {
-            timeout = true;
-            break;
-          }
-          ++uses[sb];
-          tc_fence_after();
-          const uint64_t qd = smem_desc_sw128(sbase + st * S::QB), kd = smem_desc_sw128(sbase + S::OFF_K + slot * S::TILE);
-#pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id, x > 0);
-          commit(&sh.s_full[sb]);
-          if (!both || (k & 1)) commit(&sh.k_empty[slot]);
-        }
-        kt += T;
-      }
-    } else if (warp == 10) {
-      // ---- weights with values
-      uint32_t vt = 0, uses[2] = {0, 0};
-      const uint32_t id = idesc(D, true);
+    if (warp == 8 || (NS == 2 && warp == 10)) {
+      // ---- products of one stream (or of both score buffers in turn): the scores of a step's next but one follow its
+      // weights' products, which read the same columns, in the tensor cores' order
+      const int st = NS == 2 ? (warp - 8) / 2 : 0;
+      uint32_t tiles_before = 0, kt = 0, vt = 0, uses[2] = {0, 0}, items = 0, goes = 0;
+      const uint32_t id_s = idesc(TN, false), id_o = idesc(D, true);
+      const uint64_t qd = smem_desc_sw128(sbase + st * S::QB);
       for (; it.more && !timeout; it.next(P)) {
         const bool both = both_of(it);
         const int T = it.u1 - it.u0, K = both ? 2 * T : T;
-        for (int k = 0; k < K; ++k) {
-          const int st = NS == 2 ? k & 1 : 0, sb = k & 1;
-          const uint32_t t = vt + (both ? k >> 1 : k), slot = t % NV;
-          bool ok = both && (k & 1) ? true : warp_wait(&sh.v_ready[slot], (t / NV) & 1u);
-          ok = ok && warp_wait(&sh.p_ready[sb], uses[sb] & 1u);
-          if (!ok) {
-            timeout = true;
-            break;
+        // every tile passes every stream, in order: those that it does not use it gives back at once
+        auto pass_keys = [&](uint32_t t) {
+          for (; kt < t; ++kt) {
+            if (!warp_wait(&sh.k_full[kt % NK], (kt / NK) & 1u)) return false;
+            if (lane == 0) mb_arrive(&sh.k_empty[kt % NK]);
           }
-          ++uses[sb];
+          return true;
+        };
+        auto pass_values = [&](uint32_t t) {
+          for (; vt < t; ++vt) {
+            if (!warp_wait(&sh.v_ready[vt % NV], (vt / NV) & 1u)) return false;
+            if (lane == 0) mb_arrive(&sh.v_empty[vt % NV]);
+          }
+          return true;
+        };
+        auto scores = [&](int k) {
+          const int sb = k & 1;
+          const uint32_t t = tiles_before + (both ? k >> 1 : k), slot = t % NK;
+          if (!pass_keys(t) || !warp_wait(&sh.k_full[slot], (t / NK) & 1u)) return false;
+          ++kt;
           tc_fence_after();
-          const uint64_t vd = values_desc(sbase + S::OFF_V + slot * S::TILE, TN * 128);
+          const uint64_t kd = smem_desc_sw128(sbase + S::OFF_K + slot * S::TILE);
 #pragma unroll
-          for (int x = 0; x < TN / 64; ++x)
-            mma4_values(tmem + S::O_COL + st * S::O_COLS, tmem + sb * S::S_COLS + x * 32, vd + x * (8192 / 16), id, x > 0 || k >= NS);
-          commit(&sh.pv_done[sb]);
-          if (!both || (k & 1)) commit(&sh.v_empty[slot]);
+          for (int x = 0; x < D / 64; ++x)
+            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
+          commit(&sh.s_full[sb]);
+          commit(&sh.k_empty[slot]);
+          return true;
+        };
+        if (NS == 1 || st < K) {
+          bool ok = warp_wait(&sh.q_ready[st], items & 1u);
+          ++items;
+          // of a longer item the second stream starts half a step behind, so that one's products meet the other's softmax
+          const bool skew = NS == 2 && K > 8;
+          if (st == 1 && skew) ok = ok && warp_wait(&sh.go, goes & 1u);
+          goes += skew;
+          ok = ok && scores(st);
+          if (NS == 1 && K > 1) ok = ok && scores(1);
+          for (int k = st; ok && k < K; k += NS) {
+            const int sb = k & 1;
+            const uint32_t t = tiles_before + (both ? k >> 1 : k), slot = t % NV;
+            const uint64_t vd = values_desc(sbase + S::OFF_V + slot * S::TILE, TN * 128);
+            const uint32_t od = tmem + S::O_COL + st * S::O_COLS, pa = tmem + sb * S::S_COLS;
+            ok = pass_values(t) && warp_wait(&sh.v_ready[slot], (t / NV) & 1u);
+            ++vt;
+            if (TN > 64) {
+              ok = ok && warp_wait(&sh.p_half[sb], uses[sb] & 1u);
+              if (!ok) break;
+              tc_fence_after();
+              if (skew && k == 0 && lane == 0) mb_arrive(&sh.go);
+              mma4_values(od, pa, vd, id_o, k >= NS);
+              commit(&sh.half_done[sb]);
+            }
+            ok = ok && warp_wait(&sh.p_ready[sb], uses[sb] & 1u);
+            if (!ok) break;
+            ++uses[sb];
+            tc_fence_after();
+            mma4_values(od, pa + (TN / 64 - 1) * 32, vd + (TN / 64 - 1) * (8192 / 16), id_o, TN > 64 || k >= NS);
+            if (k + 2 < K) ok = scores(k + 2);
+            commit(&sh.v_empty[slot]);
+            if (NS == 1 || k + NS >= K) commit(&sh.pv_done[sb]);
+          }
+          if (!ok) timeout = true;
         }
-        vt += T;
+        tiles_before += T;
+        if (timeout || !pass_keys(tiles_before) || !pass_values(tiles_before)) timeout = true;
       }
     } else if (warp == 9) {
       // ---- loads
@@ -1112,17 +1132,16 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
   const int r0 = me.z * ROWS, rows = min(ROWS, s.m * P.G - r0), r = 32 * blockIdx.y + lane;
   if (32 * static_cast<int>(blockIdx.y) >= rows) return;
   auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
-  float mm = -INFINITY, l = 0.f, lw = 0.f;
+  float mm = -INFINITY, l = 0.f;
   for (int p = 0; p < me.w; ++p) mm = fmaxf(mm, P.stat[slot_of(p) * ROWS + r].x);
   const float base = mm == -INFINITY ? 0.f : mm;
   for (int p = 0; p < me.w; ++p) {
-    const float4 st = P.stat[slot_of(p) * ROWS + r];
-    const float f = ex2(st.x - base);
-    l = fmaf(st.y, f, l), lw = fmaf(st.z, f, lw);
+    const float2 st = P.stat[slot_of(p) * ROWS + r];
+    l = fmaf(st.y, ex2(st.x - base), l);
   }
   const int i = (r0 + r) / P.G, g = r0 + r - i * P.G;
   const size_t row = (static_cast<size_t>(s.first) + i) * P.Hq + me.y * P.G + g;
-  const float inv = lw == 0.f ? 0.f : 1.f / lw;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   for (int x = 8 * warp; x < D; x += 32) {
     float o[8];
 #pragma unroll
@@ -1136,7 +1155,7 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
     if (r < rows) {
       uint32_t w[4];
 #pragma unroll
-      for (int z = 0; z < 4; ++z) w[z] = lw == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+      for (int z = 0; z < 4; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
       *reinterpret_cast<uint4 *>(P.out + row * D + x) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
@@ -1163,7 +1182,7 @@ AxSpace space_of(const k3moe_kv_cache &c, int B, int rows, int Hq) {
   s.first_entry = s.meta + aligned256(kAxMostBlocks * sizeof(int4));
   s.prefix = s.first_entry + aligned256((static_cast<size_t>(B) + 1) * 4);
   s.stat = s.prefix + aligned256(entries * 8);
-  s.part = s.stat + aligned256(2 * kAxMostBlocks * item * sizeof(float4));
+  s.part = s.stat + aligned256(2 * kAxMostBlocks * item * sizeof(float2));
   s.bytes = s.part + static_cast<size_t>(2) * kAxMostBlocks * item * c.dim * 4;
   return s;
 }
@@ -1245,7 +1264,7 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   uint8_t *w = static_cast<uint8_t *>(a.ws);
   P.plan = reinterpret_cast<AxPlan *>(w + s.plan), P.start = reinterpret_cast<AxStart *>(w + s.start);
   P.meta = reinterpret_cast<int4 *>(w + s.meta), P.first_entry = reinterpret_cast<int *>(w + s.first_entry);
-  P.prefix = reinterpret_cast<long long *>(w + s.prefix), P.stat = reinterpret_cast<float4 *>(w + s.stat);
+  P.prefix = reinterpret_cast<long long *>(w + s.prefix), P.stat = reinterpret_cast<float2 *>(w + s.stat);
   P.part = reinterpret_cast<float *>(w + s.part);
   const bool e = c.format == K3MOE_KV_E4M3;
   if (c.dim == 64) return e ? launch_extend<64, true>(c, P, st) : launch_extend<64, false>(c, P, st);
