@@ -78,7 +78,16 @@
 // heads of 128, bf16 (1.51 GB): 232 us, 6.5 TB/s; 64 sequences of 256 to 16384 tokens, 64 query and 8 key-value
 // heads, E4M3 (668 MB): 111 us, 6.0 TB/s; one of 131072 tokens (271 MB): 51 us, of which 8 are the start, the
 // last blocks and the join; 37 tokens of 96 heads: 3.2 us.
+//
+// First tokens that stay visible.  attn_sinks.cu builds this file once more with K3_AD_SINKS for rows that see the
+// first `sinks` places besides their window, and that are found by offsets, since some sequences may have none.  The sinks'
+// tokens lie on the line of an item before its window, in units of their own, so that the two are one run of units
+// and everything from the loads on works as it does without.
 #include <cuda_fp16.h>
+
+#ifndef K3_AD_SINKS
+#define K3_AD_SINKS 0
+#endif
 
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
@@ -90,6 +99,7 @@ namespace k3moe {
 
 namespace {
 
+constexpr bool kSinks = K3_AD_SINKS;
 constexpr int kRun = 16;                 // tokens of a product
 constexpr int kDirectTokens = 1024;      // items that see at most this many are never cut
 constexpr int kSplitTokens = 256;        // (see "More than 8 query heads" above)
@@ -199,10 +209,12 @@ struct AdParams {
   int max_pages;
   const int32_t *lens;
   int window;
+  const int32_t *offsets;  // (kSinks) first row of each sequence, which has one or none
+  int rows, sinks;
   float scale;
   uint16_t *out;
   float *lse;
-  int4 *meta;    // [2 blocks]: {first slot, parts, item, sequence} of the cut items of a piece: one that began
+  int4 *meta;    // [2 blocks]: {first slot, parts, item, row} of the cut items of a piece: one that began
                  // before it, one that begins in it and goes on (parts 0: none)
   float4 *stat;  // [2 blocks][8 NT]: {m', m, l, -}
   float4 *part;  // [2 blocks][accumulator quads][32 lanes]
@@ -215,10 +227,31 @@ __device__ __forceinline__ long long div_small(long long a, long long b) {
   return a / b;
 }
 
-// The tokens of one sequence that are seen, lo .. n - 1, and the place its units count from.
+// The tokens of one sequence that are seen, lo .. n - 1, and the place its units count from.  With sinks, places 0 ..
+// sinks - 1 are seen too: units count from t0 < split, and what lies d places behind t0 is place d of the cache below split.
 struct Seen {
   int n, lo, t0;
+  int split, sinks, row;
 };
+template <class W>
+__device__ __forceinline__ unsigned place_of(const W &w, unsigned tok) {
+  return kSinks && tok < static_cast<unsigned>(w.split) ? tok - static_cast<unsigned>(w.t0) : tok;
+}
+// Whether some of the `run` places from `place` on are seen (all of them below n), and whether all are.
+template <class W>
+__device__ __forceinline__ bool sees_some(const W &w, unsigned place, unsigned run) {
+  return place + run > static_cast<unsigned>(w.lo) || (kSinks && place < static_cast<unsigned>(w.sinks));
+}
+template <class W>
+__device__ __forceinline__ bool sees_all(const W &w, unsigned place, unsigned run) {
+  return (place >= static_cast<unsigned>(w.lo) && place + run <= static_cast<unsigned>(w.n)) ||
+         (kSinks && place + run <= static_cast<unsigned>(w.sinks));
+}
+template <class W>
+__device__ __forceinline__ bool sees(const W &w, unsigned place) {
+  return (place >= static_cast<unsigned>(w.lo) && place < static_cast<unsigned>(w.n)) ||
+         (kSinks && place < static_cast<unsigned>(w.sinks));
+}
 template <int RUN>
 __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   Seen s;
@@ -231,6 +264,25 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   }
   s.lo = P.window > 0 && s.n > P.window ? s.n - P.window : 0;
   s.t0 = s.lo & ~(RUN - 1);
+  if constexpr (kSinks) {
+    s.split = 0;
+    s.sinks = s.lo ? min(P.sinks, s.n) : 0;
+    const int before = (s.sinks + RUN - 1) / RUN * RUN;
+    if (before <= s.t0)
+      s.split = s.t0, s.t0 -= before;
+    else
+      s.t0 = 0;  // window and sinks are one stretch, or nearly
+    const int o0 = P.offsets[b], m = P.offsets[b + 1] - o0;
+    s.row = o0;
+    if (m != 1 || o0 < 0 || o0 >= P.rows) {  // no row; and nothing on the line
+      s.n = s.t0 = 0, s.row = -1;
+      if (m != 0 && report) set_status(P.status, K3MOE_DEV_BOUNDS);
+    } else if (s.n == 0 && report) {
+      set_status(P.status, K3MOE_DEV_BOUNDS);
+    }
+  } else {
+    s.row = b;
+  }
   return s;
 }
 template <int UNIT>
@@ -245,10 +297,11 @@ template <int RUN, int UNIT, int ITEM_LEN>
 struct Walk {
   int b, head, group;    // sequence, key-value head, which of its items
   int n, lo, t0;
+  int split, sinks, row;
   unsigned tok, stop;    // the warp's next run begins at tok; the piece holds the item's runs below stop
   long long begin;       // of the item
   bool more;             // whether a run is left
-  __device__ __forceinline__ int units() const { return units_of<UNIT>({n, lo, t0}); }
+  __device__ __forceinline__ int units() const { return units_of<UNIT>({n, lo, t0, 0, 0, 0}); }
   // The item's first unit at or past place x of the line.
   __device__ __forceinline__ int unit_at(long long x) const {
     const long long u = (x - begin - ITEM_LEN + kUnitLen - 1) / kUnitLen;
@@ -259,7 +312,10 @@ struct Walk {
     tok = static_cast<unsigned>(t0) + static_cast<unsigned>(unit_at(from)) * UNIT + first;
     stop = static_cast<unsigned>(t0) + static_cast<unsigned>(unit_at(to)) * UNIT + first;
   }
-  __device__ __forceinline__ void set(const Seen &s) { n = s.n, lo = s.lo, t0 = s.t0; }
+  __device__ __forceinline__ void set(const Seen &s) {
+    n = s.n, lo = s.lo, t0 = s.t0, row = s.row;
+    if constexpr (kSinks) split = s.split, sinks = s.sinks;
+  }
   __device__ __forceinline__ void next_item(const AdParams &P, long long from, long long to, int first) {
     begin += static_cast<long long>(units()) * kUnitLen + ITEM_LEN;
     more = begin + ITEM_LEN < to;
@@ -363,7 +419,7 @@ __device__ __forceinline__ void add_parts(const float4 (&s)[N][2], const float4 
 // to 127, as V's scales are, so that one factor of both would leave fp32's normal numbers where V is tiny (but for
 // the rounding of sums past 2^24, which must not make it infinite).
 template <int D, bool E4M3>
-__device__ __forceinline__ void store_quad(const AdParams &P, int b, int h0, int rows, int t, int m, const float4 &v,
+__device__ __forceinline__ void store_quad(const AdParams &P, int row, int h0, int rows, int t, int m, const float4 &v,
                                            const float (&mp)[2], const float (&mt)[2], const float (&lt)[2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, r0 = 8 * t + 2 * (lane & 3);
   float fin[2], up[2];
@@ -374,9 +430,9 @@ __device__ __forceinline__ void store_quad(const AdParams &P, int b, int h0, int
     fin[x] = __fdividef(E4M3 ? 0x1p-14f : 1.f, lt[x]);
     up[x] = E4M3 ? exp2f(fminf(pb - mb, 127.f)) : 1.f;
     if (P.lse && m == 0 && g == 0 && r0 + x < rows)
-      P.lse[static_cast<size_t>(b) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
+      P.lse[static_cast<size_t>(row) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
   }
-  uint16_t *op = P.out + (static_cast<size_t>(b) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
+  uint16_t *op = P.out + (static_cast<size_t>(row) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
   store_row2(op, fin[0], up[0], v.x, v.z, lt[0] != 0.f, r0 < rows);
   store_row2(op + D, fin[1], up[1], v.y, v.w, lt[1] != 0.f, r0 + 1 < rows);
 }
@@ -431,11 +487,11 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   auto zero_rows = [&]() {  // of the sequences that see nothing; every block takes its share
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
       const Seen s = seen_of<RUN>(P, b, false);
-      if (s.n > s.t0) continue;
+      if (s.n > s.t0 || s.row < 0) continue;
       for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += THREADS)
-        reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(b) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(s.row) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
       if (P.lse)
-        for (int i = tid; i < P.Hq; i += THREADS) P.lse[static_cast<size_t>(b) * P.Hq + i] = -INFINITY;
+        for (int i = tid; i < P.Hq; i += THREADS) P.lse[static_cast<size_t>(s.row) * P.Hq + i] = -INFINITY;
     }
   };
 
@@ -454,10 +510,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     cur.begin = 0;
     cur.more = true;
     if (cur.n <= cur.t0) {  // sees nothing
-      if (part) return;
+      if (part || cur.row < 0) return;
       const int h0 = cur.head * P.G + cur.group * NQ;
       const int rows = min(NQ, P.G - cur.group * NQ);
-      const size_t row = static_cast<size_t>(cur.b) * P.Hq + h0;
+      const size_t row = static_cast<size_t>(cur.row) * P.Hq + h0;
       for (int i = tid; i < rows * D / 8; i += THREADS)
         reinterpret_cast<uint4 *>(P.out + row * D)[i] = make_uint4(0, 0, 0, 0);
       if (P.lse && tid < rows) P.lse[row + tid] = -INFINITY;
@@ -543,11 +599,12 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   auto pages = [&]() {  // of the run at `pre`
 #pragma unroll
     for (int r = 0; r < RR; ++r) {
-      const unsigned tok = pre.tok + r * kRun;
+      const unsigned tok = pre.tok + r * kRun, at = place_of(pre, tok);
       // a run that lies in one page begins at most RUN - 1 places before the window, and needs that page.  Tiles that
       // lie in pages of their own may all be before it: those pages may have been given back, and are not looked up
-      const bool seen = tok < static_cast<unsigned>(pre.n) && (one_page || tok + kRun > static_cast<unsigned>(pre.lo));
-      if (r == 0 || !one_page) page[r] = seen ? row[tok >> P.page_shift] : -1;
+      const bool seen = tok < static_cast<unsigned>(pre.n) &&
+                        (one_page ? !kSinks || sees_some(pre, at, RUN) : sees_some(pre, at, kRun));
+      if (r == 0 || !one_page) page[r] = seen ? row[at >> P.page_shift] : -1;
     }
   };
   auto issue = [&](int st) {
@@ -558,10 +615,11 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         return static_cast<size_t>(static_cast<unsigned>(page)) * page_vecs +
                ((static_cast<unsigned>(pre.head) << P.page_shift) + (tok & place));
       };
-      if (one_page && pre.tok >= static_cast<unsigned>(pre.lo) && pre.tok + RUN <= static_cast<unsigned>(pre.n) &&
+      const unsigned here = place_of(pre, pre.tok);
+      if (one_page && sees_all(pre, here, RUN) &&
           static_cast<unsigned>(page[0]) < static_cast<unsigned>(P.pages)) {  // all of it is seen
         if (bad) bad &= ~(((1u << RR) - 1u) << (st * RR));
-        const size_t vec = vec_of(page[0], pre.tok);
+        const size_t vec = vec_of(page[0], here);
         const uint8_t *kp = klane + vec * S::ROWB, *vp = vlane + vec * S::ROWB;
 #pragma unroll
         for (int r = 0; r < RR; ++r)
@@ -577,10 +635,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
       } else {
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
-          const unsigned tok = pre.tok + r * kRun;
+          const unsigned tok = pre.tok + r * kRun, from_here = place_of(pre, tok);
           const int tile = st * RR + r, pg = one_page ? page[0] : page[r];
           if (tok >= static_cast<unsigned>(pre.n)) break;
-          if (tok + kRun <= static_cast<unsigned>(pre.lo)) {
+          if (!sees_some(pre, from_here, kRun)) {
             bad |= 1u << tile;
             continue;
           }
@@ -590,13 +648,12 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
             continue;
           }
           bad &= ~(1u << tile);
-          const size_t vec = vec_of(pg, tok);
+          const size_t vec = vec_of(pg, from_here);
           const uint8_t *kp = klane + vec * S::ROWB, *vp = vlane + vec * S::ROWB;
 #pragma unroll
           for (int i = 0; i < C / 2; ++i) {
             const uint32_t ki = C == 32 ? (i & 1) << 6 : 0, vi = C >= 8 ? ((i * RI) >> 2) << 5 : 0;
-            const unsigned at = tok + lr + i * RI;
-            const bool on = at >= static_cast<unsigned>(pre.lo) && at < static_cast<unsigned>(pre.n);
+            const bool on = sees(pre, from_here + lr + i * RI);
             cp16_or_zeros((kd ^ ki) + r * S::SUB + i * RI * S::ROWB, kp + i * 512, on);
             cp16_or_zeros((vd ^ vi) + r * S::SUB + i * RI * S::ROWB, vp + i * 512, on);
           }
@@ -635,7 +692,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = g + 8 * t;
-      const uint16_t *qp = P.q + at.b * P.q_stride + static_cast<size_t>(h0 + r) * D + c * (16 / S::ESZ);
+      const uint16_t *qp = P.q + at.row * P.q_stride + static_cast<size_t>(h0 + r) * D + c * (16 / S::ESZ);
 #pragma unroll
       for (int i = 0; i < KL; ++i)
 #pragma unroll
@@ -705,8 +762,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     __syncwarp();
     if (cur.tok < static_cast<unsigned>(cur.n)) {
       const uint32_t base0 = ring + stage * (RR * S::SUB), sbase = sring + stage * (RR * S::SCALES);
-      const bool whole = cur.tok >= static_cast<unsigned>(cur.lo) &&
-                         cur.tok + S::RUN <= static_cast<unsigned>(cur.n) && bad == 0u;
+      const bool whole = sees_all(cur, place_of(cur, cur.tok), S::RUN) && bad == 0u;
       // S^T: rows g and g + 8 are tokens tg and tg + 2 of the 16, tg = 4 (g / 2) + g % 2, columns 2c and
       // 2c + 1 query heads.  CH partial sums, so that a product does not wait for the one before it
       constexpr int CH = RR * NT >= 4 ? 1 : 2, T2 = 2 * RR;
@@ -792,8 +848,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll
         for (int j = 0; j < T2; ++j) {
           const unsigned tok = cur.tok + (j >> 1) * kRun + tg + 2 * (j & 1);
-          if (tok < static_cast<unsigned>(cur.lo) || tok >= static_cast<unsigned>(cur.n) ||
-              ((bad >> (stage * RR + (j >> 1))) & 1u)) {
+          if (!sees(cur, place_of(cur, tok)) || ((bad >> (stage * RR + (j >> 1))) & 1u)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) sc[t][0][j] = sc[t][1][j] = -INFINITY;
             if (E4M3) ve[j] = 0.f;
@@ -996,7 +1051,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         else if (parts > 1)
           shown[quad * 32 + lane] = v;
         else
-          store_quad<D, E4M3>(P, done.b, h0, rows, t, m, v, mp, mt, lt);
+          store_quad<D, E4M3>(P, done.row, h0, rows, t, m, v, mp, mt, lt);
       }
       __syncthreads();
     }
@@ -1008,7 +1063,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
             // not the first item of its block if the one before has a unit there
             2 * b0 + (done.begin - kUnitLen >= b0 * share ? 1 : 0),
             static_cast<int>(div_small(unit0 + static_cast<long long>(done.units() - 1) * kUnitLen, share)) - b0 + 1,
-            done.head * P.groups + done.group, done.b);
+            done.head * P.groups + done.group, done.row);
       }
     }
     first_item = false;
@@ -1042,7 +1097,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
           }
         }
         add_parts(s, u, v, mp, mt, lt);
-        store_quad<D, E4M3>(P, cur.b, h0, rows, t, m, v, mp, mt, lt);
+        store_quad<D, E4M3>(P, cur.row, h0, rows, t, m, v, mp, mt, lt);
       }
       cluster_sync();  // the others have read this block's
     }
@@ -1222,7 +1277,8 @@ int clusters_at_once(const AdParams &P, int parts) {
 long long items_of(const AdParams &P) { return static_cast<long long>(P.B) * P.heads * P.groups; }
 long long tokens_of(const AdParams &P) {
   const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
-  return P.window > 0 && P.window < visible ? P.window : visible;
+  const long long seen = static_cast<long long>(P.window) + (kSinks ? P.sinks : 0);
+  return P.window > 0 && seen < visible ? seen : visible;
 }
 
 // No more items than SMs: how many blocks share one, 0 where there are more or they are too long for that.
@@ -1280,11 +1336,25 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
 
 }  // namespace
 
+#if K3_AD_SINKS
+int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st) {
+  const k3moe_kv_cache &c = a.c;
+  const int B = a.B, Hq = a.Hq, max_pages = a.max_pages, window = a.window;
+  const uint16_t *q = a.q;
+  const long long q_stride = a.q_stride;
+  const int32_t *table = a.table, *lens = a.lens;
+  const float scale = a.scale;
+  uint16_t *out = a.out;
+  float *lse = a.lse;
+  void *ws = a.ws;
+  int32_t *status = a.status;
+#else
 size_t attn_decode_workspace(const k3moe_kv_cache &c, int, int Hq) { return plan_of(c, Hq).bytes; }
 
 int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q, long long q_stride,
                        const int32_t *table, int max_pages, const int32_t *lens, int window, float scale, uint16_t *out,
                        float *lse, void *ws, int32_t *status, cudaStream_t st) {
+#endif
   const AdPlan p = plan_of(c, Hq);
   AdParams P;
   P.k = static_cast<const uint8_t *>(c.k), P.v = static_cast<const uint8_t *>(c.v), P.ks = c.k_scales, P.vs = c.v_scales;
@@ -1293,6 +1363,11 @@ int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q
   P.B = B, P.Hq = Hq, P.G = Hq / c.heads, P.groups = p.groups;
   P.q = q, P.q_stride = q_stride, P.table = table, P.max_pages = max_pages, P.lens = lens;
   P.window = window, P.scale = scale, P.out = out, P.lse = lse;
+#if K3_AD_SINKS
+  P.offsets = a.offsets, P.rows = a.rows, P.sinks = a.sinks;
+#else
+  P.offsets = nullptr, P.rows = P.sinks = 0;
+#endif
   uint8_t *w = static_cast<uint8_t *>(ws);
   P.meta = reinterpret_cast<int4 *>(w + p.meta), P.stat = reinterpret_cast<float4 *>(w + p.stat);
   P.part = reinterpret_cast<float4 *>(w + p.part), P.status = status;

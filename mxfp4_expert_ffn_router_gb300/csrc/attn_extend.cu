@@ -1248,9 +1248,13 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq) { return space_of(c, B, rows, Hq).bytes; }
+size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq) {
+  const size_t several = space_of(c, B, rows, Hq).bytes, one = attn_decode_workspace(c, B, Hq);
+  return several > one ? several : one;
+}
 
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
+  if (a.max_new == 1 && !a.masks) return launch_attn_sinks(a, st);
   AxParams P;
   const k3moe_kv_cache &c = a.c;
   P.k = static_cast<const uint8_t *>(c.k), P.v = static_cast<const uint8_t *>(c.v), P.ks = c.k_scales, P.vs = c.v_scales;

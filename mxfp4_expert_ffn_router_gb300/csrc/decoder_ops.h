@@ -40,6 +40,7 @@ struct ExtendArgs {
   void *ws;
   int32_t *status;
 };
+int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st);  // at most one new token a sequence
 size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq);
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st);
 
