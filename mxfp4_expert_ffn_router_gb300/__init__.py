@@ -152,7 +152,8 @@ def _load_fast(L):
     """The binding's C++ part (csrc/torch_fast.cpp) over the loaded library."""
     from . import _k3torch
     _k3torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                    for f in (L.k3moe_rmsnorm, L.k3moe_kv_write, L.k3moe_kv_read, L.k3moe_attn_decode)))
+                    for f in (L.k3moe_rmsnorm, L.k3moe_kv_write, L.k3moe_kv_read, L.k3moe_attn_decode, L.k3moe_kv_append,
+                              L.k3moe_attn_extend, L.k3moe_attn_tree)))
     return _k3torch
 
 
@@ -562,6 +563,11 @@ def k3moe_kv_append(cache: KVCache, k, v, slots, positions, rotation: Rotation, 
     """Keys and values k, v [n, heads, dim] (bf16; the first axis may be strided) of tokens at ``positions``
     [n] (int32) into the cache's slots [n] (as k3moe_kv_write), the keys rotated; and the queries q [n, Hq,
     dim] rotated into q_out (both may be strided; q_out may be q).  Nothing of a token with a negative slot is written."""
+    if _fast is not None:
+        rc = _fast.kv_append(cache._addr, k, v, slots, positions, rotation._addr, q, q_out, dev_status,
+                             None if stream is None else stream.cuda_stream)
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_kv_append", rc)
     shape = (slots.numel(), cache.heads, cache.dim)
     n = shape[0]
     kp, ks = _rows(k, shape, "k")
@@ -610,6 +616,12 @@ def k3moe_attn_extend(cache: KVCache, q, q_offsets, block_table, seq_lens, out, 
     last ones of the seq_lens[b] cached tokens.  A token sees itself and those before it; with window > 0 of
     these the last ``window`` and the first ``sinks``.  out [rows, Hq, dim] (bf16), lse [rows, Hq] (fp32); max_new:
     no sequence has more (1 takes the kernels of single tokens); ws: k3moe_attn_extend_workspace_bytes."""
+    if _fast is not None:
+        rc = _fast.attn_extend(cache._addr, q, q_offsets, None, block_table, seq_lens, out, lse,
+                               cache.dim ** -0.5 if scale is None else scale, window, sinks, max_new, ws, dev_status,
+                               None if stream is None else stream.cuda_stream)
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_attn_extend", rc)
     rows, Hq, B, pages, qp, qs, offs, table, lens = _extend_args(cache, q, q_offsets, block_table, seq_lens)
     rc = lib().k3moe_attn_extend(cache._ref, B, rows, Hq, qp, qs, offs, rows if max_new is None else _most(max_new), table,
                                  pages, lens, _most(window), _most(sinks), cache.dim ** -0.5 if scale is None else scale,
@@ -625,6 +637,12 @@ def k3moe_attn_tree(cache: KVCache, q, q_offsets, masks, block_table, seq_lens, 
     """k3moe_attn_extend for drafted tokens: of its sequence's new tokens row r sees those whose bits its mask
     has (masks [rows, words] int64: bit j % 64 of word j // 64 stands for new token j), and all of the cached
     ones before them that the window and the sinks leave, the window counting from n - m + (new tokens seen) - 1."""
+    if _fast is not None and masks is not None:
+        rc = _fast.attn_extend(cache._addr, q, q_offsets, masks, block_table, seq_lens, out, lse,
+                               cache.dim ** -0.5 if scale is None else scale, window, sinks, None, ws, dev_status,
+                               None if stream is None else stream.cuda_stream)
+        if rc is not None:  # (None: an argument is not acceptable, and the checks below say which)
+            return _check("k3moe_attn_tree", rc)
     rows, Hq, B, pages, qp, qs, offs, table, lens = _extend_args(cache, q, q_offsets, block_table, seq_lens)
     if not isinstance(masks, torch.Tensor) or masks.dim() != 2:
         raise ValueError("masks: expected a tensor [rows, words]")
