@@ -1,5 +1,6 @@
 // attn_extend.cu -- attention of several new tokens per sequence over a paged key-value cache.
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 
 #include "decoder_ops.h"
 #include "k3moe_dev.cuh"
@@ -78,13 +79,17 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
 }
 
 // What a block's warps share besides the tiles.
-template <int NK, int NV, int NR>
+template <int NK, int NV, int NR, int TK>
 struct AxShared {
-  uint64_t k_full[NK], k_empty[NK], v_full[NV], v_ready[NV], v_empty[NV], r_full[NR], r_empty[NR];
+  uint64_t k_full[NK], k_ready[NK], k_empty[NK], v_full[NV], v_ready[NV], v_empty[NV], r_full[NR], r_empty[NR];
   uint64_t s_full[2], p_half[2], half_done[2], p_ready[2], pv_done[2], q_ready[2];
   uint64_t go;               // the second stream may start
   uint64_t j_shown, j_read;  // the streams' joint: sums shown, sums read
   float2 stat[2][128];       // the streams' statistics: reference, sum of the weights
+  alignas(16) float key_scale[8][TK];
+  alignas(16) float ones[TK];  // (E4M3) of the places of a tile, by turns
+  float row_scale[2][2][TK > 1 ? 128 : 1];  // (E4M3) of the query rows, of items by turns
+  alignas(16) uint8_t key_bytes[NK][TK > 1 ? 128 : 16];
   uint8_t lost[16];  // of a tile: bit x for the 16 places from 16 x on that lie in no page of the cache
   uint32_t odd;      // bit x: values that are not finite were left out of item x's products
   uint32_t tmem;
@@ -96,15 +101,13 @@ struct AxShape {
   static constexpr int NS = D == 256 ? 1 : 2;      // streams: 128 query rows with sums of their own
   static constexpr int ROWS = 128 * NS;            // query rows of an item
   static constexpr int QB = 128 * D * 2;           // bytes of a stream's queries
-  static constexpr int TILE = TN * D * 2;          // bytes of a tile's keys or values as operands
-  static constexpr int RAW = E4M3 ? TN * D : 0;    // as codes
-  static constexpr int NK = D == 64 ? (E4M3 ? 3 : 4) : E4M3 ? 2 : 3;
-  static constexpr int NV = D == 64 ? (E4M3 ? 3 : 4) : 2;
-  static constexpr int NR = E4M3 ? (D == 64 ? 4 : 2) : 0;
-  static constexpr int RAWB = RAW + (E4M3 ? 128 : 0);  // codes and scales
-  static constexpr int OFF_K = NS * QB, OFF_V = OFF_K + NK * TILE, OFF_R = OFF_V + NV * TILE;
-  using Shared = AxShared<NK, NV, NR ? NR : 1>;
-  static constexpr int OFF_S = OFF_R + NR * RAWB;
+  static constexpr int TILE = TN * D * 2;          // bytes of a tile's values as operands
+  static constexpr int KTILE = E4M3 ? TN * D : TILE;  // of its keys
+  static constexpr int RAWB = E4M3 ? TN * D + 128 : 0;  // of its values' codes and scales
+  static constexpr int NK = D == 64 ? 4 : 3, NV = D == 64 ? (E4M3 ? 3 : 4) : 2, NR = E4M3 ? (D == 64 ? 4 : 2) : 0;
+  static constexpr int SW = D * (E4M3 ? 1 : 2) >= 128 ? 128 : 64;  // bytes of a swizzled row of keys and queries
+  using Shared = AxShared<NK, NV, NR ? NR : 1, E4M3 ? TN : 1>;
+  static constexpr int OFF_K = NS * QB, OFF_V = OFF_K + NK * KTILE, OFF_R = OFF_V + NV * TILE, OFF_S = OFF_R + NR * RAWB;
   static constexpr int SMEM = OFF_S + sizeof(Shared);
   static constexpr int S_COLS = TN;                // columns of a score buffer
   static constexpr int O_COL = 256, O_COLS = D == 256 ? 256 : 128;
@@ -266,6 +269,17 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                : "memory");
 }
 
+// Rows of 64 bytes, 64-byte swizzle, groups of eight rows 512 bytes; or of 128 (smem_desc_sw128).
+template <int SW>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t saddr) {
+  if (SW == 128) return smem_desc_sw128(saddr);
+  return static_cast<uint64_t>((saddr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(1) << 16) |
+         (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(4) << 61);
+}
+// Instruction descriptor, kind::f8f6f4: E4M3 A and B along K, fp32 sums.
+__device__ __forceinline__ uint32_t idesc_e4m3(int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
+}
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 sums; B along K (keys) or along N (values).
 __device__ __forceinline__ uint32_t idesc(int N, bool b_along_n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_along_n ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -293,6 +307,18 @@ __device__ __forceinline__ void mma4_scores(uint32_t d, uint64_t a, uint64_t b, 
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+// Two products of 32 dimensions each in E4M3.
+__device__ __forceinline__ void mma2_scores_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t.reg .b64 a1, b1;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, %3, %3;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, q;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
@@ -378,6 +404,16 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t codes_up(uint32_t w, uint32_t sel) {
   const uint32_t x = __byte_perm(w, 0u, sel);
   return ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+}
+
+// Raw scores times their keys' scales.
+template <int N, int M>
+__device__ __forceinline__ void scale_keys(float (&v)[M], const float *ks) {
+#pragma unroll
+  for (int y = 0; y < N; y += 4) {
+    const float4 k = *reinterpret_cast<const float4 *>(ks + y);
+    v[y] *= k.x, v[y + 1] *= k.y, v[y + 2] *= k.z, v[y + 3] *= k.w;
+  }
 }
 
 // What a row sees.
@@ -514,7 +550,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
   const uint32_t sbase = su32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < NK; ++i) mb_init(&sh.k_full[i], E4M3 ? 4 : 1), mb_init(&sh.k_empty[i], NS);
+    for (int i = 0; i < NK; ++i) mb_init(&sh.k_full[i], 1), mb_init(&sh.k_ready[i], 1), mb_init(&sh.k_empty[i], NS);
     for (int i = 0; i < NV; ++i) mb_init(&sh.v_full[i], 1), mb_init(&sh.v_ready[i], 4), mb_init(&sh.v_empty[i], NS);
     for (int i = 0; i < NR; ++i) mb_init(&sh.r_full[i], 1), mb_init(&sh.r_empty[i], 4);
     for (int i = 0; i < 2; ++i) mb_init(&sh.s_full[i], 1), mb_init(&sh.p_half[i], 4), mb_init(&sh.half_done[i], 1), mb_init(&sh.p_ready[i], 4), mb_init(&sh.pv_done[i], 1), mb_init(&sh.q_ready[i], 4);
@@ -522,6 +558,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.odd = 0;
   }
+  if (E4M3 && tid < TN) sh.ones[tid] = 1.f;
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(&sh.tmem)), "r"(512)
                  : "memory");
@@ -545,15 +582,15 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     const int lrow = 32 * (warp & 3) + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
-    const float c = flat ? 1.f : fabsf(P.scale) * kLog2e;
+    const float c1 = flat ? 1.f : fabsf(P.scale) * kLog2e;
     const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = flat ? 0u : 0xFFFFFFFFu;
     // this stream's queries of an item into shared memory
+    uint32_t turn = 0;
     auto load_q = [&](const W &w) {
       constexpr int CH = D / 8, N = 8;
       const int base = w.r0 + (both_of(w) ? 128 * st : 0), left = w.r0 + w.rows - base;
       const int i0 = base / P.G, g0 = base - i0 * P.G, ch = tid % CH, first = (tid & 127) / CH;
       const uint16_t *q = P.q + (static_cast<long long>(w.s.first) + i0) * P.q_stride + static_cast<size_t>(w.head) * P.G * D + ch * 8;
-      uint8_t *to = smem + st * S::QB + (ch / 8) * (128 * 128);
 #pragma unroll
       for (int j = 0; j < CH; j += N) {
         uint4 u[N];
@@ -569,9 +606,35 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           const int rr = first + (j + x) * (128 / CH);
           u[x].x = (u[x].x ^ flip) & keep, u[x].y = (u[x].y ^ flip) & keep;
           u[x].z = (u[x].z ^ flip) & keep, u[x].w = (u[x].w ^ flip) & keep;
-          *reinterpret_cast<uint4 *>(to + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u[x];
+          if constexpr (!E4M3) {
+            *reinterpret_cast<uint4 *>(smem + st * S::QB + (ch / 8) * (128 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u[x];
+          } else {
+            // the row times a power of two, to a largest value in [128, 256), in two E4M3 numbers a value
+            uint32_t m = __vmaxu2(__vmaxu2(u[x].x & 0x7FFF7FFFu, u[x].y & 0x7FFF7FFFu),
+                                  __vmaxu2(u[x].z & 0x7FFF7FFFu, u[x].w & 0x7FFF7FFFu));
+            m = max(m >> 16, m & 0xFFFFu);
+#pragma unroll
+            for (int off = 1; off < CH; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+            const int e = m == 0 ? 0 : max(-126, min(127, 7 + 127 - static_cast<int>(m >> 7)));
+            const float up = exp2i(e);
+            const uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const float a = __uint_as_float(w[y] << 16) * up, b = __uint_as_float(w[y] & 0xFFFF0000u) * up;
+              hi[y] = m >= 0x7F80u ? 0x7F7Fu : e4m3x2(a, b);  // (a row that is not finite gives NaN)
+              const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[y]), __NV_E4M3)));
+              lo[y] = e4m3x2(a - f.x, b - f.y);
+            }
+            const int byte = ch * 8 % S::SW, sw = S::SW == 128 ? rr & 7 : (rr >> 1) & 3;
+            uint8_t *to = smem + st * S::QB + (ch * 8 / S::SW) * (128 * S::SW) + rr * S::SW + (((byte >> 4) ^ sw) << 4) + (byte & 8);
+            *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2 *>(to + 128 * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+            if (ch == 0) sh.row_scale[turn & 1][st][rr] = mx_pow2(-e);
+          }
         }
       }
+      ++turn;
       fence_async();
       __syncwarp();
       if (lane == 0) mb_arrive(&sh.q_ready[st]);
@@ -600,6 +663,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       row.lo = P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
       const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < it.rows;
       float m = -INFINITY, l = 0.f;  // the reference, in scores; the weights' sum
+      float c = c1;                  // powers of two of a score
       bool first = true;
       const int T = it.u1 - it.u0, K = both ? 2 * T : T;
       int sb = st;
@@ -612,7 +676,10 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
         ++uses[sb];
         tc_fence_after();
+        if (E4M3 && first) c = c1 * sh.row_scale[(turn - 1) & 1][st][lrow];
         if (warp_on) {
+          const float *ks = nullptr;
+          if constexpr (E4M3) ks = sh.key_scale[(tiles_before + u) & 7];
           const uint32_t sa = tmem + lane_addr + sb * S::S_COLS;
           const uint32_t lost = sh.lost[(tiles_before + u) & 15];
           float base = m == -INFINITY ? 0.f : m * c;
@@ -626,12 +693,14 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               if (lost >> (x / 16) & 1u) vis &= 0xFFFF0000u;
               if (lost >> (x / 16) & 2u) vis &= 0xFFFFu;
               tc_wait_ld(v);
+              if constexpr (E4M3) scale_keys<32>(v, ks + x);
 #pragma unroll
               for (int y = 0; y < 32; ++y)
                 if (!((vis >> y) & 1u)) v[y] = -INFINITY;
               tc_st32r(sa + x, v);
             }
             tc_wait_st();
+            if constexpr (E4M3) ks = sh.ones;  // (they are scaled)
           }
           // 64 places at a time: scores in, weights out (in place: their 32 columns lie behind what was read)
 #pragma unroll 1
@@ -639,6 +708,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             tc_ld32(sa + x, v);
             tc_ld32(sa + x + 32, v + 32);
             tc_wait_ld(v);
+            if constexpr (E4M3) scale_keys<64>(v, ks + x);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int y = 0; y < 64; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(v[y], v[y + 1]), mx[(y / 2) & 3]);
@@ -842,15 +912,16 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       // weights' products, which read the same columns, in the tensor cores' order
       const int st = NS == 2 ? (warp - 8) / 2 : 0;
       uint32_t tiles_before = 0, kt = 0, vt = 0, uses[2] = {0, 0}, items = 0, goes = 0;
-      const uint32_t id_s = idesc(TN, false), id_o = idesc(D, true);
-      const uint64_t qd = smem_desc_sw128(sbase + st * S::QB);
+      const uint32_t id_s = E4M3 ? idesc_e4m3(TN) : idesc(TN, false), id_o = idesc(D, true);
+      const uint64_t qd = rows_desc<S::SW>(sbase + st * S::QB);
+      uint64_t *const keys = E4M3 ? sh.k_ready : sh.k_full;
       for (; it.more && !timeout; it.next(P)) {
         const bool both = both_of(it);
         const int T = it.u1 - it.u0, K = both ? 2 * T : T;
         // every tile passes every stream, in order: those that it does not use it gives back at once
         auto pass_keys = [&](uint32_t t) {
           for (; kt < t; ++kt) {
-            if (!warp_wait(&sh.k_full[kt % NK], (kt / NK) & 1u)) return false;
+            if (!warp_wait(&keys[kt % NK], (kt / NK) & 1u)) return false;
             if (lane == 0) mb_arrive(&sh.k_empty[kt % NK]);
           }
           return true;
@@ -865,13 +936,22 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         auto scores = [&](int k) {
           const int sb = k & 1;
           const uint32_t t = tiles_before + (both ? k >> 1 : k), slot = t % NK;
-          if (!pass_keys(t) || !warp_wait(&sh.k_full[slot], (t / NK) & 1u)) return false;
+          if (!pass_keys(t) || !warp_wait(&keys[slot], (t / NK) & 1u)) return false;
           ++kt;
           tc_fence_after();
-          const uint64_t kd = smem_desc_sw128(sbase + S::OFF_K + slot * S::TILE);
+          const uint64_t kd = rows_desc<S::SW>(sbase + S::OFF_K + slot * S::KTILE);
+          if constexpr (E4M3) {
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
+            for (int x = 0; x < 2 * (D / 64); ++x) {  // both parts of the queries
+              const int part = x / (D / 64), y = x % (D / 64);  // 64 dimensions
+              mma2_scores_e4m3(tmem + sb * S::S_COLS, qd + (part * (128 * D) + y * 64 / S::SW * (128 * S::SW) + y * 64 % S::SW) / 16,
+                               kd + (y * 64 / S::SW * (TN * S::SW) + y * 64 % S::SW) / 16, id_s, x > 0);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
+          }
           commit(&sh.s_full[sb]);
           commit(&sh.k_empty[slot]);
           return true;
@@ -941,16 +1021,17 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             uint64_t *full;
             uint32_t dst;
             bool ok = true;
-            if constexpr (E4M3) {
-              const uint32_t slot = rt % NR;
-              if (lane == 0) ok = mb_wait(&sh.r_empty[slot], ((rt / NR) & 1u) ^ 1u);
-              full = &sh.r_full[slot], dst = sbase + S::OFF_R + slot * S::RAWB;
-              ++rt;
-            } else if (kv == 0) {
+            uint32_t bytes = 0;  // where the scales go
+            if (kv == 0) {
               const uint32_t slot = kt % NK;
               if (lane == 0) ok = mb_wait(&sh.k_empty[slot], ((kt / NK) & 1u) ^ 1u);
-              full = &sh.k_full[slot], dst = sbase + S::OFF_K + slot * S::TILE;
+              full = &sh.k_full[slot], dst = sbase + S::OFF_K + slot * S::KTILE, bytes = su32(sh.key_bytes[slot]);
               ++kt;
+            } else if constexpr (E4M3) {
+              const uint32_t slot = rt % NR;
+              if (lane == 0) ok = mb_wait(&sh.r_empty[slot], ((rt / NR) & 1u) ^ 1u);
+              full = &sh.r_full[slot], dst = sbase + S::OFF_R + slot * S::RAWB, bytes = dst + TN * D;
+              ++rt;
             } else {
               const uint32_t slot = vt % NV;
               if (lane == 0) ok = mb_wait(&sh.v_empty[slot], ((vt / NV) & 1u) ^ 1u);
@@ -973,7 +1054,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
               for (int x = 0; x < BOXES; ++x)
                 tma_load_4d(dst + x * (TN * BOX) + lane * (run * BOX), kv ? &vmap : &kmap, x * (BOX / EB), at, it.head, page, full);
               if (scales)
-                bulk_load(dst + S::RAW + lane * run,
+                bulk_load(bytes + lane * run,
                           (kv ? P.vs : P.ks) + (((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) + at), run, full);
             }
           }
@@ -983,130 +1064,123 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       if (timeout && lane == 0) {
         if constexpr (E4M3) {
           for (uint32_t i = rt < NR ? 0 : rt - NR; i < rt; ++i) mb_wait(&sh.r_full[i % NR], (i / NR) & 1u);
+          for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&sh.k_full[i % NK], (i / NK) & 1u);
         } else {
           for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&sh.k_full[i % NK], (i / NK) & 1u);
           for (uint32_t i = vt < NV ? 0 : vt - NV; i < vt; ++i) mb_wait(&sh.v_full[i % NV], (i / NV) & 1u);
         }
       }
+    } else if (E4M3 && warp == 11) {
+      // ---- the keys' scales as numbers
+      uint32_t kt = 0;
+      for (; it.more && !timeout; it.next(P)) {
+        for (int u = it.u0; u < it.u1; ++u, ++kt) {
+          if (!warp_wait(&sh.k_full[kt % NK], (kt / NK) & 1u)) {
+            timeout = true;
+            break;
+          }
+          for (int x = lane; x < TN; x += 32) sh.key_scale[kt & 7][x] = e8m0_to_f32(sh.key_bytes[kt % NK][x]);
+          __syncwarp();
+          if (lane == 0) mb_arrive(&sh.k_ready[kt % NK]);
+        }
+      }
     }
   } else {
-    // ---- codes become operands; values that a row does not see must not be other than finite
+    // ---- values: codes become bf16 operands, and what a row does not see must not be other than finite
     const int t128 = tid - 384;
-    uint32_t kt = 0, vt = 0, rt = 0, seq = 0, items = 0;
+    uint32_t vt = 0, items = 0;
     for (; it.more && !timeout; it.next(P), ++items) {
       if (t128 == 0) atomicAnd(&sh.odd, ~(1u << ((items + 16) & 31)));
-      for (int u = it.u0; u < it.u1 && !timeout; ++u, ++seq) {
+      for (int u = it.u0; u < it.u1; ++u, ++vt) {
         const int tile = it.list.tile(u);
-        uint32_t lost = 0;
-        bool check = masked<TN>(P, it.s, it.list, tile);
+        const uint32_t slot = vt % NV, rs = vt % NR;
+        if (!(E4M3 ? warp_wait(&sh.r_full[rs], (vt / NR) & 1u) && warp_wait(&sh.v_empty[slot], ((vt / NV) & 1u) ^ 1u)
+                   : warp_wait(&sh.v_full[slot], (vt / NV) & 1u))) {
+          timeout = true;
+          break;
+        }
+        const uint32_t lost = sh.lost[vt & 15];
+        const bool check = lost || masked<TN>(P, it.s, it.list, tile);
         auto there = [&](int place) {  // whether a row may see it
           return it.list.needs(it.s, place & ~15, 16) && place < it.s.n && !(lost >> ((place % TN) / 16) & 1u);
         };
+        auto finite = [&](uint32_t (&h)[4]) {  // leaves out what is not, and remembers that
+          bool odd = false;
 #pragma unroll
-        for (int kv = E4M3 ? 0 : 1; kv < 2; ++kv) {
-          uint32_t op;
-          uint64_t *ready;
-          if constexpr (E4M3) {
-            const uint32_t rs = rt % NR;
-            if (!warp_wait(&sh.r_full[rs], (rt / NR) & 1u)) timeout = true;
-            const uint32_t slot = kv ? vt % NV : kt % NK;
-            uint64_t *empty = kv ? &sh.v_empty[slot] : &sh.k_empty[slot];
-            if (!warp_wait(empty, (((kv ? vt / NV : kt / NK)) & 1u) ^ 1u)) timeout = true;
-            if (timeout) break;
-            lost = sh.lost[seq & 15], check = check || lost;
-            ready = kv ? &sh.v_ready[slot] : &sh.k_full[slot];
-            op = (kv ? S::OFF_V : S::OFF_K) + slot * S::TILE;
-            const uint8_t *raw = smem + S::OFF_R + rs * S::RAWB, *scales = raw + S::RAW;
-            constexpr int BOX = D < 128 ? D : 128, CH = D / 16;  // chunks of 16 codes in a row
-            for (int x = t128; x < TN * CH; x += 128) {
-              const int rr = x / CH, ch = x % CH;
-              uint4 u4 = *reinterpret_cast<const uint4 *>(raw + (ch * 16 / BOX) * (TN * BOX) + rr * BOX + (ch * 16) % BOX);
-              uint32_t in[4] = {u4.x, u4.y, u4.z, u4.w}, h[8];
-              const int place = tile * TN + rr;
-              uint32_t byte = scales[rr];
-              if (check) {
-                if (!there(place)) byte = 127u, in[0] = in[1] = in[2] = in[3] = 0u;
-              }
-              // 2^(byte - 127 + 120) in two factors
-              const int e = static_cast<int>(byte) - 127, e1 = min(e, 7) + 120, e2 = e - min(e, 7);
-              uint32_t f1 = static_cast<uint32_t>(e1 + 127) << 7, f2 = static_cast<uint32_t>(e2 + 127) << 7;
-              if (byte == 255u) f1 = 0x7FC0u, f2 = 0x3F80u;
-              f1 |= f1 << 16, f2 |= f2 << 16;
-              uint32_t nan = 0;
+          for (int y = 0; y < 4; ++y) {
+            if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
+            if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
+          }
+          if (odd) atomicOr(&sh.odd, 1u << (items & 31));
+          return odd;
+        };
+        uint8_t *const op = smem + S::OFF_V + slot * S::TILE;
+        if constexpr (E4M3) {
+          const uint8_t *raw = smem + S::OFF_R + rs * S::RAWB, *scales = raw + TN * D;
+          constexpr int BOX = D < 128 ? D : 128, CH = D / 16, ROWS_AT_ONCE = 128 / CH, U = 4;  // (chunks of 16 codes)
+          const int ch = t128 % CH, r0 = t128 / CH;
+          const uint8_t *from = raw + (ch * 16 / BOX) * (TN * BOX) + (ch * 16) % BOX;
+          uint8_t *to = op + (ch / 4) * (TN * 128);
+          const int c0 = (2 * ch) & 7, sw = (ch >> 2) & 1;  // (half of the lanes store the second word first: no bank twice)
+#pragma unroll 1
+          for (int j = 0; j < TN / ROWS_AT_ONCE; j += U) {
+            uint4 in[U];
+            uint32_t byte[U];
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+              const int rr = r0 + (j + x) * ROWS_AT_ONCE;
+              in[x] = *reinterpret_cast<const uint4 *>(from + rr * BOX);
+              byte[x] = scales[rr];
+            }
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+              const int rr = r0 + (j + x) * ROWS_AT_ONCE;
+              uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w}, h[8];
+              if (check && !there(tile * TN + rr)) byte[x] = 127u, w[0] = w[1] = w[2] = w[3] = 0u;
+              // 2^(byte - 127 + 120), or as much of it as bf16 holds
+              const uint32_t f = (byte[x] <= 134u ? (byte[x] + 120u) << 7 : byte[x] == 255u ? 0x7FC0u : 0x7F00u) * 0x10001u;
+              uint32_t rare = byte[x] > 134u ? 0x80808080u : 0u;
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
-                nan |= (in[y] & 0x7F7F7F7Fu) + 0x01010101u;
-                h[2 * y] = mul_bf16x2(codes_up(in[y], 0x1404), f1);
-                h[2 * y + 1] = mul_bf16x2(codes_up(in[y], 0x3424), f1);
+                rare |= (w[y] & 0x7F7F7F7Fu) + 0x01010101u;  // (a NaN's code)
+                h[2 * y] = mul_bf16x2(codes_up(w[y], 0x1404), f);
+                h[2 * y + 1] = mul_bf16x2(codes_up(w[y], 0x3424), f);
               }
-              if (e2 > 0 && byte != 255u) {
+              if (rare & 0x80808080u) {
+                const uint32_t f2 = (byte[x] > 134u && byte[x] < 255u ? byte[x] - 7u : 127u) * 0x00800080u;
 #pragma unroll
                 for (int y = 0; y < 8; ++y) h[y] = mul_bf16x2(h[y], f2);
-              }
-              if (nan & 0x80808080u) {
 #pragma unroll
                 for (int y = 0; y < 16; ++y)
-                  if (((in[y / 4] >> (8 * (y & 3))) & 0x7Fu) == 0x7Fu)
+                  if (((w[y / 4] >> (8 * (y & 3))) & 0x7Fu) == 0x7Fu)
                     h[y / 2] = (h[y / 2] & (y & 1 ? 0xFFFFu : 0xFFFF0000u)) | (y & 1 ? 0x7FC00000u : 0x7FC0u);
               }
-              if (kv && check) {
-                bool odd = false;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                  if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
-                  if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
-                }
-                if (odd) atomicOr(&sh.odd, 1u << (items & 31));
-              }
-              uint8_t *to = smem + op + (ch / 4) * (TN * 128) + rr * 128;
-              const int c0 = (2 * ch) & 7, sw = (ch >> 2) & 1;
-              const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-              *reinterpret_cast<uint4 *>(to + (((c0 + sw) ^ (rr & 7)) << 4)) = sw ? hi : lo;
-              *reinterpret_cast<uint4 *>(to + (((c0 + 1 - sw) ^ (rr & 7)) << 4)) = sw ? lo : hi;
+              uint32_t lo[4] = {h[0], h[1], h[2], h[3]}, hi[4] = {h[4], h[5], h[6], h[7]};
+              if (check) finite(lo), finite(hi);
+              const uint4 a = make_uint4(lo[0], lo[1], lo[2], lo[3]), b = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              uint8_t *row = to + rr * 128;
+              *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (rr & 7)) << 4)) = sw ? b : a;
+              *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (rr & 7)) << 4)) = sw ? a : b;
             }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) mb_arrive(&sh.r_empty[rs]);
-            ++rt;
-            kv ? ++vt : ++kt;
-          } else {
-            const uint32_t slot = vt % NV;
-            if (!warp_wait(&sh.v_full[slot], (vt / NV) & 1u)) {
-              timeout = true;
-              break;
-            }
-            lost = sh.lost[seq & 15], check = check || lost;
-            ready = &sh.v_ready[slot];
-            op = S::OFF_V + slot * S::TILE;
-            ++vt;
-            if (check) {
-              constexpr int CH = D / 8;
-              for (int x = t128; x < TN * CH; x += 128) {
-                const int rr = x / CH, ch = x % CH, place = tile * TN + rr;
-                uint4 *at = reinterpret_cast<uint4 *>(smem + op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-                if (!there(place)) {
-                  *at = make_uint4(0, 0, 0, 0);
-                  continue;
-                }
-                uint4 u4 = *at;
-                uint32_t h[4] = {u4.x, u4.y, u4.z, u4.w};
-                bool odd = false;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                  if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
-                  if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
-                }
-                if (odd) {
-                  *at = make_uint4(h[0], h[1], h[2], h[3]);
-                  atomicOr(&sh.odd, 1u << (items & 31));
-                }
-              }
-              fence_async();
-            }
-            __syncwarp();
           }
-          if (lane == 0) mb_arrive(ready);
+          fence_async();
+          __syncwarp();
+          if (lane == 0) mb_arrive(&sh.r_empty[rs]);
+        } else if (check) {
+          constexpr int CH = D / 8;
+          for (int x = t128; x < TN * CH; x += 128) {
+            const int rr = x / CH, ch = x % CH;
+            uint4 *at = reinterpret_cast<uint4 *>(op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+            uint32_t h[4] = {at->x, at->y, at->z, at->w};
+            if (!there(tile * TN + rr))
+              *at = make_uint4(0, 0, 0, 0);
+            else if (finite(h))
+              *at = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          fence_async();
         }
+        __syncwarp();
+        if (lane == 0) mb_arrive(&sh.v_ready[slot]);
       }
     }
   }
@@ -1203,7 +1277,7 @@ EncodeTiledFn encode_tiled() {
 }
 
 // Boxes of 128 bytes (or a row) by min(page_size, TN) places of one head of a page.
-bool cache_map(CUtensorMap *m, const k3moe_kv_cache &c, void *base, int TN) {
+bool cache_map(CUtensorMap *m, const k3moe_kv_cache &c, void *base, int TN, bool swizzle) {
   const EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
   const bool e = c.format == K3MOE_KV_E4M3;
@@ -1211,11 +1285,13 @@ bool cache_map(CUtensorMap *m, const k3moe_kv_cache &c, void *base, int TN) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.dim), static_cast<cuuint64_t>(c.page_size),
                               static_cast<cuuint64_t>(c.heads), static_cast<cuuint64_t>(c.pages)};
   const cuuint64_t strides[3] = {row, row * c.page_size, row * c.page_size * c.heads};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(e ? (c.dim < 128 ? c.dim : 128) : 64),
+  const cuuint32_t inner = static_cast<cuuint32_t>(e ? (c.dim < 128 ? c.dim : 128) : 64);
+  const cuuint32_t box[4] = {inner,
                              static_cast<cuuint32_t>(c.page_size < TN ? c.page_size : TN), 1, 1};
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   return fn(m, e ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, e ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : e && inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1229,7 +1305,7 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   using S = AxShape<D, E4M3>;
   static_assert(S::SMEM <= 232448, "shared memory of a block");
   CUtensorMap kmap, vmap;
-  if (!cache_map(&kmap, c, c.k, S::TN) || !cache_map(&vmap, c, c.v, S::TN)) return -1;
+  if (!cache_map(&kmap, c, c.k, S::TN, true) || !cache_map(&vmap, c, c.v, S::TN, !E4M3)) return -1;
   static PerDevice raised;
   cudaError_t err = cudaSuccess;
   raised.get(current_device(), [&] {
