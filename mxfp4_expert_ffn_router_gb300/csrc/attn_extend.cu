@@ -15,6 +15,7 @@ namespace {
 constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 and 10 products, 9 loads, 12-15 values
 constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
 constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
+constexpr int kPartTiles = 4;      // (direct) fewest tiles that a part of the longest item may have
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 16.f;    // a row's reference moves once a weight would pass 2^16
@@ -53,6 +54,7 @@ struct AxParams {
   float2 *stat;      // [2 blocks][rows of a tile]: reference, sum of the weights
   float *part;       // [2 blocks][dim][rows of a tile]
   int blocks, entries;  // pieces; room for the tiles of query rows
+  int parts, row_tiles;  // (direct) blocks of an item; items that a sequence's rows of one head take at most
   uint32_t per_head;    // ceil(2^32 / G) (token_of)
 };
 
@@ -78,6 +80,16 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
   return s;
 }
 
+// An item: up to 128 rows a stream of one sequence and head, and which of its tiles are this block's.
+struct AxItem {
+  int n, first, m, ctx;  // (Seq)
+  int b, head, t, r0, rows;  // rows 0: there is none, and none follows
+  int lo, sinks, sink_tiles, t0;   // (Tiles)
+  int clear_below, clear_above;    // tiles that all rows see whole end at most there, or begin past there or within the sinks
+  int u0, u1, units, both, slot, parts;
+  __device__ __forceinline__ int tile(int u) const { return u < sink_tiles ? u : u - sink_tiles + t0; }
+  __device__ __forceinline__ int steps() const { return both ? 2 * (u1 - u0) : u1 - u0; }
+};
 // What a block's warps share besides the tiles.
 template <int NK, int NV, int NR, int TK>
 struct AxShared {
@@ -86,6 +98,8 @@ struct AxShared {
   uint64_t go;               // the second stream may start
   uint64_t j_shown, j_read;  // the streams' joint: sums shown, sums read
   float2 stat[2][128];       // the streams' statistics: reference, sum of the weights
+  AxItem item[4];            // items by turns, as the loading warp comes to them
+  uint64_t item_full[4], item_empty[4];
   alignas(16) float key_scale[8][TK];
   alignas(16) float ones[TK];  // (E4M3) of the places of a tile, by turns
   float row_scale[2][2][TK > 1 ? 128 : 1];  // (E4M3) of the query rows, of items by turns
@@ -144,10 +158,9 @@ __device__ __forceinline__ Tiles tiles_of(const AxParams &P, const Seq &s, int r
 }
 // Whether some row does not see some place of the tile.
 template <int TN>
-__device__ __forceinline__ bool masked(const AxParams &P, const Seq &s, const Tiles &t, int tile) {
+__device__ __forceinline__ bool masked(const AxParams &P, const AxItem &I, int tile) {
   const int c0 = tile * TN, c1 = c0 + TN;
-  const int all = P.masks ? s.ctx : t.pmin + 1;  // places below are seen, the window aside
-  return c1 > all || (P.window > 0 && c1 > P.sinks && c0 <= t.pmax - P.window);
+  return c1 > I.clear_below || (c0 <= I.clear_above && c1 > P.sinks);
 }
 
 // n / G for 0 <= n < 2^16.
@@ -224,7 +237,33 @@ struct Walk {
       enter();
     } while (u0 >= u1);
   }
-  __device__ __forceinline__ bool cut() const { return u0 > 0 || u1 < list.units; }
+  __device__ __forceinline__ void direct(const AxParams &P, int block) {
+    const int item = block / P.parts, part = block - item * P.parts, per = P.heads * P.row_tiles;
+    b = item / per;
+    head = item / P.row_tiles - b * P.heads;
+    t = item - (b * P.heads + head) * P.row_tiles;
+    s = seq_of(P, b, head == 0 && t == 0 && part == 0);
+    more = t * ROWS < s.m * P.G;
+    if (!more) return;
+    measure(P);
+    u0 = list.units * part / P.parts, u1 = list.units * (part + 1) / P.parts;
+  }
+  __device__ __forceinline__ void show(const AxParams &P, AxItem &I) const {
+    I.n = s.n, I.first = s.first, I.m = s.m, I.ctx = s.ctx;
+    I.b = b, I.head = head, I.t = t, I.r0 = r0, I.rows = rows;
+    I.lo = list.lo, I.sinks = list.sinks, I.sink_tiles = list.sink_tiles, I.t0 = list.t0;
+    I.clear_below = P.masks ? s.ctx : list.pmin + 1, I.clear_above = P.window > 0 ? list.pmax - P.window : -1;
+    I.u0 = u0, I.u1 = u1, I.units = list.units, I.both = weight - 1;
+    if (P.parts) {
+      I.slot = blockIdx.x, I.parts = P.parts;
+    } else {
+      I.slot = 2 * blockIdx.x + (u0 > 0 ? 0 : 1), I.parts = u0 > 0 || u1 < list.units ? 2 : 1;
+      if (u0 == 0 && u1 < list.units) {  // the item begins here and goes on
+        const long long last = begin + kItemLen + static_cast<long long>(list.units - 1) * weight;
+        P.meta[blockIdx.x] = make_int4(b, head, t, static_cast<int>(last / P.plan->share) - static_cast<int>(blockIdx.x) + 1);
+      }
+    }
+  }
 };
 
 // ---- small device functions
@@ -255,6 +294,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
   return __all_sync(0xFFFFFFFFu, mb_wait(bar, parity));
 }
 __device__ __forceinline__ uint32_t below(int k) { return k <= 0 ? 0u : k >= 32 ? 0xFFFFFFFFu : (1u << k) - 1u; }
+__device__ __forceinline__ void cp_or_zeros16(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_or_zeros8(uint32_t dst, const void *src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(on ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
   asm volatile(
@@ -386,12 +432,6 @@ __device__ __forceinline__ void tc_st16u(uint32_t taddr, const uint32_t (&r)[16]
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tc_st32u(uint32_t taddr, const uint32_t (&r)[32]) {
-  float f[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(r[i]);
-  tc_st32r(taddr, f);
-}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -423,7 +463,7 @@ struct Row {
   bool on;               // a row of the item
 };
 // The 32 places from c on, of which bit x stands for c + x.
-__device__ __forceinline__ uint32_t sees(const AxParams &P, const Seq &s, const Row &row, int c) {
+__device__ __forceinline__ uint32_t sees(const AxParams &P, const AxItem &s, const Row &row, int c) {
   const uint32_t win = P.window > 0 ? ~below(row.lo - c) | below(P.sinks - c) : 0xFFFFFFFFu;
   if (!P.masks) return below(row.hi + 1 - c) & win;
   uint32_t v = below(s.ctx - c) & win;
@@ -435,6 +475,48 @@ __device__ __forceinline__ uint32_t sees(const AxParams &P, const Seq &s, const 
     v |= __funnelshift_r(w0, w1, j & 31) & below(s.m - j);
   }
   return v;
+}
+
+// Adds the values that are not finite to the sums of a row that sees them: those that were left out of the products, and
+// those that were not, which changes nothing (an infinity stays one, NaN stays NaN).
+template <int D, bool E4M3, int TN>
+__device__ __noinline__ void add_left_out(const AxParams &P, const AxItem &I, const Row row, int st, uint32_t oa) {
+#pragma unroll 1
+  for (int x0 = 0; x0 < D; x0 += 32) {
+    float o[32];
+    __syncwarp();
+    tc_ld32(oa + x0, o);
+    tc_wait_ld(o);
+#pragma unroll 1
+    for (int u = I.u0; u < I.u1; ++u) {
+      const int tile = I.tile(u);
+      if ((!I.both && D < 256 && ((u - I.u0) & 1) != st) || !row.on) continue;
+#pragma unroll 1
+      for (int x = 0; x < TN; ++x) {
+        const int place = tile * TN + x;
+        if (!(sees(P, I, row, place) & 1u) || place >= I.n) continue;
+        const int page = page_of(P, I.b, place);
+        if (!is_page(P, page)) continue;
+        const size_t vec = ((static_cast<size_t>(page) * P.heads + I.head) << P.page_shift) +
+                           (place & ((1 << P.page_shift) - 1));
+#pragma unroll
+        for (int y = 0; y < 32; ++y) {
+          float w;
+          if (E4M3) {
+            uint32_t a, z;
+            e4m3x4_to_f16x2(P.v[vec * D + x0 + y], a, z);
+            w = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
+          } else {
+            w = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
+          }
+          if (!isfinite(w)) o[y] += w;
+        }
+      }
+    }
+    __syncwarp();
+    tc_st32r(oa + x0, o);
+  }
+  tc_wait_st();
 }
 
 }  // namespace
@@ -540,10 +622,10 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AxParams P) {
 
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kAxThreads, 1)
-    attn_extend_kernel(const AxParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    attn_extend_kernel(const __grid_constant__ AxParams P, const __grid_constant__ CUtensorMap kmap,
+                       const __grid_constant__ CUtensorMap vmap) {
   using S = AxShape<D, E4M3>;
   constexpr int TN = S::TN, NS = S::NS, ROWS = S::ROWS, NK = S::NK, NV = S::NV, NR = S::NR > 0 ? S::NR : 1;
-  using W = Walk<TN, ROWS>;
   extern __shared__ __align__(1024) uint8_t ax_smem[];
   uint8_t *smem = ax_smem;
   typename S::Shared &sh = *reinterpret_cast<typename S::Shared *>(smem + S::OFF_S);
@@ -553,7 +635,12 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     for (int i = 0; i < NK; ++i) mb_init(&sh.k_full[i], 1), mb_init(&sh.k_ready[i], 1), mb_init(&sh.k_empty[i], NS);
     for (int i = 0; i < NV; ++i) mb_init(&sh.v_full[i], 1), mb_init(&sh.v_ready[i], 4), mb_init(&sh.v_empty[i], NS);
     for (int i = 0; i < NR; ++i) mb_init(&sh.r_full[i], 1), mb_init(&sh.r_empty[i], 4);
-    for (int i = 0; i < 2; ++i) mb_init(&sh.s_full[i], 1), mb_init(&sh.p_half[i], 4), mb_init(&sh.half_done[i], 1), mb_init(&sh.p_ready[i], 4), mb_init(&sh.pv_done[i], 1), mb_init(&sh.q_ready[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mb_init(&sh.s_full[i], 1), mb_init(&sh.p_half[i], 4), mb_init(&sh.half_done[i], 1), mb_init(&sh.p_ready[i], 4);
+      mb_init(&sh.pv_done[i], 1), mb_init(&sh.q_ready[i], 4);
+    }
+    for (int i = 0; i < 4; ++i)  // (softmax and product warps of each stream, the scales', the values')
+      mb_init(&sh.item_full[i], 1), mb_init(&sh.item_empty[i], 5 * NS + (E4M3 ? 1 : 0) + 4);
     mb_init(&sh.go, 1), mb_init(&sh.j_shown, 8), mb_init(&sh.j_read, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     sh.odd = 0;
@@ -571,67 +658,91 @@ __global__ void __launch_bounds__(kAxThreads, 1)
   bool timeout = false;
   pdl_wait();
   pdl_trigger();
+  // The next item, once the loading warp has come to it; null where there is none (or it did not come).
+  auto item_at = [&](uint32_t i) -> const AxItem * {
+    if (!warp_wait(&sh.item_full[i & 3], (i >> 2) & 1u)) {
+      timeout = true;
+      return nullptr;
+    }
+    const AxItem *I = &sh.item[i & 3];
+    return I->rows ? I : nullptr;
+  };
+  auto item_done = [&](uint32_t i) {
+    __syncwarp();
+    if (lane == 0) mb_arrive(&sh.item_empty[i & 3]);
+  };
 
-  W it;
-  it.init(P, blockIdx.x);
-  // steps of an item: both streams at every tile, or where it has rows for one stream only, the streams in turn
-  auto both_of = [&](const W &w) { return NS == 2 && w.rows > 128; };
-
-  if (warp < 8) {
+  if (warp < 4 * NS) {
+    // ---- softmax: a thread is a row
     const int st = warp >> 2;  // stream
     const int lrow = 32 * (warp & 3) + lane;
-    const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16, oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
     const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
     const float c1 = flat ? 1.f : fabsf(P.scale) * kLog2e;
-    const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = flat ? 0u : 0xFFFFFFFFu;
-    // this stream's queries of an item into shared memory
-    uint32_t turn = 0;
-    auto load_q = [&](const W &w) {
-      constexpr int CH = D / 8, N = 8;
-      const int base = w.r0 + (both_of(w) ? 128 * st : 0), left = w.r0 + w.rows - base;
-      const int i0 = base / P.G, g0 = base - i0 * P.G, ch = tid % CH, first = (tid & 127) / CH;
-      const uint16_t *q = P.q + (static_cast<long long>(w.s.first) + i0) * P.q_stride + static_cast<size_t>(w.head) * P.G * D + ch * 8;
-#pragma unroll
-      for (int j = 0; j < CH; j += N) {
-        uint4 u[N];
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-          const int rr = first + (j + x) * (128 / CH), at = g0 + rr;
-          const int ii = token_of(P, at), gg = at - ii * P.G;
-          u[x] = make_uint4(0, 0, 0, 0);
-          if (rr < left) u[x] = *reinterpret_cast<const uint4 *>(q + ii * P.q_stride + gg * D);
+    // This stream's queries of an item: asked for, and, once they have come, made operands.  A thread converts what it has
+    // copied: eight dimensions of a row, 128 / CH rows apart, all in loops, since their instructions are met cold
+    // (unrolled, these two took 25000 clocks of a short call).
+    constexpr int CH = D / 8;
+    const int ch = tid % CH, q_row = (tid & 127) / CH;
+    const uint32_t q_to = sbase + st * S::QB;
+    auto place8 = [&](int rr) -> uint32_t {  // (E4M3) of eight dimensions in a part
+      const int byte = ch * 8 % S::SW, sw = S::SW == 128 ? rr & 7 : (rr >> 1) & 3;
+      return (ch * 8 / S::SW) * (128 * S::SW) + rr * S::SW + (((byte >> 4) ^ sw) << 4) + (byte & 8);
+    };
+    auto place16 = [&](int rr) -> uint32_t { return (ch / 8) * (128 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4); };
+    auto ask_q = [&](const AxItem &I) {
+      const int base = I.r0 + (I.both ? 128 * st : 0), left = I.r0 + I.rows - base, i0 = base / P.G, g0 = base - i0 * P.G;
+      const uint16_t *q = P.q + (static_cast<long long>(I.first) + i0) * P.q_stride + static_cast<size_t>(I.head) * P.G * D + ch * 8;
+#pragma unroll 1
+      for (int rr = q_row; rr < 128; rr += 128 / CH) {
+        const int ii = token_of(P, g0 + rr), gg = g0 + rr - ii * P.G;
+        const bool on = rr < left;
+        const uint16_t *from = on ? q + ii * P.q_stride + gg * D : P.q;
+        if constexpr (E4M3) {
+          cp_or_zeros8(q_to + place8(rr), from, on);
+          cp_or_zeros8(q_to + 128 * D + place8(rr), from + 4, on);
+        } else {
+          cp_or_zeros16(q_to + place16(rr), from, on);
         }
+      }
+    };
+    uint32_t turn = 0;
+    auto take_q = [&]() {
+      cp_wait_all();
+      const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = flat ? 0u : 0xFFFFFFFFu;
+      if constexpr (E4M3) {
+#pragma unroll 1
+        for (int rr = q_row; rr < 128; rr += 128 / CH) {
+          // the row times a power of two, to a largest value in [128, 256), in two E4M3 numbers a value
+          uint2 *const to = reinterpret_cast<uint2 *>(smem + st * S::QB + place8(rr)), *const to2 = to + 128 * D / 8;
+          const uint2 u0 = *to, u1 = *to2;
+          const uint32_t w[4] = {(u0.x ^ flip) & keep, (u0.y ^ flip) & keep, (u1.x ^ flip) & keep, (u1.y ^ flip) & keep};
+          uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+          m = max(m >> 16, m & 0xFFFFu);
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-          const int rr = first + (j + x) * (128 / CH);
-          u[x].x = (u[x].x ^ flip) & keep, u[x].y = (u[x].y ^ flip) & keep;
-          u[x].z = (u[x].z ^ flip) & keep, u[x].w = (u[x].w ^ flip) & keep;
-          if constexpr (!E4M3) {
-            *reinterpret_cast<uint4 *>(smem + st * S::QB + (ch / 8) * (128 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = u[x];
-          } else {
-            // the row times a power of two, to a largest value in [128, 256), in two E4M3 numbers a value
-            uint32_t m = __vmaxu2(__vmaxu2(u[x].x & 0x7FFF7FFFu, u[x].y & 0x7FFF7FFFu),
-                                  __vmaxu2(u[x].z & 0x7FFF7FFFu, u[x].w & 0x7FFF7FFFu));
-            m = max(m >> 16, m & 0xFFFFu);
+          for (int off = 1; off < CH; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+          const int e = m == 0 ? 0 : max(-126, min(127, 7 + 127 - static_cast<int>(m >> 7)));
+          const float up = exp2i(e);
+          uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int off = 1; off < CH; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-            const int e = m == 0 ? 0 : max(-126, min(127, 7 + 127 - static_cast<int>(m >> 7)));
-            const float up = exp2i(e);
-            const uint32_t w[4] = {u[x].x, u[x].y, u[x].z, u[x].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const float a = __uint_as_float(w[y] << 16) * up, b = __uint_as_float(w[y] & 0xFFFF0000u) * up;
-              hi[y] = m >= 0x7F80u ? 0x7F7Fu : e4m3x2(a, b);  // (a row that is not finite gives NaN)
-              const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi[y]), __NV_E4M3)));
-              lo[y] = e4m3x2(a - f.x, b - f.y);
-            }
-            const int byte = ch * 8 % S::SW, sw = S::SW == 128 ? rr & 7 : (rr >> 1) & 3;
-            uint8_t *to = smem + st * S::QB + (ch * 8 / S::SW) * (128 * S::SW) + rr * S::SW + (((byte >> 4) ^ sw) << 4) + (byte & 8);
-            *reinterpret_cast<uint2 *>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-            *reinterpret_cast<uint2 *>(to + 128 * D) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-            if (ch == 0) sh.row_scale[turn & 1][st][rr] = mx_pow2(-e);
+          for (int y = 0; y < 4; ++y) {
+            const float a = __uint_as_float(w[y] << 16) * up, b = __uint_as_float(w[y] & 0xFFFF0000u) * up;
+            hi[y] = m >= 0x7F80u ? 0x7F7Fu : e4m3x2(a, b);  // (a row that is not finite gives NaN)
+            uint32_t h, z;
+            e4m3x4_to_f16x2(hi[y], h, z);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+            lo[y] = e4m3x2(a - f.x, b - f.y);
           }
+          *to = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+          *to2 = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+          if (ch == 0) sh.row_scale[turn & 1][st][rr] = mx_pow2(-e);
+        }
+      } else if (flip || !keep) {
+#pragma unroll 1
+        for (int rr = q_row; rr < 128; rr += 128 / CH) {
+          uint4 *const to = reinterpret_cast<uint4 *>(smem + st * S::QB + place16(rr));
+          const uint4 u = *to;
+          *to = make_uint4((u.x ^ flip) & keep, (u.y ^ flip) & keep, (u.z ^ flip) & keep, (u.w ^ flip) & keep);
         }
       }
       ++turn;
@@ -641,35 +752,40 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     };
     uint32_t uses[2] = {0, 0};  // steps of each score buffer
     uint32_t items = 0, joins = 0, finals = 0, tiles_before = 0;
-    auto has_steps = [&](const W &w) { return st == 0 || both_of(w) || w.u1 - w.u0 > 1; };
-    if (st < NS && it.more && has_steps(it)) load_q(it);
-    while (it.more && st < NS) {
-      const bool both = both_of(it);
+    const AxItem *ip = item_at(0);
+    if (ip && ip->steps() > st) {
+      ask_q(*ip);
+      take_q();
+    }
+    while (ip) {
+      const AxItem &I = *ip;
+      const bool both = I.both;
       const int r = (both ? 128 * st : 0) + lrow;  // row of the item
       Row row;
-      row.on = r < it.rows;
-      const int i0 = it.r0 / P.G, at = it.r0 - i0 * P.G + r;
-      const int di = token_of(P, at), g = at - di * P.G;
-      const int i = min(i0 + di, it.s.m - 1);
-      const long long grow_ = static_cast<long long>(it.s.first) + i;
-      int pos = it.s.ctx + i;
-      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? grow_ * P.words : 0));
+      row.on = r < I.rows;
+      const int i0 = I.r0 / P.G, at = I.r0 - i0 * P.G + r;
+      const int di = token_of(P, at), g = at - di * P.G, i = min(i0 + di, I.m - 1);
+      const long long qrow = static_cast<long long>(I.first) + i;
+      int pos = I.ctx + i;
+      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? qrow * P.words : 0));
       if (P.masks) {
         int seen = 0;
-        for (int w = 0; 32 * w < it.s.m; ++w) seen += __popc(row.mask[w] & below(it.s.m - 32 * w));
-        pos = it.s.ctx + max(0, seen - 1);
+#pragma unroll 1
+        for (int w = 0; 32 * w < I.m; ++w) seen += __popc(row.mask[w] & below(I.m - 32 * w));
+        pos = I.ctx + max(0, seen - 1);
       }
       row.hi = pos;
       row.lo = P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
-      const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < it.rows;
+      const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < I.rows;
       float m = -INFINITY, l = 0.f;  // the reference, in scores; the weights' sum
       float c = c1;                  // powers of two of a score
       bool first = true;
-      const int T = it.u1 - it.u0, K = both ? 2 * T : T;
+      const int K = I.steps(), u0 = I.u0;
       int sb = st;
       for (int k = NS == 2 ? st : 0; k < K; k += NS) {
         sb = k & 1;
-        const int u = both ? k >> 1 : k, tile = it.list.tile(it.u0 + u);
+        const int u = both ? k >> 1 : k, tile = I.tile(u0 + u);
+        const bool some = masked<TN>(P, I, tile);
         if (!warp_wait(&sh.s_full[sb], uses[sb] & 1u)) {
           timeout = true;
           break;
@@ -685,11 +801,11 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           float base = m == -INFINITY ? 0.f : m * c;
           float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           float v[64];
-          if (lost || masked<TN>(P, it.s, it.list, tile)) {
+          if (lost || some) {
 #pragma unroll 1
             for (int x = 0; x < TN; x += 32) {
               tc_ld32(sa + x, v);
-              uint32_t vis = sees(P, it.s, row, tile * TN + x);
+              uint32_t vis = sees(P, I, row, tile * TN + x);
               if (lost >> (x / 16) & 1u) vis &= 0xFFFF0000u;
               if (lost >> (x / 16) & 2u) vis &= 0xFFFFu;
               tc_wait_ld(v);
@@ -722,13 +838,11 @@ __global__ void __launch_bounds__(kAxThreads, 1)
 #pragma unroll
               for (int y = 0; y < 2; ++y) add[y].x *= f, add[y].y *= f;
               if (!first || x > 0) {
-                if (x > 0) {  // the products of the places before
-                  if (!warp_wait(&sh.half_done[sb], (uses[sb] - 1) & 1u)) timeout = true;
-                } else if (NS == 1) {  // of the step before (else its columns' next scores say so)
-                  if (!warp_wait(&sh.pv_done[sb ^ 1], (uses[sb ^ 1] - 1) & 1u)) timeout = true;
-                }
+                // after the products of the places before, or of the step before (two streams: these scores say so)
+                if (x > 0 ? !warp_wait(&sh.half_done[sb], (uses[sb] - 1) & 1u)
+                          : NS == 1 && !warp_wait(&sh.pv_done[sb ^ 1], (uses[sb ^ 1] - 1) & 1u))
+                  timeout = true;
                 tc_fence_after();
-                const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
                 float o[16];
 #pragma unroll 1
                 for (int y = 0; y < D; y += 16) {
@@ -739,18 +853,21 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                   for (int z = 0; z < 16; ++z) h[z] = __float_as_uint(o[z] * f);
                   tc_st16u(oa + y, h);
                 }
+                tc_wait_st();
               }
-              tc_wait_st();
             }
             const float2 c2 = make_float2(c, c), b2 = make_float2(-base, -base);
-            uint32_t pk[32];
 #pragma unroll
-            for (int y = 0; y < 64; y += 2) {
-              const float2 e = fma2(make_float2(v[y], v[y + 1]), c2, b2), w = make_float2(ex2(e.x), ex2(e.y));
-              pk[y / 2] = bf16x2(w.x, w.y);
-              add[(y / 2) & 1] = add2(add[(y / 2) & 1], w);
+            for (int h = 0; h < 64; h += 32) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int y = 0; y < 32; y += 2) {
+                const float2 e = fma2(make_float2(v[h + y], v[h + y + 1]), c2, b2), w = make_float2(ex2(e.x), ex2(e.y));
+                pk[y / 2] = bf16x2(w.x, w.y);
+                add[(y / 2) & 1] = add2(add[(y / 2) & 1], w);
+              }
+              tc_st16u(sa + (x + h) / 2, pk);
             }
-            tc_st32u(sa + x / 2, pk);
             if (x + 64 < TN) {  // these can be multiplied while the others are computed
               tc_wait_st();
               tc_fence_before();
@@ -769,11 +886,12 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         if (lane == 0) mb_arrive(&sh.p_ready[sb]);
       }
       if (timeout) break;
-      // ---- the item's end: the next one's queries, then this one's sums
+      // ---- the item's end: the next one's queries are asked for (the last scores are there: this one's are not read
+      // any more), then this one's sums
       const bool had = !first;  // whether this stream had a step
-      W nx = it;
-      nx.next(P);
-      if (nx.more && has_steps(nx)) load_q(nx);  // (the last scores are there: this one's are not read any more)
+      const AxItem *const next = item_at(items + 1);
+      const bool next_q = next && next->steps() > st;
+      if (next_q) ask_q(*next);
       if (had) {
         if (!warp_wait(&sh.pv_done[sb], (NS == 2 ? finals : uses[sb] - 1) & 1u)) {
           timeout = true;
@@ -782,47 +900,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         ++finals;
         tc_fence_after();
       }
-      const uint32_t oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
-      if ((*reinterpret_cast<volatile uint32_t *>(&sh.odd) >> (items & 31) & 1u) && had && warp_on) {
-        // values that were left out of the products are added to the rows that see them
-#pragma unroll 1
-        for (int x0 = 0; x0 < D; x0 += 32) {
-          float o[32];
-          __syncwarp();
-          tc_ld32(oa + x0, o);
-          tc_wait_ld(o);
-#pragma unroll 1
-          for (int u = it.u0; u < it.u1; ++u) {
-            const int tile = it.list.tile(u);
-            if ((!both && NS == 2 && ((u - it.u0) & 1) != st) || !row.on) continue;
-            if (!sh.lost[(tiles_before + u - it.u0) & 15] && !masked<TN>(P, it.s, it.list, tile)) continue;
-#pragma unroll 1
-            for (int x = 0; x < TN; ++x) {
-              const int place = tile * TN + x;
-              if (!(sees(P, it.s, row, place) & 1u) || place >= it.s.n) continue;
-              const int page = page_of(P, it.b, place);
-              if (!is_page(P, page)) continue;
-              const size_t vec = ((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) +
-                                 (place & ((1 << P.page_shift) - 1));
-#pragma unroll
-              for (int y = 0; y < 32; ++y) {
-                float w;
-                if (E4M3) {
-                  uint32_t a, z;
-                  e4m3x4_to_f16x2(P.v[vec * D + x0 + y], a, z);
-                  w = __half2float(__ushort_as_half(static_cast<unsigned short>(a))) * e8m0_to_f32(P.vs[vec]);
-                } else {
-                  w = bf16_bits_to_f32(reinterpret_cast<const uint16_t *>(P.v)[vec * D + x0 + y]);
-                }
-                if (!isfinite(w)) o[y] += w;
-              }
-            }
-          }
-          __syncwarp();
-          tc_st32r(oa + x0, o);
-        }
-        tc_wait_st();
-      }
+      if ((*reinterpret_cast<volatile uint32_t *>(&sh.odd) >> (items & 31) & 1u) && had && warp_on)
+        add_left_out<D, E4M3, TN>(P, I, row, st, oa);
+      if (next_q) take_q();
       float mb = m == -INFINITY ? -INFINITY : m * c, f0 = 1.f, f1 = 0.f;
       const bool split = NS == 2 && !both;  // the streams share the rows: each writes half of the dimensions
       if (split) {
@@ -846,44 +926,40 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
       }
       if (warp_on) {
-        const bool cut = it.cut();
-        const int slot = 2 * blockIdx.x + (it.u0 > 0 ? 0 : 1);
+        const bool cut = I.parts > 1;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t orow = static_cast<size_t>(grow_) * P.Hq + it.head * P.G + g;
+        const size_t orow = static_cast<size_t>(qrow) * P.Hq + I.head * P.G + g;
         const int x0 = split ? st * (D / 2) : 0, x1 = split ? x0 + D / 2 : D;
-        const uint32_t o0 = tmem + lane_addr + S::O_COL + (split ? 0 : st * S::O_COLS), o1 = o0 + S::O_COLS;
+        const uint32_t o0 = split ? tmem + lane_addr + S::O_COL : oa, o1 = o0 + S::O_COLS;
 #pragma unroll 1
-        for (int x = x0; x < x1; x += 32) {
-          float o[32];
+        for (int x = x0; x < x1; x += 16) {
+          float o[16];
           __syncwarp();
-          tc_ld32(o0 + x, o);
+          tc_ld16f(o0 + x, o);
           tc_wait_ld(o);
           if (split && K > 1) {
-            float z[32];
-            tc_ld32(o1 + x, z);
+            float z[16];
+            tc_ld16f(o1 + x, z);
             tc_wait_ld(z);
 #pragma unroll
-            for (int y = 0; y < 32; ++y) o[y] = o[y] * f0 + z[y] * f1;
+            for (int y = 0; y < 16; ++y) o[y] = o[y] * f0 + z[y] * f1;
           }
           if (row.on && cut) {
-            float *to = P.part + (static_cast<size_t>(slot) * D + x) * ROWS + r;
+            float *to = P.part + (static_cast<size_t>(I.slot) * D + x) * ROWS + r;
 #pragma unroll
-            for (int y = 0; y < 32; ++y) to[y * ROWS] = o[y];
+            for (int y = 0; y < 16; ++y) to[y * ROWS] = o[y];
           } else if (row.on) {
             uint4 *to = reinterpret_cast<uint4 *>(P.out + orow * D + x);
+            uint32_t w[8];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              uint32_t w[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                w[z] = l == 0.f ? 0u : bf16x2(o[8 * y + 2 * z] * inv, o[8 * y + 2 * z + 1] * inv);
-              to[y] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int z = 0; z < 8; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            to[1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
         if (row.on && !(split && st)) {
           if (cut)
-            P.stat[static_cast<size_t>(slot) * ROWS + r] = make_float2(mb, l);
+            P.stat[static_cast<size_t>(I.slot) * ROWS + r] = make_float2(mb, l);
           else if (P.lse)
             P.lse[orow] = l == 0.f ? -INFINITY : (mb + log2f(l)) * kLn2;
         }
@@ -898,201 +974,229 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
         ++joins;
       }
-      if (st == 0 && tid == 0 && it.u0 == 0 && it.u1 < it.list.units) {
-        const long long last = it.begin + kItemLen + static_cast<long long>(it.list.units - 1) * it.weight;
-        P.meta[blockIdx.x] = make_int4(it.b, it.head, it.t, static_cast<int>(last / P.plan->share) - blockIdx.x + 1);
-      }
-      tiles_before += T;
+      tiles_before += I.u1 - u0;
+      item_done(items);
       ++items;
-      it = nx;
+      ip = next;
     }
-  } else if (warp < 12) {
-    if (warp == 8 || (NS == 2 && warp == 10)) {
-      // ---- products of one stream (or of both score buffers in turn): the scores of a step's next but one follow its
-      // weights' products, which read the same columns, in the tensor cores' order
-      const int st = NS == 2 ? (warp - 8) / 2 : 0;
-      uint32_t tiles_before = 0, kt = 0, vt = 0, uses[2] = {0, 0}, items = 0, goes = 0;
-      const uint32_t id_s = E4M3 ? idesc_e4m3(TN) : idesc(TN, false), id_o = idesc(D, true);
-      const uint64_t qd = rows_desc<S::SW>(sbase + st * S::QB);
-      uint64_t *const keys = E4M3 ? sh.k_ready : sh.k_full;
-      for (; it.more && !timeout; it.next(P)) {
-        const bool both = both_of(it);
-        const int T = it.u1 - it.u0, K = both ? 2 * T : T;
-        // every tile passes every stream, in order: those that it does not use it gives back at once
-        auto pass_keys = [&](uint32_t t) {
-          for (; kt < t; ++kt) {
-            if (!warp_wait(&keys[kt % NK], (kt / NK) & 1u)) return false;
-            if (lane == 0) mb_arrive(&sh.k_empty[kt % NK]);
-          }
-          return true;
-        };
-        auto pass_values = [&](uint32_t t) {
-          for (; vt < t; ++vt) {
-            if (!warp_wait(&sh.v_ready[vt % NV], (vt / NV) & 1u)) return false;
-            if (lane == 0) mb_arrive(&sh.v_empty[vt % NV]);
-          }
-          return true;
-        };
-        auto scores = [&](int k) {
-          const int sb = k & 1;
-          const uint32_t t = tiles_before + (both ? k >> 1 : k), slot = t % NK;
-          if (!pass_keys(t) || !warp_wait(&keys[slot], (t / NK) & 1u)) return false;
-          ++kt;
-          tc_fence_after();
-          const uint64_t kd = rows_desc<S::SW>(sbase + S::OFF_K + slot * S::KTILE);
-          if constexpr (E4M3) {
+  } else if (warp == 8 || (NS == 2 && warp == 10)) {
+    // ---- products of one stream (or of both score buffers in turn): the scores of a step's next but one follow its
+    // weights' products, which read the same columns, in the tensor cores' order
+    const int st = NS == 2 ? (warp - 8) / 2 : 0;
+    uint32_t tiles_before = 0, kt = 0, vt = 0, uses[2] = {0, 0}, asked = 0, goes = 0;
+    const uint32_t id_s = E4M3 ? idesc_e4m3(TN) : idesc(TN, false), id_o = idesc(D, true);
+    const uint64_t qd = rows_desc<S::SW>(sbase + st * S::QB);
+    uint64_t *const keys = E4M3 ? sh.k_ready : sh.k_full;
+    const AxItem *I;
+    for (uint32_t items = 0; (I = item_at(items)) != nullptr; ++items) {
+      const bool both = I->both;
+      const int T = I->u1 - I->u0, K = I->steps();
+      // every tile passes every stream, in order: those that it does not use it gives back at once
+      auto pass_keys = [&](uint32_t t) {
+        for (; kt < t; ++kt) {
+          if (!warp_wait(&keys[kt % NK], (kt / NK) & 1u)) return false;
+          if (lane == 0) mb_arrive(&sh.k_empty[kt % NK]);
+        }
+        return true;
+      };
+      auto pass_values = [&](uint32_t t) {
+        for (; vt < t; ++vt) {
+          if (!warp_wait(&sh.v_ready[vt % NV], (vt / NV) & 1u)) return false;
+          if (lane == 0) mb_arrive(&sh.v_empty[vt % NV]);
+        }
+        return true;
+      };
+      auto scores = [&](int k) {
+        const int sb = k & 1;
+        const uint32_t t = tiles_before + (both ? k >> 1 : k), slot = t % NK;
+        if (!pass_keys(t) || !warp_wait(&keys[slot], (t / NK) & 1u)) return false;
+        ++kt;
+        tc_fence_after();
+        const uint64_t kd = rows_desc<S::SW>(sbase + S::OFF_K + slot * S::KTILE);
+        if constexpr (E4M3) {
 #pragma unroll
-            for (int x = 0; x < 2 * (D / 64); ++x) {  // both parts of the queries
-              const int part = x / (D / 64), y = x % (D / 64);  // 64 dimensions
-              mma2_scores_e4m3(tmem + sb * S::S_COLS, qd + (part * (128 * D) + y * 64 / S::SW * (128 * S::SW) + y * 64 % S::SW) / 16,
-                               kd + (y * 64 / S::SW * (TN * S::SW) + y * 64 % S::SW) / 16, id_s, x > 0);
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-              mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
+          for (int x = 0; x < 2 * (D / 64); ++x) {  // both parts of the queries
+            const int part = x / (D / 64), y = x % (D / 64);  // 64 dimensions
+            mma2_scores_e4m3(tmem + sb * S::S_COLS, qd + (part * (128 * D) + y * 64 / S::SW * (128 * S::SW) + y * 64 % S::SW) / 16,
+                             kd + (y * 64 / S::SW * (TN * S::SW) + y * 64 % S::SW) / 16, id_s, x > 0);
           }
-          commit(&sh.s_full[sb]);
-          commit(&sh.k_empty[slot]);
-          return true;
-        };
-        if (NS == 1 || st < K) {
-          bool ok = warp_wait(&sh.q_ready[st], items & 1u);
-          ++items;
-          // of a longer item the second stream starts half a step behind, so that one's products meet the other's softmax
-          const bool skew = NS == 2 && K > 8;
-          if (st == 1 && skew) ok = ok && warp_wait(&sh.go, goes & 1u);
-          goes += skew;
-          ok = ok && scores(st);
-          if (NS == 1 && K > 1) ok = ok && scores(1);
-          for (int k = st; ok && k < K; k += NS) {
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            mma4_scores(tmem + sb * S::S_COLS, qd + x * (128 * 128 / 16), kd + x * (TN * 128 / 16), id_s, x > 0);
+        }
+        commit(&sh.s_full[sb]);
+        commit(&sh.k_empty[slot]);
+        return true;
+      };
+      bool ok = true;
+      if (st < K) {
+        ok = warp_wait(&sh.q_ready[st], asked & 1u);
+        ++asked;
+        // of a longer item the second stream starts half a step behind, so that one's products meet the other's softmax
+        const bool skew = NS == 2 && K > 8;
+        if (st == 1 && skew) ok = ok && warp_wait(&sh.go, goes & 1u);
+        goes += skew;
+#pragma unroll 1
+        for (int k = st - 2; ok && k < K; k += NS) {  // (k < 0: the first scores, of one buffer or of both)
+          if (k >= 0) {
             const int sb = k & 1;
             const uint32_t t = tiles_before + (both ? k >> 1 : k), slot = t % NV;
             const uint64_t vd = values_desc(sbase + S::OFF_V + slot * S::TILE, TN * 128);
             const uint32_t od = tmem + S::O_COL + st * S::O_COLS, pa = tmem + sb * S::S_COLS;
             ok = pass_values(t) && warp_wait(&sh.v_ready[slot], (t / NV) & 1u);
             ++vt;
-            if (TN > 64) {
-              ok = ok && warp_wait(&sh.p_half[sb], uses[sb] & 1u);
+#pragma unroll
+            for (int h = 0; h < TN / 64; ++h) {  // weights of 64 places
+              ok = ok && warp_wait(h + 1 < TN / 64 ? &sh.p_half[sb] : &sh.p_ready[sb], uses[sb] & 1u);
               if (!ok) break;
               tc_fence_after();
-              if (skew && k == 0 && lane == 0) mb_arrive(&sh.go);
-              mma4_values(od, pa, vd, id_o, k >= NS);
-              commit(&sh.half_done[sb]);
+              if (skew && k == 0 && h == 0 && lane == 0) mb_arrive(&sh.go);
+              mma4_values(od, pa + h * 32, vd + h * (8192 / 16), id_o, h > 0 || k >= NS);
+              if (h + 1 < TN / 64) commit(&sh.half_done[sb]);
             }
-            ok = ok && warp_wait(&sh.p_ready[sb], uses[sb] & 1u);
             if (!ok) break;
             ++uses[sb];
-            tc_fence_after();
-            mma4_values(od, pa + (TN / 64 - 1) * 32, vd + (TN / 64 - 1) * (8192 / 16), id_o, TN > 64 || k >= NS);
             if (k + 2 < K) ok = scores(k + 2);
             commit(&sh.v_empty[slot]);
             if (NS == 1 || k + NS >= K) commit(&sh.pv_done[sb]);
-          }
-          if (!ok) timeout = true;
-        }
-        tiles_before += T;
-        if (timeout || !pass_keys(tiles_before) || !pass_values(tiles_before)) timeout = true;
-      }
-    } else if (warp == 9) {
-      // ---- loads
-      uint32_t kt = 0, vt = 0, rt = 0, seq = 0;
-      const int page_size = 1 << P.page_shift, run = min(page_size, TN), runs = TN / run;
-      constexpr int EB = E4M3 ? 1 : 2, BOX = D * EB < 128 ? D * EB : 128, BOXES = D * EB / BOX;  // bytes of a box's rows
-      for (; it.more && !timeout; it.next(P)) {
-        for (int u = it.u0; u < it.u1 && !timeout; ++u, ++seq) {
-          const int tile = it.list.tile(u);
-          uint32_t lost = 0;
-          int page = P.pages;  // (past the end: the copy fills in zeros)
-          if (lane < runs) {
-            const int place = tile * TN + lane * run;
-            if (it.list.needs(it.s, place, run)) {
-              page = page_of(P, it.b, place);
-              if (!is_page(P, page)) {
-                set_status(P.status, K3MOE_DEV_BOUNDS);
-                page = P.pages;
-                lost = below(run / 16) << (lane * run / 16);
-              }
-            }
-          }
-          lost = __reduce_or_sync(0xFFFFFFFFu, lost);
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            uint64_t *full;
-            uint32_t dst;
-            bool ok = true;
-            uint32_t bytes = 0;  // where the scales go
-            if (kv == 0) {
-              const uint32_t slot = kt % NK;
-              if (lane == 0) ok = mb_wait(&sh.k_empty[slot], ((kt / NK) & 1u) ^ 1u);
-              full = &sh.k_full[slot], dst = sbase + S::OFF_K + slot * S::KTILE, bytes = su32(sh.key_bytes[slot]);
-              ++kt;
-            } else if constexpr (E4M3) {
-              const uint32_t slot = rt % NR;
-              if (lane == 0) ok = mb_wait(&sh.r_empty[slot], ((rt / NR) & 1u) ^ 1u);
-              full = &sh.r_full[slot], dst = sbase + S::OFF_R + slot * S::RAWB, bytes = dst + TN * D;
-              ++rt;
-            } else {
-              const uint32_t slot = vt % NV;
-              if (lane == 0) ok = mb_wait(&sh.v_empty[slot], ((vt / NV) & 1u) ^ 1u);
-              full = &sh.v_full[slot], dst = sbase + S::OFF_V + slot * S::TILE;
-              ++vt;
-            }
-            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-            if (!ok) {
-              timeout = true;
-              break;
-            }
-            const bool scales = E4M3 && page < P.pages;
-            const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, lane < runs && scales));
-            if (lane == 0 && kv == 0) sh.lost[seq & 15] = lost;
-            if (lane == 0) mb_arrive_tx(full, TN * D * EB + (E4M3 ? scaled * run : 0));
-            __syncwarp();
-            if (lane < runs) {
-              const int at = (tile * TN + lane * run) & (page_size - 1);
-#pragma unroll
-              for (int x = 0; x < BOXES; ++x)
-                tma_load_4d(dst + x * (TN * BOX) + lane * (run * BOX), kv ? &vmap : &kmap, x * (BOX / EB), at, it.head, page, full);
-              if (scales)
-                bulk_load(bytes + lane * run,
-                          (kv ? P.vs : P.ks) + (((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) + at), run, full);
-            }
+          } else if (k + 2 < K) {
+            ok = scores(k + 2);
           }
         }
       }
-      // every copy has landed before the block can leave
-      if (timeout && lane == 0) {
-        if constexpr (E4M3) {
-          for (uint32_t i = rt < NR ? 0 : rt - NR; i < rt; ++i) mb_wait(&sh.r_full[i % NR], (i / NR) & 1u);
-          for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&sh.k_full[i % NK], (i / NK) & 1u);
-        } else {
-          for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&sh.k_full[i % NK], (i / NK) & 1u);
-          for (uint32_t i = vt < NV ? 0 : vt - NV; i < vt; ++i) mb_wait(&sh.v_full[i % NV], (i / NV) & 1u);
-        }
+      tiles_before += T;
+      if (!ok || !pass_keys(tiles_before) || !pass_values(tiles_before)) {
+        timeout = true;
+        break;
       }
-    } else if (E4M3 && warp == 11) {
-      // ---- the keys' scales as numbers
-      uint32_t kt = 0;
-      for (; it.more && !timeout; it.next(P)) {
-        for (int u = it.u0; u < it.u1; ++u, ++kt) {
-          if (!warp_wait(&sh.k_full[kt % NK], (kt / NK) & 1u)) {
+      item_done(items);
+    }
+  } else if (warp == 9) {
+    // ---- items, and their loads
+    uint32_t kt = 0, vt = 0, rt = 0, seq = 0, items = 0;
+    const int page_size = 1 << P.page_shift, run = min(page_size, TN), runs = TN / run;
+    constexpr int EB = E4M3 ? 1 : 2, BOX = D * EB < 128 ? D * EB : 128, BOXES = D * EB / BOX;  // bytes of a box's rows
+    Walk<TN, ROWS> it;
+    if (P.parts)
+      it.direct(P, blockIdx.x);
+    else
+      it.init(P, blockIdx.x);
+#pragma unroll 1
+    for (;; ++items) {
+      if (items >= 4 && !warp_wait(&sh.item_empty[items & 3], ((items >> 2) & 1u) ^ 1u)) timeout = true;
+      if (timeout) break;
+      if (lane == 0) {
+        AxItem &I = sh.item[items & 3];
+        if (it.more)
+          it.show(P, I);
+        else
+          I.rows = 0;
+        mb_arrive(&sh.item_full[items & 3]);
+      }
+      if (!it.more) break;
+#pragma unroll 1
+      for (int u = it.u0; u < it.u1 && !timeout; ++u, ++seq) {
+        const int tile = it.list.tile(u);
+        uint32_t lost = 0;
+        int page = P.pages;  // (past the end: the copy fills in zeros)
+        if (lane < runs) {
+          const int place = tile * TN + lane * run;
+          if (it.list.needs(it.s, place, run)) {
+            page = page_of(P, it.b, place);
+            if (!is_page(P, page)) {
+              set_status(P.status, K3MOE_DEV_BOUNDS);
+              page = P.pages;
+              lost = below(run / 16) << (lane * run / 16);
+            }
+          }
+        }
+        lost = __reduce_or_sync(0xFFFFFFFFu, lost);
+        const bool scales = E4M3 && page < P.pages;
+        const int scaled = __popc(__ballot_sync(0xFFFFFFFFu, lane < runs && scales));
+        const int at = (tile * TN + lane * run) & (page_size - 1);
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          uint64_t *full, *empty;
+          uint32_t dst, phase, bytes = 0;  // (bytes: where the scales go)
+          if (kv == 0) {
+            const uint32_t slot = kt % NK;
+            phase = kt / NK, empty = &sh.k_empty[slot], full = &sh.k_full[slot];
+            dst = sbase + S::OFF_K + slot * S::KTILE;
+            if (E4M3) bytes = su32(sh.key_bytes[slot]);
+            ++kt;
+          } else if constexpr (E4M3) {
+            const uint32_t slot = rt % NR;
+            phase = rt / NR, empty = &sh.r_empty[slot], full = &sh.r_full[slot];
+            dst = sbase + S::OFF_R + slot * S::RAWB, bytes = dst + TN * D;
+            ++rt;
+          } else {
+            const uint32_t slot = vt % NV;
+            phase = vt / NV, empty = &sh.v_empty[slot], full = &sh.v_full[slot];
+            dst = sbase + S::OFF_V + slot * S::TILE;
+            ++vt;
+          }
+          if (!warp_wait(empty, (phase & 1u) ^ 1u)) {
             timeout = true;
             break;
           }
-          for (int x = lane; x < TN; x += 32) sh.key_scale[kt & 7][x] = e8m0_to_f32(sh.key_bytes[kt % NK][x]);
+          if (lane == 0) {
+            if (kv == 0) sh.lost[seq & 15] = lost;
+            mb_arrive_tx(full, TN * D * EB + (E4M3 ? scaled * run : 0));
+          }
           __syncwarp();
-          if (lane == 0) mb_arrive(&sh.k_ready[kt % NK]);
+          if (lane < runs) {
+#pragma unroll
+            for (int x = 0; x < BOXES; ++x)
+              tma_load_4d(dst + x * (TN * BOX) + lane * (run * BOX), kv ? &vmap : &kmap, x * (BOX / EB), at, it.head, page, full);
+            if (scales)
+              bulk_load(bytes + lane * run,
+                        (kv ? P.vs : P.ks) + (((static_cast<size_t>(page) * P.heads + it.head) << P.page_shift) + at), run, full);
+          }
         }
       }
+      if (P.parts)
+        it.more = false;
+      else
+        it.next(P);
     }
-  } else {
+    // every copy has landed before the block can leave
+    if (timeout) {
+      if constexpr (E4M3) {
+        for (uint32_t i = rt < NR ? 0 : rt - NR; i < rt; ++i) mb_wait(&sh.r_full[i % NR], (i / NR) & 1u);
+      } else {
+        for (uint32_t i = vt < NV ? 0 : vt - NV; i < vt; ++i) mb_wait(&sh.v_full[i % NV], (i / NV) & 1u);
+      }
+      for (uint32_t i = kt < NK ? 0 : kt - NK; i < kt; ++i) mb_wait(&sh.k_full[i % NK], (i / NK) & 1u);
+    }
+  } else if (E4M3 && warp == 11) {
+    // ---- the keys' scales as numbers
+    uint32_t kt = 0;
+    const AxItem *I;
+    for (uint32_t items = 0; !timeout && (I = item_at(items)) != nullptr; ++items) {
+      for (const uint32_t end = kt + I->u1 - I->u0; kt < end; ++kt) {
+        if (!warp_wait(&sh.k_full[kt % NK], (kt / NK) & 1u)) {
+          timeout = true;
+          break;
+        }
+#pragma unroll
+        for (int x = lane; x < TN; x += 32) sh.key_scale[kt & 7][x] = e8m0_to_f32(sh.key_bytes[kt % NK][x]);
+        __syncwarp();
+        if (lane == 0) mb_arrive(&sh.k_ready[kt % NK]);
+      }
+      item_done(items);
+    }
+  } else if (warp >= 12) {
     // ---- values: codes become bf16 operands, and what a row does not see must not be other than finite
     const int t128 = tid - 384;
-    uint32_t vt = 0, items = 0;
-    for (; it.more && !timeout; it.next(P), ++items) {
+    uint32_t vt = 0;
+    const AxItem *ip;
+    for (uint32_t items = 0; !timeout && (ip = item_at(items)) != nullptr; ++items) {
+      const AxItem &I = *ip;
       if (t128 == 0) atomicAnd(&sh.odd, ~(1u << ((items + 16) & 31)));
-      for (int u = it.u0; u < it.u1; ++u, ++vt) {
-        const int tile = it.list.tile(u);
+#pragma unroll 1
+      for (int u = I.u0; u < I.u1; ++u, ++vt) {
+        const int tile = I.tile(u);
         const uint32_t slot = vt % NV, rs = vt % NR;
         if (!(E4M3 ? warp_wait(&sh.r_full[rs], (vt / NR) & 1u) && warp_wait(&sh.v_empty[slot], ((vt / NV) & 1u) ^ 1u)
                    : warp_wait(&sh.v_full[slot], (vt / NV) & 1u))) {
@@ -1100,88 +1204,84 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           break;
         }
         const uint32_t lost = sh.lost[vt & 15];
-        const bool check = lost || masked<TN>(P, it.s, it.list, tile);
-        auto there = [&](int place) {  // whether a row may see it
-          return it.list.needs(it.s, place & ~15, 16) && place < it.s.n && !(lost >> ((place % TN) / 16) & 1u);
-        };
-        auto finite = [&](uint32_t (&h)[4]) {  // leaves out what is not, and remembers that
-          bool odd = false;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if ((h[y] & 0x7F80u) == 0x7F80u) h[y] &= 0xFFFF0000u, odd = true;
-            if ((h[y] & 0x7F800000u) == 0x7F800000u) h[y] &= 0xFFFFu, odd = true;
-          }
-          if (odd) atomicOr(&sh.odd, 1u << (items & 31));
-          return odd;
-        };
+        const bool check = lost || masked<TN>(P, I, tile);
         uint8_t *const op = smem + S::OFF_V + slot * S::TILE;
         if constexpr (E4M3) {
+          // A lane takes 16 codes of a row; eight neighbouring lanes take four times 16 of one row and the next four of
+          // another, so that neither their loads nor their stores meet in a bank
           const uint8_t *raw = smem + S::OFF_R + rs * S::RAWB, *scales = raw + TN * D;
-          constexpr int BOX = D < 128 ? D : 128, CH = D / 16, ROWS_AT_ONCE = 128 / CH, U = 4;  // (chunks of 16 codes)
-          const int ch = t128 % CH, r0 = t128 / CH;
+          constexpr int BOX = D < 128 ? D : 128, RW = D == 64 ? 8 : D == 128 ? 4 : 2;  // rows of a warp
+          const int h = (lane >> 2) & 1, p = lane >> 3, w = warp - 12;
+          const int rr0 = D == 64 ? lane >> 2 : D == 128 ? 2 * (p >> 1) + h : h;
+          const int blk = D == 64 ? 0 : D == 128 ? (p & 1) ^ h : p ^ h;  // of 64 dimensions
+          const int ch = 4 * blk + (lane & 3);
           const uint8_t *from = raw + (ch * 16 / BOX) * (TN * BOX) + (ch * 16) % BOX;
-          uint8_t *to = op + (ch / 4) * (TN * 128);
-          const int c0 = (2 * ch) & 7, sw = (ch >> 2) & 1;  // (half of the lanes store the second word first: no bank twice)
-#pragma unroll 1
-          for (int j = 0; j < TN / ROWS_AT_ONCE; j += U) {
-            uint4 in[U];
-            uint32_t byte[U];
+          uint8_t *to = op + blk * (TN * 128);
+          const int c0 = 2 * (lane & 3);
+#pragma unroll 2
+          for (int rr = w * RW + rr0; rr < TN; rr += 4 * RW) {
+            const uint4 in = *reinterpret_cast<const uint4 *>(from + rr * BOX);
+            const uint32_t byte = scales[rr];
+            const uint32_t cw[4] = {in.x, in.y, in.z, in.w};
+            uint32_t hv[8];
+            // 2^(byte - 127 + 120), or as much of it as bf16 holds
+            const uint32_t f = (byte <= 134u ? (byte + 120u) << 7 : byte == 255u ? 0x7FC0u : 0x7F00u) * 0x10001u;
+            uint32_t rare = byte > 134u ? 0x80808080u : 0u;
 #pragma unroll
-            for (int x = 0; x < U; ++x) {
-              const int rr = r0 + (j + x) * ROWS_AT_ONCE;
-              in[x] = *reinterpret_cast<const uint4 *>(from + rr * BOX);
-              byte[x] = scales[rr];
+            for (int y = 0; y < 4; ++y) {
+              rare |= (cw[y] & 0x7F7F7F7Fu) + 0x01010101u;  // (a NaN's code)
+              hv[2 * y] = mul_bf16x2(codes_up(cw[y], 0x1404), f);
+              hv[2 * y + 1] = mul_bf16x2(codes_up(cw[y], 0x3424), f);
             }
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-              const int rr = r0 + (j + x) * ROWS_AT_ONCE;
-              uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w}, h[8];
-              if (check && !there(tile * TN + rr)) byte[x] = 127u, w[0] = w[1] = w[2] = w[3] = 0u;
-              // 2^(byte - 127 + 120), or as much of it as bf16 holds
-              const uint32_t f = (byte[x] <= 134u ? (byte[x] + 120u) << 7 : byte[x] == 255u ? 0x7FC0u : 0x7F00u) * 0x10001u;
-              uint32_t rare = byte[x] > 134u ? 0x80808080u : 0u;
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                rare |= (w[y] & 0x7F7F7F7Fu) + 0x01010101u;  // (a NaN's code)
-                h[2 * y] = mul_bf16x2(codes_up(w[y], 0x1404), f);
-                h[2 * y + 1] = mul_bf16x2(codes_up(w[y], 0x3424), f);
+            uint8_t *row = to + rr * 128;
+            const uint32_t a0 = (c0 ^ (rr & 7)) << 4, a1 = ((c0 + 1) ^ (rr & 7)) << 4;
+            *reinterpret_cast<uint4 *>(row + a0) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4 *>(row + a1) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            if (rare & 0x80808080u) {  // code by code
+              const float x = e8m0_to_f32(byte);
+#pragma unroll 1
+              for (int y = 0; y < 16; ++y) {
+                uint32_t a, z;
+                e4m3x4_to_f16x2(from[rr * BOX + y], a, z);
+                reinterpret_cast<uint16_t *>(row + (y < 8 ? a0 : a1))[y & 7] =
+                    static_cast<uint16_t>(bf16x2(__half2float(__ushort_as_half(static_cast<unsigned short>(a))) * x, 0.f));
               }
-              if (rare & 0x80808080u) {
-                const uint32_t f2 = (byte[x] > 134u && byte[x] < 255u ? byte[x] - 7u : 127u) * 0x00800080u;
-#pragma unroll
-                for (int y = 0; y < 8; ++y) h[y] = mul_bf16x2(h[y], f2);
-#pragma unroll
-                for (int y = 0; y < 16; ++y)
-                  if (((w[y / 4] >> (8 * (y & 3))) & 0x7Fu) == 0x7Fu)
-                    h[y / 2] = (h[y / 2] & (y & 1 ? 0xFFFFu : 0xFFFF0000u)) | (y & 1 ? 0x7FC00000u : 0x7FC0u);
-              }
-              uint32_t lo[4] = {h[0], h[1], h[2], h[3]}, hi[4] = {h[4], h[5], h[6], h[7]};
-              if (check) finite(lo), finite(hi);
-              const uint4 a = make_uint4(lo[0], lo[1], lo[2], lo[3]), b = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              uint8_t *row = to + rr * 128;
-              *reinterpret_cast<uint4 *>(row + (((c0 + sw) ^ (rr & 7)) << 4)) = sw ? b : a;
-              *reinterpret_cast<uint4 *>(row + (((c0 + 1 - sw) ^ (rr & 7)) << 4)) = sw ? a : b;
             }
           }
-          fence_async();
           __syncwarp();
           if (lane == 0) mb_arrive(&sh.r_empty[rs]);
-        } else if (check) {
-          constexpr int CH = D / 8;
-          for (int x = t128; x < TN * CH; x += 128) {
-            const int rr = x / CH, ch = x % CH;
-            uint4 *at = reinterpret_cast<uint4 *>(op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-            uint32_t h[4] = {at->x, at->y, at->z, at->w};
-            if (!there(tile * TN + rr))
-              *at = make_uint4(0, 0, 0, 0);
-            else if (finite(h))
-              *at = make_uint4(h[0], h[1], h[2], h[3]);
-          }
-          fence_async();
         }
+        if (check) {
+          // Places that no row sees become zeros; others that are not finite are left out, and remembered.  (Each warp its
+          // own rows: in the E4M3 case those that it has converted.)
+          constexpr int CH = D / 8, RW = D == 64 ? 8 : D == 128 ? 4 : 2;
+#pragma unroll 1
+          for (int x = t128 & 31; x < TN / 4 * CH; x += 32) {
+            const int q = x / CH, ch = x % CH, rr = q / RW * (4 * RW) + (warp - 12) * RW + q % RW, place = tile * TN + rr;
+            uint4 *at = reinterpret_cast<uint4 *>(op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+            const int g16 = place & ~15;
+            if (place >= I.n || !(g16 + 16 > I.lo || g16 < I.sinks) || (lost >> ((place % TN) / 16) & 1u)) {
+              *at = make_uint4(0, 0, 0, 0);
+              continue;
+            }
+            uint32_t hv[4] = {at->x, at->y, at->z, at->w};
+            bool odd = false;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              if ((hv[y] & 0x7F80u) == 0x7F80u) hv[y] &= 0xFFFF0000u, odd = true;
+              if ((hv[y] & 0x7F800000u) == 0x7F800000u) hv[y] &= 0xFFFFu, odd = true;
+            }
+            if (odd) {
+              *at = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+              atomicOr(&sh.odd, 1u << (items & 31));
+            }
+          }
+        }
+        if (E4M3 || check) fence_async();
         __syncwarp();
         if (lane == 0) mb_arrive(&sh.v_ready[slot]);
       }
+      item_done(items);
     }
   }
   if (timeout) set_status(P.status, K3MOE_DEV_TIMEOUT);
@@ -1194,18 +1294,26 @@ __global__ void __launch_bounds__(kAxThreads, 1)
 }
 
 // Adds the parts of an item that was cut, in the order of their pieces: block (x, y) joins 32 rows of the item that
-// begins in piece x.
+// begins in piece x (direct: of item x).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
-  const int4 me = P.meta[blockIdx.x];
+  int4 me;
+  if (P.parts) {
+    const int item = blockIdx.x, b = item / (P.heads * P.row_tiles), head = item / P.row_tiles - b * P.heads;
+    me = make_int4(b, head, item - (b * P.heads + head) * P.row_tiles, P.parts);
+  } else {
+    me = P.meta[blockIdx.x];
+  }
   if (me.w < 2) return;
   const Seq s = seq_of(P, me.x, false);
   const int r0 = me.z * ROWS, rows = min(ROWS, s.m * P.G - r0), r = 32 * blockIdx.y + lane;
   if (32 * static_cast<int>(blockIdx.y) >= rows) return;
-  auto slot_of = [&](int p) { return static_cast<size_t>(p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p)); };
+  auto slot_of = [&](int p) {
+    return static_cast<size_t>(P.parts ? P.parts * blockIdx.x + p : p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p));
+  };
   float mm = -INFINITY, l = 0.f;
   for (int p = 0; p < me.w; ++p) mm = fmaxf(mm, P.stat[slot_of(p) * ROWS + r].x);
   const float base = mm == -INFINITY ? 0.f : mm;
@@ -1216,13 +1324,15 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
   const int i = (r0 + r) / P.G, g = r0 + r - i * P.G;
   const size_t row = (static_cast<size_t>(s.first) + i) * P.Hq + me.y * P.G + g;
   const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
   for (int x = 8 * warp; x < D; x += 32) {
     float o[8];
 #pragma unroll
     for (int y = 0; y < 8; ++y) o[y] = 0.f;
     for (int p = 0; p < me.w; ++p) {
       const size_t slot = slot_of(p);
-      const float f = ex2(P.stat[slot * ROWS + r].x - base);
+      const float at = P.stat[slot * ROWS + r].x, f = ex2(at - base);
+      if (at == -INFINITY) continue;  // (a part without a step has no sums)
 #pragma unroll
       for (int y = 0; y < 8; ++y) o[y] = fmaf(P.part[(slot * D + x + y) * ROWS + r], f, o[y]);
     }
@@ -1316,10 +1426,25 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   P.blocks = min(sm_count(), kAxMostBlocks);
   P.entries = entries_of(S::ROWS, P.B, P.rows, P.G);
   P.per_head = static_cast<uint32_t>(((1ULL << 32) + P.G - 1) / P.G);
-  if (launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
-  if (launch_pdl(attn_extend_kernel<D, E4M3>, dim3(P.blocks), dim3(kAxThreads), S::SMEM, st, P, kmap, vmap) != cudaSuccess)
+  // No more items than SMs: a block each, or several where a sequence may be long; no plan, and mostly no joint.
+  const long long row_tiles = (static_cast<long long>(P.max_new) * P.G + S::ROWS - 1) / S::ROWS;
+  const long long items = static_cast<long long>(P.B) * P.heads * row_tiles;
+  P.parts = 0;
+  if (items <= P.blocks) {
+    const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
+    const long long seen = P.window > 0 ? min(visible, static_cast<long long>(P.window) + P.sinks + P.max_new) : visible;
+    P.row_tiles = static_cast<int>(row_tiles);
+    P.parts = static_cast<int>(max(1LL, min(P.blocks / items, seen / (kPartTiles * S::TN))));
+  }
+  if (!P.parts && launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
+  const int blocks = P.parts ? static_cast<int>(items) * P.parts : P.blocks;
+  if (launch_pdl(attn_extend_kernel<D, E4M3>, dim3(blocks), dim3(kAxThreads), S::SMEM, st, P, kmap, vmap) != cudaSuccess)
     return -1;
-  return launch_pdl(attn_extend_join_kernel<D, S::ROWS>, dim3(P.blocks, S::ROWS / 32), dim3(128), 0, st, P) == cudaSuccess ? 0 : -1;
+  if (P.parts == 1) return 0;
+  return launch_pdl(attn_extend_join_kernel<D, S::ROWS>, dim3(P.parts ? items : blocks, S::ROWS / 32), dim3(128), 0, st, P) ==
+                 cudaSuccess
+             ? 0
+             : -1;
 }
 
 }  // namespace
