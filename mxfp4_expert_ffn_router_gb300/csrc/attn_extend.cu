@@ -54,7 +54,7 @@ struct AxParams {
   float2 *stat;      // [2 blocks][rows of a tile]: reference, sum of the weights
   float *part;       // [2 blocks][dim][rows of a tile]
   int blocks, entries;  // pieces; room for the tiles of query rows
-  int parts, row_tiles;  // (direct) blocks of an item; items that a sequence's rows of one head take at most
+  int parts;  // (direct) blocks of an item
   uint32_t per_head;    // ceil(2^32 / G) (token_of)
 };
 
@@ -174,6 +174,31 @@ __device__ __forceinline__ int page_of(const AxParams &P, int b, int place) {
 __device__ __forceinline__ bool is_page(const AxParams &P, int page) {
   return static_cast<unsigned>(page) < static_cast<unsigned>(P.pages);
 }
+// The e-th of the items that all sequences' rows of one head make up, by a whole warp: its sequence (-1: there are fewer),
+// and which of that one's it is.
+template <int ROWS>
+__device__ __forceinline__ int sequence_of(const AxParams &P, int e, int &t, bool report) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < P.B; b0 += 32) {
+    int mine = 0;
+    if (b0 + lane < P.B) mine = static_cast<int>((static_cast<long long>(seq_of(P, b0 + lane, report).m) * P.G + ROWS - 1) / ROWS);
+    int upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += o;
+    }
+    const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > e);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      t = e - before - __shfl_sync(0xFFFFFFFFu, upto - mine, at);
+      return b0 + at;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+  }
+  return -1;
+}
 // A block's piece of the line, item by item.
 template <int TN, int ROWS>
 struct Walk {
@@ -238,13 +263,12 @@ struct Walk {
     } while (u0 >= u1);
   }
   __device__ __forceinline__ void direct(const AxParams &P, int block) {
-    const int item = block / P.parts, part = block - item * P.parts, per = P.heads * P.row_tiles;
-    b = item / per;
-    head = item / P.row_tiles - b * P.heads;
-    t = item - (b * P.heads + head) * P.row_tiles;
-    s = seq_of(P, b, head == 0 && t == 0 && part == 0);
-    more = t * ROWS < s.m * P.G;
+    const int item = block / P.parts, part = block - item * P.parts, e = item / P.heads;
+    head = item - e * P.heads;
+    b = sequence_of<ROWS>(P, e, t, block == 0);
+    more = b >= 0;
     if (!more) return;
+    s = seq_of(P, b, false);
     measure(P);
     u0 = list.units * part / P.parts, u1 = list.units * (part + 1) / P.parts;
   }
@@ -690,11 +714,13 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       return (ch * 8 / S::SW) * (128 * S::SW) + rr * S::SW + (((byte >> 4) ^ sw) << 4) + (byte & 8);
     };
     auto place16 = [&](int rr) -> uint32_t { return (ch / 8) * (128 * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4); };
+    int q_rows = 0;
     auto ask_q = [&](const AxItem &I) {
       const int base = I.r0 + (I.both ? 128 * st : 0), left = I.r0 + I.rows - base, i0 = base / P.G, g0 = base - i0 * P.G;
       const uint16_t *q = P.q + (static_cast<long long>(I.first) + i0) * P.q_stride + static_cast<size_t>(I.head) * P.G * D + ch * 8;
-#pragma unroll 1
-      for (int rr = q_row; rr < 128; rr += 128 / CH) {
+      q_rows = min(128, (left + 128 / CH - 1) & ~(128 / CH - 1));  // (whole turns of the threads: the rest is not read)
+#pragma unroll 2
+      for (int rr = q_row; rr < q_rows; rr += 128 / CH) {
         const int ii = token_of(P, g0 + rr), gg = g0 + rr - ii * P.G;
         const bool on = rr < left;
         const uint16_t *from = on ? q + ii * P.q_stride + gg * D : P.q;
@@ -711,8 +737,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       cp_wait_all();
       const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u, keep = flat ? 0u : 0xFFFFFFFFu;
       if constexpr (E4M3) {
-#pragma unroll 1
-        for (int rr = q_row; rr < 128; rr += 128 / CH) {
+#pragma unroll 2
+        for (int rr = q_row; rr < q_rows; rr += 128 / CH) {
           // the row times a power of two, to a largest value in [128, 256), in two E4M3 numbers a value
           uint2 *const to = reinterpret_cast<uint2 *>(smem + st * S::QB + place8(rr)), *const to2 = to + 128 * D / 8;
           const uint2 u0 = *to, u1 = *to2;
@@ -739,7 +765,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
       } else if (flip || !keep) {
 #pragma unroll 1
-        for (int rr = q_row; rr < 128; rr += 128 / CH) {
+        for (int rr = q_row; rr < q_rows; rr += 128 / CH) {
           uint4 *const to = reinterpret_cast<uint4 *>(smem + st * S::QB + place16(rr));
           const uint4 u = *to;
           *to = make_uint4((u.x ^ flip) & keep, (u.y ^ flip) & keep, (u.z ^ flip) & keep, (u.w ^ flip) & keep);
@@ -1254,26 +1280,35 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         if (check) {
           // Places that no row sees become zeros; others that are not finite are left out, and remembered.  (Each warp its
           // own rows: in the E4M3 case those that it has converted.)
-          constexpr int CH = D / 8, RW = D == 64 ? 8 : D == 128 ? 4 : 2;
+          constexpr int CH = D / 8, RW = D == 64 ? 8 : D == 128 ? 4 : 2, U = 4;
 #pragma unroll 1
-          for (int x = t128 & 31; x < TN / 4 * CH; x += 32) {
-            const int q = x / CH, ch = x % CH, rr = q / RW * (4 * RW) + (warp - 12) * RW + q % RW, place = tile * TN + rr;
-            uint4 *at = reinterpret_cast<uint4 *>(op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
-            const int g16 = place & ~15;
-            if (place >= I.n || !(g16 + 16 > I.lo || g16 < I.sinks) || (lost >> ((place % TN) / 16) & 1u)) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
-            }
-            uint32_t hv[4] = {at->x, at->y, at->z, at->w};
-            bool odd = false;
+          for (int x0 = lane; x0 < TN / 4 * CH; x0 += 32 * U) {
+            uint4 *at[U], was[U];
+            bool there[U];
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              if ((hv[y] & 0x7F80u) == 0x7F80u) hv[y] &= 0xFFFF0000u, odd = true;
-              if ((hv[y] & 0x7F800000u) == 0x7F800000u) hv[y] &= 0xFFFFu, odd = true;
+            for (int y = 0; y < U; ++y) {
+              const int x = x0 + 32 * y, q = x / CH, ch = x % CH;
+              const int rr = q / RW * (4 * RW) + (warp - 12) * RW + q % RW, place = tile * TN + rr, g16 = place & ~15;
+              at[y] = reinterpret_cast<uint4 *>(op + (ch / 8) * (TN * 128) + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+              there[y] = place < I.n && (g16 + 16 > I.lo || g16 < I.sinks) && !(lost >> ((place % TN) / 16) & 1u);
+              was[y] = *at[y];
             }
-            if (odd) {
-              *at = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-              atomicOr(&sh.odd, 1u << (items & 31));
+#pragma unroll
+            for (int y = 0; y < U; ++y) {
+              uint32_t hv[4] = {was[y].x, was[y].y, was[y].z, was[y].w}, odd = 0;
+#pragma unroll
+              for (int z = 0; z < 4; ++z) odd |= (hv[z] & 0x7F807F80u) + 0x00800080u;
+              if (!there[y]) {
+                *at[y] = make_uint4(0, 0, 0, 0);
+              } else if (odd & 0x80008000u) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  if ((hv[z] & 0x7F80u) == 0x7F80u) hv[z] &= 0xFFFF0000u;
+                  if ((hv[z] & 0x7F800000u) == 0x7F800000u) hv[z] &= 0xFFFFu;
+                }
+                *at[y] = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+                atomicOr(&sh.odd, 1u << (items & 31));
+              }
             }
           }
         }
@@ -1302,8 +1337,10 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
   pdl_trigger();
   int4 me;
   if (P.parts) {
-    const int item = blockIdx.x, b = item / (P.heads * P.row_tiles), head = item / P.row_tiles - b * P.heads;
-    me = make_int4(b, head, item - (b * P.heads + head) * P.row_tiles, P.parts);
+    const int e = blockIdx.x / P.heads;
+    int t = 0;
+    const int b = sequence_of<ROWS>(P, e, t, false);
+    me = make_int4(b, blockIdx.x - e * P.heads, t, b < 0 ? 0 : P.parts);
   } else {
     me = P.meta[blockIdx.x];
   }
@@ -1427,13 +1464,12 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   P.entries = entries_of(S::ROWS, P.B, P.rows, P.G);
   P.per_head = static_cast<uint32_t>(((1ULL << 32) + P.G - 1) / P.G);
   // No more items than SMs: a block each, or several where a sequence may be long; no plan, and mostly no joint.
-  const long long row_tiles = (static_cast<long long>(P.max_new) * P.G + S::ROWS - 1) / S::ROWS;
-  const long long items = static_cast<long long>(P.B) * P.heads * row_tiles;
+  const long long most = (static_cast<long long>(P.max_new) * P.G + S::ROWS - 1) / S::ROWS;
+  const long long items = min(static_cast<long long>(P.entries), P.B * most) * P.heads;
   P.parts = 0;
   if (items <= P.blocks) {
     const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
     const long long seen = P.window > 0 ? min(visible, static_cast<long long>(P.window) + P.sinks + P.max_new) : visible;
-    P.row_tiles = static_cast<int>(row_tiles);
     P.parts = static_cast<int>(max(1LL, min(P.blocks / items, seen / (kPartTiles * S::TN))));
   }
   if (!P.parts && launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
