@@ -18,7 +18,8 @@ FAST = os.path.join(HERE, "_k3torch.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["k3moe.cu", "route.cu", "bucket.cu", "ffn_gemv.cu", "ffn_gemm.cu", "combine.cu",
            "quant.cu", "k3moe_noalloc.cu", "router.cu", "expert_cache.cu", "rmsnorm.cu", "kv_cache.cu",
-           "attn_decode.cu", "kv_append.cu", "attn_extend.cu", "attn_sinks.cu"]
+           "attn_decode.cu", "kv_append.cu", "attn_extend.cu", "attn_sinks.cu",
+           "attn_rows.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -79,10 +79,16 @@
 // heads, E4M3 (668 MB): 111 us, 6.0 TB/s; one of 131072 tokens (271 MB): 51 us, of which 8 are the start, the
 // last blocks and the join; 37 tokens of 96 heads: 3.2 us.
 //
-// First tokens that stay visible.  attn_sinks.cu builds this file once more with K3_AD_SINKS for rows that see the
-// first `sinks` places besides their window, and that are found by offsets, since some sequences may have none.  The sinks'
-// tokens lie on the line of an item before its window, in units of their own, so that the two are one run of units
-// and everything from the loads on works as it does without.
+// Several new tokens, and first tokens that stay visible.  attn_sinks.cu and attn_rows.cu build this file once more, with
+// K3_AD_SINKS 1 and 2, for the rows of k3moe_attn_extend and k3moe_attn_tree, which are found by offsets: one a
+// sequence at most, and few, a key-value head's columns being its tokens' query heads.
+//  * The first `sinks` places lie on an item's line before its window, in units of their own, so that the two are one
+//    run of units and everything from the loads on works as it does without.
+//  * Columns of different tokens see different places.  What some of an item's columns do not see lies in few of its
+//    runs (the newest places, and the window's edge): there a column's scores are put to -inf one by one.  A value that is
+//    not finite would reach columns of weight 0 through the product: in such runs it is left out, and added to the sums of
+//    those that see it at the item's end.  (In the kernels of one token a sequence this costs 15 %: 64 sequences with a
+//    window of 4096, E4M3, 60 and 69 us.)
 #include <cuda_fp16.h>
 
 #ifndef K3_AD_SINKS
@@ -99,7 +105,7 @@ namespace k3moe {
 
 namespace {
 
-constexpr bool kSinks = K3_AD_SINKS;
+constexpr bool kSinks = K3_AD_SINKS >= 1, kRows = K3_AD_SINKS == 2;
 constexpr int kRun = 16;                 // tokens of a product
 constexpr int kDirectTokens = 1024;      // items that see at most this many are never cut
 constexpr int kSplitTokens = 256;        // (see "More than 8 query heads" above)
@@ -187,6 +193,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// Sets the values of a word that are not finite (of codes: NaN) to zero; not 0 where there are any.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t leave_out(uint32_t &w) {
+  const uint32_t any = E4M3 ? ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u : ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+  if (any) w &= ~(E4M3 ? (any >> 7) * 0xFFu : (any >> 15) * 0xFFFFu);
+  return any;
+}
+
 // An 8 x 8 matrix of 16-bit values, row g in lanes 4g .. 4g + 3 (two values each), transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
@@ -209,12 +223,15 @@ struct AdParams {
   int max_pages;
   const int32_t *lens;
   int window;
-  const int32_t *offsets;  // (kSinks) first row of each sequence, which has one or none
-  int rows, sinks;
+  const int32_t *offsets;  // (kSinks) first row of each sequence
+  int rows, sinks, max_new;
+  const uint64_t *masks;   // of drafted tokens, or null: each sees those before it
+  int words;
+  int cols;                // most columns that a key-value head has in a sequence (G without kRows)
   float scale;
   uint16_t *out;
   float *lse;
-  int4 *meta;    // [2 blocks]: {first slot, parts, item, row} of the cut items of a piece: one that began
+  int4 *meta;    // [2 blocks]: {first slot, parts, item, sequence} of the cut items of a piece: one that began
                  // before it, one that begins in it and goes on (parts 0: none)
   float4 *stat;  // [2 blocks][8 NT]: {m', m, l, -}
   float4 *part;  // [2 blocks][accumulator quads][32 lanes]
@@ -231,7 +248,7 @@ __device__ __forceinline__ long long div_small(long long a, long long b) {
 // sinks - 1 are seen too: units count from t0 < split, and what lies d places behind t0 is place d of the cache below split.
 struct Seen {
   int n, lo, t0;
-  int split, sinks, row;
+  int split, sinks, row, m;  // row, m: first of its rows, how many (row -1: none)
 };
 template <class W>
 __device__ __forceinline__ unsigned place_of(const W &w, unsigned tok) {
@@ -262,7 +279,15 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
     if (report) set_status(P.status, K3MOE_DEV_BOUNDS);
     s.n = len < 0 ? 0 : static_cast<int>(most);
   }
-  s.lo = P.window > 0 && s.n > P.window ? s.n - P.window : 0;
+  int new_ones = 1;
+  if constexpr (kSinks) {
+    const int o0 = P.offsets[b], o1 = P.offsets[b + 1];
+    const bool fine = o0 >= 0 && o1 >= o0 && o1 <= P.rows && o1 - o0 <= P.max_new;
+    s.m = new_ones = fine ? o1 - o0 : 0;
+    s.row = s.m ? o0 : -1;
+    if (report && (!fine || s.m > s.n)) set_status(P.status, K3MOE_DEV_BOUNDS);
+  }
+  s.lo = P.window > 0 && s.n - new_ones >= P.window ? s.n - new_ones - P.window + 1 : 0;  // (of the first of them)
   s.t0 = s.lo & ~(RUN - 1);
   if constexpr (kSinks) {
     s.split = 0;
@@ -272,16 +297,9 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
       s.split = s.t0, s.t0 -= before;
     else
       s.t0 = 0;  // window and sinks are one stretch, or nearly
-    const int o0 = P.offsets[b], m = P.offsets[b + 1] - o0;
-    s.row = o0;
-    if (m != 1 || o0 < 0 || o0 >= P.rows) {  // no row; and nothing on the line
-      s.n = s.t0 = 0, s.row = -1;
-      if (m != 0 && report) set_status(P.status, K3MOE_DEV_BOUNDS);
-    } else if (s.n == 0 && report) {
-      set_status(P.status, K3MOE_DEV_BOUNDS);
-    }
+    if (s.m == 0 || s.n == 0) s.n = s.t0 = 0;  // nothing on the line
   } else {
-    s.row = b;
+    s.row = b, s.m = 1;
   }
   return s;
 }
@@ -293,15 +311,17 @@ __device__ __forceinline__ int units_of(const Seen &s) {
 // A block's piece [from, to) of the line, and where one warp is in it.  An item that begins at
 // `begin` lies on the line as ITEM_LEN, then kUnitLen for each of its units; a unit belongs
 // to the piece in which it begins.
-template <int RUN, int UNIT, int ITEM_LEN>
+template <int RUN, int UNIT, int ITEM_LEN, int NQ>
 struct Walk {
   int b, head, group;    // sequence, key-value head, which of its items
   int n, lo, t0;
-  int split, sinks, row;
+  int split, sinks, row, m;
   unsigned tok, stop;    // the warp's next run begins at tok; the piece holds the item's runs below stop
   long long begin;       // of the item
   bool more;             // whether a run is left
-  __device__ __forceinline__ int units() const { return units_of<UNIT>({n, lo, t0, 0, 0, 0}); }
+  __device__ __forceinline__ int units() const { return units_of<UNIT>({n, lo, t0, 0, 0, 0, 0}); }
+  __device__ __forceinline__ int cols(const AdParams &P) const { return kRows ? m * P.G : P.G; }
+  __device__ __forceinline__ int groups(const AdParams &P) const { return kRows ? (m * P.G + NQ - 1) / NQ : P.groups; }
   // The item's first unit at or past place x of the line.
   __device__ __forceinline__ int unit_at(long long x) const {
     const long long u = (x - begin - ITEM_LEN + kUnitLen - 1) / kUnitLen;
@@ -314,13 +334,13 @@ struct Walk {
   }
   __device__ __forceinline__ void set(const Seen &s) {
     n = s.n, lo = s.lo, t0 = s.t0, row = s.row;
-    if constexpr (kSinks) split = s.split, sinks = s.sinks;
+    if constexpr (kSinks) split = s.split, sinks = s.sinks, m = s.m;
   }
   __device__ __forceinline__ void next_item(const AdParams &P, long long from, long long to, int first) {
     begin += static_cast<long long>(units()) * kUnitLen + ITEM_LEN;
     more = begin + ITEM_LEN < to;
     if (!more) return;
-    if (++group == P.groups) {
+    if (++group == groups(P)) {
       group = 0;
       if (++head == P.heads) {
         head = 0;
@@ -338,6 +358,30 @@ struct Walk {
     enter(from, to, first);
   }
 };
+
+// (kRows) Which of the places place + 16 (j / 2) + 2 (j % 2), j < count, that some column of the item sees, column `col` of a
+// sequence of n places, its last m in rows `row` on, sees: bit j.  Called, not inlined: it is seldom needed.
+__device__ __noinline__ uint32_t column_sees(const AdParams &P, int n, int m, int row, int col, int place, int count) {
+  const int i = min(col / P.G, m - 1), ctx = n - m;
+  const uint64_t *mask = P.masks + (P.masks ? (static_cast<long long>(row) + i) * P.words : 0);
+  int pos = ctx + i;
+  if (P.masks && P.window > 0) {
+    int seen = 0;
+    for (int x = 0; 64 * x < m; ++x) seen += __popcll(mask[x] & (m - 64 * x >= 64 ? ~0ULL : (1ULL << (m - 64 * x)) - 1ULL));
+    pos = ctx + max(0, seen - 1);
+  }
+  uint32_t bits = 0;
+  for (int j = 0; j < count; ++j) {
+    const int at = place + (j >> 1) * kRun + 2 * (j & 1);
+    bool on = P.window == 0 || at > pos - P.window || at < P.sinks;
+    if (!P.masks)
+      on = on && at <= pos;
+    else if (at >= ctx)
+      on = at < n && ((mask[(at - ctx) >> 6] >> ((at - ctx) & 63)) & 1u);
+    bits |= static_cast<uint32_t>(on) << j;
+  }
+  return bits;
+}
 
 // Warps of a block where there are few items (rows of 512 bytes: the stages of eight do not fit)
 template <int D, bool E4M3>
@@ -415,11 +459,20 @@ __device__ __forceinline__ void add_parts(const float4 (&s)[N][2], const float4 
   }
 }
 
+// Index of column `col` of key-value head `head` among the rows of all query heads; `row`: the sequence's first.
+__device__ __forceinline__ size_t row_of(const AdParams &P, int row, int head, int col) {
+  if constexpr (kRows) {
+    const int i = col / P.G;
+    return (static_cast<size_t>(row) + i) * P.Hq + head * P.G + (col - i * P.G);
+  }
+  return static_cast<size_t>(row) * P.Hq + head * P.G + col;
+}
+
 // Writes a quad of rows that are complete: out = (O' 2^-14 / l) 2^(m' - m), and with the first quad lse.  m' - m is -127
 // to 127, as V's scales are, so that one factor of both would leave fp32's normal numbers where V is tiny (but for
 // the rounding of sums past 2^24, which must not make it infinite).
 template <int D, bool E4M3>
-__device__ __forceinline__ void store_quad(const AdParams &P, int row, int h0, int rows, int t, int m, const float4 &v,
+__device__ __forceinline__ void store_quad(const AdParams &P, int row, int head, int col, int rows, int t, int m, const float4 &v,
                                            const float (&mp)[2], const float (&mt)[2], const float (&lt)[2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, r0 = 8 * t + 2 * (lane & 3);
   float fin[2], up[2];
@@ -430,10 +483,12 @@ __device__ __forceinline__ void store_quad(const AdParams &P, int row, int h0, i
     fin[x] = __fdividef(E4M3 ? 0x1p-14f : 1.f, lt[x]);
     up[x] = E4M3 ? exp2f(fminf(pb - mb, 127.f)) : 1.f;
     if (P.lse && m == 0 && g == 0 && r0 + x < rows)
-      P.lse[static_cast<size_t>(row) * P.Hq + h0 + r0 + x] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
+      P.lse[row_of(P, row, head, col + r0 + x)] = lt[x] == 0.f ? -INFINITY : (mb + log2f(lt[x])) * kLn2;
   }
-  uint16_t *op = P.out + (static_cast<size_t>(row) * P.Hq + h0 + r0) * D + quad_dim<D, E4M3>(m, g);
+  const int d = quad_dim<D, E4M3>(m, g);
+  uint16_t *op = P.out + row_of(P, row, head, col + r0) * D + d;
   store_row2(op, fin[0], up[0], v.x, v.z, lt[0] != 0.f, r0 < rows);
+  if constexpr (kRows) op = P.out + row_of(P, row, head, col + r0 + 1) * D + d - D;
   store_row2(op + D, fin[1], up[1], v.y, v.w, lt[1] != 0.f, r0 + 1 < rows);
 }
 
@@ -488,15 +543,15 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     for (int b = blockIdx.x; b < P.B; b += gridDim.x) {
       const Seen s = seen_of<RUN>(P, b, false);
       if (s.n > s.t0 || s.row < 0) continue;
-      for (size_t i = tid; i < static_cast<size_t>(P.Hq) * D / 8; i += THREADS)
+      for (size_t i = tid; i < static_cast<size_t>(s.m) * P.Hq * D / 8; i += THREADS)
         reinterpret_cast<uint4 *>(P.out + static_cast<size_t>(s.row) * P.Hq * D)[i] = make_uint4(0, 0, 0, 0);
       if (P.lse)
-        for (int i = tid; i < P.Hq; i += THREADS) P.lse[static_cast<size_t>(s.row) * P.Hq + i] = -INFINITY;
+        for (size_t i = tid; i < static_cast<size_t>(s.m) * P.Hq; i += THREADS) P.lse[static_cast<size_t>(s.row) * P.Hq + i] = -INFINITY;
     }
   };
 
   // ---- this block's piece
-  Walk<RUN, UNIT, S::ITEM_LEN> cur;
+  Walk<RUN, UNIT, S::ITEM_LEN, NQ> cur;
   int part = 0, parts = 1;  // of an item that a cluster's blocks share
   long long from = 0, to = 1LL << 62, share = 0;
   if constexpr (DIRECT) {
@@ -509,11 +564,18 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     cur.set(seen_of<RUN>(P, cur.b, tid == 0));
     cur.begin = 0;
     cur.more = true;
+    if (kRows && cur.group >= cur.groups(P)) return;
     if (cur.n <= cur.t0) {  // sees nothing
       if (part || cur.row < 0) return;
-      const int h0 = cur.head * P.G + cur.group * NQ;
-      const int rows = min(NQ, P.G - cur.group * NQ);
-      const size_t row = static_cast<size_t>(cur.row) * P.Hq + h0;
+      const int rows = min(NQ, cur.cols(P) - cur.group * NQ);
+      if constexpr (kRows) {
+        for (int i = tid; i < rows * D / 8; i += THREADS)
+          *reinterpret_cast<uint4 *>(P.out + row_of(P, cur.row, cur.head, cur.group * NQ + i / (D / 8)) * D + i % (D / 8) * 8) =
+              make_uint4(0, 0, 0, 0);
+        if (P.lse && tid < rows) P.lse[row_of(P, cur.row, cur.head, cur.group * NQ + tid)] = -INFINITY;
+        return;
+      }
+      const size_t row = static_cast<size_t>(cur.row) * P.Hq + cur.head * P.G + cur.group * NQ;
       for (int i = tid; i < rows * D / 8; i += THREADS)
         reinterpret_cast<uint4 *>(P.out + row * D)[i] = make_uint4(0, 0, 0, 0);
       if (P.lse && tid < rows) P.lse[row + tid] = -INFINITY;
@@ -527,13 +589,19 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     // every warp for itself: lane l measures sequences [l per, l per + per); a scan finds the piece
     const int per = (P.B + 31) / 32;
     const int b0 = min(P.B, lane * per), b1 = min(P.B, b0 + per);
+    int its = items;  // of sequence b
     auto length = [&](int b, bool report) {  // of an item of sequence b on the line
-      const int u = units_of<UNIT>(seen_of<RUN>(P, b, report));
+      const Seen s = seen_of<RUN>(P, b, report);
+      const int u = units_of<UNIT>(s);
+      if constexpr (kRows) its = P.heads * ((s.m * P.G + NQ - 1) / NQ);
       return u ? static_cast<long long>(u) * kUnitLen + S::ITEM_LEN : 0LL;
     };
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += length(b, blockIdx.x == 0 && warp == 0);
-    mine *= items;
+    for (int b = b0; b < b1; ++b) {
+      const long long len = length(b, blockIdx.x == 0 && warp == 0);
+      mine += kRows ? len * its : len;
+    }
+    if constexpr (!kRows) mine *= items;
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -551,8 +619,8 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
       long long len;
       for (;; ++at_b) {
         len = length(at_b, false);
-        if (from < at + len * items) break;
-        at += len * items;
+        if (from < at + len * its) break;
+        at += len * its;
       }
       at_item = static_cast<int>(div_small(from - at, len));
       at += at_item * len;
@@ -565,9 +633,9 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     const int src = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
     cur.b = __shfl_sync(0xFFFFFFFFu, at_b, src);
     at_item = __shfl_sync(0xFFFFFFFFu, at_item, src);
-    cur.head = at_item / P.groups;
-    cur.group = at_item - cur.head * P.groups;
     cur.set(seen_of<RUN>(P, cur.b, false));
+    cur.head = at_item / cur.groups(P);
+    cur.group = at_item - cur.head * cur.groups(P);
     cur.begin = __shfl_sync(0xFFFFFFFFu, at, src);
     cur.more = true;
     cur.enter(from, to, first);
@@ -589,7 +657,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   const uint32_t vdst = S::KB + lr * S::ROWB + (lx << 4);
   const uint8_t *const klane = P.k + lane * 16, *const vlane = P.v + lane * 16;
   const unsigned place = (1u << P.page_shift) - 1u, page_vecs = static_cast<unsigned>(P.heads) << P.page_shift;
-  Walk<RUN, UNIT, S::ITEM_LEN> pre = cur;
+  Walk<RUN, UNIT, S::ITEM_LEN, NQ> pre = cur;
   uint32_t bad = 0;    // bit st RR + r: 16 tokens that were not loaded: before the window, or a page outside the cache
   // a run starts at a multiple of RUN and lies in one page if pages are no smaller
   const bool one_page = (RUN - 1u) <= place;
@@ -687,12 +755,17 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
   uint2 raw[D / 16][NT];
   // of query heads 8 t + 2c + x: the scale of a raw score (in powers of two), the running maxima and l
   float sq[NT][2], o[NT][MM][4], mrun[NT][2], m_l[NT][2], l[NT][2];
-  auto load_q = [&](const Walk<RUN, UNIT, S::ITEM_LEN> &at) {
-    const int h0 = at.head * P.G + at.group * NQ, rows = min(NQ, P.G - at.group * NQ);
+  auto load_q = [&](const Walk<RUN, UNIT, S::ITEM_LEN, NQ> &at) {
+    const int h0 = at.head * P.G + at.group * NQ, rows = min(NQ, at.cols(P) - at.group * NQ);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = g + 8 * t;
       const uint16_t *qp = P.q + at.row * P.q_stride + static_cast<size_t>(h0 + r) * D + c * (16 / S::ESZ);
+      if constexpr (kRows) {
+        const int col = at.group * NQ + r, i = col / P.G;
+        qp = P.q + (static_cast<long long>(at.row) + i) * P.q_stride + static_cast<size_t>(at.head * P.G + (col - i * P.G)) * D +
+             c * (16 / S::ESZ);
+      }
 #pragma unroll
       for (int i = 0; i < KL; ++i)
 #pragma unroll
@@ -750,6 +823,8 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 
   constexpr bool kEarlyQ = D / 16 * NT <= (E4M3 && NT == 2 ? 8 : 16);  // as far as there are registers for it
   bool first_item = true;
+  uint32_t odd = 0;           // (kRows) values were left out of this item's products
+  unsigned began = cur.tok;
   int stage = 0, after = ST - 1;  // the stage in use, and the one that is loaded next
   load_q(cur);
   start_item();
@@ -762,7 +837,15 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     __syncwarp();
     if (cur.tok < static_cast<unsigned>(cur.n)) {
       const uint32_t base0 = ring + stage * (RR * S::SUB), sbase = sring + stage * (RR * S::SCALES);
-      const bool whole = sees_all(cur, place_of(cur, cur.tok), S::RUN) && bad == 0u;
+      bool whole = sees_all(cur, place_of(cur, cur.tok), S::RUN) && bad == 0u;
+      if constexpr (kRows) {  // and by all columns: those of the first token to those of the last
+        const int place = static_cast<int>(place_of(cur, cur.tok)), ctx = cur.n - cur.m;
+        const int i0 = cur.group * NQ / P.G, i1 = min((cur.group * NQ + NQ - 1) / P.G, cur.m - 1);
+        const int last = P.masks ? cur.n - 1 : ctx + i1;
+        whole = whole && place + S::RUN <= (P.masks ? ctx : ctx + i0 + 1) &&
+                (P.window == 0 || place > last - P.window || place + S::RUN <= cur.sinks);
+      }
+      uint32_t hid = 0u;  // (kRows) bit (j NT + t) 2 + x: a score of a column that does not see its place
       // S^T: rows g and g + 8 are tokens tg and tg + 2 of the 16, tg = 4 (g / 2) + g % 2, columns 2c and
       // 2c + 1 query heads.  CH partial sums, so that a product does not wait for the one before it
       constexpr int CH = RR * NT >= 4 ? 1 : 2, T2 = 2 * RR;
@@ -854,6 +937,23 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
             if (E4M3) ve[j] = 0.f;
           }
         }
+        if (kRows && (cur.m > 1 || P.masks)) {
+          const int place = static_cast<int>(place_of(cur, cur.tok)) + tg;
+          uint32_t see[2 * NT];
+#pragma unroll
+          for (int y = 0; y < 2 * NT; ++y)
+            see[y] = column_sees(P, cur.n, cur.m, cur.row, cur.group * NQ + 8 * (y >> 1) + 2 * c + (y & 1), place, T2);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int j = 0; j < T2; ++j)
+                if (!((see[2 * t + x] >> j) & 1u)) {
+                  sc[t][x][j] = -INFINITY;
+                  hid |= 1u << ((j * NT + t) * 2 + x);
+                }
+        }
       }
       float top[NT][2];
       bool grows = false;
@@ -871,7 +971,10 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
             l[t][x] = l[t][x] * ex2(m_l[t][x] - base) + add;
             m_l[t][x] = mn;
 #pragma unroll
-            for (int j = 0; j < T2; ++j) sc[t][x][j] += ve[j];
+            for (int j = 0; j < T2; ++j) {
+              sc[t][x][j] += ve[j];
+              if (kRows && ((hid >> ((j * NT + t) * 2 + x)) & 1u)) sc[t][x][j] = -INFINITY;  // (whatever the scale is)
+            }
           }
           top[t][x] = sc[t][x][0];
 #pragma unroll
@@ -938,6 +1041,12 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
               vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = vw[j][3] = 0u;
             }
           }
+          if (kRows && !whole && (cur.m > 1 || P.masks)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int w = 0; w < 4; ++w) odd |= leave_out<E4M3>(vw[j][w]);
+          }
           constexpr int VW = C >= 8 ? 4 : 2;  // 32-bit words a lane holds of a token
 #pragma unroll
           for (int w = 0; w < VW; ++w) {
@@ -969,10 +1078,47 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     cur.tok += UNIT;
     if (cur.tok < cur.stop) continue;
 
+    if constexpr (kRows) {
+      if (__any_sync(0xFFFFFFFFu, odd != 0u)) {  // add what is not finite to the columns that see it (an infinity that is one
+                                                 // already stays one, NaN stays NaN)
+        const int32_t *pages_of = P.table + static_cast<size_t>(cur.b) * P.max_pages;
+#pragma unroll 1
+        for (unsigned at = began; at < cur.tok && at < static_cast<unsigned>(cur.n); at += UNIT)
+#pragma unroll 1
+          for (unsigned tok = at; tok < at + RUN && tok < static_cast<unsigned>(cur.n); ++tok) {
+            const unsigned where = place_of(cur, tok);
+            const int pg = sees(cur, where) ? pages_of[where >> P.page_shift] : -1;
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(P.pages)) continue;
+            const size_t vec = static_cast<size_t>(static_cast<unsigned>(pg)) * page_vecs +
+                               ((static_cast<unsigned>(cur.head) << P.page_shift) + (where & place));
+            uint32_t see = 0;
+            for (int y = 0; y < 2 * NT; ++y)
+              see |= column_sees(P, cur.n, cur.m, cur.row, cur.group * NQ + 8 * (y >> 1) + 2 * c + (y & 1),
+                                 static_cast<int>(where), 1) << y;
+#pragma unroll
+            for (int m = 0; m < MM; ++m) {
+              const size_t e = vec * D + quad_dim<D, E4M3>(m, g);
+              float u[2];
+              if constexpr (E4M3) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) u[y] = (P.v[e + y] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.f;
+              } else {
+                const uint32_t both = *reinterpret_cast<const uint32_t *>(P.v + 2 * e);
+                u[0] = __uint_as_float(both << 16), u[1] = __uint_as_float(both & 0xFFFF0000u);
+              }
+              if (isfinite(u[0]) && isfinite(u[1])) continue;
+#pragma unroll
+              for (int x = 0; x < 4 * NT; ++x)
+                if (!isfinite(u[(x >> 1) & 1]) && ((see >> (2 * (x >> 2) + (x & 1))) & 1u)) o[x >> 2][m][x & 3] += u[(x >> 1) & 1];
+            }
+          }
+        odd = 0;
+      }
+    }
     // ---- the item ends here (or is cut here): join the warps
-    const Walk<RUN, UNIT, S::ITEM_LEN> done = cur;
+    const Walk<RUN, UNIT, S::ITEM_LEN, NQ> done = cur;
     const bool began_before = !DIRECT && done.unit_at(from) > 0, cut = began_before || (!DIRECT && done.unit_at(to) < done.units());
-    const int h0 = done.head * P.G + done.group * NQ, rows = min(NQ, P.G - done.group * NQ);
+    const int rows = min(NQ, done.cols(P) - done.group * NQ);
     if (DIRECT)
       cur.more = false;
     else
@@ -1051,7 +1197,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         else if (parts > 1)
           shown[quad * 32 + lane] = v;
         else
-          store_quad<D, E4M3>(P, done.row, h0, rows, t, m, v, mp, mt, lt);
+          store_quad<D, E4M3>(P, done.row, done.head, done.group * NQ, rows, t, m, v, mp, mt, lt);
       }
       __syncthreads();
     }
@@ -1063,13 +1209,14 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
             // not the first item of its block if the one before has a unit there
             2 * b0 + (done.begin - kUnitLen >= b0 * share ? 1 : 0),
             static_cast<int>(div_small(unit0 + static_cast<long long>(done.units() - 1) * kUnitLen, share)) - b0 + 1,
-            done.head * P.groups + done.group, done.row);
+            done.head * P.groups + done.group, done.b);
       }
     }
     first_item = false;
     if (!cur.more) break;
     if (!kEarlyQ) load_q(cur);
     start_item();
+    if constexpr (kRows) began = cur.tok;
     if (QS) __syncthreads();
   }
   cp_wait<0>();
@@ -1081,7 +1228,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
         if (tid < NQ) shown_stat[tid] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
       }
       cluster_sync();
-      const int h0 = cur.head * P.G + cur.group * NQ, rows = min(NQ, P.G - cur.group * NQ);
+      const int rows = min(NQ, cur.cols(P) - cur.group * NQ);
       for (int quad = part + parts * warp; quad < S::QUADS; quad += parts * W) {
         const int t = quad / MM, m = quad - t * MM, r0 = 8 * t + 2 * c;
         float4 s[8][2], u[8], v;
@@ -1097,7 +1244,7 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
           }
         }
         add_parts(s, u, v, mp, mt, lt);
-        store_quad<D, E4M3>(P, cur.row, h0, rows, t, m, v, mp, mt, lt);
+        store_quad<D, E4M3>(P, cur.row, cur.head, cur.group * NQ, rows, t, m, v, mp, mt, lt);
       }
       cluster_sync();  // the others have read this block's
     }
@@ -1194,8 +1341,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(const AdPara
     }
     if (in && sub == 0) {
       const int head = me.z / P.groups, group = me.z - head * P.groups;
-      const int h0 = head * P.G + group * NQ, rows = min(NQ, P.G - group * NQ);
-      store_quad<D, E4M3>(P, me.w, h0, rows, t, m, v, mp, mt, lt);
+      int row = me.w, cols = P.G;
+      if constexpr (kSinks) row = P.offsets[me.w];
+      if constexpr (kRows) cols = (P.offsets[me.w + 1] - row) * P.G;
+      const int rows = min(NQ, cols - group * NQ);
+      store_quad<D, E4M3>(P, row, head, group * NQ, rows, t, m, v, mp, mt, lt);
     }
   }
 }
@@ -1207,9 +1357,8 @@ struct AdPlan {
   size_t meta, stat, part, bytes;
 };
 
-AdPlan plan_of(const k3moe_kv_cache &c, int Hq) {
+AdPlan plan_of(const k3moe_kv_cache &c, int G) {  // G: most columns that a key-value head has in a sequence
   AdPlan p;
-  const int G = Hq / c.heads;
   p.NT = G <= 8 ? 1 : 2;
   p.groups = (G + 8 * p.NT - 1) / (8 * p.NT);
   p.quads = c.dim / 16 * p.NT;
@@ -1277,7 +1426,7 @@ int clusters_at_once(const AdParams &P, int parts) {
 long long items_of(const AdParams &P) { return static_cast<long long>(P.B) * P.heads * P.groups; }
 long long tokens_of(const AdParams &P) {
   const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
-  const long long seen = static_cast<long long>(P.window) + (kSinks ? P.sinks : 0);
+  const long long seen = static_cast<long long>(P.window) + (kSinks ? static_cast<long long>(P.sinks) + P.max_new - 1 : 0);
   return P.window > 0 && seen < visible ? seen : visible;
 }
 
@@ -1310,7 +1459,7 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
   const int parts = few_parts<D, E4M3, NT>(P);
   if constexpr (NT == 2) {
     AdParams Q = P;
-    Q.groups = (P.G + 7) / 8;
+    Q.groups = (P.cols + 7) / 8;
     const int split = few_parts<D, E4M3, 1>(Q);
     if (split && (split >= parts || tokens <= kDirectTokens)) return launch_few<D, E4M3, 1>(Q, split, st);
     if (tokens <= (parts ? kSplitTokens : kDirectTokens) &&
@@ -1337,7 +1486,13 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
 }  // namespace
 
 #if K3_AD_SINKS
+#if K3_AD_SINKS == 2
+size_t attn_rows_workspace(const k3moe_kv_cache &c) { return plan_of(c, 16).bytes; }
+
+int launch_attn_rows(const ExtendArgs &a, cudaStream_t st) {
+#else
 int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st) {
+#endif
   const k3moe_kv_cache &c = a.c;
   const int B = a.B, Hq = a.Hq, max_pages = a.max_pages, window = a.window;
   const uint16_t *q = a.q;
@@ -1349,13 +1504,17 @@ int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st) {
   void *ws = a.ws;
   int32_t *status = a.status;
 #else
-size_t attn_decode_workspace(const k3moe_kv_cache &c, int, int Hq) { return plan_of(c, Hq).bytes; }
+size_t attn_decode_workspace(const k3moe_kv_cache &c, int, int Hq) { return plan_of(c, Hq / c.heads).bytes; }
 
 int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q, long long q_stride,
                        const int32_t *table, int max_pages, const int32_t *lens, int window, float scale, uint16_t *out,
                        float *lse, void *ws, int32_t *status, cudaStream_t st) {
 #endif
-  const AdPlan p = plan_of(c, Hq);
+#if K3_AD_SINKS
+  const AdPlan p = plan_of(c, a.max_new * (Hq / c.heads));
+#else
+  const AdPlan p = plan_of(c, Hq / c.heads);
+#endif
   AdParams P;
   P.k = static_cast<const uint8_t *>(c.k), P.v = static_cast<const uint8_t *>(c.v), P.ks = c.k_scales, P.vs = c.v_scales;
   P.heads = c.heads, P.pages = c.pages, P.page_shift = 0;
@@ -1364,9 +1523,11 @@ int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q
   P.q = q, P.q_stride = q_stride, P.table = table, P.max_pages = max_pages, P.lens = lens;
   P.window = window, P.scale = scale, P.out = out, P.lse = lse;
 #if K3_AD_SINKS
-  P.offsets = a.offsets, P.rows = a.rows, P.sinks = a.sinks;
+  P.offsets = a.offsets, P.rows = a.rows, P.sinks = a.sinks, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
+  P.cols = a.max_new * P.G;
 #else
-  P.offsets = nullptr, P.rows = P.sinks = 0;
+  P.offsets = nullptr, P.masks = nullptr, P.rows = P.sinks = P.max_new = P.words = 0;
+  P.cols = P.G;
 #endif
   uint8_t *w = static_cast<uint8_t *>(ws);
   P.meta = reinterpret_cast<int4 *>(w + p.meta), P.stat = reinterpret_cast<float4 *>(w + p.stat);

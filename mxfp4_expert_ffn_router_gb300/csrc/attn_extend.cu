@@ -1485,13 +1485,22 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
 
 }  // namespace
 
+namespace {
+// Whether the kernels of few columns are the faster ones.
+bool few_columns(const ExtendArgs &a) {
+  const int G = a.Hq / a.c.heads;
+  return static_cast<long long>(a.max_new) * G <= 32;
+}
+}  // namespace
+
 size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq) {
-  const size_t several = space_of(c, B, rows, Hq).bytes, one = attn_decode_workspace(c, B, Hq);
+  const size_t several = space_of(c, B, rows, Hq).bytes, one = attn_rows_workspace(c);
   return several > one ? several : one;
 }
 
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   if (a.max_new == 1 && !a.masks) return launch_attn_sinks(a, st);
+  if (few_columns(a)) return launch_attn_rows(a, st);
   AxParams P;
   const k3moe_kv_cache &c = a.c;
   P.k = static_cast<const uint8_t *>(c.k), P.v = static_cast<const uint8_t *>(c.v), P.ks = c.k_scales, P.vs = c.v_scales;

@@ -40,7 +40,11 @@ struct ExtendArgs {
   void *ws;
   int32_t *status;
 };
-int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st);  // at most one new token a sequence
+// The same for at most one new token a sequence, without masks (attn_sinks.cu), and where a key-value head's rows of a
+// sequence are few (attn_rows.cu); the workspace is that of both.
+size_t attn_rows_workspace(const k3moe_kv_cache &c);
+int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st);
+int launch_attn_rows(const ExtendArgs &a, cudaStream_t st);
 size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq);
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st);
 
