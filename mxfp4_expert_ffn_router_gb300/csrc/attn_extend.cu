@@ -15,9 +15,11 @@ namespace {
 constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 and 10 products, 9 loads, 12-15 values
 constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
 constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
-constexpr int kPartTiles = 4;      // (direct) fewest tiles that a part of the longest item may have
+constexpr int kPartTiles = 2;      // (direct) fewest tiles that a part of the longest item may have
+constexpr int kJoinParts = 4;      // parts that are added at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -3.4e38f;  // reference of a part without a step, which has no sums (those of a row are -inf, or far above)
 constexpr float kGrowth = 16.f;    // a row's reference moves once a weight would pass 2^16
 
 struct AxStart {  // where a block's piece of the line begins
@@ -985,7 +987,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
         if (row.on && !(split && st)) {
           if (cut)
-            P.stat[static_cast<size_t>(I.slot) * ROWS + r] = make_float2(mb, l);
+            P.stat[static_cast<size_t>(I.slot) * ROWS + r] = make_float2(K > 0 ? mb : kNone, l);
           else if (P.lse)
             P.lse[orow] = l == 0.f ? -INFINITY : (mb + log2f(l)) * kLn2;
         }
@@ -1328,10 +1330,12 @@ __global__ void __launch_bounds__(kAxThreads, 1)
   }
 }
 
-// Adds the parts of an item that was cut, in the order of their pieces: block (x, y) joins 32 rows of the item that
-// begins in piece x (direct: of item x).
+// Adds the parts of an item that was cut, in the order of their pieces: block (x, y, z) joins 32 dimensions of 32 rows of the
+// item that begins in piece x (direct: of item x).  kJoinParts parts are loaded at once (one after the other, nine of them
+// took 20 us).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P) {
+  __shared__ float s_f[kAxMostBlocks][32];  // the parts' factors
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
   pdl_trigger();
@@ -1344,43 +1348,63 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
   } else {
     me = P.meta[blockIdx.x];
   }
-  if (me.w < 2) return;
+  const int parts = me.w;
+  if (parts < 2) return;
   const Seq s = seq_of(P, me.x, false);
   const int r0 = me.z * ROWS, rows = min(ROWS, s.m * P.G - r0), r = 32 * blockIdx.y + lane;
   if (32 * static_cast<int>(blockIdx.y) >= rows) return;
   auto slot_of = [&](int p) {
-    return static_cast<size_t>(P.parts ? P.parts * blockIdx.x + p : p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p));
+    return static_cast<size_t>(P.parts ? parts * blockIdx.x + p : p == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + p));
   };
   float mm = -INFINITY, l = 0.f;
-  for (int p = 0; p < me.w; ++p) mm = fmaxf(mm, P.stat[slot_of(p) * ROWS + r].x);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  for (int p = 0; p < me.w; ++p) {
-    const float2 st = P.stat[slot_of(p) * ROWS + r];
-    l = fmaf(st.y, ex2(st.x - base), l);
+  for (int p0 = 0; p0 < parts; p0 += kJoinParts) {
+    float2 st[kJoinParts];
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x)
+      st[x] = p0 + x < parts ? P.stat[slot_of(p0 + x) * ROWS + r] : make_float2(kNone, 0.f);
+    float top = mm;
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x) top = fmaxf(top, st[x].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    l *= ex2(mm - base);
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x) {
+      if (st[x].x != kNone) l = fmaf(st[x].y, ex2(st[x].x - base), l);
+      if (p0 + x < parts && (x & 3) == warp) s_f[p0 + x][lane] = st[x].x;
+    }
+    mm = top;
   }
+  __syncthreads();
+  const float base = mm == -INFINITY ? 0.f : mm;
+  const int x0 = 32 * blockIdx.z + 8 * warp;
+  float o[8];
+#pragma unroll
+  for (int y = 0; y < 8; ++y) o[y] = 0.f;
+  for (int p0 = 0; p0 < parts; p0 += kJoinParts) {
+    float u[kJoinParts][8], f[kJoinParts];
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x) {
+      f[x] = p0 + x < parts ? s_f[p0 + x][lane] : kNone;
+      const float *from = P.part + (slot_of(p0 + x < parts ? p0 + x : 0) * D + x0) * ROWS + r;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) u[x][y] = f[x] == kNone ? 0.f : from[y * ROWS];
+    }
+#pragma unroll
+    for (int x = 0; x < kJoinParts; ++x) {
+      const float g = ex2(f[x] - base);
+#pragma unroll
+      for (int y = 0; y < 8; ++y) o[y] = fmaf(u[x][y], g, o[y]);
+    }
+  }
+  if (r >= rows) return;
   const int i = (r0 + r) / P.G, g = r0 + r - i * P.G;
   const size_t row = (static_cast<size_t>(s.first) + i) * P.Hq + me.y * P.G + g;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-  for (int x = 8 * warp; x < D; x += 32) {
-    float o[8];
+  uint32_t w[4];
 #pragma unroll
-    for (int y = 0; y < 8; ++y) o[y] = 0.f;
-    for (int p = 0; p < me.w; ++p) {
-      const size_t slot = slot_of(p);
-      const float at = P.stat[slot * ROWS + r].x, f = ex2(at - base);
-      if (at == -INFINITY) continue;  // (a part without a step has no sums)
-#pragma unroll
-      for (int y = 0; y < 8; ++y) o[y] = fmaf(P.part[(slot * D + x + y) * ROWS + r], f, o[y]);
-    }
-    if (r < rows) {
-      uint32_t w[4];
-#pragma unroll
-      for (int z = 0; z < 4; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
-      *reinterpret_cast<uint4 *>(P.out + row * D + x) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  if (P.lse && warp == 0 && r < rows) P.lse[row] = l == 0.f ? -INFINITY : (mm + log2f(l)) * kLn2;
+  for (int z = 0; z < 4; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+  *reinterpret_cast<uint4 *>(P.out + row * D + x0) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (P.lse && x0 == 0) P.lse[row] = l == 0.f ? -INFINITY : (mm + log2f(l)) * kLn2;
 }
 
 namespace {
@@ -1464,12 +1488,11 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   P.entries = entries_of(S::ROWS, P.B, P.rows, P.G);
   P.per_head = static_cast<uint32_t>(((1ULL << 32) + P.G - 1) / P.G);
   // No more items than SMs: a block each, or several where a sequence may be long; no plan, and mostly no joint.
-  const long long most = (static_cast<long long>(P.max_new) * P.G + S::ROWS - 1) / S::ROWS;
-  const long long items = min(static_cast<long long>(P.entries), P.B * most) * P.heads;
+  const long long items = static_cast<long long>(P.entries) * P.heads;
   P.parts = 0;
   if (items <= P.blocks) {
     const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
-    const long long seen = P.window > 0 ? min(visible, static_cast<long long>(P.window) + P.sinks + P.max_new) : visible;
+    const long long seen = P.window > 0 ? min(visible, static_cast<long long>(P.window) + P.sinks + S::ROWS / P.G) : visible;
     P.parts = static_cast<int>(max(1LL, min(P.blocks / items, seen / (kPartTiles * S::TN))));
   }
   if (!P.parts && launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
@@ -1477,7 +1500,7 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   if (launch_pdl(attn_extend_kernel<D, E4M3>, dim3(blocks), dim3(kAxThreads), S::SMEM, st, P, kmap, vmap) != cudaSuccess)
     return -1;
   if (P.parts == 1) return 0;
-  return launch_pdl(attn_extend_join_kernel<D, S::ROWS>, dim3(P.parts ? items : blocks, S::ROWS / 32), dim3(128), 0, st, P) ==
+  return launch_pdl(attn_extend_join_kernel<D, S::ROWS>, dim3(P.parts ? items : blocks, S::ROWS / 32, D / 32), dim3(128), 0, st, P) ==
                  cudaSuccess
              ? 0
              : -1;
