@@ -227,6 +227,7 @@ struct AdParams {
   int rows, sinks, max_new;
   const uint64_t *masks;   // of drafted tokens, or null: each sees those before it
   int words;
+  int entries;             // (kRows) items of one head that all sequences' rows make up at most; 0: blocks go by sequence
   int cols;                // most columns that a key-value head has in a sequence (G without kRows)
   float scale;
   uint16_t *out;
@@ -561,6 +562,32 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
     const int item = block - cur.b * items;
     cur.head = item / P.groups;
     cur.group = item - cur.head * P.groups;
+    if (kRows && P.entries) {  // blocks for as many items as the rows can make up, not for the most of each sequence
+      if (blockIdx.x == 0)  // (of sequences without an item too)
+        for (int b = tid; b < P.B; b += THREADS) seen_of<RUN>(P, b, true);
+      const int e = block / P.heads;
+      cur.head = block - e * P.heads;
+      int before = 0;
+      cur.b = -1;
+      for (int b0 = 0; b0 < P.B && cur.b < 0; b0 += 32) {
+        int mine = 0;
+        if (b0 + lane < P.B) mine = (seen_of<RUN>(P, b0 + lane, false).m * P.G + NQ - 1) / NQ;
+        int upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+          if (lane >= off) upto += o;
+        }
+        const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + upto > e);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          cur.group = e - before - __shfl_sync(0xFFFFFFFFu, upto - mine, at);
+          cur.b = b0 + at;
+        }
+        before += __shfl_sync(0xFFFFFFFFu, upto, 31);
+      }
+      if (cur.b < 0) return;
+    }
     cur.set(seen_of<RUN>(P, cur.b, tid == 0));
     cur.begin = 0;
     cur.more = true;
@@ -1041,7 +1068,8 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
               vw[j][0] = u.x, vw[j][1] = u.y, vw[j][2] = vw[j][3] = 0u;
             }
           }
-          if (kRows && !whole && (cur.m > 1 || P.masks)) {
+          if (kRows && (!E4M3 || (!whole && (cur.m > 1 || P.masks)))) {  // (bf16 weights are two numbers: the second may be
+                                                                         // negative, and an infinity times both is NaN)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -1422,8 +1450,16 @@ int clusters_at_once(const AdParams &P, int parts) {
   }));
 }
 
+// (Long batches go by sequence: a block would read all of their offsets.)
+int entries_of(const AdParams &P, int NQ) {
+  const long long n = static_cast<long long>(P.rows) * P.G / NQ + P.B;
+  return P.B <= 256 && n < static_cast<long long>(P.B) * P.groups ? static_cast<int>(n) : 0;
+}
+
 // Items of at most 8 NT query heads, and the most tokens that one can see.
-long long items_of(const AdParams &P) { return static_cast<long long>(P.B) * P.heads * P.groups; }
+long long items_of(const AdParams &P) {
+  return P.entries ? static_cast<long long>(P.entries) * P.heads : static_cast<long long>(P.B) * P.heads * P.groups;
+}
 long long tokens_of(const AdParams &P) {
   const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
   const long long seen = static_cast<long long>(P.window) + (kSinks ? static_cast<long long>(P.sinks) + P.max_new - 1 : 0);
@@ -1460,6 +1496,7 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
   if constexpr (NT == 2) {
     AdParams Q = P;
     Q.groups = (P.cols + 7) / 8;
+    if (kRows) Q.entries = entries_of(Q, 8);
     const int split = few_parts<D, E4M3, 1>(Q);
     if (split && (split >= parts || tokens <= kDirectTokens)) return launch_few<D, E4M3, 1>(Q, split, st);
     if (tokens <= (parts ? kSplitTokens : kDirectTokens) &&
@@ -1525,8 +1562,9 @@ int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q
 #if K3_AD_SINKS
   P.offsets = a.offsets, P.rows = a.rows, P.sinks = a.sinks, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
   P.cols = a.max_new * P.G;
+  P.entries = kRows ? entries_of(P, 8 * p.NT) : 0;
 #else
-  P.offsets = nullptr, P.masks = nullptr, P.rows = P.sinks = P.max_new = P.words = 0;
+  P.offsets = nullptr, P.masks = nullptr, P.rows = P.sinks = P.max_new = P.words = P.entries = 0;
   P.cols = P.G;
 #endif
   uint8_t *w = static_cast<uint8_t *>(ws);

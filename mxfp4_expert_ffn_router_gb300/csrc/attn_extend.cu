@@ -179,12 +179,12 @@ __device__ __forceinline__ bool is_page(const AxParams &P, int page) {
 // The e-th of the items that all sequences' rows of one head make up, by a whole warp: its sequence (-1: there are fewer),
 // and which of that one's it is.
 template <int ROWS>
-__device__ __forceinline__ int sequence_of(const AxParams &P, int e, int &t, bool report) {
+__device__ __forceinline__ int sequence_of(const AxParams &P, int e, int &t) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int b0 = 0; b0 < P.B; b0 += 32) {
     int mine = 0;
-    if (b0 + lane < P.B) mine = static_cast<int>((static_cast<long long>(seq_of(P, b0 + lane, report).m) * P.G + ROWS - 1) / ROWS);
+    if (b0 + lane < P.B) mine = static_cast<int>((static_cast<long long>(seq_of(P, b0 + lane, false).m) * P.G + ROWS - 1) / ROWS);
     int upto = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -267,7 +267,9 @@ struct Walk {
   __device__ __forceinline__ void direct(const AxParams &P, int block) {
     const int item = block / P.parts, part = block - item * P.parts, e = item / P.heads;
     head = item - e * P.heads;
-    b = sequence_of<ROWS>(P, e, t, block == 0);
+    if (block == 0)
+      for (int x = threadIdx.x & 31; x < P.B; x += 32) seq_of(P, x, true);
+    b = sequence_of<ROWS>(P, e, t);
     more = b >= 0;
     if (!more) return;
     s = seq_of(P, b, false);
@@ -1343,7 +1345,7 @@ __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P)
   if (P.parts) {
     const int e = blockIdx.x / P.heads;
     int t = 0;
-    const int b = sequence_of<ROWS>(P, e, t, false);
+    const int b = sequence_of<ROWS>(P, e, t);
     me = make_int4(b, blockIdx.x - e * P.heads, t, b < 0 ? 0 : P.parts);
   } else {
     me = P.meta[blockIdx.x];
@@ -1491,9 +1493,12 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   const long long items = static_cast<long long>(P.entries) * P.heads;
   P.parts = 0;
   if (items <= P.blocks) {
+    // (not where the bound of the items would leave SMs idle for long: a plan shares those evenly)
     const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
     const long long seen = P.window > 0 ? min(visible, static_cast<long long>(P.window) + P.sinks + S::ROWS / P.G) : visible;
     P.parts = static_cast<int>(max(1LL, min(P.blocks / items, seen / (kPartTiles * S::TN))));
+    const long long real = P.heads * max(static_cast<long long>(P.B), (static_cast<long long>(P.rows) * P.G + S::ROWS - 1) / S::ROWS);
+    if (seen > 12LL * S::TN * P.parts && real * P.parts * 20 < 17LL * P.blocks) P.parts = 0;
   }
   if (!P.parts && launch_pdl(attn_plan_kernel<S::TN, S::ROWS>, dim3(1), dim3(1024), 0, st, P) != cudaSuccess) return -1;
   const int blocks = P.parts ? static_cast<int>(items) * P.parts : P.blocks;
@@ -1509,10 +1514,23 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
 }  // namespace
 
 namespace {
-// Whether the kernels of few columns are the faster ones.
+// Whether the kernels of few columns (attn_rows.cu) are the faster ones.  They read a sequence's keys and values once for
+// each 16 rows of a head, with little to start and end; those of tiles once for 256 (128 at dim 256), but take 9 to 25 us
+// whatever the work.  So: where a sequence has about 16 rows a head at most; and as long as each 16 rows have an SM, and
+// read little in all.  Measured where the two meet (128 wide, 8 query heads a key):
+//   16 items, E4M3   30000 tokens  37 and 50 us        128 items, E4M3   1000 tokens  19 and 27 us
+//   32                6000         22     34                             6000         55     42
+//                    30000         62     52             128, bf16       100           8     16
+//   64                6000         36     36                             1000         26     21
 bool few_columns(const ExtendArgs &a) {
-  const int G = a.Hq / a.c.heads;
-  return static_cast<long long>(a.max_new) * G <= 32;
+  const k3moe_kv_cache &c = a.c;
+  const long long columns = static_cast<long long>(a.rows) * (a.Hq / c.heads);
+  const long long items = c.heads * max(static_cast<long long>(a.B), (columns + 15) / 16);
+  const long long places = static_cast<long long>(a.max_pages) * c.page_size;
+  const long long seen = a.window > 0 ? min(places, static_cast<long long>(a.window) + a.sinks + a.max_new) : places;
+  const bool e = c.format == K3MOE_KV_E4M3;
+  const double bytes = static_cast<double>(items) * seen * 2 * c.dim * (e ? 1 : 2);
+  return columns <= 16LL * a.B || (items <= sm_count() && bytes <= (e ? 64e6 : 38e6) * (1 + 48.0 / items));
 }
 }  // namespace
 
