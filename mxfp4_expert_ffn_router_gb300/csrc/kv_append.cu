@@ -78,75 +78,85 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(const ApParams P)
   const int half = P.pairs / 8;  // words of a half
   const bool turn = sub < half;
   const int wa = turn && !P.neighbours ? sub : 2 * sub, wb = turn && !P.neighbours ? sub + half : 2 * sub + 1;
-  // (a group's lanes stay together: all of a vector's, or none)
-  for (int base = 0; base < TOKENS * nv; base += G) {
-    const int it = base + tid / L, tt = it / nv, vec = v0 + it - tt * nv, t = t0 + tt;
-    const int slot = it < TOKENS * nv ? s_slot[tt] : -1;
-    const bool on = slot >= 0, is_q = vec < P.Hq, is_v = vec >= P.Hq + P.heads;
-    const int head = is_q ? vec : is_v ? vec - P.Hq - P.heads : vec - P.Hq;
-    float f[16];
-    if (on) {
-      const uint16_t *src = (is_q ? P.q_in + t * P.q_stride : is_v ? P.v_in + t * P.v_stride : P.k_in + t * P.k_stride) +
-                            static_cast<size_t>(head) * D;
-      const uint4 a = reinterpret_cast<const uint4 *>(src)[wa], b = reinterpret_cast<const uint4 *>(src)[wb];
-      const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  // (a group's lanes stay together: all of a vector's, or none.)  Two vectors a turn, loaded before the first is used
+  constexpr int U = 2;
+  for (int base = 0; base < TOKENS * nv; base += U * G) {
+    uint4 in[U][2];
+    int slot[U], tt[U], vec[U];
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int it = base + x * G + tid / L;
+      tt[x] = it / nv, vec[x] = v0 + it - tt[x] * nv;
+      slot[x] = it < TOKENS * nv ? s_slot[tt[x]] : -1;
+      in[x][0] = in[x][1] = make_uint4(0, 0, 0, 0);
+      if (slot[x] >= 0) {
+        const int t = t0 + tt[x], k = vec[x] - P.Hq, v = k - P.heads;  // (k, v: of keys, of values)
+        const uint16_t *src = k < 0 ? P.q_in + t * P.q_stride + static_cast<size_t>(vec[x]) * D
+                              : v < 0 ? P.k_in + t * P.k_stride + static_cast<size_t>(k) * D
+                                      : P.v_in + t * P.v_stride + static_cast<size_t>(v) * D;
+        in[x][0] = reinterpret_cast<const uint4 *>(src)[wa], in[x][1] = reinterpret_cast<const uint4 *>(src)[wb];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const bool on = slot[x] >= 0, is_q = vec[x] < P.Hq, is_v = vec[x] >= P.Hq + P.heads;
+      const int t = t0 + tt[x], head = is_q ? vec[x] : is_v ? vec[x] - P.Hq - P.heads : vec[x] - P.Hq;
+      const uint32_t w[8] = {in[x][0].x, in[x][0].y, in[x][0].z, in[x][0].w, in[x][1].x, in[x][1].y, in[x][1].z, in[x][1].w};
+      float f[16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         f[2 * i] = __uint_as_float(w[i] << 16);
         f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       }
-      if (turn && !is_v) {
-        const float4 *cs = reinterpret_cast<const float4 *>(&s_cs[tt][8 * sub]);
+      if (on && turn && !is_v) {
+        const float4 *cs = reinterpret_cast<const float4 *>(&s_cs[tt[x]][8 * sub]);
         if (P.neighbours) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 c = cs[i];
-            const float x = f[4 * i], y = f[4 * i + 1], z = f[4 * i + 2], u = f[4 * i + 3];
-            f[4 * i] = x * c.x - y * c.y, f[4 * i + 1] = y * c.x + x * c.y;
+            const float a = f[4 * i], y = f[4 * i + 1], z = f[4 * i + 2], u = f[4 * i + 3];
+            f[4 * i] = a * c.x - y * c.y, f[4 * i + 1] = y * c.x + a * c.y;
             f[4 * i + 2] = z * c.z - u * c.w, f[4 * i + 3] = u * c.z + z * c.w;
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 c = cs[i];
-            const float x = f[2 * i], y = f[2 * i + 8], z = f[2 * i + 1], u = f[2 * i + 9];
-            f[2 * i] = x * c.x - y * c.y, f[2 * i + 8] = y * c.x + x * c.y;
+            const float a = f[2 * i], y = f[2 * i + 8], z = f[2 * i + 1], u = f[2 * i + 9];
+            f[2 * i] = a * c.x - y * c.y, f[2 * i + 8] = y * c.x + a * c.y;
             f[2 * i + 1] = z * c.z - u * c.w, f[2 * i + 9] = u * c.z + z * c.w;
           }
         }
       }
-    } else {
+      uint32_t byte = 0;
+      if constexpr (E4M3) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = 0.f;
-    }
-    uint32_t byte = 0;
-    if constexpr (E4M3) {
-      uint32_t m = 0;
+        for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+        for (int off = 1; off < L; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+        byte = mx8_scale_byte(m);
+      }
+      if (!on) continue;
+      const size_t at = ((static_cast<size_t>(slot[x] >> P.page_shift) * P.heads + head) << P.page_shift) +
+                        (slot[x] & ((1 << P.page_shift) - 1));
+      if (E4M3 && !is_q) {
+        float lo[8], hi[8];
 #pragma unroll
-      for (int off = 1; off < L; off <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-      byte = mx8_scale_byte(m);
-    }
-    if (!on) continue;
-    const size_t at = (((static_cast<size_t>(slot >> P.page_shift) * P.heads + head) << P.page_shift) +
-                       (slot & ((1 << P.page_shift) - 1)));
-    if (E4M3 && !is_q) {
-      float lo[8], hi[8];
+        for (int i = 0; i < 8; ++i) lo[i] = f[i], hi[i] = f[8 + i];
+        uint2 *dst = reinterpret_cast<uint2 *>((is_v ? P.v : P.k) + at * D);
+        dst[wa] = mx8_codes(lo, byte);
+        dst[wb] = mx8_codes(hi, byte);
+        if (sub == 0) (is_v ? P.vs : P.ks)[at] = static_cast<uint8_t>(byte);
+      } else {
+        uint32_t r[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) lo[i] = f[i], hi[i] = f[8 + i];
-      uint2 *dst = reinterpret_cast<uint2 *>((is_v ? P.v : P.k) + at * D);
-      dst[wa] = mx8_codes(lo, byte);
-      dst[wb] = mx8_codes(hi, byte);
-      if (sub == 0) (is_v ? P.vs : P.ks)[at] = static_cast<uint8_t>(byte);
-    } else {
-      uint32_t r[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = bf16x2(f[2 * i], f[2 * i + 1]);
-      uint4 *dst = is_q ? reinterpret_cast<uint4 *>(P.q_out + t * P.q_out_stride + static_cast<size_t>(head) * D)
-                        : reinterpret_cast<uint4 *>((is_v ? P.v : P.k) + at * (2 * D));
-      dst[wa] = make_uint4(r[0], r[1], r[2], r[3]);
-      dst[wb] = make_uint4(r[4], r[5], r[6], r[7]);
+        for (int i = 0; i < 8; ++i) r[i] = bf16x2(f[2 * i], f[2 * i + 1]);
+        uint4 *dst = is_q ? reinterpret_cast<uint4 *>(P.q_out + t * P.q_out_stride + static_cast<size_t>(head) * D)
+                          : reinterpret_cast<uint4 *>((is_v ? P.v : P.k) + at * (2 * D));
+        dst[wa] = make_uint4(r[0], r[1], r[2], r[3]);
+        dst[wb] = make_uint4(r[4], r[5], r[6], r[7]);
+      }
     }
   }
 }
