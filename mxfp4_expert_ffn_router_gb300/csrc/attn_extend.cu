@@ -12,7 +12,7 @@ namespace k3moe {
 
 namespace {
 
-constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 and 10 products, 9 loads, 12-15 values
+constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 and 10 products, 9 loads, 11 the keys' scales, 12-15 values
 constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
 constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
 constexpr int kPartTiles = 2;      // (direct) fewest tiles that a part of the longest item may have
@@ -1248,45 +1248,32 @@ __global__ void __launch_bounds__(kAxThreads, 1)
           const uint8_t *from = raw + (ch * 16 / BOX) * (TN * BOX) + (ch * 16) % BOX;
           uint8_t *to = op + blk * (TN * 128);
           const int c0 = 2 * (lane & 3);
-          constexpr int U = 4;  // loads in flight (one after the other, a tile took 1400 clocks alone; so 860)
-          uint32_t rare = 0;
-#pragma unroll 1
-          for (int r0 = w * RW + rr0; r0 < TN; r0 += 4 * RW * U) {
-            uint4 in[U];
-            uint32_t byte[U];
+#pragma unroll 2
+          for (int rr = w * RW + rr0; rr < TN; rr += 4 * RW) {
+            const uint4 in = *reinterpret_cast<const uint4 *>(from + rr * BOX);
+            const uint32_t byte = scales[rr];
+            const uint32_t cw[4] = {in.x, in.y, in.z, in.w};
+            uint32_t hv[8];
+            // 2^(byte - 127 + 120), or as much of it as bf16 holds
+            const uint32_t f = (byte <= 134u ? (byte + 120u) << 7 : byte == 255u ? 0x7FC0u : 0x7F00u) * 0x10001u;
+            uint32_t rare = byte > 134u ? 0x80808080u : 0u;
 #pragma unroll
-            for (int x = 0; x < U; ++x) {
-              in[x] = *reinterpret_cast<const uint4 *>(from + (r0 + 4 * RW * x) * BOX);
-              byte[x] = scales[r0 + 4 * RW * x];
+            for (int y = 0; y < 4; ++y) {
+              rare |= (cw[y] & 0x7F7F7F7Fu) + 0x01010101u;  // (a NaN's code)
+              hv[2 * y] = mul_bf16x2(codes_up(cw[y], 0x1404), f);
+              hv[2 * y + 1] = mul_bf16x2(codes_up(cw[y], 0x3424), f);
             }
-#pragma unroll
-            for (int x = 0; x < U; ++x) {
-              const int rr = r0 + 4 * RW * x;
-              const uint32_t cw[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-              uint32_t hv[8];
-              const uint32_t f = ((byte[x] + 120u) << 7) * 0x10001u;  // 2^(byte - 127 + 120)
-              if (byte[x] > 134u) rare = 0x80808080u;                 // (past bf16's numbers)
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                rare |= (cw[y] & 0x7F7F7F7Fu) + 0x01010101u;  // (a NaN's code)
-                hv[2 * y] = mul_bf16x2(codes_up(cw[y], 0x1404), f);
-                hv[2 * y + 1] = mul_bf16x2(codes_up(cw[y], 0x3424), f);
-              }
-              uint8_t *row = to + rr * 128;
-              *reinterpret_cast<uint4 *>(row + ((c0 ^ (rr & 7)) << 4)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-              *reinterpret_cast<uint4 *>(row + (((c0 + 1) ^ (rr & 7)) << 4)) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
-            }
-          }
-          if (rare & 0x80808080u) {  // once more, code by code
-#pragma unroll 1
-            for (int rr = w * RW + rr0; rr < TN; rr += 4 * RW) {
-              const float x = e8m0_to_f32(scales[rr]);
-              uint8_t *row = to + rr * 128;
+            uint8_t *row = to + rr * 128;
+            const uint32_t a0 = (c0 ^ (rr & 7)) << 4, a1 = ((c0 + 1) ^ (rr & 7)) << 4;
+            *reinterpret_cast<uint4 *>(row + a0) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4 *>(row + a1) = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            if (rare & 0x80808080u) {  // code by code
+              const float x = e8m0_to_f32(byte);
 #pragma unroll 1
               for (int y = 0; y < 16; ++y) {
                 uint32_t a, z;
                 e4m3x4_to_f16x2(from[rr * BOX + y], a, z);
-                reinterpret_cast<uint16_t *>(row + (((c0 + (y >> 3)) ^ (rr & 7)) << 4))[y & 7] =
+                reinterpret_cast<uint16_t *>(row + (y < 8 ? a0 : a1))[y & 7] =
                     static_cast<uint16_t>(bf16x2(__half2float(__ushort_as_half(static_cast<unsigned short>(a))) * x, 0.f));
               }
             }
