@@ -534,6 +534,12 @@ def k3moe_attn_decode(cache: KVCache, q, block_table, seq_lens, out, lse=None, s
         _check("k3moe_attn_decode", rc)
 
 
+def _turns(inv_freq):
+    """Angles as turns of 2^-64 modulo 2^64, in signed numbers of 64 bits."""
+    turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
+    return [t - 2 ** 64 if t >> 63 else t for t in turns]
+
+
 class Rotation:
     """The rotation of positions for k3moe_kv_append: the first ``dim`` dimensions of a head's vector (a
     multiple of 16) are pairs (i, i + dim/2), or (2i, 2i + 1) with ``neighbours``; at position p pair i
@@ -550,10 +556,8 @@ class Rotation:
             raise ValueError(f"inv_freq: expected {dim // 2} numbers, got {len(inv_freq)}")
         if not all(math.isfinite(f) for f in inv_freq):
             raise ValueError("inv_freq: must be finite")
-        # turns of 2^-64 modulo 2^64, as signed numbers
-        turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in inv_freq]
         self.dim, self.neighbours, self.scale = int(dim), bool(neighbours), float(scale)
-        self.turns = torch.tensor([t - 2 ** 64 if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+        self.turns = torch.tensor(_turns(inv_freq), dtype=torch.int64, device=device)
         self._c = _RotationC(self.dim, int(self.neighbours), self.scale, _ptr(self.turns, torch.int64, "turns"))
         self._ref, self._addr = ctypes.byref(self._c), ctypes.addressof(self._c)
 

@@ -8,14 +8,20 @@ key-value cache, then the MoE half, for a batch of sequences with one new token 
     a = a + o Wo;  h = norm(a)                            torch.matmul, k3moe_rmsnorm
     x' = sum over the routed experts of h                 k3moe_router, _bucket, _expert_ffn, _combine
 
-``step`` returns (x', a): the next layer's norm adds them.  (The pages' engine has 96 attention
+``extend`` takes several new tokens of a sequence at once: a prompt's chunk, or a tree of drafted tokens to be
+verified (``tree_masks``; ``accept`` keeps the ones that hold).  There, and wherever the layer has a rotation or sinks:
+
+    cache[slots] = rotated k, v; q = rotated q            k3moe_kv_append
+    o = attention of the new tokens over the cache        k3moe_attn_extend, k3moe_attn_tree
+
+``step`` and ``extend`` return (x', a): the next layer's norm adds them.  (The pages' engine has 96 attention
 heads: "kimi-k3-in-c" overview, pomoai.com; every size is an argument here.)  Nothing in a step synchronises the host or
 allocates, so a step can be captured in a CUDA graph: tables, lengths and slots are read on the device.  What makes room
 for the new tokens does: ``PageTable`` keeps its lists on the host and copies the whole table for every ``append`` (1.0 ms for
 64 sequences of up to 256 pages, 7.0 ms for 2048).  The attention chooses its way by the table's width, so a table
 much wider than the sequences costs short ones 4 us a layer.
 
-``python -m mxfp4_expert_ffn_router_gb300.decoder`` decodes a few tokens with random weights.
+``python -m mxfp4_expert_ffn_router_gb300.decoder`` decodes a few tokens with random weights, then verifies drafted ones.
 """
 from __future__ import annotations
 
@@ -23,9 +29,10 @@ from collections import Counter
 
 import torch
 
-from . import (K3MOE_FFN_AUTO, K3MOE_KV_E4M3, K3MOE_OP_BUCKET, K3MOE_OP_EXPERT_FFN, KVCache, Shape, Weights,
-               k3moe_attn_decode, k3moe_attn_decode_workspace_bytes, k3moe_bucket, k3moe_combine, k3moe_expert_ffn,
-               k3moe_kv_read, k3moe_kv_write, k3moe_rmsnorm, k3moe_router, k3moe_workspace_bytes)
+from . import (K3MOE_FFN_AUTO, K3MOE_KV_E4M3, K3MOE_OP_BUCKET, K3MOE_OP_EXPERT_FFN, KVCache, Rotation, Shape, Weights,
+               k3moe_attn_decode, k3moe_attn_decode_workspace_bytes, k3moe_attn_extend, k3moe_attn_extend_workspace_bytes,
+               k3moe_attn_tree, k3moe_bucket, k3moe_combine, k3moe_expert_ffn, k3moe_kv_append, k3moe_kv_read,
+               k3moe_kv_write, k3moe_rmsnorm, k3moe_router, k3moe_workspace_bytes)
 
 
 class PageTable:
@@ -71,6 +78,21 @@ class PageTable:
         self.owned[b], self.lens[b] = [], 0
         self._upload()
 
+    def truncate(self, b: int, count: int):
+        """Forget the last ``count`` tokens of sequence b; pages that held only those come back."""
+        if not 0 <= count <= self.lens[b]:
+            raise ValueError(f"sequence {b} has {self.lens[b]} tokens, not {count} to forget")
+        self.lens[b] -= count
+        left = -(-self.lens[b] // self.page_size)
+        self.free += reversed(self.owned[b][left:])
+        del self.owned[b][left:]
+        self._upload()
+
+    def positions_of(self, which, count: int = 1) -> torch.Tensor:
+        """Positions of the last ``count`` tokens of each sequence in ``which`` (int32), in the order of append's slots."""
+        at = [self.lens[b] - count + i for b in which for i in range(count)]
+        return torch.tensor(at, dtype=torch.int32, device=self.table.device)
+
     def slots_of(self, b: int) -> torch.Tensor:
         """The slots of all of sequence b's tokens, for k3moe_kv_read."""
         s = [self.owned[b][i // self.page_size] * self.page_size + i % self.page_size for i in range(self.lens[b])]
@@ -82,13 +104,52 @@ class PageTable:
         self.seq_lens.copy_(torch.tensor(self.lens, dtype=torch.int32))
 
 
+def tree_masks(parents, device="cuda"):
+    """Drafted trees as k3moe_attn_tree takes them.  ``parents``: for each sequence the parents of its drafted tokens, each
+    an earlier one's index, or -1 for one that follows the sequence's last token.  Returns the masks int64 [rows, words] (a
+    token sees its ancestors and itself), the q_offsets int32 [B + 1], and each row's depth (0: follows the last token),
+    which is its position behind the context."""
+    rows, depths, offsets = [], [], [0]
+    for tree in parents:
+        first = len(rows)
+        for i, p in enumerate(tree):
+            if not -1 <= p < i:
+                raise ValueError(f"the parent of drafted token {i} must be an earlier one or -1, not {p}")
+            rows.append((rows[first + p] if p >= 0 else 0) | 1 << i)
+            depths.append(depths[first + p] + 1 if p >= 0 else 0)
+        offsets.append(len(rows))
+    words = max(1, -(-max((len(t) for t in parents), default=0) // 64))
+    parts = [[(r >> 64 * w) & (2 ** 64 - 1) for w in range(words)] for r in rows]
+    signed = [[x - 2 ** 64 if x >> 63 else x for x in row] for row in parts]
+    return (torch.tensor(signed, dtype=torch.int64, device=device).view(len(rows), words),
+            torch.tensor(offsets, dtype=torch.int32, device=device), depths)
+
+
+def accept(cache: KVCache, pages: PageTable, b: int, count: int, kept, status=None):
+    """Of sequence b's last ``count`` tokens, drafted ones, keep those at the ascending indices ``kept`` (a path of the
+    tree, whose positions follow one another): their cached vectors move up to the first places, and the rest is
+    forgotten.  Reading an E4M3 vector back and writing it again gives the same values."""
+    kept = list(kept)
+    if kept != sorted(set(kept)) or (kept and not 0 <= kept[0] <= kept[-1] < count):
+        raise ValueError(f"kept: ascending indices below {count}, not {kept}")
+    if kept != list(range(len(kept))):
+        slots = pages.slots_of(b)[pages.lens[b] - count:]
+        kv = [torch.empty(len(kept), cache.heads, cache.dim, dtype=torch.bfloat16, device=slots.device) for _ in range(2)]
+        k3moe_kv_read(cache, slots[torch.tensor(kept, device=slots.device)], *kv, status)
+        k3moe_kv_write(cache, *kv, slots[:len(kept)].contiguous(), status)
+    pages.truncate(b, count - len(kept))
+
+
 class DecoderLayer:
     """Weights (bf16 but for the MXFP4 experts): wqkv [(Hq + 2 heads) dim, H], wo [H, Hq dim],
-    w_router [E, H], norm1 and norm2 [H].  ``shape``: T (the batch), H, I, E, k."""
+    w_router [E, H], norm1 and norm2 [H].  ``shape``: T (the rows: a batch, or all of its
+    new tokens), H, I, E, k.  ``rotation``: of the positions; ``sinks``: first tokens that stay visible beside a window."""
 
     def __init__(self, shape, cache: KVCache, q_heads: int, wqkv, wo, w_router, norm1, norm2, experts: Weights,
-                 eps: float = 1e-6, window: int = 0, mode: int = K3MOE_FFN_AUTO):
+                 eps: float = 1e-6, window: int = 0, mode: int = K3MOE_FFN_AUTO, rotation: Rotation | None = None,
+                 sinks: int = 0):
         s = self.s = Shape.of(shape)
+        self.rotation, self.sinks = rotation, sinks
         self.cache, self.q_heads, self.eps, self.window, self.mode = cache, q_heads, eps, window, mode
         self.wqkv, self.wo, self.w_router, self.norm1, self.norm2, self.experts = wqkv, wo, w_router, norm1, norm2, experts
         dev, bf, f32, i32, u8 = wqkv.device, torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -100,22 +161,46 @@ class DecoderLayer:
         self.status = torch.zeros(1, dtype=i32, device=dev)
         self.h, self.a, self.a2, self.o = (new(bf, s.T, s.H) for _ in range(4))
         self.qkv = new(bf, s.T, q_heads + 2 * cache.heads, cache.dim)
-        self.att, self.lse = new(bf, s.T, q_heads, cache.dim), new(f32, s.T, q_heads)
+        self.att, self.lse = new(bf, s.T, q_heads, cache.dim).zero_(), new(f32, s.T, q_heads)  # (rows of no token keep theirs)
         self.ws_attn = new(u8, k3moe_attn_decode_workspace_bytes(cache, s.T, q_heads))
+        self.ws_extend = None  # (of the largest batch that extend has seen)
+        self.one_each = torch.arange(s.T + 1, dtype=i32, device=dev)
         self.logits, self.idx, self.w = new(f32, s.T, s.E), new(i32, s.T, s.k), new(f32, s.T, s.k)
         self.counts, self.offsets, self.perm, self.inv = new(i32, s.E), new(i32, s.E + 1), new(i32, A), new(i32, A)
         self.ws_bucket = new(u8, max(1, k3moe_workspace_bytes(s, K3MOE_OP_BUCKET)))
         self.ws_ffn = new(u8, max(1, k3moe_workspace_bytes(s, K3MOE_OP_EXPERT_FFN, mode)))
         self.Y, self.out = new(f32, A, s.H), new(bf, s.T, s.H)
 
-    def attention(self, x, residual, block_table, seq_lens, slots):
-        """The attention half: (o Wo, a) of the new tokens x [T, H] (residual may be None)."""
+    def attention(self, x, residual, block_table, seq_lens, slots, positions=None, q_offsets=None, masks=None,
+                  max_new=None):
+        """The attention half: (o Wo, a) of the new tokens x [T, H] (residual may be None); with q_offsets several of a
+        sequence, as in ``extend``."""
         hq, hk = self.q_heads, self.cache.heads
+        if (self.rotation is None) != (positions is None):
+            raise ValueError("positions belong to a layer with a rotation, and to each of its calls")
+        if q_offsets is None and self.sinks:
+            q_offsets, max_new = self.one_each, 1
+        if masks is not None and q_offsets is None:
+            raise ValueError("masks: drafted tokens need q_offsets")
         k3moe_rmsnorm(x, self.norm1, self.eps, residual=residual, residual_out=self.a, y=self.h)
         torch.matmul(self.h, self.wqkv.t(), out=self.qkv.view(self.s.T, -1))
-        k3moe_kv_write(self.cache, self.qkv[:, hq:hq + hk], self.qkv[:, hq + hk:], slots, self.status)
-        k3moe_attn_decode(self.cache, self.qkv[:, :hq], block_table, seq_lens, self.att, lse=self.lse,
-                          window=self.window, ws=self.ws_attn, dev_status=self.status)
+        q, k, v = self.qkv[:, :hq], self.qkv[:, hq:hq + hk], self.qkv[:, hq + hk:]
+        if self.rotation is None:
+            k3moe_kv_write(self.cache, k, v, slots, self.status)
+        else:
+            k3moe_kv_append(self.cache, k, v, slots, positions, self.rotation, q=q, q_out=q, dev_status=self.status)
+        if q_offsets is None:
+            k3moe_attn_decode(self.cache, q, block_table, seq_lens, self.att, lse=self.lse, window=self.window,
+                              ws=self.ws_attn, dev_status=self.status)
+        else:
+            need = k3moe_attn_extend_workspace_bytes(self.cache, len(seq_lens), self.s.T, hq)
+            if self.ws_extend is None or self.ws_extend.numel() < need:
+                self.ws_extend = torch.empty(need, dtype=torch.uint8, device=x.device)
+            rest = dict(lse=self.lse, window=self.window, sinks=self.sinks, ws=self.ws_extend, dev_status=self.status)
+            if masks is None:
+                k3moe_attn_extend(self.cache, q, q_offsets, block_table, seq_lens, self.att, max_new=max_new, **rest)
+            else:
+                k3moe_attn_tree(self.cache, q, q_offsets, masks, block_table, seq_lens, self.att, **rest)
         torch.matmul(self.att.view(self.s.T, -1), self.wo.t(), out=self.o)
         return self.o, self.a
 
@@ -129,10 +214,18 @@ class DecoderLayer:
         k3moe_combine(s, self.Y, self.w, self.inv, self.out)
         return self.out, self.a2
 
-    def step(self, x, residual, block_table, seq_lens, slots):
+    def step(self, x, residual, block_table, seq_lens, slots, positions=None):
         """One new token of each sequence through the layer: (x', a).  seq_lens counts the new
-        tokens; slots (int32 [T]) are theirs, negative for an empty row of the batch."""
-        return self.moe(*self.attention(x, residual, block_table, seq_lens, slots))
+        tokens; slots (int32 [T]) are theirs, negative for an empty row of the batch (with sinks every row is a
+        token's); positions (int32 [T]) where the layer has a rotation."""
+        return self.moe(*self.attention(x, residual, block_table, seq_lens, slots, positions))
+
+    def extend(self, x, residual, block_table, seq_lens, slots, q_offsets, positions=None, masks=None, max_new=None):
+        """Several new tokens of each sequence through the layer: (x', a).  Rows q_offsets[b] .. q_offsets[b + 1] - 1
+        (int32 [B + 1]) of x [T, H] are sequence b's, which seq_lens counts; slots (int32 [T]) are theirs, negative for
+        rows of no sequence.  With masks (``tree_masks``) they are a drafted tree's.  The workspace is that of
+        the largest batch so far: a call that is captured comes after one like it."""
+        return self.moe(*self.attention(x, residual, block_table, seq_lens, slots, positions, q_offsets, masks, max_new))
 
 
 def main(tokens: int = 8):
@@ -151,9 +244,9 @@ def main(tokens: int = 8):
     experts = Weights.from_stacked(codes(E, 2 * I, H // 2), codes(E, 2 * I, H // 32, lo=119, hi=124),
                                    codes(E, H, I // 2), codes(E, H, I // 32, lo=119, hi=124))
     cache = KVCache.empty(32, hk, page, dim, K3MOE_KV_E4M3, dev)
-    layer = DecoderLayer(Shape(B, H, I, E, k), cache, hq, bf((hq + 2 * hk) * dim, H, scale=H ** -0.5),
-                         bf(H, hq * dim, scale=H ** -0.5), bf(E, H, scale=H ** -0.5), bf(H, scale=0.1) + 1,
-                         bf(H, scale=0.1) + 1, experts)
+    weights = (bf((hq + 2 * hk) * dim, H, scale=H ** -0.5), bf(H, hq * dim, scale=H ** -0.5), bf(E, H, scale=H ** -0.5),
+               bf(H, scale=0.1) + 1, bf(H, scale=0.1) + 1, experts)
+    layer = DecoderLayer(Shape(B, H, I, E, k), cache, hq, *weights)
     pages = PageTable(B, cache.pages, page, 8, dev)
     x, a = bf(B, H), None
     for t in range(tokens):
@@ -165,6 +258,16 @@ def main(tokens: int = 8):
     kv = [torch.empty(len(prefix), hk, dim, dtype=torch.bfloat16, device=dev) for _ in range(2)]
     k3moe_kv_read(cache, prefix, *kv, layer.status)
     print(f"read back {len(prefix)} tokens of sequence 0; device status {int(layer.status.item())}")
+    # drafted tokens of every sequence, verified in one call; of each tree one path is kept
+    tree, path = [-1, 0, 0, 1, 2], [0, 2, 4]
+    masks, offsets, depths = tree_masks([tree] * B, dev)
+    verify = DecoderLayer(Shape(B * len(tree), H, I, E, k), cache, hq, *weights)
+    slots = pages.append(range(B), len(tree))
+    x, a = verify.extend(bf(B * len(tree), H), None, pages.table, pages.seq_lens, slots, offsets, masks=masks)
+    for b in range(B):
+        accept(cache, pages, b, len(tree), path, verify.status)
+    print(f"verified {len(tree)} drafted tokens a sequence, kept {len(path)}; longest {max(pages.lens)}, "
+          f"device status {int(verify.status.item())}")
 
 
 if __name__ == "__main__":
