@@ -20,7 +20,7 @@ constexpr int kJoinParts = 4;      // parts that are added at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -3.4e38f;  // reference of a part without a step, which has no sums (those of a row are -inf, or far above)
-constexpr float kGrowth = 16.f;    // a row's reference moves once a weight would pass 2^16
+constexpr float kGrowth = 8.f;     // a row's reference moves once a weight would pass 2^8 (values up to 2^119 stay within fp32)
 
 struct AxStart {  // where a block's piece of the line begins
   long long begin;  // of the item that it begins in
