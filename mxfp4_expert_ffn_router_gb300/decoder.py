@@ -125,18 +125,23 @@ def tree_masks(parents, device="cuda"):
             torch.tensor(offsets, dtype=torch.int32, device=device), depths)
 
 
-def accept(cache: KVCache, pages: PageTable, b: int, count: int, kept, status=None):
+def accept(cache, pages: PageTable, b: int, count: int, kept, status=None):
     """Of sequence b's last ``count`` tokens, drafted ones, keep those at the ascending indices ``kept`` (a path of the
     tree, whose positions follow one another): their cached vectors move up to the first places, and the rest is
-    forgotten.  Reading an E4M3 vector back and writing it again gives the same values."""
-    kept = list(kept)
+    forgotten.  ``cache``: the KVCache, or those of all layers that the pages are shared by (a second call would forget
+    other tokens).  Reading an E4M3 vector back and writing it again gives the same values."""
+    caches, kept = [cache] if isinstance(cache, KVCache) else list(cache), list(kept)
+    if not 0 <= count <= pages.lens[b]:
+        raise ValueError(f"sequence {b} has {pages.lens[b]} tokens, not {count} drafted ones")
     if kept != sorted(set(kept)) or (kept and not 0 <= kept[0] <= kept[-1] < count):
         raise ValueError(f"kept: ascending indices below {count}, not {kept}")
     if kept != list(range(len(kept))):
         slots = pages.slots_of(b)[pages.lens[b] - count:]
-        kv = [torch.empty(len(kept), cache.heads, cache.dim, dtype=torch.bfloat16, device=slots.device) for _ in range(2)]
-        k3moe_kv_read(cache, slots[torch.tensor(kept, device=slots.device)], *kv, status)
-        k3moe_kv_write(cache, *kv, slots[:len(kept)].contiguous(), status)
+        come, go = slots[torch.tensor(kept, device=slots.device)], slots[:len(kept)].contiguous()
+        for c in caches:
+            kv = [torch.empty(len(kept), c.heads, c.dim, dtype=torch.bfloat16, device=slots.device) for _ in range(2)]
+            k3moe_kv_read(c, come, *kv, status)
+            k3moe_kv_write(c, *kv, go, status)
     pages.truncate(b, count - len(kept))
 
 
@@ -163,7 +168,7 @@ class DecoderLayer:
         self.qkv = new(bf, s.T, q_heads + 2 * cache.heads, cache.dim)
         self.att, self.lse = new(bf, s.T, q_heads, cache.dim).zero_(), new(f32, s.T, q_heads)  # (rows of no token keep theirs)
         self.ws_attn = new(u8, k3moe_attn_decode_workspace_bytes(cache, s.T, q_heads))
-        self.ws_extend = None  # (of the largest batch that extend has seen)
+        self.ws_extend = []  # (the last is in use; smaller ones stay, since captured calls may hold them)
         self.one_each = torch.arange(s.T + 1, dtype=i32, device=dev)
         self.logits, self.idx, self.w = new(f32, s.T, s.E), new(i32, s.T, s.k), new(f32, s.T, s.k)
         self.counts, self.offsets, self.perm, self.inv = new(i32, s.E), new(i32, s.E + 1), new(i32, A), new(i32, A)
@@ -194,9 +199,9 @@ class DecoderLayer:
                               ws=self.ws_attn, dev_status=self.status)
         else:
             need = k3moe_attn_extend_workspace_bytes(self.cache, len(seq_lens), self.s.T, hq)
-            if self.ws_extend is None or self.ws_extend.numel() < need:
-                self.ws_extend = torch.empty(need, dtype=torch.uint8, device=x.device)
-            rest = dict(lse=self.lse, window=self.window, sinks=self.sinks, ws=self.ws_extend, dev_status=self.status)
+            if not self.ws_extend or self.ws_extend[-1].numel() < need:
+                self.ws_extend.append(torch.empty(need, dtype=torch.uint8, device=x.device))
+            rest = dict(lse=self.lse, window=self.window, sinks=self.sinks, ws=self.ws_extend[-1], dev_status=self.status)
             if masks is None:
                 k3moe_attn_extend(self.cache, q, q_offsets, block_table, seq_lens, self.att, max_new=max_new, **rest)
             else:
@@ -223,8 +228,8 @@ class DecoderLayer:
     def extend(self, x, residual, block_table, seq_lens, slots, q_offsets, positions=None, masks=None, max_new=None):
         """Several new tokens of each sequence through the layer: (x', a).  Rows q_offsets[b] .. q_offsets[b + 1] - 1
         (int32 [B + 1]) of x [T, H] are sequence b's, which seq_lens counts; slots (int32 [T]) are theirs, negative for
-        rows of no sequence.  With masks (``tree_masks``) they are a drafted tree's.  The workspace is that of
-        the largest batch so far: a call that is captured comes after one like it."""
+        rows of no sequence.  With masks (``tree_masks``) they are a drafted tree's.  The workspace is made for
+        the largest batch so far: a call that is captured comes after one like it, so that it allocates nothing."""
         return self.moe(*self.attention(x, residual, block_table, seq_lens, slots, positions, q_offsets, masks, max_new))
 
 

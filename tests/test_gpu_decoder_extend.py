@@ -134,6 +134,35 @@ def test_accept_refuses(kept, count):
     assert pages.lens == [20]
 
 
+def test_accept_refuses_more_than_there_are():
+    m = Model(k3.K3MOE_KV_BF16, 0, 0, False)
+    pages = decoder.PageTable(1, 60, PAGE, 12)
+    pages.append([0], 3)
+    before = m.cache.k.view(torch.int16).clone()  # (bits: the memory may hold NaN)
+    with pytest.raises(ValueError):
+        decoder.accept(m.cache, pages, 0, 5, [1, 3])
+    assert pages.lens == [3] and torch.equal(m.cache.k.view(torch.int16), before)
+
+
+def test_accept_of_two_layers():
+    # pages are shared by the layers: both caches keep the path, and the tokens are forgotten once
+    caches = [k3.KVCache.empty(12, heads, PAGE, D, f) for heads, f in ((HK, k3.K3MOE_KV_BF16), (1, k3.K3MOE_KV_E4M3))]
+    pages = decoder.PageTable(1, 12, PAGE, 12)
+    slots = pages.append([0], 20)
+    want = []
+    for i, c in enumerate(caches):
+        k3.k3moe_kv_write(c, _bf(60 + i, 20, c.heads, D), _bf(70 + i, 20, c.heads, D), slots)
+        kv = [torch.empty(18, c.heads, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        k3.k3moe_kv_read(c, slots[torch.tensor([*range(16), 17, 19], device="cuda")], *kv)
+        want.append(kv)
+    decoder.accept(caches, pages, 0, 4, [1, 3])
+    assert pages.lens == [18]
+    for c, w in zip(caches, want):
+        kv = [torch.empty(18, c.heads, D, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        k3.k3moe_kv_read(c, pages.slots_of(0), *kv)
+        assert all(torch.equal(x, y) for x, y in zip(kv, w))
+
+
 def test_calls_that_do_not_fit_the_layer():
     m = Model(k3.K3MOE_KV_BF16, 0, 0, True)
     pages = decoder.PageTable(1, 60, PAGE, 12)
@@ -163,6 +192,24 @@ def test_a_captured_call_gives_the_same():
     layer.out.zero_()
     graph.replay()
     assert torch.equal(layer.out, out) and torch.equal(layer.a2, a)
+
+
+def test_a_captured_call_after_a_larger_batch():
+    m = Model(k3.K3MOE_KV_E4M3, 0, 0, False)
+    layer = m.layer(32)
+    few, many = decoder.PageTable(2, 30, PAGE, 12), decoder.PageTable(200, 30, PAGE, 12)
+    slots, x, offs = torch.cat([few.append([0], 20), few.append([1], 12)]), _bf(30, 32, H), i32([0, 20, 32])
+    out = layer.extend(x, None, few.table, few.seq_lens, slots, offs)[0].clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        layer.extend(x, None, few.table, few.seq_lens, slots, offs)
+    held = layer.ws_extend[0]
+    layer.extend(x, None, many.table, many.seq_lens, torch.full_like(slots, -1), i32([0] * 201))  # 200 sequences without a token
+    assert len(layer.ws_extend) == 2 and layer.ws_extend[0] is held
+    layer.out.zero_()
+    graph.replay()
+    assert torch.equal(layer.out, out) and int(layer.status.item()) == 0
 
 
 def test_the_command_runs(capsys):
