@@ -849,10 +849,10 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             if constexpr (E4M3) ks = sh.ones;  // (they are scaled)
           }
           // 64 places at a time: scores in, weights out (in place: their 32 columns lie behind what was read)
-#pragma unroll 1
+          tc_ld32(sa, v);
+          tc_ld32(sa + 32, v + 32);
+#pragma unroll
           for (int x = 0; x < TN; x += 64) {
-            tc_ld32(sa + x, v);
-            tc_ld32(sa + x + 32, v + 32);
             tc_wait_ld(v);
             if constexpr (E4M3) scale_keys<64>(v, ks + x);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -897,6 +897,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                 add[(y / 2) & 1] = add2(add[(y / 2) & 1], w);
               }
               tc_st16u(sa + (x + h) / 2, pk);
+              if (x + 64 < TN) tc_ld32(sa + x + 64 + h, v + h);  // (the next ones are on their way meanwhile)
             }
             if (x + 64 < TN) {  // these can be multiplied while the others are computed
               tc_wait_st();
