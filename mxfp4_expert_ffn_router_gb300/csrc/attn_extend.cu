@@ -705,6 +705,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     const int st = warp >> 2;  // stream
     const int lrow = 32 * (warp & 3) + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16, oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
+    constexpr bool AHEAD = !E4M3;  // whether a tile's next scores are loaded while weights are computed, in code without a loop
     const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
     const float c1 = flat ? 1.f : fabsf(P.scale) * kLog2e;
     // This stream's queries of an item: asked for, and, once they have come, made operands.  A thread converts what it has
@@ -723,17 +724,22 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       const int base = I.r0 + (I.both ? 128 * st : 0), left = I.r0 + I.rows - base, i0 = base / P.G, g0 = base - i0 * P.G;
       const uint16_t *q = P.q + (static_cast<long long>(I.first) + i0) * P.q_stride + static_cast<size_t>(I.head) * P.G * D + ch * 8;
       q_rows = min(128, (left + 128 / CH - 1) & ~(128 / CH - 1));  // (whole turns of the threads: the rest is not read)
+      const int ii = token_of(P, g0 + q_row), step = token_of(P, 128 / CH), more = 128 / CH - step * P.G;
+      int gg = g0 + q_row - ii * P.G;
+      const long long by = step * P.q_stride + more * D, wrap = P.q_stride - static_cast<long long>(P.G) * D;
+      q += ii * P.q_stride + gg * D;
 #pragma unroll 2
       for (int rr = q_row; rr < q_rows; rr += 128 / CH) {
-        const int ii = token_of(P, g0 + rr), gg = g0 + rr - ii * P.G;
         const bool on = rr < left;
-        const uint16_t *from = on ? q + ii * P.q_stride + gg * D : P.q;
+        const uint16_t *from = on ? q : P.q;
         if constexpr (E4M3) {
           cp_or_zeros8(q_to + place8(rr), from, on);
           cp_or_zeros8(q_to + 128 * D + place8(rr), from + 4, on);
         } else {
           cp_or_zeros16(q_to + place16(rr), from, on);
         }
+        q += by, gg += more;
+        if (gg >= P.G) q += wrap, gg -= P.G;
       }
     };
     uint32_t turn = 0;
@@ -793,11 +799,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       const int r = (both ? 128 * st : 0) + lrow;  // row of the item
       Row row;
       row.on = r < I.rows;
-      const int i0 = I.r0 / P.G, at = I.r0 - i0 * P.G + r;
-      const int di = token_of(P, at), g = at - di * P.G, i = min(i0 + di, I.m - 1);
-      const long long qrow = static_cast<long long>(I.first) + i;
+      const int i0 = I.r0 / P.G, i = min(i0 + token_of(P, I.r0 - i0 * P.G + r), I.m - 1);  // token
       int pos = I.ctx + i;
-      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? qrow * P.words : 0));
+      row.mask = reinterpret_cast<const uint32_t *>(P.masks + (P.masks ? (static_cast<long long>(I.first) + i) * P.words : 0));
       if (P.masks) {
         int seen = 0;
 #pragma unroll 1
@@ -849,10 +853,12 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             if constexpr (E4M3) ks = sh.ones;  // (they are scaled)
           }
           // 64 places at a time: scores in, weights out (in place: their 32 columns lie behind what was read)
-          tc_ld32(sa, v);
-          tc_ld32(sa + 32, v + 32);
-#pragma unroll
+#pragma unroll AHEAD ? TN / 64 : 1
           for (int x = 0; x < TN; x += 64) {
+            if (!AHEAD || x == 0) {
+              tc_ld32(sa + x, v);
+              tc_ld32(sa + x + 32, v + 32);
+            }
             tc_wait_ld(v);
             if constexpr (E4M3) scale_keys<64>(v, ks + x);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -897,7 +903,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
                 add[(y / 2) & 1] = add2(add[(y / 2) & 1], w);
               }
               tc_st16u(sa + (x + h) / 2, pk);
-              if (x + 64 < TN) tc_ld32(sa + x + 64 + h, v + h);  // (the next ones are on their way meanwhile)
+              if (AHEAD && x + 64 < TN) tc_ld32(sa + x + 64 + h, v + h);  // (the next ones are on their way meanwhile)
             }
             if (x + 64 < TN) {  // these can be multiplied while the others are computed
               tc_wait_st();
@@ -959,33 +965,61 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       if (warp_on) {
         const bool cut = I.parts > 1;
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t orow = static_cast<size_t>(qrow) * P.Hq + I.head * P.G + g;
+        // (computed here, so that it takes no registers before)
+        const int at = I.r0 % P.G + r, token = token_of(P, at);
+        const size_t orow = (static_cast<size_t>(I.first) + I.r0 / P.G + token) * P.Hq + I.head * P.G + at - token * P.G;
         const int x0 = split ? st * (D / 2) : 0, x1 = split ? x0 + D / 2 : D;
         const uint32_t o0 = split ? tmem + lane_addr + S::O_COL : oa, o1 = o0 + S::O_COLS;
+        // Written from their own lanes, a row each, 16 bytes would be a line of their own, 32 a store (5900 clocks an
+        // item); four lanes exchange theirs, and write 64 bytes of each of their rows in turn.
+        const int j = lane & 3;
 #pragma unroll 1
-        for (int x = x0; x < x1; x += 16) {
-          float o[16];
+        for (int x = x0; x < x1; x += 32) {
+          float o[32];
           __syncwarp();
-          tc_ld16f(o0 + x, o);
+          tc_ld32(o0 + x, o);
           tc_wait_ld(o);
           if (split && K > 1) {
-            float z[16];
-            tc_ld16f(o1 + x, z);
-            tc_wait_ld(z);
 #pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = o[y] * f0 + z[y] * f1;
+            for (int h = 0; h < 32; h += 16) {
+              float z[16];
+              tc_ld16f(o1 + x + h, z);
+              tc_wait_ld(z);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[h + y] = o[h + y] * f0 + z[y] * f1;
+            }
           }
-          if (row.on && cut) {
-            float *to = P.part + (static_cast<size_t>(I.slot) * D + x) * ROWS + r;
+          if (cut) {
+            if (!row.on) continue;
+            float *part = P.part + (static_cast<size_t>(I.slot) * D + x) * ROWS + r;
 #pragma unroll
-            for (int y = 0; y < 16; ++y) to[y * ROWS] = o[y];
-          } else if (row.on) {
-            uint4 *to = reinterpret_cast<uint4 *>(P.out + orow * D + x);
-            uint32_t w[8];
+            for (int y = 0; y < 32; ++y) part[y * ROWS] = o[y];
+          } else {
+            uint32_t w[4][4];
 #pragma unroll
-            for (int z = 0; z < 8; ++z) w[z] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
-            to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int z = 0; z < 16; ++z) w[z / 4][z % 4] = l == 0.f ? 0u : bf16x2(o[2 * z] * inv, o[2 * z + 1] * inv);
+#pragma unroll
+            for (int s = 1; s < 4; s <<= 1) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if (y & s) continue;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, j & s ? w[y][z] : w[y + s][z], s);
+                  if (j & s)
+                    w[y][z] = got;
+                  else
+                    w[y + s][z] = got;
+                }
+              }
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              // (a row's index fits 32 bits: out would not fit the device else)
+              const size_t to = __shfl_sync(0xFFFFFFFFu, static_cast<uint32_t>(orow), lane - j + y);
+              if (r - j + y < I.rows)
+                *reinterpret_cast<uint4 *>(P.out + to * D + x + 8 * j) = make_uint4(w[y][0], w[y][1], w[y][2], w[y][3]);
+            }
           }
         }
         if (row.on && !(split && st)) {
