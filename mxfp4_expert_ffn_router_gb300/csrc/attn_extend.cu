@@ -1122,8 +1122,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             if (!ok) break;
             ++uses[sb];
+            if (E4M3) commit(&sh.v_empty[slot]);  // (they are converted meanwhile)
             if (k + 2 < K) ok = scores(k + 2);
-            commit(&sh.v_empty[slot]);
+            if (!E4M3) commit(&sh.v_empty[slot]);
             if (NS == 1 || k + NS >= K) commit(&sh.pv_done[sb]);
           } else if (k + 2 < K) {
             ok = scores(k + 2);
