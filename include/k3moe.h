@@ -461,7 +461,10 @@ int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const ui
  * more than max_new rows sets K3MOE_DEV_BOUNDS and its rows are left as they were; one with more new
  * tokens than cached ones sets it too, and those that have no place see nothing.
  * Accumulation: exact products summed in fp32, softmax in fp32; the weights are rounded before
- * the product with V as the comment in attn_extend.cu says.
+ * the product with V: to bf16 where a sequence has many rows; where it has few, or max_new is 1, as in
+ * k3moe_attn_decode.  Over an E4M3 cache with many rows a query row counts to 2^-19 of its largest value
+ * (exact above 2^-10 of it), one that holds an infinity gives NaN, and so may keys beyond 2^110.
+ * Calls that run at the same time, captured ones too, need workspaces of their own.
  * Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, window and sinks >= 0, max_pages >= 1, rows * Hq / heads
  * below 2^31. */
 size_t k3moe_attn_extend_workspace_bytes(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq);

@@ -1,4 +1,48 @@
 // attn_extend.cu -- attention of several new tokens per sequence over a paged key-value cache.
+//
+// A row (a new token's query head) sees places c of its sequence: all up to its own, within a window and the first `sinks`, or
+// the context and the drafted tokens that its mask names.  With a running reference m and sum l of the weights:
+//   s_c = scale q . K_c ;  w_c = 2^((s_c - m) log2 e) ;  l = sum w_c ;  out = (sum w_c V_c) / l ;  lse = m + ln l
+// The reference is that of the row's first tile; it moves, and the sums with it, only when a weight would pass 2^8, which
+// seldom happens after the first tiles.  Statistics and sums are fp32.
+//
+// The query heads of one key-value head read the same keys, so an item is 256 rows (tokens x heads) of one key-value
+// head: two streams of 128, the rows of one tcgen05.mma, over the same tiles of 128 places.  (128 rows or fewer: the streams
+// take every other tile, and are added at the end.  Head size 256: one stream, 64 places, as two do not fit.)  While one
+// stream's scores become weights, the tensor cores multiply for the other.  A block is 16 warps:
+//   0-7    softmax: a thread is a row; scores from tensor memory, weights back into the columns that the scores had
+//   8, 10  products of one stream: scores q K^T, and weights (from tensor memory) by values
+//   9      items and their tiles, by TMA, a page or a tile a copy; a place that no row needs comes as zeros
+//   11     (E4M3) the keys' scales as numbers
+//   12-15  values: E4M3 to bf16; values that not all rows see, if not finite, are left out of the product (0 times them is
+//          not 0) and added to the sums of the rows that do see them
+// Tensor memory is full: 2 x 128 columns of scores or weights, 2 x 128 (or 256) of sums.  Shared memory holds the queries (2 x
+// 32 KB), three tiles of keys and two of values at 128 wide.
+//
+// E4M3: keys are operands as they are stored (kind::f8f6f4).  A query row, times a power of two that brings its largest value
+// into [128, 256), is the sum of two E4M3 numbers (exact down to 2^-10 of the row's largest; below that an error of 2^-19 of
+// it), each with a product of its own, and the raw score is scaled by the key's and the row's power of two.  Values become
+// bf16 exactly: codes shifted into place and times one bf16 power of two.
+//
+// Roundings: a weight to bf16 once, by 2^-8 of itself at most, as the output is; l sums the weights before that.  (As two
+// bf16 numbers, 16 bits, the products with V are twice as many: a prompt of 8192 took 1064 us for 919.)
+//
+// How the work is cut.  Where the items fill at most one block an SM: one block an item, or several to a long item.
+// Otherwise a line of all items' tiles is cut into equal pieces, one an SM, by a kernel of one block, and pieces of cut items are
+// added by another, in the order of the pieces.  Results repeat bit for bit: the only atomics set bits.
+//
+// What bounds it.  A pair of tiles (256 rows x 128 places x 128 wide) is 2050 clocks of products at the tensor cores' rate and 2100
+// of softmax (exponentials 1024, the rest adds, maxima, conversions) on the four schedulers, at once where the streams
+// alternate.  Measured 3700 clocks (bf16) and 5500 (E4M3, whose values' conversion runs on the same schedulers, 900 to
+// 1400 clocks, and pulls the streams into step): waits for loads from tensor memory, for barriers and for instructions, of which a
+// pass over this code needs more than the nearest cache holds.
+//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   863 us, 956 TFLOP/s (0.51 of a large product's rate)
+//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   325 us, 794 TFLOP/s; 0.84 TB/s
+//   64 drafted tokens on each of 16 sequences up to 16384, E4M3:       180 us, 290 TFLOP/s
+//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      186 us, 437 TFLOP/s
+//   24 prompts of up to 301 tokens, 16 heads on one of 64, bf16:        26 us: launch, first tile, end
+// Tried without gain: registers moved from the other warps to the softmax warps; eight warps for the values; a handshake a step that
+// holds the second stream half a step behind; helpers called instead of inlined; scores 32 at a time.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -549,7 +593,8 @@ __device__ __noinline__ void add_left_out(const AxParams &P, const AxItem &I, co
 
 }  // namespace
 
-// The pieces of the line: one block.
+// The pieces of the line: one block measures the sequences, sums their lengths and finds where each piece begins.  Latency
+// of a few scans; 3 to 5 us, which is why short calls go without.
 template <int TN, int ROWS>
 __global__ void __launch_bounds__(1024) attn_plan_kernel(const AxParams P) {
   __shared__ long long s_scan[32];
@@ -705,7 +750,9 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     const int st = warp >> 2;  // stream
     const int lrow = 32 * (warp & 3) + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16, oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
-    constexpr bool AHEAD = !E4M3;  // whether a tile's next scores are loaded while weights are computed, in code without a loop
+    // Whether a tile's second half of scores is loaded while the first one's weights are computed, in code without a loop: over
+    // bf16 a prompt takes 891 us for 919, over E4M3 chunks 214 for 187, by the longer code and its registers.
+    constexpr bool AHEAD = !E4M3;
     const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
     const float c1 = flat ? 1.f : fabsf(P.scale) * kLog2e;
     // This stream's queries of an item: asked for, and, once they have come, made operands.  A thread converts what it has
@@ -1122,7 +1169,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             if (!ok) break;
             ++uses[sb];
-            if (E4M3) commit(&sh.v_empty[slot]);  // (they are converted meanwhile)
+            // (E4M3: the next values are converted meanwhile, 338 -> 325 us of a long tree; bf16: no difference to the copies)
+            if (E4M3) commit(&sh.v_empty[slot]);
             if (k + 2 < K) ok = scores(k + 2);
             if (!E4M3) commit(&sh.v_empty[slot]);
             if (NS == 1 || k + NS >= K) commit(&sh.pv_done[sb]);
@@ -1369,7 +1417,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
 }
 
 // Adds the parts of an item that was cut, in the order of their pieces: block (x, y, z) joins 32 dimensions of 32 rows of the
-// item that begins in piece x (direct: of item x).  kJoinParts parts are loaded at once (one after the other, nine of them
+// item that begins in piece x (direct: of item x).  Bound by the sums' bytes, read once from L2: out = sum_p o_p 2^(m_p - m) over
+// the same of l.  18 MB of a tree on 16000 tokens in 9 parts: 12 us cold, 8 beside the rest.  kJoinParts parts are loaded at once (one after the other, nine of them
 // took 20 us).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(128) attn_extend_join_kernel(const AxParams P) {
