@@ -976,6 +976,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       const AxItem *const next = item_at(items + 1);
       const bool next_q = next && next->steps() > st;
       if (next_q) ask_q(*next);
+      if (next_q) take_q();
       if (had) {
         if (!warp_wait(&sh.pv_done[sb], (NS == 2 ? finals : uses[sb] - 1) & 1u)) {
           timeout = true;
@@ -986,7 +987,6 @@ __global__ void __launch_bounds__(kAxThreads, 1)
       }
       if ((*reinterpret_cast<volatile uint32_t *>(&sh.odd) >> (items & 31) & 1u) && had && warp_on)
         add_left_out<D, E4M3, TN>(P, I, row, st, oa);
-      if (next_q) take_q();
       float mb = m == -INFINITY ? -INFINITY : m * c, f0 = 1.f, f1 = 0.f;
       const bool split = NS == 2 && !both;  // the streams share the rows: each writes half of the dimensions
       if (split) {
