@@ -912,7 +912,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
 #pragma unroll
             for (int y = 0; y < 64; y += 2) mx[(y / 2) & 3] = fmaxf(fmaxf(v[y], v[y + 1]), mx[(y / 2) & 3]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (__any_sync(0xFFFFFFFFu, (top - m) * c > kGrowth)) {
+            // (behind the item's last row there are no queries, but what shared memory held: those rows have no say)
+            if (__any_sync(0xFFFFFFFFu, row.on && (top - m) * c > kGrowth)) {
               // the row's reference moves up: sums by the quotient
               const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
               m = mn;
