@@ -36,13 +36,14 @@
 // alternate.  Measured 3700 clocks (bf16) and 5500 (E4M3, whose values' conversion runs on the same schedulers, 900 to
 // 1400 clocks, and pulls the streams into step): waits for loads from tensor memory, for barriers and for instructions, of which a
 // pass over this code needs more than the nearest cache holds.
-//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   863 us, 956 TFLOP/s (0.51 of a large product's rate)
-//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   325 us, 794 TFLOP/s; 0.84 TB/s
-//   64 drafted tokens on each of 16 sequences up to 16384, E4M3:       180 us, 290 TFLOP/s
-//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      186 us, 437 TFLOP/s
+//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   853 us, 968 TFLOP/s (0.51 of a large product's rate)
+//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   322 us, 801 TFLOP/s; 0.85 TB/s
+//   64 drafted tokens on each of 16 sequences up to 16384, E4M3:       170 us, 307 TFLOP/s
+//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      188 us, 433 TFLOP/s
 //   24 prompts of up to 301 tokens, 16 heads on one of 64, bf16:        26 us: launch, first tile, end
 // Tried without gain: registers moved from the other warps to the softmax warps; eight warps for the values; a handshake a step that
-// holds the second stream half a step behind; helpers called instead of inlined; scores 32 at a time.
+// holds the second stream half a step behind; helpers called instead of inlined; scores 32 at a time; the
+// next item's queries asked for a step earlier (prompt 846 -> 854 us, chunks 189 -> 197: longer code).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
