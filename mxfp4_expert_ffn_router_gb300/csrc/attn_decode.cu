@@ -1116,31 +1116,48 @@ __global__ void __launch_bounds__(W * 32, (AdShape<D, E4M3, NT, W, DIRECT>::BLOC
 #pragma unroll 1
         for (unsigned at = began; at < cur.tok && at < static_cast<unsigned>(cur.n); at += UNIT)
 #pragma unroll 1
-          for (unsigned tok = at; tok < at + RUN && tok < static_cast<unsigned>(cur.n); ++tok) {
-            const unsigned where = place_of(cur, tok);
-            const int pg = sees(cur, where) ? pages_of[where >> P.page_shift] : -1;
+          for (unsigned tile = at; tile < at + RUN && tile < static_cast<unsigned>(cur.n); tile += kRun) {
+            const unsigned first_of = place_of(cur, tile);
+            const int pg = sees_some(cur, first_of, kRun) ? pages_of[first_of >> P.page_shift] : -1;
             if (static_cast<unsigned>(pg) >= static_cast<unsigned>(P.pages)) continue;
-            const size_t vec = static_cast<size_t>(static_cast<unsigned>(pg)) * page_vecs +
-                               ((static_cast<unsigned>(cur.head) << P.page_shift) + (where & place));
-            uint32_t see = 0;
-            for (int y = 0; y < 2 * NT; ++y)
-              see |= column_sees(P, cur.n, cur.m, cur.row, cur.group * NQ + 8 * (y >> 1) + 2 * c + (y & 1),
-                                 static_cast<int>(where), 1) << y;
+            const size_t vec0 = static_cast<size_t>(static_cast<unsigned>(pg)) * page_vecs +
+                                ((static_cast<unsigned>(cur.head) << P.page_shift) + (first_of & place));
+            // Which of the 16 places have something: a lane looks at words lane, lane + 32, .. of them, so that a run
+            // without costs a read (2 drafted tokens on 16000 places, E4M3, 31 us: 38 with a NaN; 404 where each place
+            // was gone through)
+            uint32_t some = 0;
 #pragma unroll
-            for (int m = 0; m < MM; ++m) {
-              const size_t e = vec * D + quad_dim<D, E4M3>(m, g);
-              float u[2];
-              if constexpr (E4M3) {
+            for (int i = 0; i < C / 2; ++i) {
+              uint4 u = reinterpret_cast<const uint4 *>(P.v + vec0 * S::ROWB)[i * 32 + lane];
+              if (leave_out<E4M3>(u.x) | leave_out<E4M3>(u.y) | leave_out<E4M3>(u.z) | leave_out<E4M3>(u.w))
+                some |= 1u << ((i * 32 + lane) / C);
+            }
+            some = __reduce_or_sync(0xFFFFFFFFu, some);
+            while (some) {
+              const unsigned x = __ffs(some) - 1, where = first_of + x;
+              some &= some - 1;
+              if (!sees(cur, where)) continue;
+              const size_t vec = vec0 + x;
+              uint32_t see = 0;
+              for (int y = 0; y < 2 * NT; ++y)
+                see |= column_sees(P, cur.n, cur.m, cur.row, cur.group * NQ + 8 * (y >> 1) + 2 * c + (y & 1),
+                                   static_cast<int>(where), 1) << y;
 #pragma unroll
-                for (int y = 0; y < 2; ++y) u[y] = (P.v[e + y] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.f;
-              } else {
-                const uint32_t both = *reinterpret_cast<const uint32_t *>(P.v + 2 * e);
-                u[0] = __uint_as_float(both << 16), u[1] = __uint_as_float(both & 0xFFFF0000u);
+              for (int m = 0; m < MM; ++m) {
+                const size_t e = vec * D + quad_dim<D, E4M3>(m, g);
+                float u[2];
+                if constexpr (E4M3) {
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) u[y] = (P.v[e + y] & 0x7Fu) == 0x7Fu ? __uint_as_float(0x7FC00000u) : 0.f;
+                } else {
+                  const uint32_t both = *reinterpret_cast<const uint32_t *>(P.v + 2 * e);
+                  u[0] = __uint_as_float(both << 16), u[1] = __uint_as_float(both & 0xFFFF0000u);
+                }
+                if (isfinite(u[0]) && isfinite(u[1])) continue;
+#pragma unroll
+                for (int x = 0; x < 4 * NT; ++x)
+                  if (!isfinite(u[(x >> 1) & 1]) && ((see >> (2 * (x >> 2) + (x & 1))) & 1u)) o[x >> 2][m][x & 3] += u[(x >> 1) & 1];
               }
-              if (isfinite(u[0]) && isfinite(u[1])) continue;
-#pragma unroll
-              for (int x = 0; x < 4 * NT; ++x)
-                if (!isfinite(u[(x >> 1) & 1]) && ((see >> (2 * (x >> 2) + (x & 1))) & 1u)) o[x >> 2][m][x & 3] += u[(x >> 1) & 1];
             }
           }
         odd = 0;

@@ -67,3 +67,25 @@ def test_beside_a_page_outside_the_cache(fmt):
     dims = [0]  # (3205 and 3300; 3240 lies in the page that is lost, and would be here too)
     assert not torch.isfinite(out[:60][..., dims]).any()
     assert torch.equal(out[:60][..., 1:], good[0][:60][..., 1:]) and torch.equal(out[60:], good[0][60:])
+
+
+# (few rows a head: a cluster's blocks share an item, or pieces of the line do; 8 and 16 columns)
+@pytest.mark.parametrize("fmt,dim", [(E4, 128), (BF, 128), (E4, 64), (BF, 256)])
+@pytest.mark.parametrize("plan,Hq,tree", [([(6000, 2)], 32, True), ([(60000, 2), (900, 1)], 64, True), ([(60000, 2), (900, 1)], 32, False)])
+def test_one_value_among_few_rows(plan, Hq, tree, fmt, dim):
+    c = LargeCase(plan, Hq, 8, dim, 64, fmt, tree=tree)
+    dims, (ctx, m) = [3, dim - 1], plan[0]
+    good, before = c.run(), c.us()
+    _spoil(c, 0, ctx + m - 1, dims)
+    _check(c, good, [i == m - 1 for i in range(m)], dims)
+    after = c.us()
+    assert after < 2.5 * before + 50, (before, after)
+
+
+def test_a_value_in_the_context_among_few_rows():
+    """bf16: left out wherever it lies, and added for all."""
+    c = LargeCase([(6000, 2), (50, 3)], 16, 8, 128, 64, BF, tree=True)
+    good = c.run()
+    for p in (0, 17, 4095, 5999):
+        _spoil(c, 0, p, [p % 7])
+    _check(c, good, [True, True], sorted({p % 7 for p in (0, 17, 4095, 5999)}))
