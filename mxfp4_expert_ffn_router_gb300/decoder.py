@@ -89,8 +89,18 @@ class PageTable:
         self._upload()
 
     def positions_of(self, which, count: int = 1) -> torch.Tensor:
-        """Positions of the last ``count`` tokens of each sequence in ``which`` (int32), in the order of append's slots."""
-        at = [self.lens[b] - count + i for b in which for i in range(count)]
+        """Positions of the last ``count`` tokens of each sequence in ``which`` (int32), in the order of append's slots: of a
+        sequence that is named more than once, the last tokens are its last naming's."""
+        which = list(which)
+        left = Counter(which)
+        for b, times in left.items():
+            if not 0 <= count * times <= self.lens[b]:
+                raise ValueError(f"sequence {b} has {self.lens[b]} tokens, not {count * times}")
+        at = []
+        for b in which:
+            first = self.lens[b] - count * left[b]
+            left[b] -= 1
+            at += range(first, first + count)
         return torch.tensor(at, dtype=torch.int32, device=self.table.device)
 
     def slots_of(self, b: int) -> torch.Tensor:
