@@ -479,7 +479,9 @@ int k3moe_attn_extend(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int3
  *           sequence's new token j (its own bit, if it is to see itself, included; bits past m mean nothing)
  *   words : 1 .. 16
  * A window counts from the token's position n - m + max(0, s - 1), s being the number of new tokens that it
- * sees (its ancestors and itself), and with the sinks it limits the context alone. */
+ * sees (its ancestors and itself), and with the sinks it limits the context alone: of a tree deeper than its
+ * window the masks leave out the ancestors that lie `window` or more positions before a token, as decoding
+ * would (with `window` bits or more no place of the context is within the window, as it should be). */
 int k3moe_attn_tree(const k3moe_kv_cache *cache, int32_t B, int32_t rows, int32_t Hq, const uint16_t *q,
                     int64_t q_stride, const int32_t *q_offsets, const int64_t *masks, int32_t words,
                     const int32_t *block_table, int32_t max_pages, const int32_t *seq_lens, int32_t window, int32_t sinks,

@@ -640,7 +640,8 @@ def k3moe_attn_tree(cache: KVCache, q, q_offsets, masks, block_table, seq_lens, 
                     window: int = 0, sinks: int = 0, ws=None, dev_status=None, stream=None):
     """k3moe_attn_extend for drafted tokens: of its sequence's new tokens row r sees those whose bits its mask
     has (masks [rows, words] int64: bit j % 64 of word j // 64 stands for new token j), and all of the cached
-    ones before them that the window and the sinks leave, the window counting from n - m + (new tokens seen) - 1."""
+    ones before them that the window and the sinks leave, the window counting from n - m + (new tokens seen) - 1 (it takes
+    no new token away: a tree deeper than its window has masks without the far ancestors, decoder.tree_masks)."""
     if _fast is not None and masks is not None:
         rc = _fast.attn_extend(cache._addr, q, q_offsets, masks, block_table, seq_lens, out, lse,
                                cache.dim ** -0.5 if scale is None else scale, window, sinks, None, ws, dev_status,

@@ -114,19 +114,37 @@ class PageTable:
         self.seq_lens.copy_(torch.tensor(self.lens, dtype=torch.int32))
 
 
-def tree_masks(parents, device="cuda"):
+def tree_masks(parents, device="cuda", window: int = 0, sinks: int = 0, lens=None):
     """Drafted trees as k3moe_attn_tree takes them.  ``parents``: for each sequence the parents of its drafted tokens, each
     an earlier one's index, or -1 for one that follows the sequence's last token.  Returns the masks int64 [rows, words] (a
     token sees its ancestors and itself), the q_offsets int32 [B + 1], and each row's depth (0: follows the last token),
-    which is its position behind the context."""
+    which is its position behind the context.
+
+    ``window`` and ``sinks``: the layer's.  A decoded token sees no other that lies ``window`` or more positions before it, but for
+    the first ``sinks``, drafted or not; the call drops cached ones alone, and a tree deeper than its window needs masks
+    without the ancestors that are too far.  ``lens``: the tokens of each sequence before the drafted ones (with sinks: a
+    drafted token at a position below them stays visible)."""
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks are at least 0")
+    parents = list(parents)
+    if window and sinks:
+        if lens is None:
+            raise ValueError("sinks: which drafted tokens they are goes by lens, the tokens before them")
+        if len(lens := list(lens)) != len(parents):
+            raise ValueError(f"lens: {len(lens)} sequences, not {len(parents)}")
     rows, depths, offsets = [], [], [0]
-    for tree in parents:
-        first = len(rows)
+    for b, tree in enumerate(parents):
+        first, kept = len(rows), sinks - lens[b] if window and sinks else 0  # depths below `kept` are first tokens
+        line = []  # of each token its ancestors and itself, from the first on
         for i, p in enumerate(tree):
             if not -1 <= p < i:
                 raise ValueError(f"the parent of drafted token {i} must be an earlier one or -1, not {p}")
-            rows.append((rows[first + p] if p >= 0 else 0) | 1 << i)
             depths.append(depths[first + p] + 1 if p >= 0 else 0)
+            if not window:
+                rows.append((rows[first + p] if p >= 0 else 0) | 1 << i)
+                continue
+            line.append((line[p] if p >= 0 else []) + [i])
+            rows.append(sum(1 << j for d, j in enumerate(line[i]) if d > depths[-1] - window or d < kept))
         offsets.append(len(rows))
     words = max(1, -(-max((len(t) for t in parents), default=0) // 64))
     parts = [[(r >> 64 * w) & (2 ** 64 - 1) for w in range(words)] for r in rows]
@@ -238,8 +256,9 @@ class DecoderLayer:
     def extend(self, x, residual, block_table, seq_lens, slots, q_offsets, positions=None, masks=None, max_new=None):
         """Several new tokens of each sequence through the layer: (x', a).  Rows q_offsets[b] .. q_offsets[b + 1] - 1
         (int32 [B + 1]) of x [T, H] are sequence b's, which seq_lens counts; slots (int32 [T]) are theirs, negative for
-        rows of no sequence.  With masks (``tree_masks``) they are a drafted tree's.  The workspace is made for
-        the largest batch so far: a call that is captured comes after one like it, so that it allocates nothing."""
+        rows of no sequence.  With masks (``tree_masks``, which takes the layer's window and sinks: without them a token sees
+        ancestors beyond its window, and scores as it would not be decoded) they are a drafted tree's.  The workspace is made
+        for the largest batch so far: a call that is captured comes after one like it, so that it allocates nothing."""
         return self.moe(*self.attention(x, residual, block_table, seq_lens, slots, positions, q_offsets, masks, max_new))
 
 
