@@ -459,7 +459,8 @@ int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const ui
  * A row that sees nothing gives out = 0, lse = -inf.  What lies in places that a row does not
  * see does not touch it, whatever they hold.  A sequence whose offsets descend, leave 0 .. rows or span
  * more than max_new rows sets K3MOE_DEV_BOUNDS and its rows are left as they were; one with more new
- * tokens than cached ones sets it too, and those that have no place see nothing.
+ * tokens than cached ones sets it too, and those that have no place see nothing (but in k3moe_attn_extend,
+ * where max_new or rows is 1, a row of a sequence of length 0 is an empty slot of the batch: nothing is set).
  * Accumulation: exact products summed in fp32, softmax in fp32; the weights are rounded before
  * the product with V: to bf16 where a sequence has many rows; where it has few, or max_new is 1, as in
  * k3moe_attn_decode.  Over an E4M3 cache with many rows a query row counts to 2^-19 of its largest value

@@ -289,7 +289,8 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
     const bool fine = o0 >= 0 && o1 >= o0 && o1 <= P.rows && o1 - o0 <= P.max_new;
     s.m = new_ones = fine ? o1 - o0 : 0;
     s.row = s.m ? o0 : -1;
-    if (report && (!fine || s.m > s.n)) set_status(P.status, K3MOE_DEV_BOUNDS);
+    // (one token a sequence: a row of an empty sequence is a batch's empty slot)
+    if (report && (!fine || (s.m > s.n && (kRows || len != 0)))) set_status(P.status, K3MOE_DEV_BOUNDS);
   }
   s.lo = P.window > 0 && s.n - new_ones >= P.window ? s.n - new_ones - P.window + 1 : 0;  // (of the first of them)
   s.t0 = s.lo & ~(RUN - 1);

@@ -249,8 +249,8 @@ class DecoderLayer:
 
     def step(self, x, residual, block_table, seq_lens, slots, positions=None):
         """One new token of each sequence through the layer: (x', a).  seq_lens counts the new
-        tokens; slots (int32 [T]) are theirs, negative for an empty row of the batch (with sinks every row is a
-        token's); positions (int32 [T]) where the layer has a rotation."""
+        tokens; slots (int32 [T]) are theirs, negative for an empty row of the batch (its sequence has length
+        0); positions (int32 [T]) where the layer has a rotation."""
         return self.moe(*self.attention(x, residual, block_table, seq_lens, slots, positions))
 
     def extend(self, x, residual, block_table, seq_lens, slots, q_offsets, positions=None, masks=None, max_new=None):
