@@ -194,7 +194,7 @@ class DecoderLayer:
         self.status = torch.zeros(1, dtype=i32, device=dev)
         self.h, self.a, self.a2, self.o = (new(bf, s.T, s.H) for _ in range(4))
         self.qkv = new(bf, s.T, q_heads + 2 * cache.heads, cache.dim)
-        self.att, self.lse = new(bf, s.T, q_heads, cache.dim).zero_(), new(f32, s.T, q_heads)  # (rows of no token keep theirs)
+        self.att, self.lse = new(bf, s.T, q_heads, cache.dim), new(f32, s.T, q_heads)
         self.ws_attn = new(u8, k3moe_attn_decode_workspace_bytes(cache, s.T, q_heads))
         self.ws_extend = []  # (the last is in use; smaller ones stay, since captured calls may hold them)
         self.one_each = torch.arange(s.T + 1, dtype=i32, device=dev)
@@ -211,7 +211,8 @@ class DecoderLayer:
         hq, hk = self.q_heads, self.cache.heads
         if (self.rotation is None) != (positions is None):
             raise ValueError("positions belong to a layer with a rotation, and to each of its calls")
-        if q_offsets is None and self.sinks:
+        every_row = q_offsets is None  # (is a sequence's)
+        if every_row and self.sinks:
             q_offsets, max_new = self.one_each, 1
         if masks is not None and q_offsets is None:
             raise ValueError("masks: drafted tokens need q_offsets")
@@ -229,6 +230,8 @@ class DecoderLayer:
             need = k3moe_attn_extend_workspace_bytes(self.cache, len(seq_lens), self.s.T, hq)
             if not self.ws_extend or self.ws_extend[-1].numel() < need:
                 self.ws_extend.append(torch.empty(need, dtype=torch.uint8, device=x.device))
+            if not every_row:  # rows of no sequence keep what is there, which must not be an earlier call's
+                self.att.zero_()
             rest = dict(lse=self.lse, window=self.window, sinks=self.sinks, ws=self.ws_extend[-1], dev_status=self.status)
             if masks is None:
                 k3moe_attn_extend(self.cache, q, q_offsets, block_table, seq_lens, self.att, max_new=max_new, **rest)
@@ -256,9 +259,10 @@ class DecoderLayer:
     def extend(self, x, residual, block_table, seq_lens, slots, q_offsets, positions=None, masks=None, max_new=None):
         """Several new tokens of each sequence through the layer: (x', a).  Rows q_offsets[b] .. q_offsets[b + 1] - 1
         (int32 [B + 1]) of x [T, H] are sequence b's, which seq_lens counts; slots (int32 [T]) are theirs, negative for
-        rows of no sequence.  With masks (``tree_masks``, which takes the layer's window and sinks: without them a token sees
-        ancestors beyond its window, and scores as it would not be decoded) they are a drafted tree's.  The workspace is made
-        for the largest batch so far: a call that is captured comes after one like it, so that it allocates nothing."""
+        rows of no sequence (whose attention is 0).  With masks (``tree_masks``, which takes the layer's window and sinks:
+        without them a token sees ancestors beyond its window, and scores as it would not be decoded) they are a drafted
+        tree's.  The workspace is made for the largest batch so far: a call that is captured comes after one like it, so that it
+        allocates nothing."""
         return self.moe(*self.attention(x, residual, block_table, seq_lens, slots, positions, q_offsets, masks, max_new))
 
 
