@@ -211,11 +211,11 @@ class DecoderLayer:
         hq, hk = self.q_heads, self.cache.heads
         if (self.rotation is None) != (positions is None):
             raise ValueError("positions belong to a layer with a rotation, and to each of its calls")
+        if masks is not None and q_offsets is None:
+            raise ValueError("masks: drafted tokens need q_offsets")
         every_row = q_offsets is None  # (is a sequence's)
         if every_row and self.sinks:
             q_offsets, max_new = self.one_each, 1
-        if masks is not None and q_offsets is None:
-            raise ValueError("masks: drafted tokens need q_offsets")
         k3moe_rmsnorm(x, self.norm1, self.eps, residual=residual, residual_out=self.a, y=self.h)
         torch.matmul(self.h, self.wqkv.t(), out=self.qkv.view(self.s.T, -1))
         q, k, v = self.qkv[:, :hq], self.qkv[:, hq:hq + hk], self.qkv[:, hq + hk:]

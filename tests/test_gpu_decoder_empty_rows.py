@@ -53,3 +53,11 @@ def test_rows_of_empty_sequences(ctx, fmt):
         lens[1] = n
         c.run(window=20, sinks=3, max_new=most, lens=lens, dev_status=status)
         assert status.item() == k3.K3MOE_DEV_BOUNDS
+
+
+def test_masks_without_offsets_are_refused_with_sinks_too():
+    m = Model(E4, 24, 3, False)
+    pages = decoder.PageTable(2, 60, PAGE, 12)
+    layer, slots = m.layer(2), pages.append([0, 1])
+    with pytest.raises(ValueError):
+        layer.attention(_bf(1, 2, H), None, pages.table, pages.seq_lens, slots, masks=torch.ones(2, 1, dtype=torch.int64, device="cuda"))
