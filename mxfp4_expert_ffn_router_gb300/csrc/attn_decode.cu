@@ -114,6 +114,7 @@ constexpr int kDirectTokens = 1024;      // items that see at most this many are
 constexpr int kSplitTokens = 256;        // (see "More than 8 query heads" above)
 constexpr long long kPartBytes = 256 << 10;  // most bytes of keys that one of eight-warp blocks takes
 constexpr int kMinTokens = 256;          // smallest piece of a block
+constexpr int kSparse = 8;               // (kRows) blocks by sequence for each that can have work, past which the line is taken
 constexpr int kUnitLen = 4;              // length of a unit on the line
 constexpr int kJoinWarps = 8, kJoinParts = 4;  // warps of a joining block, parts that one adds at once
 constexpr int kAdMostBlocks = 152 * 2;   // pieces (bounds the workspace)
@@ -1471,9 +1472,12 @@ int clusters_at_once(const AdParams &P, int parts) {
   }));
 }
 
+// Items of one head that all sequences' rows make up at most.
+long long most_entries(const AdParams &P, int NQ) { return static_cast<long long>(P.rows) * P.G / NQ + P.B; }
+
 // (Long batches go by sequence: a block would read all of their offsets.)
 int entries_of(const AdParams &P, int NQ) {
-  const long long n = static_cast<long long>(P.rows) * P.G / NQ + P.B;
+  const long long n = most_entries(P, NQ);
   return P.B <= 256 && n < static_cast<long long>(P.B) * P.groups ? static_cast<int>(n) : 0;
 }
 
@@ -1525,11 +1529,17 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
       return start<D, E4M3, 1, 4, true>(Q, items_of(Q), 1, st) == cudaSuccess ? 0 : -1;
   }
   if (parts) return launch_few<D, E4M3, NT>(P, parts, st);
+  // A long batch's blocks are as many as if each sequence had max_new rows.  Where fewer than one in 8 would have work, the
+  // line, which measures the rows, is faster (64 / 8 heads, E4M3, 512 trees of 2 tokens on 500: by sequence 437 us, 16 blocks an
+  // item, on the line 251; the same without masks and with max_new left at all rows 6906 and 240; trees of 8, 6.4 blocks, on
+  // 500: 1041 and 902, on 60: 507 and 567; of 4 with 32 / 32 heads, 3.2 blocks, on 60: 312 and 521)
+  const bool sparse =
+      kRows && !P.entries && static_cast<long long>(P.B) * P.groups > kSparse * most_entries(P, 8 * NT);
   constexpr int kOneWarp = S::ROWB > 256 ? 256 : 128;  // most tokens of a warp's item
-  if (tokens <= kOneWarp && items < (1LL << 31) &&
+  if (!sparse && tokens <= kOneWarp && items < (1LL << 31) &&
       items > static_cast<long long>(sm_count()) * AdShape<D, E4M3, NT, 4, true>::BLOCKS)
     return start<D, E4M3, NT, 1, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
-  if (tokens <= kDirectTokens && items < (1LL << 31))
+  if (!sparse && tokens <= kDirectTokens && items < (1LL << 31))
     return start<D, E4M3, NT, 4, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
   long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;
   if (blocks > kAdMostBlocks) blocks = kAdMostBlocks;
