@@ -91,7 +91,7 @@
 //    window of 4096, E4M3, 60 and 69 us.)
 // Bound as the calls above.  Measured: 64 sequences of up to 16384 tokens with a window of 4096 and 4 sinks, 64 / 8 heads of
 // 128, E4M3 (324 MB) 60 us, 5.4 TB/s; one of 700 tokens, 96 heads, 7.4 us; a tree of 8 drafted tokens on 500, 96 heads (13 MB),
-// 9.9 us, a block of eight warps each.  What they cost beside the kernels of tiles: few_columns in attn_extend.cu.
+// 9.9 us, a block of eight warps each.  What they cost beside the kernels of tiles: ways_of in attn_extend.cu.
 #include <cuda_fp16.h>
 
 #ifndef K3_AD_SINKS
@@ -232,7 +232,7 @@ struct AdParams {
   const uint64_t *masks;   // of drafted tokens, or null: each sees those before it
   int words;
   int entries;             // (kRows) items of one head that all sequences' rows make up at most; 0: blocks go by sequence
-  int cols;                // most columns that a key-value head has in a sequence (G without kRows)
+  int cols;                // most columns that a key-value head has in a sequence (G without kRows; with, others are left alone)
   float scale;
   uint16_t *out;
   float *lse;
@@ -288,7 +288,7 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   if constexpr (kSinks) {
     const int o0 = P.offsets[b], o1 = P.offsets[b + 1];
     const bool fine = o0 >= 0 && o1 >= o0 && o1 <= P.rows && o1 - o0 <= P.max_new;
-    s.m = new_ones = fine ? o1 - o0 : 0;
+    s.m = new_ones = fine && (!kRows || (o1 - o0) * P.G <= P.cols) ? o1 - o0 : 0;
     s.row = s.m ? o0 : -1;
     // (one token a sequence: a row of an empty sequence is a batch's empty slot)
     if (report && (!fine || (s.m > s.n && (kRows || len != 0)))) set_status(P.status, K3MOE_DEV_BOUNDS);
@@ -1487,7 +1487,7 @@ long long items_of(const AdParams &P) {
 }
 long long tokens_of(const AdParams &P) {
   const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
-  const long long seen = static_cast<long long>(P.window) + (kSinks ? static_cast<long long>(P.sinks) + P.max_new - 1 : 0);
+  const long long seen = static_cast<long long>(P.window) + (kSinks ? static_cast<long long>(P.sinks) + P.cols / P.G - 1 : 0);
   return P.window > 0 && seen < visible ? seen : visible;
 }
 
@@ -1557,7 +1557,7 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
 #if K3_AD_SINKS == 2
 size_t attn_rows_workspace(const k3moe_kv_cache &c) { return plan_of(c, 16).bytes; }
 
-int launch_attn_rows(const ExtendArgs &a, cudaStream_t st) {
+int launch_attn_rows(const ExtendArgs &a, int most, cudaStream_t st) {
 #else
 int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st) {
 #endif
@@ -1578,8 +1578,12 @@ int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q
                        const int32_t *table, int max_pages, const int32_t *lens, int window, float scale, uint16_t *out,
                        float *lse, void *ws, int32_t *status, cudaStream_t st) {
 #endif
-#if K3_AD_SINKS
-  const AdPlan p = plan_of(c, a.max_new * (Hq / c.heads));
+#if K3_AD_SINKS == 2
+  const int cols = min(most, a.max_new * (Hq / c.heads));
+  const AdPlan p = plan_of(c, cols);
+#elif K3_AD_SINKS
+  const int cols = Hq / c.heads;  // (a.max_new is 1)
+  const AdPlan p = plan_of(c, cols);
 #else
   const AdPlan p = plan_of(c, Hq / c.heads);
 #endif
@@ -1592,7 +1596,7 @@ int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q
   P.window = window, P.scale = scale, P.out = out, P.lse = lse;
 #if K3_AD_SINKS
   P.offsets = a.offsets, P.rows = a.rows, P.sinks = a.sinks, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
-  P.cols = a.max_new * P.G;
+  P.cols = cols;
   P.entries = kRows ? entries_of(P, 8 * p.NT) : 0;
 #else
   P.offsets = nullptr, P.masks = nullptr, P.rows = P.sinks = P.max_new = P.words = P.entries = 0;

@@ -83,6 +83,7 @@ struct AxParams {
   long long q_stride;
   const int32_t *offsets;
   int max_new;
+  int others;  // sequences of at most this many rows a head are left alone
   const uint64_t *masks;
   int words;
   const int32_t *table;
@@ -119,7 +120,7 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
   s.m = 0;
   if (o0 < 0 || o1 < o0 || o1 > P.rows || o1 - o0 > P.max_new)
     bad = true;
-  else
+  else if ((o1 - o0) * P.G > P.others)
     s.m = o1 - o0;
   s.ctx = s.n - s.m;
   if (s.m > s.n) bad = true;
@@ -1630,23 +1631,33 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
 }  // namespace
 
 namespace {
-// Whether the kernels of few columns (attn_rows.cu) are the faster ones.  They read a sequence's keys and values once for
-// each 16 rows of a head, with little to start and end; those of tiles once for 256 (128 at dim 256), but take 9 to 25 us
-// whatever the work.  So: where a sequence has about 16 rows a head at most; and as long as each 16 rows have an SM, and
-// read little in all.  Measured where the two meet (128 wide, 8 query heads a key):
+// Which kernels take the call: those of few columns (attn_rows.cu), of tiles, or both.  The former read a sequence's keys
+// and values once for each 16 rows of a head, with little to start and end; those of tiles once for 256 (128 at dim 256), but
+// take 9 to 25 us whatever the work.  So the former where each 16 rows have an SM and read little in all; and where a
+// sequence has about 16 rows a head, taken over the batch.  Measured where the two meet (128 wide, 8 query heads a key):
 //   16 items, E4M3   30000 tokens  37 and 50 us        128 items, E4M3   1000 tokens  19 and 27 us
 //   32                6000         22     34                             6000         55     42
 //                    30000         62     52             128, bf16       100           8     16
 //   64                6000         36     36                             1000         26     21
-bool few_columns(const ExtendArgs &a) {
+// One sequence of such a batch may have many rows, a prompt beside single tokens.  Where the host's bounds allow that its
+// reads by 16 rows pass kApart bytes, both kinds are launched, and each sequence is its rows' kind's.  255 single tokens on
+// 1000 and a prompt of 3800, 96 / 96 heads, E4M3: 11630 us in columns, 3890 in tiles, 2170 in both; 32 / 32 heads, bf16: 5620,
+// 1260, 940; a prompt of 257 beside tokens on 4000, 64 / 8 heads, E4M3: 725, 1050, 507.  Launches without work cost 18 us
+// (256 sequences of 2 tokens on 2000 with max_new left at all rows 285 and 307).
+enum class Ways { kFew, kTiles, kBoth };
+constexpr double kApart = 1e9;
+constexpr int kFewRows = 32;  // (kBoth) most rows a head of a sequence in columns (56 of 40 beside 200 of 8: 601 us for 686 in columns)
+Ways ways_of(const ExtendArgs &a) {
   const k3moe_kv_cache &c = a.c;
-  const long long columns = static_cast<long long>(a.rows) * (a.Hq / c.heads);
+  const long long G = a.Hq / c.heads, columns = a.rows * G;
   const long long items = c.heads * max(static_cast<long long>(a.B), (columns + 15) / 16);
   const long long places = static_cast<long long>(a.max_pages) * c.page_size;
   const long long seen = a.window > 0 ? min(places, static_cast<long long>(a.window) + a.sinks + a.max_new) : places;
   const bool e = c.format == K3MOE_KV_E4M3;
-  const double bytes = static_cast<double>(items) * seen * 2 * c.dim * (e ? 1 : 2);
-  return columns <= 16LL * a.B || (items <= sm_count() && bytes <= (e ? 64e6 : 38e6) * (1 + 48.0 / items));
+  const double bytes = static_cast<double>(seen) * 2 * c.dim * (e ? 1 : 2);  // of an item
+  if (items <= sm_count() && items * bytes <= (e ? 64e6 : 38e6) * (1 + 48.0 / items)) return Ways::kFew;
+  if (columns > 16LL * a.B) return Ways::kTiles;
+  return static_cast<double>(a.max_new) * G / 16 * c.heads * bytes > kApart && a.max_new * G > kFewRows ? Ways::kBoth : Ways::kFew;
 }
 }  // namespace
 
@@ -1657,7 +1668,11 @@ size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq) {
 
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   if (a.max_new == 1 && !a.masks) return launch_attn_sinks(a, st);
-  if (few_columns(a)) return launch_attn_rows(a, st);
+  const Ways ways = ways_of(a);
+  if (ways != Ways::kTiles) {
+    const int rc = launch_attn_rows(a, ways == Ways::kBoth ? kFewRows : INT32_MAX, st);
+    if (rc || ways == Ways::kFew) return rc;
+  }
   AxParams P;
   const k3moe_kv_cache &c = a.c;
   P.k = static_cast<const uint8_t *>(c.k), P.v = static_cast<const uint8_t *>(c.v), P.ks = c.k_scales, P.vs = c.v_scales;
@@ -1667,6 +1682,7 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   P.q = a.q, P.q_stride = a.q_stride, P.offsets = a.offsets, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
   P.table = a.table, P.max_pages = a.max_pages, P.lens = a.lens, P.window = a.window, P.sinks = a.sinks;
   P.scale = a.scale, P.out = a.out, P.lse = a.lse, P.status = a.status;
+  P.others = ways == Ways::kBoth ? kFewRows : 0;
   const AxSpace s = space_of(c, a.B, a.rows, a.Hq);
   uint8_t *w = static_cast<uint8_t *>(a.ws);
   P.plan = reinterpret_cast<AxPlan *>(w + s.plan), P.start = reinterpret_cast<AxStart *>(w + s.start);

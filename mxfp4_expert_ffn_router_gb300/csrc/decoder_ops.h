@@ -41,10 +41,11 @@ struct ExtendArgs {
   int32_t *status;
 };
 // The same for at most one new token a sequence, without masks (attn_sinks.cu), and where a key-value head's rows of a
-// sequence are few (attn_rows.cu); the workspace is that of both.
+// sequence are few (attn_rows.cu: rows of sequences with more than `most` of them a head are left alone); the workspace is
+// that of both.
 size_t attn_rows_workspace(const k3moe_kv_cache &c);
 int launch_attn_sinks(const ExtendArgs &a, cudaStream_t st);
-int launch_attn_rows(const ExtendArgs &a, cudaStream_t st);
+int launch_attn_rows(const ExtendArgs &a, int most, cudaStream_t st);
 size_t attn_extend_workspace(const k3moe_kv_cache &c, int B, int rows, int Hq);
 int launch_attn_extend(const ExtendArgs &a, cudaStream_t st);
 
