@@ -903,7 +903,8 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         }
         ++uses[sb];
         tc_fence_after();
-        if (E4M3 && first) c = c1 * sh.row_scale[(turn - 1) & 1][st][lrow];
+        // (not 0, times which a reference of -inf would be NaN; raw scores are below 2^128, so that they count for nothing)
+        if (E4M3 && first) c = fmaxf(c1 * sh.row_scale[(turn - 1) & 1][st][lrow], 0x1p-149f);
         if (warp_on) {
           const float *ks = nullptr;
           if constexpr (E4M3) ks = sh.key_scale[(tiles_before + u) & 7];
