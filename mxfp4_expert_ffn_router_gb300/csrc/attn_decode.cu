@@ -369,6 +369,7 @@ struct Walk {
 // sequence of n places, its last m in rows `row` on, sees: bit j.  Called, not inlined: it is seldom needed.
 __device__ __noinline__ uint32_t column_sees(const AdParams &P, int n, int m, int row, int col, int place, int count) {
   const int i = min(col / P.G, m - 1), ctx = n - m;
+  if (ctx + i < 0) return 0u;  // (more new tokens than cached ones: it has no place)
   const uint64_t *mask = P.masks + (P.masks ? (static_cast<long long>(row) + i) * P.words : 0);
   int pos = ctx + i;
   if (P.masks && P.window > 0) {

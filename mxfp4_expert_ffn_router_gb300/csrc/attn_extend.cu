@@ -532,7 +532,7 @@ __device__ __forceinline__ void scale_keys(float (&v)[M], const float *ks) {
 
 // What a row sees.
 struct Row {
-  int hi, lo;            // (causal) last place seen; first of the window
+  int hi, lo;            // its place, the last one that it sees (causal; below 0: it has none); first of the window
   const uint32_t *mask;  // (drafted) its words
   bool on;               // a row of the item
 };
@@ -540,6 +540,7 @@ struct Row {
 __device__ __forceinline__ uint32_t sees(const AxParams &P, const AxItem &s, const Row &row, int c) {
   const uint32_t win = P.window > 0 ? ~below(row.lo - c) | below(P.sinks - c) : 0xFFFFFFFFu;
   if (!P.masks) return below(row.hi + 1 - c) & win;
+  if (row.hi < 0) return 0u;
   uint32_t v = below(s.ctx - c) & win;
   const int j = c - s.ctx;  // the new token that bit 0 stands for
   if (j > -32 && j < s.m) {
@@ -885,7 +886,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
         for (int w = 0; 32 * w < I.m; ++w) seen += __popc(row.mask[w] & below(I.m - 32 * w));
         pos = I.ctx + max(0, seen - 1);
       }
-      row.hi = pos;
+      row.hi = I.ctx + i;
       row.lo = P.window > 0 && pos >= P.window ? pos - P.window + 1 : 0;
       const bool warp_on = (both ? 128 * st : 0) + 32 * (warp & 3) < I.rows;
       float m = -INFINITY, l = 0.f;  // the reference, in scores; the weights' sum
