@@ -463,8 +463,9 @@ int k3moe_kv_append(const k3moe_kv_cache *cache, int32_t n, int32_t Hq, const ui
  * where max_new or rows is 1, a row of a sequence of length 0 is an empty slot of the batch: nothing is set).
  * Accumulation: exact products summed in fp32, softmax in fp32; the weights are rounded before
  * the product with V: to bf16 where a sequence has many rows; where it has few, or max_new is 1, as in
- * k3moe_attn_decode.  Over an E4M3 cache with many rows a query row counts to 2^-19 of its largest value
- * (exact above 2^-10 of it), one that holds an infinity gives NaN, and so may keys beyond 2^110.
+ * k3moe_attn_decode.  Over an E4M3 cache with many rows a query row counts to 2^-17 of its largest value
+ * (exact from 2^-9 of it on; with few rows from 2^-28 on), one that holds an infinity gives NaN, and so may keys
+ * beyond 2^110.
  * Calls that run at the same time, captured ones too, need workspaces of their own.
  * Hq a multiple of heads, Hq <= 16384, 0 <= B <= 65535, window and sinks >= 0, max_pages >= 1, rows * Hq / heads
  * below 2^31. */

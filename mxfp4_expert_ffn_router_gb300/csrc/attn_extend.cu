@@ -20,9 +20,10 @@
 // 32 KB), three tiles of keys and two of values at 128 wide.
 //
 // E4M3: keys are operands as they are stored (kind::f8f6f4).  A query row, times a power of two that brings its largest value
-// into [128, 256), is the sum of two E4M3 numbers (exact down to 2^-10 of the row's largest; below that an error of 2^-19 of
-// it), each with a product of its own, and the raw score is scaled by the key's and the row's power of two.  Values become
-// bf16 exactly: codes shifted into place and times one bf16 power of two.
+// into [128, 256), is the sum of two E4M3 numbers, each with a product of its own, and the raw score is scaled by the key's
+// and the row's power of two.  The second number's smallest step is 2^-9: the sum is exact from 2^-2 on, 2^-9 of the row's
+// largest, and below that off by 2^-10 at most, 2^-17 of it (a row with one large channel loses bits of the others).  Values
+// become bf16 exactly: codes shifted into place and times one bf16 power of two.
 //
 // Roundings: a weight to bf16 once, by 2^-8 of itself at most, as the output is; l sums the weights before that.  (As two
 // bf16 numbers, 16 bits, the products with V are twice as many: a prompt of 8192 took 1064 us for 919.)
