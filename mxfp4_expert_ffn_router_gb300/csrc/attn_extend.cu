@@ -26,7 +26,7 @@
 // become bf16 exactly: codes shifted into place and times one bf16 power of two.
 //
 // Roundings: a weight to bf16 once, by 2^-8 of itself at most, as the output is; l sums the weights before that.  (As two
-// bf16 numbers, 16 bits, the products with V are twice as many: a prompt of 8192 took 1064 us for 919.)
+// bf16 numbers, 16 bits, the products with V are twice as many, which takes a prompt of 8192 16 % more time.)
 //
 // How the work is cut.  Where the items fill at most one block an SM: one block an item, or several to a long item.
 // Otherwise a line of all items' tiles is cut into equal pieces, one an SM, by a kernel of one block, and pieces of cut items are
@@ -37,14 +37,14 @@
 // alternate.  Measured 3700 clocks (bf16) and 5500 (E4M3, whose values' conversion runs on the same schedulers, 900 to
 // 1400 clocks, and pulls the streams into step): waits for loads from tensor memory, for barriers and for instructions, of which a
 // pass over this code needs more than the nearest cache holds.
-//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   853 us, 968 TFLOP/s (0.51 of a large product's rate)
-//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   322 us, 801 TFLOP/s; 0.85 TB/s
-//   64 drafted tokens on each of 16 sequences up to 16384, E4M3:       170 us, 307 TFLOP/s
-//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      188 us, 433 TFLOP/s
-//   24 prompts of up to 301 tokens, 16 heads on one of 64, bf16:        26 us: launch, first tile, end
+//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   864 us, 956 TFLOP/s (0.51 of a large product's rate)
+//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   325 us, 793 TFLOP/s; 0.84 TB/s
+//   64 drafted tokens on each of 16 sequences up to 16384, E4M3:       170 us, 307 TFLOP/s (bf16: 138)
+//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      185 us, 440 TFLOP/s (bf16: 143)
+//   24 prompts of up to 301 tokens, 16 heads on one of 64, bf16:        26 us: first tile, few steps, end
 // Tried without gain: registers moved from the other warps to the softmax warps; eight warps for the values; a handshake a step that
 // holds the second stream half a step behind; helpers called instead of inlined; scores 32 at a time; the
-// next item's queries asked for a step earlier (prompt 846 -> 854 us, chunks 189 -> 197: longer code).
+// next item's queries asked for a step earlier (1 % more for a prompt, 4 % for chunks: longer code).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -60,8 +60,13 @@ namespace {
 
 constexpr int kAxThreads = 512;    // warps 0-7 softmax, 8 and 10 products, 9 loads, 11 the keys' scales, 12-15 values
 constexpr int kAxMostBlocks = 160; // pieces of the line (bounds the workspace)
-constexpr int kItemLen = 3;        // what an item costs besides its tiles, in units of the line
-constexpr int kPartTiles = 2;      // (direct) fewest tiles that a part of the longest item may have
+// What an item costs besides its tiles, in units of the line (a tile of up to 128 rows is one, of more two).  Prompt of 4096, 64 / 8
+// heads, bf16, with 1, 2, 3, 5 and 8: 352, 342, 327, 316 and 314 us; 6 ragged chunks, 32 / 4 heads, E4M3: 417, 414, 393, 364
+// and 335; 16 trees, 64 / 8 heads, bf16: 266, 266, 271, 271 and 274; 7 trees, 256 wide: 59, 59, 59, 61 and 63.
+constexpr int kItemLen = 3;
+// (direct) Fewest tiles that a part of the longest item may have.  1, 2 and 4 take the same time within 2 us, but for 3
+// sequences of 100 tokens on 1000, 32 / 4 heads, bf16, where it is 29, 33 and 33.
+constexpr int kPartTiles = 2;
 constexpr int kJoinParts = 4;      // parts that are added at once
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -783,7 +788,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
     const int lrow = 32 * (warp & 3) + lane;
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16, oa = tmem + lane_addr + S::O_COL + st * S::O_COLS;
     // Whether a tile's second half of scores is loaded while the first one's weights are computed, in code without a loop: over
-    // bf16 a prompt takes 891 us for 919, over E4M3 chunks 214 for 187, by the longer code and its registers.
+    // bf16 a prompt takes 3 % less time so, over E4M3 chunks 14 % more, by the longer code and its registers.
     constexpr bool AHEAD = !E4M3;
     const bool flat = fabsf(P.scale) * kLog2e == 0.f;  // (queries of zeros then)
     const float c1 = flat ? 1.f : fabsf(P.scale) * kLog2e;
@@ -1203,7 +1208,7 @@ __global__ void __launch_bounds__(kAxThreads, 1)
             }
             if (!ok) break;
             ++uses[sb];
-            // (E4M3: the next values are converted meanwhile, 338 -> 325 us of a long tree; bf16: no difference to the copies)
+            // (E4M3: the next values are converted meanwhile, 4 % of a long tree; bf16: no difference to the copies)
             if (E4M3) commit(&sh.v_empty[slot]);
             if (k + 2 < K) ok = scores(k + 2);
             if (!E4M3) commit(&sh.v_empty[slot]);
@@ -1613,7 +1618,10 @@ int launch_extend(const k3moe_kv_cache &c, AxParams &P, cudaStream_t st) {
   const long long items = static_cast<long long>(P.entries) * P.heads;
   P.parts = 0;
   if (items <= P.blocks) {
-    // (not where the bound of the items would leave SMs idle for long: a plan shares those evenly)
+    // (Not where parts are long, past 12 tiles, and the items that there must be fill less than 17 of 20 blocks: a plan shares
+    // them evenly.  Direct and planned: 4 sequences of 60 on 20000, 32 / 4 heads, E4M3, 166 and 127 us; 8 ragged ones 66 and
+    // 59; 7 of 13, 256 wide, bf16, 68 and 58; but 2 of 200 on 8000, 32 / 4, bf16, 87 and 102.  Short parts: one of 60 on 16000,
+    // 64 / 8, E4M3, 67 and 73; 2 of 60 on 4000 42 and 49; 3 of 100 on 1000 33 and 42.)
     const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
     const long long seen = P.window > 0 ? min(visible, static_cast<long long>(P.window) + P.sinks + S::ROWS / P.G) : visible;
     P.parts = static_cast<int>(max(1LL, min(P.blocks / items, seen / (kPartTiles * S::TN))));
@@ -1642,6 +1650,8 @@ namespace {
 //   32                6000         22     34                             6000         55     42
 //                    30000         62     52             128, bf16       100           8     16
 //   64                6000         36     36                             1000         26     21
+// Other widths go by the bytes (E4M3): 16 items on 30000, 64 wide, 39 and 60 us, 256 wide 128 and 118; 64 items on 6000 29
+// and 36, 100 and 69; 256 items on 1000, which are the tiles', 23 and 27, 42 and 65.
 // One sequence of such a batch may have many rows, a prompt beside single tokens.  Where the host's bounds allow that its
 // reads by 16 rows pass kApart bytes, both kinds are launched, and each sequence is its rows' kind's.  255 single tokens on
 // 1000 and a prompt of 3800, 96 / 96 heads, E4M3: 11630 us in columns, 3890 in tiles, 2170 in both; 32 / 32 heads, bf16: 5620,

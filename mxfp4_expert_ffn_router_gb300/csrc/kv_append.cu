@@ -15,9 +15,9 @@
 //
 // Bound by memory where there are many tokens, and by launch and two trips to it where there are few.  A block takes four
 // tokens (one where that leaves SMs idle), whose sines and cosines its threads compute once for all heads; a lane has two vectors' loads
-// under way (one: 39.1 us for 36.2).  Measured: 4096 tokens, 64 query and 8 key-value heads of 128, E4M3 (159 MB) 36.2 us, 4.4
-// TB/s, 0.65 of a copy's rate: issue 49 %, 63 registers, the rest waits for the loads of a block's one or two turns; 777 tokens
-// of 15 / 5 heads of 64, bf16, 3.1 us; 13 tokens of 96 / 96 heads 3 us.
+// under way (one: 39.1 us).  Measured: 4096 tokens, 64 query and 8 key-value heads of 128, E4M3 (159 MB) 36.2 us, 4.4
+// TB/s, 0.65 of a copy's rate: issue 49 %, 63 registers, the rest waits for the loads of a block's one or two turns; bf16 (168 MB)
+// 33.8 us, 5.0 TB/s; 777 tokens of 15 / 5 heads of 64, bf16, 3.3 us; 13 tokens of 96 / 96 heads 3 us (bf16 2.5).
 #include <type_traits>
 
 #include "decoder_ops.h"
