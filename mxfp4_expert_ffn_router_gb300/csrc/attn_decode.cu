@@ -1544,7 +1544,9 @@ int launch_attn(const AdParams &P, cudaStream_t st) {
     return start<D, E4M3, NT, 4, true>(P, items, 1, st) == cudaSuccess ? 0 : -1;
   long long blocks = static_cast<long long>(sm_count()) * S::BLOCKS;
   if (blocks > kAdMostBlocks) blocks = kAdMostBlocks;
-  const long long most = (items * ((tokens + S::RUN + S::UNIT - 2) / S::UNIT * S::UNIT) + kMinTokens - 1) / kMinTokens;
+  // (more items than this fill the GPU however short they are; the product stays within 64 bits)
+  const long long units = (tokens + S::RUN + S::UNIT - 2) / S::UNIT;
+  const long long most = items > (1 << 20) ? blocks : (items * (units * S::UNIT) + kMinTokens - 1) / kMinTokens;
   if (blocks > most) blocks = most;
   if (start<D, E4M3, NT, 4, false>(P, blocks, 1, st) != cudaSuccess) return -1;
   return launch_pdl(attn_join_kernel<D, E4M3, NT>, dim3(static_cast<unsigned>(blocks)), dim3(kJoinWarps * 32), 0, st, P) == cudaSuccess
