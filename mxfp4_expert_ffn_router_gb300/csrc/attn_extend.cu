@@ -1659,9 +1659,7 @@ namespace {
 // (256 sequences of 2 tokens on 2000 with max_new left at all rows 285 and 307).
 enum class Ways { kFew, kTiles, kBoth };
 constexpr double kApart = 1e9;
-// (kBoth) Most rows a head of a sequence in columns, but for those of one token: 56 sequences of 40 beside 200 of 8 take 601 us
-// so, and 686 with all in columns.
-int most_in_columns(const ExtendArgs &a) { return max(32, a.Hq / a.c.heads); }
+constexpr int kFewRows = 32;  // (kBoth) most rows a head of a sequence in columns (56 of 40 beside 200 of 8: 601 us for 686 in columns)
 Ways ways_of(const ExtendArgs &a) {
   const k3moe_kv_cache &c = a.c;
   const long long G = a.Hq / c.heads, columns = a.rows * G;
@@ -1672,7 +1670,7 @@ Ways ways_of(const ExtendArgs &a) {
   const double bytes = static_cast<double>(seen) * 2 * c.dim * (e ? 1 : 2);  // of an item
   if (items <= sm_count() && items * bytes <= (e ? 64e6 : 38e6) * (1 + 48.0 / items)) return Ways::kFew;
   if (columns > 16LL * a.B) return Ways::kTiles;
-  return static_cast<double>(a.max_new) * G / 16 * c.heads * bytes > kApart && a.max_new * G > most_in_columns(a) ? Ways::kBoth : Ways::kFew;
+  return static_cast<double>(a.max_new) * G / 16 * c.heads * bytes > kApart && a.max_new * G > kFewRows ? Ways::kBoth : Ways::kFew;
 }
 }  // namespace
 
@@ -1685,7 +1683,7 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   if (a.max_new == 1 && !a.masks) return launch_attn_sinks(a, st);
   const Ways ways = ways_of(a);
   if (ways != Ways::kTiles) {
-    const int rc = launch_attn_rows(a, ways == Ways::kBoth ? most_in_columns(a) : INT32_MAX, st);
+    const int rc = launch_attn_rows(a, ways == Ways::kBoth ? kFewRows : INT32_MAX, st);
     if (rc || ways == Ways::kFew) return rc;
   }
   AxParams P;
@@ -1697,7 +1695,7 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   P.q = a.q, P.q_stride = a.q_stride, P.offsets = a.offsets, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
   P.table = a.table, P.max_pages = a.max_pages, P.lens = a.lens, P.window = a.window, P.sinks = a.sinks;
   P.scale = a.scale, P.out = a.out, P.lse = a.lse, P.status = a.status;
-  P.others = ways == Ways::kBoth ? most_in_columns(a) : 0;
+  P.others = ways == Ways::kBoth ? kFewRows : 0;
   const AxSpace s = space_of(c, a.B, a.rows, a.Hq);
   uint8_t *w = static_cast<uint8_t *>(a.ws);
   P.plan = reinterpret_cast<AxPlan *>(w + s.plan), P.start = reinterpret_cast<AxStart *>(w + s.start);

@@ -59,19 +59,3 @@ def test_captured():
     c.out.fill_(9), c.lse.fill_(9)
     graph.replay()
     assert torch.equal(c.out, good[0]) and torch.equal(c.lse, good[1])
-
-
-@pytest.mark.parametrize("fmt", [E4, BF])
-def test_one_token_s_heads_stay_together(fmt):
-    """More query heads a key than a sequence of the kernels of few rows has rows: single tokens are theirs all the same."""
-    plan = [(60 + b % 90, b % 3 == 0) for b in range(200)]
-    plan = [(n, 1) if m else (0, 0) for n, m in plan]
-    plan[33] = (50, 9)
-    c = ExtendCase(plan, 40, 1, 64, 32, fmt, seed=3)
-    table = np.pad(c.table, ((0, 0), (0, 60000 - c.table.shape[1])), constant_values=-1)
-    look = lambda b, i: b % 15 == 0 or b == 33  # noqa: E731
-    c.check(*c.run(table=table), rows=look)
-    singles, prompt = [(2000, 1)] * 100 + [(0, 0)] * 200, [(0, 19)]
-    both, a, b = (LargeCase(p, 40, 1, 128, 64, fmt, width=2000) for p in (singles + prompt, singles, prompt))
-    t, parts = both.us(), a.us(max_new=1) + b.us()
-    assert t < 2 * parts + 60, (t, parts)
