@@ -1659,7 +1659,9 @@ namespace {
 // (256 sequences of 2 tokens on 2000 with max_new left at all rows 285 and 307).
 enum class Ways { kFew, kTiles, kBoth };
 constexpr double kApart = 1e9;
-constexpr int kFewRows = 32;  // (kBoth) most rows a head of a sequence in columns (56 of 40 beside 200 of 8: 601 us for 686 in columns)
+// (kBoth) Most rows a head of a sequence in columns.  56 sequences of 40 rows beside 200 of 8: 686 us in columns, 601 so; 250 single
+// tokens of 64 / 4 heads on 2000: 561 and 410, of 128 / 1 heads of 256 in bf16 on 3000: 233 and 232.
+constexpr int kFewRows = 32;
 Ways ways_of(const ExtendArgs &a) {
   const k3moe_kv_cache &c = a.c;
   const long long G = a.Hq / c.heads, columns = a.rows * G;
@@ -1670,7 +1672,8 @@ Ways ways_of(const ExtendArgs &a) {
   const double bytes = static_cast<double>(seen) * 2 * c.dim * (e ? 1 : 2);  // of an item
   if (items <= sm_count() && items * bytes <= (e ? 64e6 : 38e6) * (1 + 48.0 / items)) return Ways::kFew;
   if (columns > 16LL * a.B) return Ways::kTiles;
-  return static_cast<double>(a.max_new) * G / 16 * c.heads * bytes > kApart && a.max_new * G > kFewRows ? Ways::kBoth : Ways::kFew;
+  if (static_cast<double>(a.max_new) * G / 16 * c.heads * bytes <= kApart || a.max_new * G <= kFewRows) return Ways::kFew;
+  return G > kFewRows ? Ways::kTiles : Ways::kBoth;
 }
 }  // namespace
 

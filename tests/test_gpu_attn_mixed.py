@@ -59,3 +59,13 @@ def test_captured():
     c.out.fill_(9), c.lse.fill_(9)
     graph.replay()
     assert torch.equal(c.out, good[0]) and torch.equal(c.lse, good[1])
+
+
+@pytest.mark.parametrize("fmt", [E4, BF])
+def test_single_tokens_of_many_heads(fmt):
+    """More query heads a key than a sequence of the kernels of few rows has rows: the tiles take single tokens too."""
+    plan = [(60 + b % 90, 1) if b % 3 == 0 else (0, 0) for b in range(200)]
+    plan[33] = (50, 9)
+    c = ExtendCase(plan, 40, 1, 64, 32, fmt, seed=3)
+    table = np.pad(c.table, ((0, 0), (0, 60000 - c.table.shape[1])), constant_values=-1)
+    c.check(*c.run(table=table), rows=lambda b, i: b % 15 == 0 or b == 33)
