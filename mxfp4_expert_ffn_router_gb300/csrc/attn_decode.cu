@@ -229,10 +229,11 @@ struct AdParams {
   int window;
   const int32_t *offsets;  // (kSinks) first row of each sequence
   int rows, sinks, max_new;
+  int own;                 // (kSinks) sequences of more new tokens are left alone; max_new at most
   const uint64_t *masks;   // of drafted tokens, or null: each sees those before it
   int words;
   int entries;             // (kRows) items of one head that all sequences' rows make up at most; 0: blocks go by sequence
-  int cols;                // most columns that a key-value head has in a sequence (G without kRows; with, others are left alone)
+  int cols;                // most columns that a key-value head has in a sequence (G without kRows)
   float scale;
   uint16_t *out;
   float *lse;
@@ -287,11 +288,11 @@ __device__ __forceinline__ Seen seen_of(const AdParams &P, int b, bool report) {
   int new_ones = 1;
   if constexpr (kSinks) {
     const int o0 = P.offsets[b], o1 = P.offsets[b + 1];
-    const bool fine = o0 >= 0 && o1 >= o0 && o1 <= P.rows && o1 - o0 <= P.max_new;
-    s.m = new_ones = fine && (!kRows || (o1 - o0) * P.G <= P.cols) ? o1 - o0 : 0;
+    const bool fine = o0 >= 0 && o1 >= o0 && o1 <= P.rows;
+    s.m = new_ones = fine && o1 - o0 <= P.own ? o1 - o0 : 0;
     s.row = s.m ? o0 : -1;
     // (one token a sequence: a row of an empty sequence is a batch's empty slot)
-    if (report && (!fine || (s.m > s.n && (kRows || len != 0)))) set_status(P.status, K3MOE_DEV_BOUNDS);
+    if (report && (!fine || o1 - o0 > P.max_new || (s.m > s.n && (kRows || len != 0)))) set_status(P.status, K3MOE_DEV_BOUNDS);
   }
   s.lo = P.window > 0 && s.n - new_ones >= P.window ? s.n - new_ones - P.window + 1 : 0;  // (of the first of them)
   s.t0 = s.lo & ~(RUN - 1);
@@ -369,7 +370,6 @@ struct Walk {
 // sequence of n places, its last m in rows `row` on, sees: bit j.  Called, not inlined: it is seldom needed.
 __device__ __noinline__ uint32_t column_sees(const AdParams &P, int n, int m, int row, int col, int place, int count) {
   const int i = min(col / P.G, m - 1), ctx = n - m;
-  if (ctx + i < 0) return 0u;  // (more new tokens than cached ones: it has no place)
   const uint64_t *mask = P.masks + (P.masks ? (static_cast<long long>(row) + i) * P.words : 0);
   int pos = ctx + i;
   if (P.masks && P.window > 0) {
@@ -384,7 +384,7 @@ __device__ __noinline__ uint32_t column_sees(const AdParams &P, int n, int m, in
     if (!P.masks)
       on = on && at <= pos;
     else if (at >= ctx)
-      on = at < n && ((mask[(at - ctx) >> 6] >> ((at - ctx) & 63)) & 1u);
+      on = at < n && ctx + i >= 0 && ((mask[(at - ctx) >> 6] >> ((at - ctx) & 63)) & 1u);
     bits |= static_cast<uint32_t>(on) << j;
   }
   return bits;
@@ -1488,7 +1488,7 @@ long long items_of(const AdParams &P) {
 }
 long long tokens_of(const AdParams &P) {
   const long long visible = static_cast<long long>(P.max_pages) << P.page_shift;
-  const long long seen = static_cast<long long>(P.window) + (kSinks ? static_cast<long long>(P.sinks) + P.cols / P.G - 1 : 0);
+  const long long seen = static_cast<long long>(P.window) + (kSinks ? static_cast<long long>(P.sinks) + P.own - 1 : 0);
   return P.window > 0 && seen < visible ? seen : visible;
 }
 
@@ -1599,10 +1599,10 @@ int launch_attn_decode(const k3moe_kv_cache &c, int B, int Hq, const uint16_t *q
   P.window = window, P.scale = scale, P.out = out, P.lse = lse;
 #if K3_AD_SINKS
   P.offsets = a.offsets, P.rows = a.rows, P.sinks = a.sinks, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
-  P.cols = cols;
+  P.cols = cols, P.own = cols / P.G;
   P.entries = kRows ? entries_of(P, 8 * p.NT) : 0;
 #else
-  P.offsets = nullptr, P.masks = nullptr, P.rows = P.sinks = P.max_new = P.words = P.entries = 0;
+  P.offsets = nullptr, P.masks = nullptr, P.rows = P.sinks = P.max_new = P.own = P.words = P.entries = 0;
   P.cols = P.G;
 #endif
   uint8_t *w = static_cast<uint8_t *>(ws);

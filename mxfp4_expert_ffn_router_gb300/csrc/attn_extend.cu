@@ -37,10 +37,10 @@
 // alternate.  Measured 3700 clocks (bf16) and 5500 (E4M3, whose values' conversion runs on the same schedulers, 900 to
 // 1400 clocks, and pulls the streams into step): waits for loads from tensor memory, for barriers and for instructions, of which a
 // pass over this code needs more than the nearest cache holds.
-//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   864 us, 956 TFLOP/s (0.51 of a large product's rate)
-//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   325 us, 793 TFLOP/s; 0.84 TB/s
+//   8192 tokens of a prompt, 64 / 8 heads of 128, window 4096, bf16:   853 us, 968 TFLOP/s (0.51 of a large product's rate)
+//   60 drafted tokens on 131072, 64 / 8 heads, E4M3:                   322 us, 801 TFLOP/s; 0.85 TB/s
 //   64 drafted tokens on each of 16 sequences up to 16384, E4M3:       170 us, 307 TFLOP/s (bf16: 138)
-//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      185 us, 440 TFLOP/s (bf16: 143)
+//   chunks of up to 1000 tokens of 6 sequences up to 12000, E4M3:      187 us, 435 TFLOP/s (bf16: 143)
 //   24 prompts of up to 301 tokens, 16 heads on one of 64, bf16:        26 us: first tile, few steps, end
 // Tried without gain: registers moved from the other warps to the softmax warps; eight warps for the values; a handshake a step that
 // holds the second stream half a step behind; helpers called instead of inlined; scores 32 at a time; the
@@ -89,7 +89,7 @@ struct AxParams {
   long long q_stride;
   const int32_t *offsets;
   int max_new;
-  int others;  // sequences of at most this many rows a head are left alone
+  int others;  // sequences of at most this many new tokens are left alone
   const uint64_t *masks;
   int words;
   const int32_t *table;
@@ -126,7 +126,7 @@ __device__ __forceinline__ Seq seq_of(const AxParams &P, int b, bool report) {
   s.m = 0;
   if (o0 < 0 || o1 < o0 || o1 > P.rows || o1 - o0 > P.max_new)
     bad = true;
-  else if ((o1 - o0) * P.G > P.others)
+  else if (o1 - o0 > P.others)
     s.m = o1 - o0;
   s.ctx = s.n - s.m;
   if (s.m > s.n) bad = true;
@@ -536,9 +536,11 @@ __device__ __forceinline__ void scale_keys(float (&v)[M], const float *ks) {
   }
 }
 
+__device__ const uint32_t g_no_mask[32] = {};  // of a drafted token that sees nothing
+
 // What a row sees.
 struct Row {
-  int hi, lo;            // its place, the last one that it sees (causal; below 0: it has none); first of the window
+  int hi, lo;            // its place (causal: the last that it sees; below 0: it has none); first of the window
   const uint32_t *mask;  // (drafted) its words
   bool on;               // a row of the item
 };
@@ -546,10 +548,9 @@ struct Row {
 __device__ __forceinline__ uint32_t sees(const AxParams &P, const AxItem &s, const Row &row, int c) {
   const uint32_t win = P.window > 0 ? ~below(row.lo - c) | below(P.sinks - c) : 0xFFFFFFFFu;
   if (!P.masks) return below(row.hi + 1 - c) & win;
-  if (row.hi < 0) return 0u;
   uint32_t v = below(s.ctx - c) & win;
   const int j = c - s.ctx;  // the new token that bit 0 stands for
-  if (j > -32 && j < s.m) {
+  if (j > -32 && j < s.m && row.hi >= 0) {  // (a row without a place has no context: this is all that it could see)
     const int at = j >> 5, most = 2 * P.words;
     const uint32_t w0 = at >= 0 && at < most ? row.mask[at] : 0u;
     const uint32_t w1 = at + 1 >= 0 && at + 1 < most ? row.mask[at + 1] : 0u;
@@ -1698,7 +1699,7 @@ int launch_attn_extend(const ExtendArgs &a, cudaStream_t st) {
   P.q = a.q, P.q_stride = a.q_stride, P.offsets = a.offsets, P.max_new = a.max_new, P.masks = a.masks, P.words = a.words;
   P.table = a.table, P.max_pages = a.max_pages, P.lens = a.lens, P.window = a.window, P.sinks = a.sinks;
   P.scale = a.scale, P.out = a.out, P.lse = a.lse, P.status = a.status;
-  P.others = ways == Ways::kBoth ? kFewRows : 0;
+  P.others = ways == Ways::kBoth ? kFewRows / P.G : 0;
   const AxSpace s = space_of(c, a.B, a.rows, a.Hq);
   uint8_t *w = static_cast<uint8_t *>(a.ws);
   P.plan = reinterpret_cast<AxPlan *>(w + s.plan), P.start = reinterpret_cast<AxStart *>(w + s.start);
